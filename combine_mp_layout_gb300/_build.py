@@ -1,6 +1,6 @@
 """Builds the in-tree CUDA library ``libmp_layout.so`` for sm_103a.
 
-The three translation units are compiled in parallel with nvcc and linked
+The translation units are compiled in parallel with nvcc and linked
 into a shared library next to this file (no torch extension machinery, no
 cmake).  Intermediate objects go to ``_build/`` at the repository root.
 """
@@ -15,7 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmp_layout.so")
-UNITS = ["mp_abi", "mp_layout_kernels", "mp_copy_kernels", "mp_noalloc"]
+UNITS = ["mp_abi", "mp_layout_kernels", "mp_copy_kernels", "mp_noalloc", "mp_expert_abi",
+         "mp_route", "mp_expert_matmul", "mp_expert_wgrad", "mp_swiglu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 

@@ -21,8 +21,13 @@ MP_ERR_CUDA = 2
 MP_ERR_CAPACITY = 4
 MP_ERR_BAD_EXPERT = 8
 MP_ERR_TIMEOUT = 16
+MP_ERR_BAD_VALUE = 32
 MP_BF16 = 0
 MP_E4M3 = 1
+MP_FP32 = 2
+# score functions of the router
+MP_SOFTMAX = 0
+MP_SIGMOID = 1
 SCALE_BLOCK = 128
 # formats of the low-latency dispatch's in-kernel quantisation
 MP_Q_E4M3 = 0
@@ -86,6 +91,16 @@ def lib() -> ctypes.CDLL:
         L.mp_dispatch_ll_rows_quant.argtypes = [i32] * 5 + [P, P, i64, P, P, P]
         L.mp_dispatch_ll_quant.argtypes = [i32] * 7 + [P] * 3 + [i64] + [P] * 8
         L.mp_allgatherv_multi.argtypes = [i32, i32, P, P, P, P, P]
+        f32 = ctypes.c_float
+        L.mp_route_workspace_size.argtypes = [i32, i32, i32]
+        L.mp_route_workspace_size.restype = ctypes.c_size_t
+        L.mp_route.argtypes = [i32] * 6 + [P] * 3 + [i32, f32, f32] + [P] * 8
+        L.mp_route_backward.argtypes = [i32] * 6 + [P] * 2 + [i32, f32, f32] + [P] * 7
+        L.mp_expert_matmul_e4m3.argtypes = [i32] * 4 + [P] * 8
+        L.mp_expert_matmul_dgrad_e4m3.argtypes = [i32] * 4 + [P] * 8
+        L.mp_expert_matmul_wgrad_e4m3.argtypes = [i32] * 4 + [P] * 8
+        L.mp_swiglu_e4m3.argtypes = [i32] * 2 + [P] * 6
+        L.mp_swiglu_backward_e4m3.argtypes = [i32] * 2 + [P] * 8
         L.mp_dispatch_ll.argtypes = [i32] * 7 + [P] * 4 + [i64] + [P] * 8
         for f in ("mp_layout", "mp_dispatch", "mp_dispatch_offsets", "mp_dispatch_rows",
                   "mp_dispatch_rows_e4m3", "mp_dispatch_rows_mxfp8", "mp_dispatch_offsets_global",
@@ -97,7 +112,9 @@ def lib() -> ctypes.CDLL:
                   "mp_dispatch_rows_mxfp4", "mp_dispatch_rows_bulk",
                   "mp_layout_and_offsets", "mp_dispatch_noalloc", "mp_allgatherv_multi",
                   "mp_dispatch_ll", "mp_layout_dispatch", "mp_dispatch_ll_rows_quant",
-                  "mp_dispatch_ll_quant"):
+                  "mp_dispatch_ll_quant", "mp_route", "mp_route_backward",
+                  "mp_expert_matmul_e4m3", "mp_expert_matmul_dgrad_e4m3",
+                  "mp_expert_matmul_wgrad_e4m3", "mp_swiglu_e4m3", "mp_swiglu_backward_e4m3"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -417,3 +434,127 @@ def mp_dispatch_ll_quant(R, N, K, E, H, qformat, rank_major, x, topk_idx, num_to
         _dev(recv_src_token, "recv_src_token"), _dev(slot_row, "slot_row"),
         _dev(recv_x, "recv_x"), _dev(recv_scales, "recv_scales"), _dev(dev_err, "dev_err"),
         _stream(stream))
+
+
+def _arr(t, name, dtype, numel):
+    """The device pointer of a dense CUDA tensor of this type with room for `numel` elements."""
+    if t is None:
+        return None
+    p = _dev(t, name)
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    if t.numel() < numel:
+        raise ValueError("%s holds %d elements, %d are needed" % (name, t.numel(), numel))
+    return p
+
+
+def mp_route_workspace_size(R: int, N: int, E: int) -> int:
+    return int(lib().mp_route_workspace_size(R, N, E))
+
+
+def _logits(t, name, numel):
+    if t is not None and t.dtype is torch.bfloat16:
+        return MP_BF16, _arr(t, name, torch.bfloat16, numel)
+    return MP_FP32, _arr(t, name, torch.float32, numel)
+
+
+def mp_route(R, N, K, E, scoring, logits, bias, active, normalize, scale, loss_coef, topk_idx,
+             topk_weights, num_tokens_per_expert, num_routed, balance_loss, dev_err, workspace,
+             stream=None) -> int:
+    """The router: top-K experts, weights, per-expert counts and balance loss of the fp32 or
+    bf16 logits [R][N][E] (see the C header)."""
+    dtype, lp = _logits(logits, "logits", R * N * E)
+    return lib().mp_route(
+        R, N, K, E, int(scoring), dtype, lp, _arr(bias, "bias", torch.float32, E),
+        _arr(active, "active", torch.uint8, R * N), int(bool(normalize)), float(scale),
+        float(loss_coef), _arr(topk_idx, "topk_idx", torch.int32, R * N * K),
+        _arr(topk_weights, "topk_weights", torch.float32, R * N * K),
+        _arr(num_tokens_per_expert, "num_tokens_per_expert", torch.int32, R * E),
+        _arr(num_routed, "num_routed", torch.int32, R),
+        _arr(balance_loss, "balance_loss", torch.float32, R),
+        _arr(dev_err, "dev_err", torch.int32, 1),
+        _arr(workspace, "workspace", torch.uint8, mp_route_workspace_size(R, N, E)),
+        _stream(stream))
+
+
+def mp_route_backward(R, N, K, E, scoring, logits, active, normalize, scale, loss_coef, topk_idx,
+                      d_topk_weights, num_tokens_per_expert, num_routed, d_balance_loss, d_logits,
+                      stream=None) -> int:
+    """The gradient of mp_route's weights and loss with respect to the logits."""
+    dtype, lp = _logits(logits, "logits", R * N * E)
+    return lib().mp_route_backward(
+        R, N, K, E, int(scoring), dtype, lp, _arr(active, "active", torch.uint8, R * N),
+        int(bool(normalize)), float(scale), float(loss_coef),
+        _arr(topk_idx, "topk_idx", torch.int32, R * N * K),
+        _arr(d_topk_weights, "d_topk_weights", torch.float32, R * N * K),
+        _arr(num_tokens_per_expert, "num_tokens_per_expert", torch.int32, R * E),
+        _arr(num_routed, "num_routed", torch.int32, R),
+        _arr(d_balance_loss, "d_balance_loss", torch.float32, R),
+        _arr(d_logits, "d_logits", torch.bfloat16 if dtype == MP_BF16 else torch.float32,
+             R * N * E), _stream(stream))
+
+
+_F8 = torch.float8_e4m3fn
+
+
+def mp_expert_matmul_e4m3(E, rows, N, K, a, a_scales, w, w_scales, expert_offsets, out, dev_err,
+                          stream=None) -> int:
+    """out[r] = a[r] w[e]^T for the rows of every expert: e4m3 with one fp32 scale per 128
+    channels of a row and per 128 x 128 block of a weight, bf16 out."""
+    return lib().mp_expert_matmul_e4m3(
+        E, rows, N, K, _arr(a, "a", _F8, rows * K),
+        _arr(a_scales, "a_scales", torch.float32, rows * (K // SCALE_BLOCK)),
+        _arr(w, "w", _F8, E * N * K),
+        _arr(w_scales, "w_scales", torch.float32, E * -(-N // SCALE_BLOCK) * (K // SCALE_BLOCK)),
+        _arr(expert_offsets, "expert_offsets", torch.int32, E + 1),
+        _arr(out, "out", torch.bfloat16, rows * N), _arr(dev_err, "dev_err", torch.int32, 1),
+        _stream(stream))
+
+
+def mp_expert_matmul_dgrad_e4m3(E, rows, N, K, dy, dy_scales, w, w_scales, expert_offsets, dx,
+                                dev_err, stream=None) -> int:
+    """dx[r] = dy[r] w[e]: the gradient of the rows, with the weights as they are stored."""
+    return lib().mp_expert_matmul_dgrad_e4m3(
+        E, rows, N, K, _arr(dy, "dy", _F8, rows * N),
+        _arr(dy_scales, "dy_scales", torch.float32, rows * (N // SCALE_BLOCK)),
+        _arr(w, "w", _F8, E * N * K),
+        _arr(w_scales, "w_scales", torch.float32, E * -(-N // SCALE_BLOCK) * (K // SCALE_BLOCK)),
+        _arr(expert_offsets, "expert_offsets", torch.int32, E + 1),
+        _arr(dx, "dx", torch.bfloat16, rows * K), _arr(dev_err, "dev_err", torch.int32, 1),
+        _stream(stream))
+
+
+def mp_expert_matmul_wgrad_e4m3(E, rows, N, K, dy, dy_scales, a, a_scales, expert_offsets, dw,
+                                dev_err, stream=None) -> int:
+    """dw[e] = dy^T a over the rows of every expert, bf16 (zeros for an expert without rows)."""
+    return lib().mp_expert_matmul_wgrad_e4m3(
+        E, rows, N, K, _arr(dy, "dy", _F8, rows * N),
+        _arr(dy_scales, "dy_scales", torch.float32, rows * (N // SCALE_BLOCK)),
+        _arr(a, "a", _F8, rows * K),
+        _arr(a_scales, "a_scales", torch.float32, rows * (K // SCALE_BLOCK)),
+        _arr(expert_offsets, "expert_offsets", torch.int32, E + 1),
+        _arr(dw, "dw", torch.bfloat16, E * N * K), _arr(dev_err, "dev_err", torch.int32, 1),
+        _stream(stream))
+
+
+def mp_swiglu_e4m3(rows, I, gate_up, row_weights, num_rows, out, out_scales, stream=None) -> int:
+    """row_weights * silu(gate) * up of bf16 [rows][2I], quantised to e4m3 with one fp32 scale
+    per 128 channels."""
+    return lib().mp_swiglu_e4m3(
+        rows, I, _arr(gate_up, "gate_up", torch.bfloat16, rows * 2 * I),
+        _arr(row_weights, "row_weights", torch.float32, rows),
+        _arr(num_rows, "num_rows", torch.int32, 1), _arr(out, "out", _F8, rows * I),
+        _arr(out_scales, "out_scales", torch.float32, rows * (I // SCALE_BLOCK)),
+        _stream(stream))
+
+
+def mp_swiglu_backward_e4m3(rows, I, gate_up, row_weights, d_out, num_rows, d_gate_up,
+                            d_gate_up_scales, d_row_weights, stream=None) -> int:
+    """The gradient of mp_swiglu_e4m3: d_gate_up quantised the same way, d_row_weights fp32."""
+    return lib().mp_swiglu_backward_e4m3(
+        rows, I, _arr(gate_up, "gate_up", torch.bfloat16, rows * 2 * I),
+        _arr(row_weights, "row_weights", torch.float32, rows),
+        _arr(d_out, "d_out", torch.bfloat16, rows * I), _arr(num_rows, "num_rows", torch.int32, 1),
+        _arr(d_gate_up, "d_gate_up", _F8, rows * 2 * I),
+        _arr(d_gate_up_scales, "d_gate_up_scales", torch.float32, rows * (2 * I // SCALE_BLOCK)),
+        _arr(d_row_weights, "d_row_weights", torch.float32, rows), _stream(stream))

@@ -63,6 +63,7 @@ const char* mp_status_string(int status) {
   if (status & MP_ERR_CAPACITY) return "receive capacity exceeded";
   if (status & MP_ERR_BAD_EXPERT) return "expert id outside [-1, E)";
   if (status & MP_ERR_TIMEOUT) return "device-side wait timed out";
+  if (status & MP_ERR_BAD_VALUE) return "router logit is NaN or +inf";
   return "unknown status";
 }
 

@@ -203,4 +203,41 @@ cudaError_t launch_allgatherv(int R, int64_t S, int64_t row_bytes, const void* i
 cudaError_t launch_allgatherv_multi(int R, int n, const int64_t* row_bytes, int64_t S,
                                     const void* const* in, void* const* out, cudaStream_t stream);
 
+// The router (forward, gradient) and its workspace: MP_MAX_RANKS done counters
+// and routed sums, then the [R][E] fixed-point share sums and counts; zero
+// before and after every launch.
+size_t route_workspace_bytes(int R, int E);
+cudaError_t launch_route(int R, int N, int K, int E, int scoring, int dtype, const void* logits,
+                         const float* bias, const uint8_t* active, int normalize, float scale,
+                         float loss_coef, int32_t* topk_idx, float* topk_weights,
+                         int32_t* num_tokens_per_expert, int32_t* num_routed, float* balance_loss,
+                         int32_t* dev_err, unsigned char* workspace, cudaStream_t stream);
+cudaError_t launch_route_backward(int R, int N, int K, int E, int scoring, int dtype,
+                                  const void* logits, const uint8_t* active, int normalize,
+                                  float scale, float loss_coef, const int32_t* topk_idx,
+                                  const float* d_topk_weights,
+                                  const int32_t* num_tokens_per_expert, const int32_t* num_routed,
+                                  const float* d_balance_loss, void* d_logits,
+                                  cudaStream_t stream);
+
+// Products of the experts on e4m3 rows: out = a w^T (dgrad = false) or, with a
+// = dy, out = dy w (dgrad = true); and the weights' gradient.
+cudaError_t launch_expert_matmul(int E, int rows, int N, int K, bool dgrad, const void* a,
+                                 const float* a_scales, const void* w, const float* w_scales,
+                                 const int32_t* expert_offsets, void* out, int32_t* dev_err,
+                                 cudaStream_t stream);
+cudaError_t launch_expert_wgrad(int E, int rows, int N, int K, const void* dy,
+                                const float* dy_scales, const void* a, const float* a_scales,
+                                const int32_t* expert_offsets, void* dw, int32_t* dev_err,
+                                cudaStream_t stream);
+
+// The gated activation with e4m3 quantisation, and its gradient.
+cudaError_t launch_swiglu(int rows, int I, const void* gate_up, const float* row_weights,
+                          const int32_t* num_rows, void* out, float* out_scales,
+                          cudaStream_t stream);
+cudaError_t launch_swiglu_backward(int rows, int I, const void* gate_up, const float* row_weights,
+                                   const void* d_out, const int32_t* num_rows, void* d_gate_up,
+                                   float* d_gate_up_scales, float* d_row_weights,
+                                   cudaStream_t stream);
+
 }  // namespace mp

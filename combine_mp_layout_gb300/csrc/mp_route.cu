@@ -1,0 +1,532 @@
+// mp_route.cu -- the router: scores, top-K experts, weights, per-expert counts
+// and the balance loss in one pass over the logits, and the gradient of the
+// weights and the loss with respect to the logits.
+//
+// Per token, over the experts e whose logit is not -inf:
+//   score  s_e = softmax(l)_e  or  1 / (1 + exp(-l_e))
+//   key        = l_e (softmax), s_e + bias_e (sigmoid): the K largest keys are
+//                chosen, ties going to the lower expert
+//   weight w_k = scale * s_k, or scale * s_k / sum of the chosen s
+//   share  p_e = s_e / sum of all s
+// Per source rank, T its tokens with a chosen expert, c_e its counts:
+//   loss = coef * E / (K * T^2) * sum_e c_e * sum_t p_{t,e}
+//
+// A warp (up to 1,024 experts) or a block of eight warps (beyond) holds one
+// token's logits in registers, V per thread, so they are read once.
+//
+// The sums over tokens are order-free and so the same on every run: counts are
+// integers, and each block's share sums (fp32, added in a fixed order) enter
+// the global sums as fixed-point integers with as many fraction bits as 2^63 /
+// (N + 1) leaves.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <type_traits>
+
+#include "../../include/mp_layout.h"
+#include "mp_common.cuh"
+#include "mp_internal.h"
+
+namespace mp {
+
+namespace {
+
+constexpr int kRouteWarps = 8;
+constexpr int kRouteThreads = kRouteWarps * kWarp;
+
+struct RouteArgs {
+  int R, N, K, E;
+  int normalize;
+  float scale, loss_coef;
+  const void* logits;
+  const float* bias;        // or NULL
+  const uint8_t* active;    // or NULL
+  int32_t* topk_idx;
+  float* topk_weights;
+  int32_t* counts;          // [R][E]
+  int32_t* routed;          // [R]
+  float* loss;              // [R]
+  int32_t* dev_err;
+  // workspace: done counters and routed sums [MP_MAX_RANKS], then [R][E] sums and counts
+  uint32_t* ws_done;
+  int32_t* ws_routed;
+  unsigned long long* ws_mass;
+  int32_t* ws_count;
+  float fix;                // 2^fraction bits of ws_mass
+  // gradient
+  const float* d_weights;   // [R][N][K] or NULL
+  const float* d_loss;      // [R] or NULL
+  void* d_logits;
+};
+
+// Reductions over the W warps that share a token; every thread gets the result.
+// `red` holds kRouteWarps words (unused for W = 1).
+template <int W, typename T, typename Op>
+__device__ __forceinline__ T team_reduce(T v, T* red, Op op) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(kFull, v, o));
+  if constexpr (W > 1) {
+    __syncthreads();  // the words of the reduction before are free
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v = op(v, red[w]);
+  }
+  return v;
+}
+struct OpSum {
+  __device__ float operator()(float a, float b) const { return a + b; }
+};
+struct OpMax {
+  __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+template <int W>
+__device__ __forceinline__ uint32_t team_max(uint32_t v, uint32_t* red) {
+  v = __reduce_max_sync(kFull, v);
+  if constexpr (W > 1) {
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v = max(v, red[w]);
+  }
+  return v;
+}
+template <int W>
+__device__ __forceinline__ uint32_t team_min(uint32_t v, uint32_t* red) {
+  return ~team_max<W>(~v, red);
+}
+
+template <typename T>
+__device__ __forceinline__ float load_logit(const T* p) {
+  if constexpr (std::is_same<T, float>::value)
+    return __ldg(p);
+  else
+    return __uint_as_float(uint32_t(__ldg(reinterpret_cast<const uint16_t*>(p))) << 16);
+}
+
+__device__ __forceinline__ float sigmoid_exact(float x) {
+  return __fdiv_rn(1.0f, 1.0f + expf(-x));  // the selection key: correctly rounded division
+}
+
+// Floats to integers with the same order (-0 and +0 alike); 0 means "cannot be chosen".
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// A token's logits and scores, V experts per thread: expert j * (W * 32) + t.
+template <typename T, int V, int W, bool SIG>
+struct TokenScores {
+  float s[V];   // scores, 0 where the expert is not allowed
+  float inv;    // share = s * inv
+  bool live;    // finite or -inf everywhere, and active
+  float m, inv_total;  // softmax: s = exp(l - m) * inv_total
+
+  // the score of one more logit of the same token
+  __device__ __forceinline__ float score_of(float x) const {
+    if constexpr (SIG) return x > -INFINITY ? sigmoid_exact(x) : 0.0f;
+    return x > -INFINITY ? expf(x - m) * inv_total : 0.0f;
+  }
+
+  // x: the token's logits, -inf past the last expert
+  __device__ __forceinline__ void compute(float (&x)[V], bool active, float* red) {
+    bool bad = false;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      bad |= !(x[j] < INFINITY);  // NaN or +inf
+      mx = fmaxf(mx, x[j]);
+    }
+    // one reduction for both: a bad value makes the maximum +inf
+    mx = team_reduce<W>(bad ? INFINITY : mx, red, OpMax());
+    live = active && mx < INFINITY;
+    m = mx > -INFINITY ? mx : 0.0f;
+    float total = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (!live) x[j] = -INFINITY;
+      if constexpr (SIG)
+        s[j] = x[j] > -INFINITY ? sigmoid_exact(x[j]) : 0.0f;
+      else
+        s[j] = x[j] > -INFINITY ? expf(x[j] - m) : 0.0f;
+      total += s[j];
+    }
+    total = team_reduce<W>(total, red, OpSum());
+    inv_total = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
+    inv = SIG ? inv_total : 1.0f;
+    if constexpr (!SIG) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) s[j] *= inv_total;
+    }
+  }
+};
+
+template <typename T, int V, int W>
+__device__ __forceinline__ void load_token(const T* row, int E, int t, float (&x)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int e = j * (W * kWarp) + t;
+    x[j] = e < E ? load_logit(row + e) : -INFINITY;
+  }
+}
+
+// grid (blocks per rank, R).  W = 1: a warp per token; W = 8: a block per token.
+template <typename T, int V, int W, bool SIG>
+__global__ void __launch_bounds__(kRouteThreads)
+mp_k_route(const RouteArgs p) {
+  constexpr int kTeam = W * kWarp;
+  constexpr int kTeams = kRouteWarps / W;
+  extern __shared__ int sm_count_[];  // [E] counts
+  __shared__ float red[kRouteWarps];
+  __shared__ uint32_t redu[kRouteWarps];
+  __shared__ float stage[W == 1 ? kRouteWarps * 256 : 1];
+  __shared__ double dred[kRouteWarps];
+  __shared__ int s_routed;
+  __shared__ int s_last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = threadIdx.x % kTeam;   // thread within the token's team
+  const int team = threadIdx.x / kTeam;
+  const int rank = blockIdx.y;
+  const int E = p.E, K = p.K;
+  for (int e = threadIdx.x; e < E; e += kRouteThreads) sm_count_[e] = 0;
+  if (threadIdx.x == 0) s_routed = 0;
+  __syncthreads();
+
+  float mass[V];  // this thread's experts: sum of shares over the team's tokens
+#pragma unroll
+  for (int j = 0; j < V; ++j) mass[j] = 0.0f;
+  int routed = 0;
+
+  for (int n = blockIdx.x * kTeams + team; n < p.N; n += gridDim.x * kTeams) {
+    const int64_t tok = int64_t(rank) * p.N + n;
+    const T* row = static_cast<const T*>(p.logits) + tok * E;
+    float x[V];
+    load_token<T, V, W>(row, E, t, x);
+    TokenScores<T, V, W, SIG> sc;
+    const bool active = p.active == nullptr || p.active[tok] != 0;
+    sc.compute(x, active, red);
+    if (active && !sc.live && t == 0) raise_error(p.dev_err, MP_ERR_BAD_VALUE);
+
+    uint32_t key[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float k = x[j];
+      if constexpr (SIG) {
+        const int e = j * kTeam + t;
+        k = sc.s[j] + (p.bias != nullptr && e < E ? __ldg(p.bias + e) : 0.0f);
+      }
+      key[j] = x[j] > -INFINITY && k > -INFINITY ? order_key(k) : 0u;
+    }
+    // K rounds: the largest key, among equals the lowest expert
+    uint32_t best = 0;
+    int bestj = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (key[j] > best) { best = key[j]; bestj = j; }
+    int mine = -1;  // lane k of the (first) warp: the k-th choice
+    bool any = false;
+    for (int k = 0; k < K; ++k) {
+      const uint32_t top = team_max<W>(best, redu);
+      if (top == 0) break;
+      any = true;
+      const uint32_t e = team_min<W>(best == top ? uint32_t(bestj * kTeam + t) : 0xffffffffu, redu);
+      if (t == k) mine = int(e);
+      if (best == top && uint32_t(bestj * kTeam + t) == e) {
+        best = 0;
+        const int gone = bestj;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          if (j == gone) key[j] = 0;
+          if (key[j] > best) { best = key[j]; bestj = j; }
+        }
+      }
+    }
+    if (W == 1 || warp == 0) {
+      float w = mine >= 0 ? sc.score_of(load_logit(row + mine)) : 0.0f;
+      if (p.normalize) {
+        float total = w;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
+        w = total > 0.0f ? __fdiv_rn(w, total) : 0.0f;
+      }
+      w *= p.scale;
+      if (lane < K) {
+        p.topk_idx[tok * K + lane] = mine;
+        p.topk_weights[tok * K + lane] = w;
+        if (mine >= 0) atomicAdd(&sm_count_[mine], 1);
+      }
+    }
+    if (any) {
+      ++routed;
+#pragma unroll
+      for (int j = 0; j < V; ++j) mass[j] += sc.s[j] * sc.inv;
+    }
+  }
+
+  // the block's sums into the rank's
+  if (t == 0 && routed) atomicAdd(&s_routed, routed);
+  unsigned long long* gm = p.ws_mass + int64_t(rank) * E;
+  int32_t* gc = p.ws_count + int64_t(rank) * E;
+  if constexpr (W == 1) {
+    constexpr int kChunk = V < 8 ? V : 8;  // 256 experts at a time
+#pragma unroll
+    for (int c = 0; c < V; c += kChunk) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) stage[warp * 256 + j * kWarp + lane] = mass[c + j];
+      __syncthreads();
+      const int e = c * kWarp + int(threadIdx.x);
+      if (threadIdx.x < kChunk * kWarp && e < E) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kRouteWarps; ++w) sum += stage[w * 256 + threadIdx.x];
+        if (sum != 0.0f) atomicAdd(gm + e, (unsigned long long)(sum * p.fix));
+      }
+    }
+  } else {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int e = j * kTeam + t;
+      if (e < E && mass[j] != 0.0f) atomicAdd(gm + e, (unsigned long long)(mass[j] * p.fix));
+    }
+  }
+  for (int e = threadIdx.x; e < E; e += kRouteThreads)
+    if (sm_count_[e]) atomicAdd(gc + e, sm_count_[e]);
+  if (threadIdx.x == 0 && s_routed) atomicAdd(p.ws_routed + rank, s_routed);
+
+  // the rank's last block writes its counts and loss and clears the workspace
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0)
+    s_last = atom_add_acq_rel_u32(p.ws_done + rank, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  double sum = 0.0;
+  for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+    const int c = __ldcg(gc + e);
+    const unsigned long long f = __ldcg(gm + e);
+    p.counts[int64_t(rank) * E + e] = c;
+    sum += double(c) * double(f);
+    gc[e] = 0;
+    gm[e] = 0;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  if (lane == 0) dred[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double all = 0.0;
+    for (int w = 0; w < kRouteWarps; ++w) all += dred[w];
+    const int T_ = __ldcg(p.ws_routed + rank);
+    const double T2 = double(T_ > 0 ? T_ : 1) * double(T_ > 0 ? T_ : 1);
+    p.routed[rank] = T_;
+    p.loss[rank] = float(double(p.loss_coef) * E / (double(K) * T2) * (all / double(p.fix)));
+    p.ws_routed[rank] = 0;
+    p.ws_done[rank] = 0;
+  }
+}
+
+// Gradient.  With c_e = d_loss * coef * E * counts_e / (K T^2) (the share's
+// gradient; the counts are constants) and g_k the chosen scores' gradient,
+//   softmax: dl_e = p_e (h_e - sum_j p_j h_j),  h = c + g at the chosen
+//   sigmoid: dl_e = s_e (1 - s_e) ((c_e - sum_j p_j c_j) / sum_j s_j + g_e)
+//   g_k = scale * dw_k, or scale / S * (dw_k - sum_j dw_j s_j / S), S = sum of the chosen s.
+template <typename T, int V, int W, bool SIG>
+__global__ void __launch_bounds__(kRouteThreads)
+mp_k_route_backward(const RouteArgs p) {
+  constexpr int kTeam = W * kWarp;
+  constexpr int kTeams = kRouteWarps / W;
+  extern __shared__ float sm_g[];  // [kTeams][E]: the chosen scores' gradients
+  __shared__ float red[kRouteWarps];
+  __shared__ int s_any;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = threadIdx.x % kTeam;
+  const int team = threadIdx.x / kTeam;
+  const int rank = blockIdx.y;
+  const int E = p.E, K = p.K;
+  float* g = sm_g + team * E;
+  for (int e = t; e < E; e += kTeam) g[e] = 0.0f;
+  float c[V];  // the share's gradient, the same for every routed token of the rank
+  {
+    const int routed = __ldg(p.routed + rank);
+    const float T_ = float(routed > 0 ? routed : 1);
+    const float f = p.d_loss != nullptr
+        ? __ldg(p.d_loss + rank) * p.loss_coef * float(E) / (float(K) * T_ * T_) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int e = j * kTeam + t;
+      c[j] = e < E && p.d_loss != nullptr ? f * float(__ldg(p.counts + int64_t(rank) * E + e)) : 0.0f;
+    }
+  }
+  if constexpr (W > 1) __syncthreads(); else __syncwarp();
+
+  for (int n = blockIdx.x * kTeams + team; n < p.N; n += gridDim.x * kTeams) {
+    const int64_t tok = int64_t(rank) * p.N + n;
+    const T* row = static_cast<const T*>(p.logits) + tok * E;
+    float x[V];
+    load_token<T, V, W>(row, E, t, x);
+    TokenScores<T, V, W, SIG> sc;
+    const bool active = p.active == nullptr || p.active[tok] != 0;
+    sc.compute(x, active, red);
+
+    int id = -1;
+    bool any;
+    if (W == 1 || warp == 0) {
+      if (lane < K) id = __ldg(p.topk_idx + tok * K + lane);
+      if (uint32_t(id) >= uint32_t(E)) id = -1;
+      any = __any_sync(kFull, id >= 0);
+      float s = 0.0f, d = 0.0f;
+      if (id >= 0 && sc.live) {
+        s = sc.score_of(load_logit(row + id));
+        if (p.d_weights != nullptr) d = __ldg(p.d_weights + tok * K + lane) * p.scale;
+      }
+      if (p.normalize) {
+        float total = s, dot = d * s;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          total += __shfl_xor_sync(kFull, total, o);
+          dot += __shfl_xor_sync(kFull, dot, o);
+        }
+        const float inv = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
+        d = (d - dot * inv) * inv;
+      }
+      if (id >= 0) g[id] = d;
+      if (W > 1 && lane == 0) s_any = any;
+    }
+    if constexpr (W > 1) {
+      __syncthreads();
+      any = s_any;
+    } else {
+      __syncwarp();
+    }
+    float h[V];
+    float dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int e = j * kTeam + t;
+      const float gj = e < E ? g[e] : 0.0f;
+      const float cj = any ? c[j] : 0.0f;
+      if constexpr (SIG) {
+        h[j] = gj;
+        dot += sc.s[j] * sc.inv * cj;
+      } else {
+        h[j] = gj + cj;
+        dot += sc.s[j] * h[j];
+      }
+    }
+    dot = team_reduce<W>(dot, red, OpSum());  // (for W > 1 its barriers follow every read of g)
+    if constexpr (W == 1) __syncwarp();
+    if ((W == 1 || warp == 0) && id >= 0) g[id] = 0.0f;  // cleared for the next token
+    T* out = static_cast<T*>(p.d_logits) + tok * E;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int e = j * kTeam + t;
+      float d;
+      if constexpr (SIG)
+        d = sc.s[j] * (1.0f - sc.s[j]) * (h[j] + ((any ? c[j] : 0.0f) - dot) * sc.inv);
+      else
+        d = sc.s[j] * (h[j] - dot);
+      if (e < E) {
+        if constexpr (std::is_same<T, float>::value)
+          out[e] = d;
+        else
+          out[e] = __float2bfloat16_rn(d);
+      }
+    }
+    if constexpr (W == 1) __syncwarp(); else __syncthreads();
+  }
+}
+
+template <typename T, int V, int W, bool SIG>
+cudaError_t launch_route_as(const RouteArgs& p, bool backward, cudaStream_t st) {
+  constexpr int kTeams = kRouteWarps / W;
+  // enough blocks to fill the GPU a few times over, spread over the ranks
+  const int64_t need = (int64_t(p.N) + kTeams - 1) / kTeams;
+  const int64_t most = std::max<int64_t>(1, int64_t(sm_count()) * (W == 1 ? 4 : 2) / p.R);
+  const dim3 grid(unsigned(std::max<int64_t>(1, std::min(need, most))), unsigned(p.R));
+  if (backward) {
+    const size_t smem = size_t(kTeams) * p.E * 4;
+    mp_k_route_backward<T, V, W, SIG><<<grid, kRouteThreads, smem, st>>>(p);
+  } else {
+    mp_k_route<T, V, W, SIG><<<grid, kRouteThreads, size_t(p.E) * 4, st>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+template <typename T, bool SIG>
+cudaError_t launch_route_v(const RouteArgs& p, bool backward, cudaStream_t st) {
+  const int E = p.E;
+  if (E <= 32) return launch_route_as<T, 1, 1, SIG>(p, backward, st);
+  if (E <= 64) return launch_route_as<T, 2, 1, SIG>(p, backward, st);
+  if (E <= 128) return launch_route_as<T, 4, 1, SIG>(p, backward, st);
+  if (E <= 256) return launch_route_as<T, 8, 1, SIG>(p, backward, st);
+  if (E <= 512) return launch_route_as<T, 16, 1, SIG>(p, backward, st);
+  if (E <= 1024) return launch_route_as<T, 32, 1, SIG>(p, backward, st);
+  if (E <= 2048) return launch_route_as<T, 8, 8, SIG>(p, backward, st);
+  if (E <= 4096) return launch_route_as<T, 16, 8, SIG>(p, backward, st);
+  return launch_route_as<T, 32, 8, SIG>(p, backward, st);
+}
+
+cudaError_t launch_route_t(const RouteArgs& p, int scoring, int dtype, bool backward,
+                           cudaStream_t st) {
+  if (dtype == MP_FP32)
+    return scoring == MP_SIGMOID ? launch_route_v<float, true>(p, backward, st)
+                                 : launch_route_v<float, false>(p, backward, st);
+  return scoring == MP_SIGMOID ? launch_route_v<__nv_bfloat16, true>(p, backward, st)
+                               : launch_route_v<__nv_bfloat16, false>(p, backward, st);
+}
+
+}  // namespace
+
+size_t route_workspace_bytes(int R, int E) {
+  return size_t(MP_MAX_RANKS) * 8 + size_t(R) * E * 12;
+}
+
+cudaError_t launch_route(int R, int N, int K, int E, int scoring, int dtype, const void* logits,
+                         const float* bias, const uint8_t* active, int normalize, float scale,
+                         float loss_coef, int32_t* topk_idx, float* topk_weights,
+                         int32_t* num_tokens_per_expert, int32_t* num_routed, float* balance_loss,
+                         int32_t* dev_err, unsigned char* workspace, cudaStream_t st) {
+  RouteArgs p = {};
+  p.R = R; p.N = N; p.K = K; p.E = E;
+  p.normalize = normalize; p.scale = scale; p.loss_coef = loss_coef;
+  p.logits = logits; p.bias = bias; p.active = active;
+  p.topk_idx = topk_idx; p.topk_weights = topk_weights;
+  p.counts = num_tokens_per_expert; p.routed = num_routed; p.loss = balance_loss;
+  p.dev_err = dev_err;
+  p.ws_done = reinterpret_cast<uint32_t*>(workspace);
+  p.ws_routed = reinterpret_cast<int32_t*>(workspace + size_t(MP_MAX_RANKS) * 4);
+  p.ws_mass = reinterpret_cast<unsigned long long*>(workspace + size_t(MP_MAX_RANKS) * 8);
+  p.ws_count = reinterpret_cast<int32_t*>(workspace + size_t(MP_MAX_RANKS) * 8 + size_t(R) * E * 8);
+  int bits = 62;  // the largest sum, N, stays below 2^63
+  for (int64_t n = N; n > 0; n >>= 1) --bits;
+  p.fix = ldexpf(1.0f, bits);
+  return launch_route_t(p, scoring, dtype, false, st);
+}
+
+cudaError_t launch_route_backward(int R, int N, int K, int E, int scoring, int dtype,
+                                  const void* logits, const uint8_t* active, int normalize,
+                                  float scale, float loss_coef, const int32_t* topk_idx,
+                                  const float* d_topk_weights,
+                                  const int32_t* num_tokens_per_expert, const int32_t* num_routed,
+                                  const float* d_balance_loss, void* d_logits, cudaStream_t st) {
+  if (N == 0) return cudaSuccess;
+  RouteArgs p = {};
+  p.R = R; p.N = N; p.K = K; p.E = E;
+  p.normalize = normalize; p.scale = scale; p.loss_coef = loss_coef;
+  p.logits = logits; p.active = active;
+  p.topk_idx = const_cast<int32_t*>(topk_idx);
+  p.counts = const_cast<int32_t*>(num_tokens_per_expert);
+  p.routed = const_cast<int32_t*>(num_routed);
+  p.d_weights = d_topk_weights; p.d_loss = d_balance_loss; p.d_logits = d_logits;
+  return launch_route_t(p, scoring, dtype, true, st);
+}
+
+}  // namespace mp

@@ -67,11 +67,13 @@ enum {
   MP_ERR_CUDA = 2,        /* a CUDA launch or attribute call failed               */
   MP_ERR_CAPACITY = 4,    /* more receive rows than recv_capacity / y_rows        */
   MP_ERR_BAD_EXPERT = 8,  /* topk_idx entry outside [-1, E)                       */
-  MP_ERR_TIMEOUT = 16     /* a bounded device-side wait gave up (about a second)  */
+  MP_ERR_TIMEOUT = 16,    /* a bounded device-side wait gave up (about a second)  */
+  MP_ERR_BAD_VALUE = 32   /* a router logit is NaN or +inf                        */
 };
 
-/* Payload element types of mp_dispatch. */
-enum { MP_BF16 = 0, MP_E4M3 = 1 };
+/* Element types: payloads of mp_dispatch (MP_BF16, MP_E4M3) and logits of
+ * mp_route (MP_BF16, MP_FP32). */
+enum { MP_BF16 = 0, MP_E4M3 = 1, MP_FP32 = 2 };
 
 #define MP_MAX_RANKS 32     /* is_token_in_rank is one 32-bit mask per token  */
 #define MP_MAX_TOPK 32
@@ -633,6 +635,171 @@ int mp_dispatch_ll_quant(int R, int N, int K, int E, int H, int qformat, int ran
                          int32_t *bin_offsets, int32_t *bin_src_offsets, int32_t *recv_src_token,
                          int32_t *slot_row, void *recv_x, void *recv_scales, int32_t *dev_err,
                          mp_stream_t stream);
+
+/*
+ * The expert layer's own operators: the router that produces topk_idx and
+ * topk_weights, and what the experts compute on the expert-major rows of the
+ * low-latency dispatch, each with its gradient.  No counterpart in the pages;
+ * a layer is
+ *   mp_route -> mp_dispatch_ll_quant (MP_Q_E4M3) -> mp_expert_matmul_e4m3
+ *   -> mp_swiglu_e4m3 -> mp_expert_matmul_e4m3 -> mp_combine_ll.
+ */
+
+/* Score functions of the router. */
+enum { MP_SOFTMAX = 0, MP_SIGMOID = 1 };
+
+/* Bytes of workspace of mp_route (device memory, zero-filled once by the
+ * caller; every call leaves it zero-filled; calls that share one are ordered
+ * on one stream).  Returns 0 for arguments mp_route would reject. */
+size_t mp_route_workspace_size(int R, int N, int E);
+
+/*
+ * mp_route -- scores, top-K experts, their weights, per-expert counts and the
+ * balance loss of each source rank's tokens, in one pass over the logits.
+ *   in   logits                dtype (MP_FP32 or MP_BF16) [R][N][E]
+ *   in   bias                  fp32 [E] added to the scores for the choice
+ *                              only (MP_SIGMOID), or NULL
+ *   in   active                uint8 [R][N]: 0 marks a padding token; or NULL
+ *   out  topk_idx              int32 [R][N][K], -1 where no expert is left
+ *   out  topk_weights          fp32 [R][N][K], 0 where topk_idx is -1
+ *   out  num_tokens_per_expert int32 [R][E], as mp_layout counts topk_idx
+ *   out  num_routed            int32 [R]: tokens with at least one expert
+ *   out  balance_loss          fp32 [R]
+ * Scores of a token: softmax of its logits, or 1 / (1 + exp(-logit)); 0 for a
+ * logit of -inf, which is never chosen.  The K largest logits (MP_SOFTMAX) or
+ * scores + bias (MP_SIGMOID) are chosen in descending order, among equals the
+ * lower expert first; an expert whose sum is -inf or NaN is not chosen.
+ * Weight: scale * score, divided by the sum of the chosen scores with
+ * normalize != 0 (0 if that sum is 0).  Share p: score / sum of all scores.
+ * With T = num_routed[r] and c = num_tokens_per_expert[r]:
+ *   balance_loss[r] = loss_coef * E / (K T^2) * sum_e c[e] * sum_t p[t][e],
+ * t over the routed tokens; 0 if T is 0.  The sum over tokens does not depend
+ * on the order in which blocks finish: every run gives the same bits.
+ * A token that is not active, has a NaN or +inf logit (MP_ERR_BAD_VALUE) or
+ * only -inf logits is routed nowhere and enters no count and no sum.
+ * Checks: 1 <= R <= 32, N >= 0, 1 <= K <= 32, K <= E <= 8192, R*N*K < 2^31,
+ *   scoring and dtype as above, bias NULL for MP_SOFTMAX, non-NULL buffers
+ *   (bias and active may be NULL; logits and the token outputs when N == 0),
+ *   alignment to the element size, workspace to 16 bytes.
+ * Device errors: MP_ERR_BAD_VALUE.
+ */
+int mp_route(int R, int N, int K, int E, int scoring, int dtype, const void *logits,
+             const float *bias, const uint8_t *active, int normalize, float scale,
+             float loss_coef, int32_t *topk_idx, float *topk_weights,
+             int32_t *num_tokens_per_expert, int32_t *num_routed, float *balance_loss,
+             int32_t *dev_err, void *workspace, mp_stream_t stream);
+
+/*
+ * mp_route_backward -- the gradient of mp_route's topk_weights and balance_loss
+ * with respect to the logits (the choice and the counts are constants).
+ *   in   logits, active, normalize, scale, loss_coef   as given to mp_route
+ *   in   topk_idx, num_tokens_per_expert, num_routed   as mp_route wrote them
+ *        (ids outside [0, E) count as not chosen)
+ *   in   d_topk_weights  fp32 [R][N][K], or NULL (zeros)
+ *   in   d_balance_loss  fp32 [R], or NULL (zeros)
+ *   out  d_logits        dtype [R][N][E]; zeros for tokens routed nowhere
+ * Checks as mp_route.  No device errors.
+ */
+int mp_route_backward(int R, int N, int K, int E, int scoring, int dtype, const void *logits,
+                      const uint8_t *active, int normalize, float scale, float loss_coef,
+                      const int32_t *topk_idx, const float *d_topk_weights,
+                      const int32_t *num_tokens_per_expert, const int32_t *num_routed,
+                      const float *d_balance_loss, void *d_logits, mp_stream_t stream);
+
+/*
+ * mp_expert_matmul_e4m3 -- each expert's product with its weights on e4m3 rows
+ * with one fp32 scale per 128 channels:
+ *   out[r][n] = bf16( sum over blocks b of 128 channels of
+ *                     a_scales[r][b] * w_scales[e][n/128][b]
+ *                     * sum over k in b of a[r][k] * w[e][n][k] )
+ * for the rows expert_offsets[e] <= r < expert_offsets[e+1] of every expert e,
+ * sums in fp32, one rounding.
+ *   in   a, a_scales     e4m3 [rows][K], fp32 [rows][K/128]: the receive rows
+ *                        of the quantising dispatches
+ *   in   w, w_scales     e4m3 [E][N][K], fp32 [E][ceil(N/128)][K/128]: one
+ *                        scale per block of 128 x 128
+ *   in   expert_offsets  int32 [E+1] as the expert-major low-latency dispatch
+ *                        writes it, or NULL for E == 1 (all rows)
+ *   out  out             bf16 [rows][N]; rows of no expert are not written
+ * Checks: 1 <= E <= 8192, rows >= 0, K % 128 == 0, N % 16 == 0 (both > 0),
+ *   E*N < 2^31, (rows/128 + E) * ceil(N/64) < 2^31, non-NULL buffers (a, out
+ *   and the scales of a when rows == 0), a, w and out 16-byte aligned.
+ * Device errors: MP_ERR_CAPACITY (an offset past `rows`; it is cut off there),
+ *   MP_ERR_INVALID_ARG (offsets that decrease or are negative; nothing is
+ *   written then), MP_ERR_TIMEOUT.
+ */
+int mp_expert_matmul_e4m3(int E, int rows, int N, int K, const void *a, const float *a_scales,
+                          const void *w, const float *w_scales, const int32_t *expert_offsets,
+                          void *out, int32_t *dev_err, mp_stream_t stream);
+
+/*
+ * mp_expert_matmul_dgrad_e4m3 -- the gradient of the rows, with the same
+ * weights as they are stored (no transposed copy):
+ *   dx[r][k] = bf16( sum over blocks b of 128 channels of
+ *                    dy_scales[r][b] * w_scales[e][b][k/128]
+ *                    * sum over n in b of dy[r][n] * w[e][n][k] )
+ *   in   dy, dy_scales   e4m3 [rows][N], fp32 [rows][N/128]
+ *   out  dx              bf16 [rows][K]
+ * Checks and device errors as mp_expert_matmul_e4m3, with N % 128 == 0 and
+ *   (rows/128 + E) * ceil(K/64) < 2^31.
+ */
+int mp_expert_matmul_dgrad_e4m3(int E, int rows, int N, int K, const void *dy,
+                                const float *dy_scales, const void *w, const float *w_scales,
+                                const int32_t *expert_offsets, void *dx, int32_t *dev_err,
+                                mp_stream_t stream);
+
+/*
+ * mp_expert_matmul_wgrad_e4m3 -- the gradient of the weights:
+ *   dw[e][n][k] = bf16( sum over the rows r of expert e of
+ *                       (dy_scales[r][n/128] * dy[r][n]) * (a_scales[r][k/128] * a[r][k]) )
+ * each factor rounded to bf16 (8 significant bits; an e4m3 code has 4), the
+ * products exact, the sum over rows in fp32.  Experts without rows get zeros
+ * (so do, here, those whose offsets decrease; a negative offset counts as 0).
+ *   out  dw              bf16 [E][N][K]
+ * Checks and device errors as mp_expert_matmul_e4m3, with N % 128 == 0 and
+ *   E * (N/128) * ceil(K/256) < 2^31.
+ */
+int mp_expert_matmul_wgrad_e4m3(int E, int rows, int N, int K, const void *dy,
+                                const float *dy_scales, const void *a, const float *a_scales,
+                                const int32_t *expert_offsets, void *dw, int32_t *dev_err,
+                                mp_stream_t stream);
+
+/*
+ * mp_swiglu_e4m3 -- the gated activation between an expert's two products,
+ * quantised for the second:
+ *   z[r][i] = w[r] * g / (1 + exp(-g)) * u,   g = gate_up[r][i], u = gate_up[r][I + i],
+ * in fp32, then per 128 channels scale = amax / 448 (NaNs left out of the
+ * amax; 1 where that is below 2^-126) and code = e4m3(z / scale).
+ *   in   gate_up      bf16 [rows][2I]: the gate's channels, then the up ones
+ *   in   row_weights  fp32 [rows] (the weight each row has in the combine), or
+ *                     NULL for 1.  With the weight applied here, rows combine
+ *                     with weight 1 and the gradient of the combine is a plain
+ *                     dispatch of the output's gradient.
+ *   in   num_rows     int32 [1] on the device: rows in use (for the expert-major
+ *                     rows, expert_offsets + E), or NULL for all
+ *   out  out          e4m3 [rows][I], out_scales fp32 [rows][I/128]; rows past
+ *                     num_rows are not written
+ * Checks: rows >= 0, I > 0, I % 128 == 0, non-NULL buffers when rows > 0,
+ *   gate_up and out 16-byte aligned.  No device errors (num_rows is cut to
+ *   [0, rows]).
+ */
+int mp_swiglu_e4m3(int rows, int I, const void *gate_up, const float *row_weights,
+                   const int32_t *num_rows, void *out, float *out_scales, mp_stream_t stream);
+
+/*
+ * mp_swiglu_backward_e4m3 -- its gradient (the quantisation counts as the
+ * identity), quantised for the gradient products:
+ *   with s = 1 / (1 + exp(-g)) and d = w[r] * d_out[r][i]:
+ *   d_gate_up[r][i] = d * u * s * (1 + g * (1 - s)),  d_gate_up[r][I + i] = d * g * s,
+ *   d_row_weights[r] = sum over i of d_out[r][i] * g * s * u   (fp32, fixed order)
+ *   in   d_out          bf16 [rows][I]
+ *   out  d_gate_up      e4m3 [rows][2I], d_gate_up_scales fp32 [rows][2I/128]
+ *   out  d_row_weights  fp32 [rows], or NULL
+ * Checks as mp_swiglu_e4m3, d_out and d_gate_up 16-byte aligned too.
+ */
+int mp_swiglu_backward_e4m3(int rows, int I, const void *gate_up, const float *row_weights,
+                            const void *d_out, const int32_t *num_rows, void *d_gate_up,
+                            float *d_gate_up_scales, float *d_row_weights, mp_stream_t stream);
 
 #ifdef __cplusplus
 }
