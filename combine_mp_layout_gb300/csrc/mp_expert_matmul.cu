@@ -164,7 +164,7 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_a,
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   MMTail<BN>* tail = reinterpret_cast<MMTail<BN>*>(stages + size_t(S::kStages) * S::kStage);
   int* pre = reinterpret_cast<int*>(tail + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
@@ -193,7 +193,7 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_a,
   if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 0) {
     // ---- loads: one lane keeps the ring of stages full
-    if (lane == 0) {
+    if (elect_one()) {
       uint32_t it = 0;
       bool ok = true;
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
@@ -232,7 +232,7 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_a,
     }
   } else if (warp == 1) {
     // ---- products: one lane issues the MMAs of a stage into one of two accumulators
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idesc = mma_idesc_f8(kBM, BN, /*a_mn=*/false, /*b_mn=*/TB);
       uint32_t it = 0;
       bool ok = true;

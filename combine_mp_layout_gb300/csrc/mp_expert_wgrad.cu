@@ -111,7 +111,7 @@ mp_k_expert_wgrad(const WgradArgs p) {
   unsigned char* stages = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   WgradTail* tail = reinterpret_cast<WgradTail*>(stages + size_t(kWStages) * kWStage);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kWStages; ++i) {
       mbar_init(&tail->full[i], kConvWarps);
@@ -242,7 +242,7 @@ mp_k_expert_wgrad(const WgradArgs p) {
         ++nt;
       }
     }
-  } else if (lane == 0) {
+  } else if (elect_one()) {
     // ---- products: four K = 16 MMAs a stage into the tile's accumulator
     constexpr uint32_t idesc = mma_idesc_bf16(kWM, kWN, true, true);
     uint32_t it = 0, nt = 0;

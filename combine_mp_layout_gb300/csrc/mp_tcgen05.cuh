@@ -51,6 +51,22 @@ inline bool make_map_2d(CUtensorMap* map, const void* base, int elem, uint64_t c
 // ---------------------------------------------------------------------------
 // Device
 // ---------------------------------------------------------------------------
+// True for one lane of the (whole, converged) warp.  tcgen05 and TMA
+// instructions stand in branches on this and on warp_index(), which tell the
+// compiler that one thread of a uniform warp issues them: in a branch on a lane
+// number each MMA cost about 120 clocks to issue, here less than 64 (128 x 64 x
+// 128 e4m3 products back to back: 480 clocks per four MMAs against 264).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(p)::"memory");
+  return p != 0;
+}
+__device__ __forceinline__ int warp_index() {
+  return __shfl_sync(kFull, int(threadIdx.x >> 5), 0);
+}
+
 __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* map, int x, int y,
                                             uint64_t* bar) {
   asm volatile(
