@@ -50,9 +50,11 @@ bool matmul_args_ok(int E, int rows, int N, int K, const void* a, const float* a
          aligned_to(dev_err, 4);
 }
 
-// Row tiles of at most 128 rows times column tiles of at least 64 channels.
+// Row tiles of 64 rows or more, at most one short one per expert, times column
+// tiles of 256 channels; a tile's last row index stays an int.
 bool tiles_ok(int E, int rows, int cols) {
-  return (int64_t(rows) / 128 + E + 1) * ((int64_t(cols) + 63) / 64) < k31;
+  return rows <= INT32_MAX - 1024 &&
+         (int64_t(rows) / 64 + E) * ((int64_t(cols) + 255) / 256) < k31;
 }
 
 }  // namespace

@@ -3,15 +3,23 @@
 //
 // Forward   y[r][n]  = sum_kb sa[r][kb] * sw[e][n/128][kb] * P(r, n, kb),
 //           P(r, n, kb) = sum over the 128 channels k of block kb of a[r][k] * w[e][n][k]
-// Gradient of the rows (TB = true: the same weights, read along the other axis)
+// Gradient of the rows (DGRAD: the same weights, read along the other axis)
 //           dx[r][k] = sum_nb sd[r][nb] * sw[e][nb][k/128] * sum_{n in nb} dy[r][n] * w[e][n][k]
 // for every row r of expert e (rows expert_offsets[e] .. expert_offsets[e+1]).
 //
 // The scales change every 128 channels of the reduction, so the tensor core
-// sums one block (four K = 32 steps of kind::f8f6f4, exact products, fp32
-// accumulation in TMEM) and the block sums are added up in fp32 registers with
-// their scale: one packed FMA per two outputs and block.  A thread owns one
-// output row (one TMEM lane), so the product of the two scales is one register.
+// sums one block (four K = 32 steps of kind::f8f6f4: exact products, fp32 sums
+// in TMEM) and the block sums are added up in fp32 registers with their scale,
+// a packed FMA per two outputs and block.
+//
+// Layout.  A tile is 128 rows by 256 output channels.  The rows are the M side
+// (one TMEM lane each), so the scale of a row is one register of the thread that
+// owns the lane: with the weights there and the rows as columns, reading a scale
+// per column from shared memory took as long as the products.
+//
+// Warps of a block: one loads (TMA, a ring of stages), one issues the MMAs, two work out the scales of the next steps, the
+// others add up the block sums.
+#include <algorithm>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -25,17 +33,24 @@ namespace mp {
 
 namespace {
 
-constexpr int kBM = 128;             // rows per tile: the M of one MMA
+constexpr int kBM = 128;             // rows per block
+constexpr int kBN = 256;             // output channels per tile
 constexpr int kBK = 128;             // reduction channels per stage: one scale block
-constexpr int kABox = 32;            // rows per TMA box of the A tile: a short last tile of an
-                                     // expert loads only the boxes that hold rows
-constexpr int kEpiWarps = 8;         // two warpgroups, each BN / 2 columns of all 128 rows
-constexpr int kMMThreads = 128 + kEpiWarps * 32;
-constexpr int kBand = 16;            // m-tiles per band of the tile order
+constexpr int kShortBox = 32;        // rows per TMA box of a tile that is not full
+constexpr int kEpiWarps = 8;         // two warpgroups, half of the channels each
+constexpr int kEpiFirst = 4;         // warps before them: loads, products, scales (2)
+constexpr int kMMThreads = (kEpiFirst + kEpiWarps) * 32;
+constexpr int kCols = kBN * 4 / kEpiWarps;  // channels per warp, of 32 rows
+constexpr int kTileRing = 8;         // tiles whose place is kept for the epilogue
+constexpr int kBandRows = 2048;      // rows per band of the tile order
+constexpr int kMaxStages = 6;
+constexpr int kMaxSmem = 232448;     // bytes of shared memory a block may have
 
 struct MMArgs {
   int E, rows, out_cols, red_blocks;  // out_cols: N (forward) or K (dgrad)
   int w_rows;                         // weight rows per expert (N)
+  int stages;
+  int out32;                          // out is 32-byte aligned
   const float* a_scales;              // [rows][red_blocks]
   const float* w_scales;              // [E][ceil(N/128)][K/128]
   int64_t ws_expert;                  // strides of w_scales, in floats
@@ -50,29 +65,28 @@ struct Tile {
   int e, row0, nrows, col0;
 };
 
-template <int BN>
-struct MMShape {
-  static constexpr int kStageA = kBM * kBK;
-  static constexpr int kStageB = BN * kBK;
-  static constexpr int kStage = kStageA + kStageB;
-  static constexpr int kStages = BN == 256 ? 4 : 6;
-  static constexpr int kTmemCols = 2 * BN;
-};
+constexpr int kStageR = kBM * kBK;
+constexpr int kStageW = kBN * kBK;
+constexpr int kStage = kStageR + kStageW;
 
-// Shared memory after the 1024-byte aligned stages.
-template <int BN>
+// Shared memory after the stages (1024-byte aligned, as the swizzle wants them).
+// ready[slot]: the loads of a step have landed, its scales are in place and its
+// accumulator is free.
+// done[slot]: its products are finished, so the stage may be loaded again and
+// the accumulator read.  One barrier each way per step: the thread that issues
+// the products needs about 260 clocks for one wait, four MMAs and one commit,
+// and with two waits and two commits it could not keep up with the products.
 struct MMTail {
-  uint64_t full[MMShape<BN>::kStages], empty[MMShape<BN>::kStages];
-  uint64_t tfull[2], tempty[2];
+  uint64_t ready[kMaxStages], done[kMaxStages];
+  float scale[kMaxStages][2][kBM];            // [half of the channels][row]
+  int4 tile[kTileRing];                       // first row, rows, first channel
   uint32_t tmem;
   int failed;
   int scan[kMMThreads / 32];
 };
 
-template <int BN>
-size_t mm_smem_bytes(int E) {
-  return 1024 + size_t(MMShape<BN>::kStages) * MMShape<BN>::kStage + sizeof(MMTail<BN>) +
-         size_t(E + 1) * 4;
+size_t mm_smem_bytes(int E, int stages) {
+  return size_t(stages) * kStage + sizeof(MMTail) + size_t(E + 1) * 4;
 }
 
 // First and one-past-last row of expert e, forced into [0, rows].
@@ -86,7 +100,7 @@ __device__ __forceinline__ void expert_range(const MMArgs& p, int e, int& lo, in
   hi = max(lo, min(__ldg(p.expert_offsets + e + 1), p.rows));
 }
 
-// Exclusive prefix over experts of their number of m-tiles, into pre[0 .. E].
+// Exclusive prefix over experts of their number of row tiles, into pre[0 .. E].
 // Offsets that are negative or decrease leave no tiles at all (overlapping
 // experts could make more of them than the launcher's check allows for).
 __device__ void tile_prefix(const MMArgs& p, int* pre, int* scan) {
@@ -127,11 +141,11 @@ __device__ void tile_prefix(const MMArgs& p, int* pre, int* scan) {
   __syncthreads();
 }
 
-// Tile t in the order: experts ascending; within an expert, bands of kBand
-// m-tiles, in a band columns slowest, so that the tiles running at one time
-// share few weight columns and a band's rows.
-template <int BN>
+// Tile t in the order: experts ascending; within an expert, bands of kBandRows
+// rows, in a band channels slowest, so that the tiles running at one time share
+// few weight channels and a band's rows.
 __device__ __forceinline__ Tile tile_at(const MMArgs& p, const int* pre, int ncol, int t) {
+  constexpr int kBand = kBandRows / kBM;
   int lo = 0, hi = p.E;  // pre[lo] * ncol <= t < pre[hi] * ncol
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -149,213 +163,304 @@ __device__ __forceinline__ Tile tile_at(const MMArgs& p, const int* pre, int nco
   tile.e = lo;
   tile.row0 = r0 + m * kBM;
   tile.nrows = min(kBM, r1 - tile.row0);
-  tile.col0 = nt * BN;
+  tile.col0 = nt * kBN;
   return tile;
 }
 
-template <int BN, bool TB>
-__global__ void __launch_bounds__(kMMThreads, 1)
-mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_a,
-                   const __grid_constant__ CUtensorMap map_w, const MMArgs p) {
-  using S = MMShape<BN>;
-  constexpr int kHalf = BN / 2;  // columns per epilogue warpgroup
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* stages = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  MMTail<BN>* tail = reinterpret_cast<MMTail<BN>*>(stages + size_t(S::kStages) * S::kStage);
-  int* pre = reinterpret_cast<int*>(tail + 1);
-  const int warp = warp_index(), lane = threadIdx.x & 31;
-
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(&tail->full[i], 1);
-      mbar_init(&tail->empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&tail->tfull[i], 1);
-      mbar_init(&tail->tempty[i], kEpiWarps);
-    }
-    tail->failed = 0;
-    mbar_init_fence();
-  }
-  if (warp == 1) tmem_alloc(&tail->tmem, S::kTmemCols);
-  tile_prefix(p, pre, tail->scan);  // (its barriers also publish the mbarriers and the TMEM base)
-  tcgen05_fence_after();
-  const uint32_t tmem = tail->tmem;
-  const int ncol = (p.out_cols + BN - 1) / BN;
-  const int tiles = pre[p.E] * ncol;  // below 2^31: the launcher checks
-  volatile int* failed = &tail->failed;
-
-  // The accumulators of BN = 256 need more registers than a twelfth of the
-  // file: the four warps that only issue give theirs up (128 * 72 + 256 * 216
-  // = the launch's 384 * 168).
-  if (warp < 4) {
-  if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  if (warp == 0) {
-    // ---- loads: one lane keeps the ring of stages full
-    if (elect_one()) {
-      uint32_t it = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const Tile tl = tile_at<BN>(p, pre, ncol, t);
-        const int boxes = (tl.nrows + kABox - 1) / kABox;
-        const uint32_t bytes = uint32_t(boxes) * kABox * kBK + S::kStageB;
-        for (int kb = 0; kb < p.red_blocks; ++kb, ++it) {
-          const uint32_t st = it % S::kStages, use = it / S::kStages;
-          if (use > 0 && !bounded_wait(&tail->empty[st], (use - 1) & 1u, failed)) {
-            ok = false;
-            break;
-          }
-          unsigned char* sa = stages + size_t(st) * S::kStage;
-          unsigned char* sb = sa + S::kStageA;
-          mbar_arrive_expect_tx(&tail->full[st], bytes);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(sa + b * kABox * kBK, &map_a, kb * kBK, tl.row0 + b * kABox,
-                        &tail->full[st]);
-          if constexpr (TB) {
-#pragma unroll
-            for (int c = 0; c < BN / 128; ++c)
-              tma_load_2d(sb + c * 128 * kBK, &map_w, tl.col0 + c * 128,
-                          tl.e * p.w_rows + kb * kBK, &tail->full[st]);
-          } else {
-            tma_load_2d(sb, &map_w, kb * kBK, tl.e * p.w_rows + tl.col0, &tail->full[st]);
-          }
-        }
-      }
-      // every load that was issued lands before the block may end
-      for (uint32_t i = it > uint32_t(S::kStages) ? it - S::kStages : 0; i < it; ++i) {
-        uint32_t n = 0;
-        while (!mbar_try_wait(&tail->full[i % S::kStages], (i / S::kStages) & 1u) &&
-               ++n < kSpinLimit) {
-        }
-      }
-    }
-  } else if (warp == 1) {
-    // ---- products: one lane issues the MMAs of a stage into one of two accumulators
-    if (elect_one()) {
-      constexpr uint32_t idesc = mma_idesc_f8(kBM, BN, /*a_mn=*/false, /*b_mn=*/TB);
-      uint32_t it = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        for (int kb = 0; kb < p.red_blocks; ++kb, ++it) {
-          const uint32_t st = it % S::kStages, buf = it & 1u;
-          if (!bounded_wait(&tail->full[st], (it / S::kStages) & 1u, failed) ||
-              (it >= 2 && !bounded_wait(&tail->tempty[buf], ((it >> 1) - 1) & 1u, failed))) {
-            ok = false;
-            break;
-          }
-          tcgen05_fence_after();
-          const uint32_t sa = smem_addr(stages + size_t(st) * S::kStage);
-          const uint32_t sb = sa + S::kStageA;
-          const uint64_t da = smem_desc_sw128(sa, 16, 1024);
-          const uint64_t db = smem_desc_sw128(sb, TB ? 128 * kBK : 16, 1024);
-#pragma unroll
-          for (int k = 0; k < kBK / 32; ++k)
-            mma_f8(tmem + buf * BN, da + ((k * 32) >> 4),
-                   db + (TB ? ((k * 32 * 128) >> 4) : ((k * 32) >> 4)), idesc, k > 0);
-          mma_commit(&tail->empty[st]);
-          mma_commit(&tail->tfull[buf]);
-        }
-      }
-      if (it >= 1) {  // the last products finish before TMEM is given back
-        const uint32_t last = it - 1;
-        uint32_t n = 0;
-        while (!mbar_try_wait(&tail->tfull[last & 1u], (last >> 1) & 1u) && ++n < kSpinLimit) {
-        }
-      }
+// A position in a ring of n slots: the slot and how often the ring went round.
+struct Ring {
+  int slot = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++slot == n) {
+      slot = 0;
+      ++round;
     }
   }
-  } else {
-    if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    // ---- block sums from TMEM into fp32 registers, then bf16 rows
-    const int ew = warp - 4;
-    const int half = ew >> 2;                // which half of the columns
-    const int lrow = (ew & 3) * 32 + lane;   // row of the tile = TMEM lane
-    uint32_t it = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Tile tl = tile_at<BN>(p, pre, ncol, t);
-      const bool warp_has_rows = (ew & 3) * 32 < tl.nrows;
-      const bool has_row = lrow < tl.nrows;
-      const int64_t row = tl.row0 + (has_row ? lrow : 0);
-      const float* sa = p.a_scales + row * p.red_blocks;
-      const int cb = min((tl.col0 + half * kHalf) >> 7, (p.out_cols - 1) >> 7);
-      const float* sw = p.w_scales + tl.e * p.ws_expert + int64_t(cb) * p.ws_out;
-      float2 acc[kHalf / 2];
-#pragma unroll
-      for (int j = 0; j < kHalf / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
-      float s_next = __ldg(sa) * __ldg(sw);
-      for (int kb = 0; kb < p.red_blocks; ++kb, ++it) {
-        const float s = s_next;
-        if (kb + 1 < p.red_blocks) s_next = __ldg(sa + kb + 1) * __ldg(sw + int64_t(kb + 1) * p.ws_red);
-        const uint32_t buf = it & 1u;
-        if (!bounded_wait_warp(&tail->tfull[buf], (it >> 1) & 1u, failed)) {
-          ok = false;
-          break;
-        }
-        tcgen05_fence_after();
-        if (warp_has_rows) {
-          const uint32_t src = tmem + buf * BN + half * kHalf + (uint32_t(ew & 3) << 21);
-          const float2 s2 = make_float2(s, s);
-#pragma unroll
-          for (int c = 0; c < kHalf / 32; ++c) {
-            float2 v[16];
-            tmem_ld_x32(src + c * 32, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) acc[c * 16 + j] = fma2(v[j], s2, acc[c * 16 + j]);
-          }
-        }
-        tcgen05_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tail->tempty[buf]);
-      }
-      if (ok && has_row) {
-        uint16_t* dst = p.out + row * p.out_cols + tl.col0 + half * kHalf;
-        const int left = p.out_cols - (tl.col0 + half * kHalf);  // a multiple of 16 (or <= 0)
-#pragma unroll
-        for (int c = 0; c < kHalf / 8; ++c) {
-          if (c * 8 < left) {
-            int4 o;
-            o.x = int(pack_bf16x2_rn(acc[c * 4].x, acc[c * 4].y));
-            o.y = int(pack_bf16x2_rn(acc[c * 4 + 1].x, acc[c * 4 + 1].y));
-            o.z = int(pack_bf16x2_rn(acc[c * 4 + 2].x, acc[c * 4 + 2].y));
-            o.w = int(pack_bf16x2_rn(acc[c * 4 + 3].x, acc[c * 4 + 3].y));
-            *reinterpret_cast<int4*>(dst + c * 8) = o;
-          }
-        }
-      }
-    }
-  }
+};
 
+// Every warp's end: nothing of the block is in use after it.
+__device__ __forceinline__ void block_end() {
   __syncwarp();
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, S::kTmemCols);
-  if (threadIdx.x == 0 && tail->failed) raise_error(p.dev_err, MP_ERR_TIMEOUT);
 }
 
-template <int BN, bool TB>
-cudaError_t launch_mm(const MMArgs& p, const CUtensorMap& ma, const CUtensorMap& mw,
-                      cudaStream_t st) {
+template <bool DGRAD>
+__global__ void __launch_bounds__(kMMThreads, 1)
+mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
+                   const __grid_constant__ CUtensorMap map_short,
+                   const __grid_constant__ CUtensorMap map_w, const MMArgs p) {
+  // (aligned by its declaration: a pointer rounded up by hand is no longer known
+  // to be shared memory, and generic loads of the scales cost the epilogue time)
+  extern __shared__ __align__(1024) unsigned char stages[];
+  MMTail* tail = reinterpret_cast<MMTail*>(stages + size_t(p.stages) * kStage);
+  int* pre = reinterpret_cast<int*>(tail + 1);
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&tail->ready[i], 1 + 2 + kEpiWarps);
+      mbar_init(&tail->done[i], 1);
+    }
+    tail->failed = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_alloc(&tail->tmem, 2 * kBN);
+  tile_prefix(p, pre, tail->scan);
+  tcgen05_fence_after();
+  const uint32_t tmem = tail->tmem;
+  const int ncol = (p.out_cols + kBN - 1) / kBN;
+  const int tiles = pre[p.E] * ncol;  // below 2^31: the C ABI checks
+  const int first = blockIdx.x, step = gridDim.x;
+  // steps of this block: every tile's reduction blocks, one after the other
+  const int64_t steps =
+      tiles > first ? int64_t((tiles - first + step - 1) / step) * p.red_blocks : 0;
+  volatile int* failed = &tail->failed;
+
+  // The sums need more registers than a twelfth of the file: the four warps
+  // before them give theirs up (128 * 96 + 256 * 200 is less than the launch's
+  // 384 * 168).  Each side has its own end, which keeps the two budgets apart.
+  if (warp < kEpiFirst) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+  if (warp == 0) {
+    // ---- loads: one lane keeps the ring of stages full
+    if (elect_one()) {
+      Ring s;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step) {
+        const Tile tl = tile_at(p, pre, ncol, t);
+        const int boxes = (tl.nrows + kShortBox - 1) / kShortBox;
+        const uint32_t bytes = uint32_t(boxes) * kShortBox * kBK + kStageW;
+        for (int kb = 0; kb < p.red_blocks; ++kb, s.next(p.stages)) {
+          if (s.round > 0 && !bounded_wait(&tail->done[s.slot], (s.round - 1) & 1u, failed)) {
+            ok = false;
+            break;
+          }
+          unsigned char* sr = stages + size_t(s.slot) * kStage;
+          unsigned char* sw = sr + kStageR;
+          uint64_t* ready = &tail->ready[s.slot];
+          mbar_arrive_expect_tx(ready, bytes);
+          if (boxes == kBM / kShortBox) {
+            tma_load_2d(sr, &map_rows, kb * kBK, tl.row0, ready);
+          } else {
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d(sr + i * kShortBox * kBK, &map_short, kb * kBK,
+                          tl.row0 + i * kShortBox, ready);
+          }
+          if constexpr (DGRAD) {
+#pragma unroll
+            for (int c = 0; c < kBN / 128; ++c)
+              tma_load_2d(sw + c * 128 * kBK, &map_w, tl.col0 + c * 128,
+                          tl.e * p.w_rows + kb * kBK, ready);
+          } else {
+            tma_load_2d(sw, &map_w, kb * kBK, tl.e * p.w_rows + tl.col0, ready);
+          }
+        }
+      }
+      // every load has landed and been used before the block may end
+      for (int i = 0; i < p.stages; ++i, s.next(p.stages))
+        if (s.round > 0) bounded_wait(&tail->done[s.slot], (s.round - 1) & 1u, failed);
+    }
+  } else if (warp == 1) {
+    // ---- products: one lane issues the MMAs of a stage into one of two accumulators
+    if (elect_one()) {
+      constexpr uint32_t idesc = mma_idesc_f8(kBM, kBN, /*a_mn=*/false, /*b_mn=*/DGRAD);
+      Ring s;
+      uint32_t acc = tmem;
+      for (int64_t i = 0; i < steps; ++i, s.next(p.stages), acc ^= kBN) {
+        if (!bounded_wait(&tail->ready[s.slot], s.round & 1u, failed)) break;
+        tcgen05_fence_after();
+        const uint32_t sr = smem_addr(stages + size_t(s.slot) * kStage);
+        const uint64_t dr = smem_desc_sw128(sr, 16, 1024);
+        const uint64_t dw = smem_desc_sw128(sr + kStageR, DGRAD ? 128 * kBK : 16, 1024);
+#pragma unroll
+        for (int k = 0; k < kBK / 32; ++k)
+          mma_f8(acc, dr + ((k * 32) >> 4),
+                       dw + (DGRAD ? ((k * 32 * 128) >> 4) : ((k * 32) >> 4)), idesc, k > 0);
+        mma_commit(&tail->done[s.slot]);
+      }
+    }
+  } else {
+    // ---- scales of the next steps: row times weight scale, this warp for one
+    // half of the channels.  Four steps are loaded at a time, one such group
+    // ahead of the one in use: a row's scales lie red_blocks apart, so every
+    // load is a trip to L2.
+    const int half = warp - 2;
+    const bool vec = p.red_blocks % 4 == 0 && (reinterpret_cast<uintptr_t>(p.a_scales) & 15) == 0;
+    Ring s;
+    // a slot's old scales are used up when the step two after theirs, which took
+    // their accumulator over, is done: `behind` is that step
+    Ring behind;
+    behind.slot = 2;
+    int count = 0;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += step, ++count) {
+      const Tile tl = tile_at(p, pre, ncol, t);
+      const float* src[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        src[i] = p.a_scales + int64_t(tl.row0 + min(lane + i * 32, tl.nrows - 1)) * p.red_blocks;
+      const int cb = min((tl.col0 >> 7) + half, (p.out_cols - 1) >> 7);
+      const float* sw = p.w_scales + tl.e * p.ws_expert + int64_t(cb) * p.ws_out;
+      float ahead[4][4], wahead[4];
+      auto load4 = [&](int kb) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          wahead[u] = kb + u < p.red_blocks ? __ldg(sw + int64_t(kb + u) * p.ws_red) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (vec) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(src[i] + kb));
+            ahead[i][0] = v.x;
+            ahead[i][1] = v.y;
+            ahead[i][2] = v.z;
+            ahead[i][3] = v.w;
+          } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              ahead[i][u] = kb + u < p.red_blocks ? __ldg(src[i] + kb + u) : 0.0f;
+          }
+        }
+      };
+      load4(0);
+      for (int kb0 = 0; kb0 < p.red_blocks && ok; kb0 += 4) {
+        float v[4][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[u][i] = ahead[i][u] * wahead[u];
+        if (kb0 + 4 < p.red_blocks) load4(kb0 + 4);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (kb0 + u < p.red_blocks && ok) {
+            if (s.round > 0) {
+              ok = bounded_wait_warp(&tail->done[behind.slot], behind.round & 1u, failed);
+              behind.next(p.stages);
+            }
+            if (ok) {
+              // (a tile's place is overwritten kTileRing tiles later, and at most
+              // as many steps as there are stages are prepared ahead)
+              if (kb0 + u == 0 && half == 0 && lane == 0)
+                tail->tile[count % kTileRing] = make_int4(tl.row0, tl.nrows, tl.col0, 0);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) tail->scale[s.slot][half][lane + i * 32] = v[u][i];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&tail->ready[s.slot]);
+              s.next(p.stages);
+            }
+          }
+        }
+      }
+    }
+  }
+  block_end();
+  if (warp == 1) tmem_dealloc(tmem, 2 * kBN);
+  if (threadIdx.x == 0 && tail->failed) raise_error(p.dev_err, MP_ERR_TIMEOUT);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    // ---- block sums from TMEM into fp32 registers, then bf16 rows
+    const int q = warp & 3;                        // the TMEM lanes this warp may read: 32 q ..
+    const int col = ((warp - kEpiFirst) >> 2) * kCols;  // its columns of the accumulator
+    const int lrow = q * 32 + lane;
+    Ring s;
+    int free_slot = 0;  // the step that gets this step's accumulator next
+    auto hand_back = [&] {
+      tcgen05_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tail->ready[free_slot]);
+      if (++free_slot == p.stages) free_slot = 0;
+    };
+    hand_back();  // both accumulators are free at the start
+    hand_back();
+    uint32_t src = tmem + col + (uint32_t(q) << 21);
+    const int64_t count = steps / p.red_blocks;
+    for (int64_t i = 0; i < count; ++i) {
+      float2 acc[kCols / 2];
+#pragma unroll
+      for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
+      bool ok = true, some = false;
+      for (int kb = 0; kb < p.red_blocks; ++kb, s.next(p.stages), src ^= kBN) {
+        ok = bounded_wait_warp(&tail->done[s.slot], s.round & 1u, failed);
+        if (!ok) break;
+        tcgen05_fence_after();
+        if (kb == 0) some = q * 32 < tail->tile[i % kTileRing].y;
+        if (some) {
+          const float sc = tail->scale[s.slot][col >> 7][lrow];
+          const float2 s2 = make_float2(sc, sc);
+          // groups of 16 channels: one on its way from TMEM while the one before
+          // is added up
+          float2 v[2][8];
+          tmem_ld_x16(src, v[0]);
+          tmem_wait_ld(v[0]);
+#pragma unroll
+          for (int c = 0; c < kCols / 16; ++c) {
+            if (c + 1 < kCols / 16)
+              tmem_ld_x16(src + (c + 1) * 16, v[(c + 1) & 1]);
+            else
+              hand_back();  // the last group is in registers
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[c * 8 + j] = fma2(v[c & 1][j], s2, acc[c * 8 + j]);
+            if (c + 1 < kCols / 16) tmem_wait_ld(v[(c + 1) & 1]);
+          }
+        } else {
+          hand_back();
+        }
+      }
+      if (!ok) break;
+      const int4 tl = tail->tile[i % kTileRing];
+      if (lrow < tl.y) {
+        uint16_t* dst =
+            p.out + int64_t(tl.x + lrow) * p.out_cols + tl.z + col;
+        const int left = p.out_cols - (tl.z + col);  // a multiple of 16 (or <= 0)
+#pragma unroll
+        for (int c = 0; c < kCols / 16; ++c) {  // 16 channels: one 32-byte sector
+          if (c * 16 < left) {
+            Words<8> o;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              o.w[j] = pack_bf16x2_rn(acc[c * 8 + j].x, acc[c * 8 + j].y);
+            if (p.out32) {
+              st_stream_w<8>(reinterpret_cast<Words<8>*>(dst + c * 16), o);
+            } else {
+              int4* d = reinterpret_cast<int4*>(dst + c * 16);
+              d[0] = make_int4(o.w[0], o.w[1], o.w[2], o.w[3]);
+              d[1] = make_int4(o.w[4], o.w[5], o.w[6], o.w[7]);
+            }
+          }
+        }
+      }
+    }
+    block_end();
+  }
+}
+
+template <bool DGRAD>
+cudaError_t launch_mm(MMArgs p, const void* a, const void* w, int K, int red, cudaStream_t st) {
+  CUtensorMap mr, ms, mw;
+  if (!make_map_2d(&mr, a, 1, uint64_t(red), uint64_t(p.rows), kBK, kBM) ||
+      !make_map_2d(&ms, a, 1, uint64_t(red), uint64_t(p.rows), kBK, kShortBox) ||
+      !make_map_2d(&mw, w, 1, uint64_t(K), uint64_t(p.E) * p.w_rows, kBK, DGRAD ? kBK : kBN))
+    return cudaErrorInvalidValue;
+  p.stages = kMaxStages;
+  while (mm_smem_bytes(p.E, p.stages) > size_t(kMaxSmem)) --p.stages;
+  const int smem = int(mm_smem_bytes(p.E, p.stages));
   static thread_local int configured_smem[64] = {0};
-  const int smem = int(mm_smem_bytes<BN>(p.E));
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || configured_smem[dev] < smem) {
-    e = cudaFuncSetAttribute(mp_k_expert_matmul<BN, TB>,
+    e = cudaFuncSetAttribute(mp_k_expert_matmul<DGRAD>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured_smem[dev] = smem;
   }
-  // at most one tile per row block and expert
-  const int64_t mt = (int64_t(p.rows) + kBM - 1) / kBM + (p.E - 1);
-  const int64_t tiles = mt * ((p.out_cols + BN - 1) / BN);
-  if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  const int grid = int(tiles < sm_count() ? tiles : sm_count());
-  mp_k_expert_matmul<BN, TB><<<grid, kMMThreads, size_t(smem), st>>>(ma, mw, p);
+  // at most one short tile per expert
+  const int64_t row_tiles = std::min<int64_t>(p.rows, int64_t(p.rows) / kBM + p.E);
+  const int64_t tiles = row_tiles * ((p.out_cols + kBN - 1) / kBN);
+  mp_k_expert_matmul<DGRAD><<<unsigned(std::min<int64_t>(tiles, sm_count())), kMMThreads,
+                              size_t(smem), st>>>(mr, ms, mw, p);
   return cudaGetLastError();
 }
 
@@ -381,13 +486,9 @@ cudaError_t launch_expert_matmul(int E, int rows, int N, int K, bool dgrad, cons
   p.ws_red = dgrad ? kb : 1;
   p.expert_offsets = expert_offsets;
   p.out = static_cast<uint16_t*>(out);
+  p.out32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   p.dev_err = dev_err;
-  const int BN = 256;
-  CUtensorMap ma, mw;
-  if (!make_map_2d(&ma, a, 1, uint64_t(red), uint64_t(rows), kBK, kABox) ||
-      !make_map_2d(&mw, w, 1, uint64_t(K), uint64_t(E) * N, kBK, dgrad ? kBK : BN))
-    return cudaErrorInvalidValue;
-  return dgrad ? launch_mm<256, true>(p, ma, mw, st) : launch_mm<256, false>(p, ma, mw, st);
+  return dgrad ? launch_mm<true>(p, a, w, K, red, st) : launch_mm<false>(p, a, w, K, red, st);
 }
 
 }  // namespace mp

@@ -214,24 +214,24 @@ mp_k_expert_wgrad(const WgradArgs p) {
       tcgen05_fence_after();
       uint16_t* dst = p.dw + (int64_t(w.e) * p.N + w.n0 + q * 32 + lane) * p.K + w.k0;
 #pragma unroll
-      for (int c = 0; c < kWN / 32; ++c) {
-        float2 v[16];
+      for (int c = 0; c < kWN / 16; ++c) {
+        float2 v[8];
         if (some) {
-          tmem_ld_x32(tmem + buf * kWN + c * 32 + (uint32_t(q) << 21), v);
-          tmem_wait_ld();
+          tmem_ld_x16(tmem + buf * kWN + c * 16 + (uint32_t(q) << 21), v);
+          tmem_wait_ld(v);
         } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = make_float2(0.0f, 0.0f);
+          for (int j = 0; j < 8; ++j) v[j] = make_float2(0.0f, 0.0f);
         }
-        if (w.k0 + c * 32 < p.K) {
+        if (w.k0 + c * 16 < p.K) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 2; ++j) {
             uint4 o;
             o.x = pack_bf16x2_rn(v[4 * j].x, v[4 * j].y);
             o.y = pack_bf16x2_rn(v[4 * j + 1].x, v[4 * j + 1].y);
             o.z = pack_bf16x2_rn(v[4 * j + 2].x, v[4 * j + 2].y);
             o.w = pack_bf16x2_rn(v[4 * j + 3].x, v[4 * j + 3].y);
-            reinterpret_cast<uint4*>(dst + c * 32)[j] = o;
+            reinterpret_cast<uint4*>(dst + c * 16)[j] = o;
           }
         }
       }

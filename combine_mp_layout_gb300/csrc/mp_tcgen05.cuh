@@ -67,6 +67,7 @@ __device__ __forceinline__ int warp_index() {
   return __shfl_sync(kFull, int(threadIdx.x >> 5), 0);
 }
 
+// A TMA load of one box; its bytes are counted on the mbarrier.
 __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* map, int x, int y,
                                             uint64_t* bar) {
   asm volatile(
@@ -79,19 +80,25 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// Bounded wait on an mbarrier phase (about a second) by one thread; false, with
-// the failure noted in the block's flag, when it gives up or another role of
-// the block has given up.
+// Bounded wait on an mbarrier phase by one thread (2^26 attempts of some 20
+// clocks, about a second); false, with the failure noted in the block's flag,
+// when it gives up.  Every role of a block that waits for another one gives up
+// by itself.  The loop is three instructions: whatever else it does is added
+// to the time from one role to the next, which the products wait for.
 __device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity,
                                              volatile int* failed) {
-  uint32_t spins = 0;
-  while (!mbar_try_wait(bar, parity)) {
-    if (++spins > kSpinLimit || *failed) {
-      *failed = 1;
-      return false;
-    }
-  }
-  return true;
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+      "$MP_TRY_%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " @p bra $MP_END_%=;\n add.u32 n, n, 1;\n setp.lt.u32 p, n, 67108864;\n"
+      " @p bra $MP_TRY_%=;\n setp.ne.u32 p, n, n;\n"
+      "$MP_END_%=:\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  if (!ok) *failed = 1;
+  return ok != 0;
 }
 // The same for a whole warp, with one answer for all its lanes.
 __device__ __forceinline__ bool bounded_wait_warp(uint64_t* bar, uint32_t parity,
@@ -163,22 +170,24 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
       : "memory");
 }
 
-// 32 columns of this warp's 32 TMEM lanes: v[j] = columns 2j, 2j + 1 of lane.
-__device__ __forceinline__ void tmem_ld_x32(uint32_t src, float2 (&v)[16]) {
+// 16 columns of this warp's 32 TMEM lanes: v[j] = columns 2j, 2j + 1 of lane.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t src, float2 (&v)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=f"(v[0].x), "=f"(v[0].y), "=f"(v[1].x), "=f"(v[1].y), "=f"(v[2].x), "=f"(v[2].y),
         "=f"(v[3].x), "=f"(v[3].y), "=f"(v[4].x), "=f"(v[4].y), "=f"(v[5].x), "=f"(v[5].y),
-        "=f"(v[6].x), "=f"(v[6].y), "=f"(v[7].x), "=f"(v[7].y), "=f"(v[8].x), "=f"(v[8].y),
-        "=f"(v[9].x), "=f"(v[9].y), "=f"(v[10].x), "=f"(v[10].y), "=f"(v[11].x), "=f"(v[11].y),
-        "=f"(v[12].x), "=f"(v[12].y), "=f"(v[13].x), "=f"(v[13].y), "=f"(v[14].x),
-        "=f"(v[14].y), "=f"(v[15].x), "=f"(v[15].y)
+        "=f"(v[6].x), "=f"(v[6].y), "=f"(v[7].x), "=f"(v[7].y)
       : "r"(src));
 }
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+// Waits for this thread's TMEM loads.  The loaded values pass through, so that
+// no use of them can be moved ahead of the wait.
+__device__ __forceinline__ void tmem_wait_ld(float2 (&v)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0].x), "+f"(v[0].y), "+f"(v[1].x), "+f"(v[1].y), "+f"(v[2].x),
+                 "+f"(v[2].y), "+f"(v[3].x), "+f"(v[3].y), "+f"(v[4].x), "+f"(v[4].y),
+                 "+f"(v[5].x), "+f"(v[5].y), "+f"(v[6].x), "+f"(v[6].y), "+f"(v[7].x),
+                 "+f"(v[7].y)::"memory");
 }
 
 // Two fp32 FMAs in one instruction.

@@ -722,7 +722,8 @@ int mp_route_backward(int R, int N, int K, int E, int scoring, int dtype, const 
  *                        writes it, or NULL for E == 1 (all rows)
  *   out  out             bf16 [rows][N]; rows of no expert are not written
  * Checks: 1 <= E <= 8192, rows >= 0, K % 128 == 0, N % 16 == 0 (both > 0),
- *   E*N < 2^31, (rows/128 + E) * ceil(N/64) < 2^31, non-NULL buffers (a, out
+ *   E*N < 2^31, (rows/64 + E) * ceil(N/256) < 2^31, rows <= 2^31 - 1025,
+ *   non-NULL buffers (a, out
  *   and the scales of a when rows == 0), a, w and out 16-byte aligned.
  * Device errors: MP_ERR_CAPACITY (an offset past `rows`; it is cut off there),
  *   MP_ERR_INVALID_ARG (offsets that decrease or are negative; nothing is
@@ -741,7 +742,7 @@ int mp_expert_matmul_e4m3(int E, int rows, int N, int K, const void *a, const fl
  *   in   dy, dy_scales   e4m3 [rows][N], fp32 [rows][N/128]
  *   out  dx              bf16 [rows][K]
  * Checks and device errors as mp_expert_matmul_e4m3, with N % 128 == 0 and
- *   (rows/128 + E) * ceil(K/64) < 2^31.
+ *   (rows/64 + E) * ceil(K/256) < 2^31.
  */
 int mp_expert_matmul_dgrad_e4m3(int E, int rows, int N, int K, const void *dy,
                                 const float *dy_scales, const void *w, const float *w_scales,
