@@ -207,7 +207,7 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
     tail->failed = 0;
     mbar_init_fence();
   }
-  if (warp == 1) tmem_alloc(&tail->tmem, 2 * kBN);
+  if (warp == 1) tmem_alloc<false>(&tail->tmem, 2 * kBN);
   tile_prefix(p, pre, tail->scan);
   tcgen05_fence_after();
   const uint32_t tmem = tail->tmem;
@@ -279,7 +279,7 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
         for (int k = 0; k < kBK / 32; ++k)
           mma_f8(acc, dr + ((k * 32) >> 4),
                        dw + (DGRAD ? ((k * 32 * 128) >> 4) : ((k * 32) >> 4)), idesc, k > 0);
-        mma_commit(&tail->done[s.slot]);
+        mma_commit<false>(&tail->done[s.slot]);
       }
     }
   } else {
@@ -356,7 +356,7 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
     }
   }
   block_end();
-  if (warp == 1) tmem_dealloc(tmem, 2 * kBN);
+  if (warp == 1) tmem_dealloc<false>(tmem, 2 * kBN);
   if (threadIdx.x == 0 && tail->failed) raise_error(p.dev_err, MP_ERR_TIMEOUT);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");

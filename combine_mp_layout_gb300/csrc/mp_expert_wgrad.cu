@@ -10,6 +10,18 @@
 // scale) is rounded once to bf16 (8 significant bits: an error of at most
 // 2^-8 of the value, where e4m3 itself carries up to 2^-4), the products are
 // exact and summed in fp32 in TMEM over all rows of the expert.
+//
+// A pair of blocks (cta_group::2) works on 256 x 256 weights: each block
+// dequantises the 128 dy channels of its half of M and the 128 a channels of
+// its half of N, 64 rows per stage.  Per stage and block that is 16,384 values
+// to convert and 32 KB to write to and 32 KB to read from shared memory per 512
+// clocks of MMA; one block alone on 128 x 256 has to convert and move half as
+// much again for the same products.  Both operands are MN-major: a row of
+// channels stays a row in shared memory, nothing is transposed.
+//
+// Warps of a block: eight convert (global memory to registers some stages
+// ahead, across tiles too, then to shared memory), four write finished tiles,
+// one (in the first block) issues the MMAs.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_fp16.h>
@@ -24,14 +36,13 @@ namespace mp {
 
 namespace {
 
-constexpr int kWM = 128;            // dy channels per tile (one scale block): the M of the MMA
-constexpr int kWN = 256;            // a channels per tile (two scale blocks): its N
+constexpr int kWC = 128;            // dy and a channels per block: one scale block each
 constexpr int kWRows = 64;          // rows per stage: four K = 16 steps of kind::f16
-constexpr int kWStages = 4;
-constexpr int kWStageA = kWRows * kWM * 2;
-constexpr int kWStageB = kWRows * kWN * 2;
-constexpr int kWStage = kWStageA + kWStageB;
-constexpr int kConvWarps = 8;       // global -> registers -> bf16 -> shared memory
+constexpr int kWStages = 6;
+constexpr int kWOperand = kWRows * kWC * 2;
+constexpr int kWStage = 2 * kWOperand;
+constexpr int kConvWarps = 8;
+constexpr int kAhead = 3;           // stages whose global loads are in flight
 constexpr int kWThreads = (kConvWarps + 4 + 1) * 32;  // 4 epilogue warps, 1 MMA warp
 constexpr int kLbo = kWRows * 128;  // 64 bf16 channels (128 bytes) of all of a stage's rows
 
@@ -44,6 +55,7 @@ struct WgradArgs {
   const int32_t* expert_offsets;
   uint16_t* dw;
   int32_t* dev_err;
+  int out32;                        // dw is 32-byte aligned
 };
 
 struct WgradTail {
@@ -51,21 +63,21 @@ struct WgradTail {
   uint32_t tmem;
   int failed;
 };
-constexpr size_t kWSmem = 1024 + size_t(kWStages) * kWStage + sizeof(WgradTail);
+constexpr size_t kWSmem = size_t(kWStages) * kWStage + sizeof(WgradTail);
 
 struct WTile {
-  int e, lo, hi, n0, k0;
+  int e, lo, hi, n0, k0;  // n0, k0: of the pair
 };
 
 // Experts ascending, then n, with k fastest: the tiles running at one time
 // share the rows of an expert.
 __device__ __forceinline__ WTile wtile_at(const WgradArgs& p, int t) {
-  const int kt = (p.K + kWN - 1) / kWN, nt = p.N / kWM;
+  const int kt = (p.K + 2 * kWC - 1) / (2 * kWC), nt = (p.N + 2 * kWC - 1) / (2 * kWC);
   WTile w;
   w.e = t / (kt * nt);
   const int rem = t - w.e * (kt * nt);
-  w.n0 = (rem / kt) * kWM;
-  w.k0 = (rem % kt) * kWN;
+  w.n0 = (rem / kt) * 2 * kWC;
+  w.k0 = (rem % kt) * 2 * kWC;
   if (p.expert_offsets == nullptr) {
     w.lo = 0;
     w.hi = p.rows;
@@ -105,26 +117,25 @@ __device__ __forceinline__ void store16(unsigned char* tile, int r, int c, const
   *reinterpret_cast<uint4*>(row + (((odd ? u : u + 1) ^ sw) << 4)) = odd ? x : y;
 }
 
-__global__ void __launch_bounds__(kWThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
 mp_k_expert_wgrad(const WgradArgs p) {
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* stages = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) unsigned char stages[];
   WgradTail* tail = reinterpret_cast<WgradTail*>(stages + size_t(kWStages) * kWStage);
   const int warp = warp_index(), lane = threadIdx.x & 31;
+  const int rank = int(cluster_rank());
   if (threadIdx.x == 0) {
     for (int i = 0; i < kWStages; ++i) {
-      mbar_init(&tail->full[i], kConvWarps);
+      mbar_init(&tail->full[i], 2 * kConvWarps);
       mbar_init(&tail->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tail->tfull[i], 1);
-      mbar_init(&tail->tempty[i], 4);
+      mbar_init(&tail->tempty[i], 2 * 4);
     }
     tail->failed = 0;
     mbar_init_fence();
   }
-  if (warp == kConvWarps + 4) tmem_alloc(&tail->tmem, 512);
+  if (warp == kConvWarps + 4) tmem_alloc<true>(&tail->tmem, 512);
   if (p.expert_offsets != nullptr && blockIdx.x == 0) {
     int bad = 0;
     for (int e = threadIdx.x; e < p.E; e += kWThreads) {
@@ -135,158 +146,184 @@ mp_k_expert_wgrad(const WgradArgs p) {
     if (bad) raise_error(p.dev_err, bad);
   }
   __syncthreads();
+  cluster_sync_all();  // both blocks' mbarriers and TMEM are ready
   tcgen05_fence_after();
   const uint32_t tmem = tail->tmem;
-  const int tiles = p.E * (p.N / kWM) * ((p.K + kWN - 1) / kWN);
+  const int tiles = p.E * ((p.N + 2 * kWC - 1) / (2 * kWC)) * ((p.K + 2 * kWC - 1) / (2 * kWC));
+  const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
   volatile int* failed = &tail->failed;
 
   if (warp < kConvWarps) {
-    // ---- rows from global memory, dequantised, into the ring of stages
+    // ---- rows from global memory, dequantised, into the ring of stages.  A
+    // thread has 16 channels of rows r and r + 32 of each operand.
+    const int r = threadIdx.x >> 3, c = threadIdx.x & 7;
     const int nb = p.N / 128, kb = p.K / 128;
-    const int ra = threadIdx.x >> 3, ca = threadIdx.x & 7;    // dy: 8 lanes a row, 2 x 32 rows
-    const int rb = threadIdx.x >> 4, cbk = threadIdx.x & 15;  // a: 16 lanes a row, 4 x 16 rows
-    uint32_t it = 0;
+    // where the next loads come from
+    int t = first - stride, row = r, end = 0;  // (no rows: the first load finds a tile)
+    bool more = true, n_in = false, k_in = false;
+    const unsigned char *pd = nullptr, *pa = nullptr;
+    const float *psd = nullptr, *psa = nullptr;
+    auto next_tile = [&] {  // the next tile with rows
+      do {
+        t += stride;
+        if (t >= tiles) {
+          more = false;
+          return;
+        }
+        const WTile w = wtile_at(p, t);
+        row = w.lo + r;
+        end = w.hi;
+        if (w.lo == w.hi) continue;
+        const int n = w.n0 + rank * kWC, k = w.k0 + rank * kWC;
+        n_in = n < p.N;
+        k_in = k < p.K;
+        pd = p.dy + int64_t(row) * p.N + n + c * 16;
+        pa = p.a + int64_t(row) * p.K + k + c * 16;
+        psd = p.dy_scales + int64_t(row) * nb + n / 128;
+        psa = p.a_scales + int64_t(row) * kb + k / 128;
+        return;
+      } while (true);
+    };
+    uint4 v[kAhead][4];
+    float s[kAhead][4];
+    bool have[kAhead];
+    auto load = [&](uint4 (&v)[4], float (&s)[4], bool& have) {
+      if (more && row - r >= end) next_tile();
+      have = more;
+      if (!more) return;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool in = row + i * 32 < end;
+        v[i] = in && n_in ? __ldg(reinterpret_cast<const uint4*>(pd + int64_t(i) * 32 * p.N))
+                          : make_uint4(0, 0, 0, 0);
+        s[i] = in && n_in ? __ldg(psd + int64_t(i) * 32 * nb) : 0.0f;
+        v[2 + i] = in && k_in ? __ldg(reinterpret_cast<const uint4*>(pa + int64_t(i) * 32 * p.K))
+                              : make_uint4(0, 0, 0, 0);
+        s[2 + i] = in && k_in ? __ldg(psa + int64_t(i) * 32 * kb) : 0.0f;
+      }
+      row += kWRows;
+      pd += int64_t(kWRows) * p.N;
+      pa += int64_t(kWRows) * p.K;
+      psd += int64_t(kWRows) * nb;
+      psa += int64_t(kWRows) * kb;
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(v[i], s[i], have[i]);
+    int slot = 0;
+    uint32_t round = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const WTile w = wtile_at(p, t);
-      const int steps = (w.hi - w.lo + kWRows - 1) / kWRows;
-      const bool b_in = w.k0 + cbk * 16 < p.K;
-      uint4 va[2], vb[4];
-      float sa[2], sb[4];
-      auto load = [&](int step) {
-        const int r0 = w.lo + step * kWRows;
+    while (ok) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int64_t r = r0 + ra + i * 32;
-          const bool in = r < w.hi;
-          va[i] = in ? __ldg(reinterpret_cast<const uint4*>(p.dy + r * p.N + w.n0) + ca)
-                     : make_uint4(0, 0, 0, 0);
-          sa[i] = in ? __ldg(p.dy_scales + r * nb + w.n0 / 128) : 0.0f;
-        }
+      for (int i = 0; i < kAhead; ++i) {
+        ok = ok && have[i];
+        if (ok && round > 0) ok = bounded_wait_warp(&tail->empty[slot], (round - 1) & 1u, failed);
+        if (ok) {
+          unsigned char* td = stages + slot * kWStage;
+          uint32_t o[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t r = r0 + rb + i * 16;
-          const bool in = r < w.hi && b_in;
-          vb[i] = in ? __ldg(reinterpret_cast<const uint4*>(p.a + r * p.K + w.k0) + cbk)
-                     : make_uint4(0, 0, 0, 0);
-          sb[i] = in ? __ldg(p.a_scales + r * kb + (w.k0 + cbk * 16) / 128) : 0.0f;
+          for (int j = 0; j < 2; ++j) {
+            dequant16(v[i][j], s[i][j], o);
+            store16(td, r + j * 32, c, o);
+            dequant16(v[i][2 + j], s[i][2 + j], o);
+            store16(td + kWOperand, r + j * 32, c, o);
+          }
+          load(v[i], s[i], have[i]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_first(&tail->full[slot], rank);
+          if (++slot == kWStages) {
+            slot = 0;
+            ++round;
+          }
         }
-      };
-      if (steps > 0) load(0);
-      for (int step = 0; step < steps; ++step, ++it) {
-        const uint32_t st = it % kWStages, use = it / kWStages;
-        if (use > 0 && !bounded_wait_warp(&tail->empty[st], (use - 1) & 1u, failed)) {
-          ok = false;
-          break;
-        }
-        unsigned char* ta = stages + size_t(st) * kWStage;
-        unsigned char* tb = ta + kWStageA;
-        uint32_t o[8];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          dequant16(va[i], sa[i], o);
-          store16(ta, ra + i * 32, ca, o);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dequant16(vb[i], sb[i], o);
-          store16(tb, rb + i * 16, cbk, o);
-        }
-        if (step + 1 < steps) load(step + 1);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tail->full[st]);
       }
     }
   } else if (warp < kConvWarps + 4) {
     // ---- accumulators to bf16 weights' gradients; an expert without rows gets zeros
     const int q = warp & 3;
     uint32_t nt = 0;  // tiles with products so far
-    bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+    for (int t = first; t < tiles; t += stride) {
       const WTile w = wtile_at(p, t);
       const bool some = w.hi > w.lo;
       const uint32_t buf = nt & 1u;
-      if (some && !bounded_wait_warp(&tail->tfull[buf], (nt >> 1) & 1u, failed)) {
-        ok = false;
-        break;
-      }
+      if (some && !bounded_wait_warp(&tail->tfull[buf], (nt >> 1) & 1u, failed)) break;
       tcgen05_fence_after();
-      uint16_t* dst = p.dw + (int64_t(w.e) * p.N + w.n0 + q * 32 + lane) * p.K + w.k0;
+      const int n = w.n0 + rank * kWC + q * 32 + lane;
+      uint16_t* dst = p.dw + (int64_t(w.e) * p.N + n) * p.K + w.k0;
 #pragma unroll
-      for (int c = 0; c < kWN / 16; ++c) {
+      for (int c = 0; c < 2 * kWC / 16; ++c) {
         float2 v[8];
         if (some) {
-          tmem_ld_x16(tmem + buf * kWN + c * 16 + (uint32_t(q) << 21), v);
+          tmem_ld_x16(tmem + buf * 256 + c * 16 + (uint32_t(q) << 21), v);
           tmem_wait_ld(v);
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] = make_float2(0.0f, 0.0f);
         }
-        if (w.k0 + c * 16 < p.K) {
+        if (n < p.N && w.k0 + c * 16 < p.K) {
+          Words<8> o;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint4 o;
-            o.x = pack_bf16x2_rn(v[4 * j].x, v[4 * j].y);
-            o.y = pack_bf16x2_rn(v[4 * j + 1].x, v[4 * j + 1].y);
-            o.z = pack_bf16x2_rn(v[4 * j + 2].x, v[4 * j + 2].y);
-            o.w = pack_bf16x2_rn(v[4 * j + 3].x, v[4 * j + 3].y);
-            reinterpret_cast<uint4*>(dst + c * 16)[j] = o;
+          for (int j = 0; j < 8; ++j) o.w[j] = pack_bf16x2_rn(v[j].x, v[j].y);
+          if (p.out32) {
+            st_stream_w<8>(reinterpret_cast<Words<8>*>(dst + c * 16), o);
+          } else {
+            uint4* d = reinterpret_cast<uint4*>(dst + c * 16);
+            d[0] = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
+            d[1] = make_uint4(o.w[4], o.w[5], o.w[6], o.w[7]);
           }
         }
       }
       if (some) {
         tcgen05_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&tail->tempty[buf]);
+        if (lane == 0) mbar_arrive_first(&tail->tempty[buf], rank);
         ++nt;
       }
     }
-  } else if (elect_one()) {
+  } else if (rank == 0 && elect_one()) {
     // ---- products: four K = 16 MMAs a stage into the tile's accumulator
-    constexpr uint32_t idesc = mma_idesc_bf16(kWM, kWN, true, true);
-    uint32_t it = 0, nt = 0;
+    constexpr uint32_t idesc = mma_idesc_bf16(2 * kWC, 2 * kWC, true, true);
+    uint32_t nt = 0;
+    int slot = 0;
+    uint32_t round = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+    for (int t = first; t < tiles && ok; t += stride) {
       const WTile w = wtile_at(p, t);
       const int steps = (w.hi - w.lo + kWRows - 1) / kWRows;
       if (steps == 0) continue;
       const uint32_t buf = nt & 1u;
-      if (nt >= 2 && !bounded_wait(&tail->tempty[buf], ((nt >> 1) - 1) & 1u, failed)) break;
-      for (int step = 0; step < steps; ++step, ++it) {
-        const uint32_t st = it % kWStages;
-        if (!bounded_wait(&tail->full[st], (it / kWStages) & 1u, failed)) {
-          ok = false;
-          break;
-        }
+      if (nt >= 2) ok = bounded_wait(&tail->tempty[buf], ((nt >> 1) - 1) & 1u, failed);
+      for (int step = 0; step < steps && ok; ++step) {
+        ok = bounded_wait(&tail->full[slot], round & 1u, failed);
+        if (!ok) break;
         tcgen05_fence_after();
-        const uint32_t sa = smem_addr(stages + size_t(st) * kWStage);
-        const uint64_t da = smem_desc_sw128(sa, kLbo, 1024);
-        const uint64_t db = smem_desc_sw128(sa + kWStageA, kLbo, 1024);
+        const uint32_t sd = smem_addr(stages + slot * kWStage);
+        const uint64_t dd = smem_desc_sw128(sd, kLbo, 1024);
+        const uint64_t da = smem_desc_sw128(sd + kWOperand, kLbo, 1024);
 #pragma unroll
         for (int k = 0; k < kWRows / 16; ++k)
-          mma_bf16(tmem + buf * kWN, da + ((k * 16 * 128) >> 4), db + ((k * 16 * 128) >> 4), idesc,
-                   step > 0 || k > 0);
-        mma_commit(&tail->empty[st]);
+          mma_bf16_pair(tmem + buf * 256, dd + ((k * 16 * 128) >> 4), da + ((k * 16 * 128) >> 4),
+                        idesc, step > 0 || k > 0);
+        mma_commit<true>(&tail->empty[slot]);
+        if (++slot == kWStages) {
+          slot = 0;
+          ++round;
+        }
       }
-      if (!ok) break;
-      mma_commit(&tail->tfull[buf]);
+      if (ok) mma_commit<true>(&tail->tfull[buf]);
       ++nt;
     }
-    if (it >= 1) {  // the last products finish before TMEM is given back
-      const uint32_t last = it - 1;
-      uint32_t n = 0;
-      while (!mbar_try_wait(&tail->empty[last % kWStages], (last / kWStages) & 1u) &&
-             ++n < kSpinLimit) {
-      }
-    }
+    // the last products finish before TMEM is given back
+    const int last = slot > 0 ? slot - 1 : kWStages - 1;
+    if (slot > 0 || round > 0)
+      bounded_wait(&tail->empty[last], (slot > 0 ? round : round - 1) & 1u, failed);
   }
 
   __syncwarp();
   tcgen05_fence_before();
-  __syncthreads();
+  cluster_sync_all();  // nothing of either block is in use any more
   tcgen05_fence_after();
-  if (warp == kConvWarps + 4) tmem_dealloc(tmem, 512);
+  if (warp == kConvWarps + 4) tmem_dealloc<true>(tmem, 512);
   if (threadIdx.x == 0 && tail->failed) raise_error(p.dev_err, MP_ERR_TIMEOUT);
 }
 
@@ -315,10 +352,11 @@ cudaError_t launch_expert_wgrad(int E, int rows, int N, int K, const void* dy,
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev] = 1;
   }
-  const int64_t tiles = int64_t(E) * (N / kWM) * ((K + kWN - 1) / kWN);
-  if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  const int grid = int(std::min<int64_t>(tiles, sm_count()));
-  mp_k_expert_wgrad<<<grid, kWThreads, kWSmem, st>>>(p);
+  p.out32 = (reinterpret_cast<uintptr_t>(dw) & 31u) == 0;
+  const int64_t tiles = int64_t(E) * ((N + 2 * kWC - 1) / (2 * kWC)) *
+                        ((K + 2 * kWC - 1) / (2 * kWC));  // below 2^31: the C ABI checks
+  const int pairs = int(std::min<int64_t>(tiles, sm_count() / 2));
+  mp_k_expert_wgrad<<<2 * pairs, kWThreads, kWSmem, st>>>(p);
   return cudaGetLastError();
 }
 
