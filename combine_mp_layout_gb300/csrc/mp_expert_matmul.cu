@@ -234,7 +234,7 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
         const int boxes = (tl.nrows + kShortBox - 1) / kShortBox;
         const uint32_t bytes = uint32_t(boxes) * kShortBox * kBK + kStageW;
         for (int kb = 0; kb < p.red_blocks; ++kb, s.next(p.stages)) {
-          if (s.round > 0 && !bounded_wait(&tail->done[s.slot], (s.round - 1) & 1u, failed)) {
+          if (s.round > 0 && !bounded_wait_idle(&tail->done[s.slot], (s.round - 1) & 1u, failed)) {
             ok = false;
             break;
           }
@@ -336,7 +336,7 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
         for (int u = 0; u < 4; ++u) {
           if (kb0 + u < p.red_blocks && ok) {
             if (s.round > 0) {
-              ok = bounded_wait_warp(&tail->done[behind.slot], behind.round & 1u, failed);
+              ok = bounded_wait_idle_warp(&tail->done[behind.slot], behind.round & 1u, failed);
               behind.next(p.stages);
             }
             if (ok) {

@@ -19,9 +19,12 @@
 // much again for the same products.  Both operands are MN-major: a row of
 // channels stays a row in shared memory, nothing is transposed.
 //
-// Warps of a block: eight convert (global memory to registers some stages
+// Warps of a block: sixteen convert (global memory to registers some stages
 // ahead, across tiles too, then to shared memory), four write finished tiles,
-// one (in the first block) issues the MMAs.
+// one (in the first block) issues the MMAs, and one hands each converted stage
+// over to the tensor core's proxy.  The hand-over is its own because a proxy
+// fence waits for the loads that its thread has in flight: in the converting
+// warps it made every stage as long as a load.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_fp16.h>
@@ -41,9 +44,10 @@ constexpr int kWRows = 64;          // rows per stage: four K = 16 steps of kind
 constexpr int kWStages = 6;
 constexpr int kWOperand = kWRows * kWC * 2;
 constexpr int kWStage = 2 * kWOperand;
-constexpr int kConvWarps = 8;
+constexpr int kConvWarps = 16;
+constexpr int kPer = kWRows / (kConvWarps * 4);  // rows of each operand per thread and stage
 constexpr int kAhead = 3;           // stages whose global loads are in flight
-constexpr int kWThreads = (kConvWarps + 4 + 1) * 32;  // 4 epilogue warps, 1 MMA warp
+constexpr int kWThreads = (kConvWarps + 4 + 2) * 32;  // 4 epilogue warps, MMAs, hand-over
 constexpr int kLbo = kWRows * 128;  // 64 bf16 channels (128 bytes) of all of a stage's rows
 
 struct WgradArgs {
@@ -59,6 +63,7 @@ struct WgradArgs {
 };
 
 struct WgradTail {
+  uint64_t conv[kWStages];          // a block's half of a stage is written
   uint64_t full[kWStages], empty[kWStages], tfull[2], tempty[2];
   uint32_t tmem;
   int failed;
@@ -91,6 +96,7 @@ __device__ __forceinline__ WTile wtile_at(const WgradArgs& p, int t) {
 // 16 e4m3 values times s, rounded to bf16: 8 words.
 __device__ __forceinline__ void dequant16(const uint4& v, float s, uint32_t (&o)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const float2 s2 = make_float2(s, s);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t h0, h1;  // f16 pairs: every e4m3 value is exact in f16
@@ -98,23 +104,21 @@ __device__ __forceinline__ void dequant16(const uint4& v, float s, uint32_t (&o)
         " cvt.rn.f16x2.e4m3x2 %0, lo;\n cvt.rn.f16x2.e4m3x2 %1, hi;\n}"
         : "=r"(h0), "=r"(h1)
         : "r"(w[i]));
-    const float2 f0 = __half22float2(*reinterpret_cast<__half2*>(&h0));
-    const float2 f1 = __half22float2(*reinterpret_cast<__half2*>(&h1));
-    o[2 * i] = pack_bf16x2_rn(f0.x * s, f0.y * s);
-    o[2 * i + 1] = pack_bf16x2_rn(f1.x * s, f1.y * s);
+    const float2 f0 = mul2(__half22float2(*reinterpret_cast<__half2*>(&h0)), s2);
+    const float2 f1 = mul2(__half22float2(*reinterpret_cast<__half2*>(&h1)), s2);
+    o[2 * i] = pack_bf16x2_rn(f0.x, f0.y);
+    o[2 * i + 1] = pack_bf16x2_rn(f1.x, f1.y);
   }
 }
 
 // The 16 channels 16c .. 16c+15 of stage row r, at the 128-byte swizzle of the
-// MN-major tile.  Lanes with an odd 64-channel group store their second half
-// first, so that eight neighbouring lanes hit eight different 16-byte banks.
+// MN-major tile.  (Eight neighbouring lanes have four chunks of two rows, whose
+// swizzles differ in the lowest bit: eight different 16-byte banks.)
 __device__ __forceinline__ void store16(unsigned char* tile, int r, int c, const uint32_t (&o)[8]) {
   unsigned char* row = tile + (c >> 2) * kLbo + r * 128;
   const int u = (c & 3) * 2, sw = r & 7;
-  const uint4 x = make_uint4(o[0], o[1], o[2], o[3]), y = make_uint4(o[4], o[5], o[6], o[7]);
-  const bool odd = (c >> 2) & 1;
-  *reinterpret_cast<uint4*>(row + (((odd ? u + 1 : u) ^ sw) << 4)) = odd ? y : x;
-  *reinterpret_cast<uint4*>(row + (((odd ? u : u + 1) ^ sw) << 4)) = odd ? x : y;
+  *reinterpret_cast<uint4*>(row + ((u ^ sw) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+  *reinterpret_cast<uint4*>(row + (((u + 1) ^ sw) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
@@ -125,7 +129,8 @@ mp_k_expert_wgrad(const WgradArgs p) {
   const int rank = int(cluster_rank());
   if (threadIdx.x == 0) {
     for (int i = 0; i < kWStages; ++i) {
-      mbar_init(&tail->full[i], 2 * kConvWarps);
+      mbar_init(&tail->conv[i], kConvWarps);
+      mbar_init(&tail->full[i], 2);
       mbar_init(&tail->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -155,57 +160,57 @@ mp_k_expert_wgrad(const WgradArgs p) {
 
   if (warp < kConvWarps) {
     // ---- rows from global memory, dequantised, into the ring of stages.  A
-    // thread has 16 channels of rows r and r + 32 of each operand.
-    const int r = threadIdx.x >> 3, c = threadIdx.x & 7;
+    // thread has 16 channels of kPer of a stage's rows of each operand.  There are
+    // no branches in a stage: rows past the expert's last one are read as
+    // the last one, with scale 0, and channels past the matrix as its last block
+    // (nothing of theirs is stored).  (With a branch around each load the
+    // warps, not the products, set the pace: 1,540 clocks a stage.)
+    const int c = (lane & 3) | ((lane >> 1) & 4);
+    const int r = warp * 4 + ((lane >> 2) & 1) + ((lane >> 3) & 2);
     const int nb = p.N / 128, kb = p.K / 128;
-    // where the next loads come from
-    int t = first - stride, row = r, end = 0;  // (no rows: the first load finds a tile)
-    bool more = true, n_in = false, k_in = false;
-    const unsigned char *pd = nullptr, *pa = nullptr;
-    const float *psd = nullptr, *psa = nullptr;
-    auto next_tile = [&] {  // the next tile with rows
-      do {
-        t += stride;
-        if (t >= tiles) {
-          more = false;
-          return;
-        }
-        const WTile w = wtile_at(p, t);
-        row = w.lo + r;
-        end = w.hi;
-        if (w.lo == w.hi) continue;
-        const int n = w.n0 + rank * kWC, k = w.k0 + rank * kWC;
-        n_in = n < p.N;
-        k_in = k < p.K;
-        pd = p.dy + int64_t(row) * p.N + n + c * 16;
-        pa = p.a + int64_t(row) * p.K + k + c * 16;
-        psd = p.dy_scales + int64_t(row) * nb + n / 128;
-        psa = p.a_scales + int64_t(row) * kb + k / 128;
-        return;
-      } while (true);
-    };
-    uint4 v[kAhead][4];
-    float s[kAhead][4];
+    // where the next loads come from: rows row0 .. of the expert ending at `end`
+    int t = first - stride, row0 = 0, end = 0;
+    bool more = true;
+    const unsigned char *pd = p.dy, *pa = p.a;
+    const float *psd = p.dy_scales, *psa = p.a_scales;
+    uint4 v[kAhead][2 * kPer];
+    float s[kAhead][2 * kPer];
     bool have[kAhead];
-    auto load = [&](uint4 (&v)[4], float (&s)[4], bool& have) {
-      if (more && row - r >= end) next_tile();
+    auto load = [&](uint4 (&v)[2 * kPer], float (&s)[2 * kPer], bool& have) {
+      if (row0 >= end) {  // on to the next tile with rows
+        WTile w;
+        do {
+          t += stride;
+          if (t >= tiles) {
+            more = false;
+            break;
+          }
+          w = wtile_at(p, t);
+        } while (w.lo == w.hi);
+        if (more) {
+          row0 = w.lo;
+          end = w.hi;
+          const int n = min(w.n0 + rank * kWC, p.N - kWC), k = min(w.k0 + rank * kWC, p.K - kWC);
+          pd = p.dy + n + c * 16;
+          pa = p.a + k + c * 16;
+          psd = p.dy_scales + n / 128;
+          psa = p.a_scales + k / 128;
+        }
+      }
       have = more;
       if (!more) return;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const bool in = row + i * 32 < end;
-        v[i] = in && n_in ? __ldg(reinterpret_cast<const uint4*>(pd + int64_t(i) * 32 * p.N))
-                          : make_uint4(0, 0, 0, 0);
-        s[i] = in && n_in ? __ldg(psd + int64_t(i) * 32 * nb) : 0.0f;
-        v[2 + i] = in && k_in ? __ldg(reinterpret_cast<const uint4*>(pa + int64_t(i) * 32 * p.K))
-                              : make_uint4(0, 0, 0, 0);
-        s[2 + i] = in && k_in ? __ldg(psa + int64_t(i) * 32 * kb) : 0.0f;
+      for (int i = 0; i < kPer; ++i) {
+        const int row = row0 + r + i * (kWRows / kPer);
+        const int64_t at = min(row, end - 1);
+        v[i] = __ldg(reinterpret_cast<const uint4*>(pd + at * p.N));
+        v[kPer + i] = __ldg(reinterpret_cast<const uint4*>(pa + at * p.K));
+        const float sd = __ldg(psd + at * nb);
+        const float sk = __ldg(psa + at * kb);
+        s[i] = row < end ? sd : 0.0f;
+        s[kPer + i] = row < end ? sk : 0.0f;
       }
-      row += kWRows;
-      pd += int64_t(kWRows) * p.N;
-      pa += int64_t(kWRows) * p.K;
-      psd += int64_t(kWRows) * nb;
-      psa += int64_t(kWRows) * kb;
+      row0 += kWRows;
     };
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) load(v[i], s[i], have[i]);
@@ -217,24 +222,22 @@ mp_k_expert_wgrad(const WgradArgs p) {
       for (int i = 0; i < kAhead; ++i) {
         ok = ok && have[i];
         if (ok && round > 0) ok = bounded_wait_warp(&tail->empty[slot], (round - 1) & 1u, failed);
-        if (ok) {
-          unsigned char* td = stages + slot * kWStage;
-          uint32_t o[8];
+        if (!ok) break;
+        unsigned char* td = stages + slot * kWStage;
+        uint32_t o[8];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            dequant16(v[i][j], s[i][j], o);
-            store16(td, r + j * 32, c, o);
-            dequant16(v[i][2 + j], s[i][2 + j], o);
-            store16(td + kWOperand, r + j * 32, c, o);
-          }
-          load(v[i], s[i], have[i]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_first(&tail->full[slot], rank);
-          if (++slot == kWStages) {
-            slot = 0;
-            ++round;
-          }
+        for (int j = 0; j < kPer; ++j) {
+          dequant16(v[i][j], s[i][j], o);
+          store16(td, r + j * (kWRows / kPer), c, o);
+          dequant16(v[i][kPer + j], s[i][kPer + j], o);
+          store16(td + kWOperand, r + j * (kWRows / kPer), c, o);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tail->conv[slot]);
+        load(v[i], s[i], have[i]);
+        if (++slot == kWStages) {
+          slot = 0;
+          ++round;
         }
       }
     }
@@ -246,7 +249,7 @@ mp_k_expert_wgrad(const WgradArgs p) {
       const WTile w = wtile_at(p, t);
       const bool some = w.hi > w.lo;
       const uint32_t buf = nt & 1u;
-      if (some && !bounded_wait_warp(&tail->tfull[buf], (nt >> 1) & 1u, failed)) break;
+      if (some && !bounded_wait_idle_warp(&tail->tfull[buf], (nt >> 1) & 1u, failed)) break;
       tcgen05_fence_after();
       const int n = w.n0 + rank * kWC + q * 32 + lane;
       uint16_t* dst = p.dw + (int64_t(w.e) * p.N + n) * p.K + w.k0;
@@ -278,6 +281,27 @@ mp_k_expert_wgrad(const WgradArgs p) {
         __syncwarp();
         if (lane == 0) mbar_arrive_first(&tail->tempty[buf], rank);
         ++nt;
+      }
+    }
+  } else if (warp == kConvWarps + 5) {
+    // ---- each stage that this block's warps have written, on to the products
+    if (elect_one()) {
+      int slot = 0;
+      uint32_t round = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += stride) {
+        const WTile w = wtile_at(p, t);
+        const int steps = (w.hi - w.lo + kWRows - 1) / kWRows;
+        for (int step = 0; step < steps; ++step) {
+          ok = bounded_wait(&tail->conv[slot], round & 1u, failed);
+          if (!ok) break;
+          fence_proxy_async_smem();
+          mbar_arrive_first(&tail->full[slot], rank);
+          if (++slot == kWStages) {
+            slot = 0;
+            ++round;
+          }
+        }
       }
     }
   } else if (rank == 0 && elect_one()) {

@@ -100,7 +100,21 @@ __device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity,
   if (!ok) *failed = 1;
   return ok != 0;
 }
-// The same for a whole warp, with one answer for all its lanes.
+// The same for roles that are ahead of the others and have time: suspended
+// between attempts (up to 1 us each), so that they take no issue slots and no
+// turns at the barrier unit from those that are waited for.
+__device__ __forceinline__ bool bounded_wait_idle(uint64_t* bar, uint32_t parity,
+                                                  volatile int* failed) {
+  for (uint32_t n = 0; n < kSpinLimit; ++n)
+    if (mbar_try_wait(bar, parity)) return true;
+  *failed = 1;
+  return false;
+}
+__device__ __forceinline__ bool bounded_wait_idle_warp(uint64_t* bar, uint32_t parity,
+                                                       volatile int* failed) {
+  return __all_sync(kFull, bounded_wait_idle(bar, parity, failed));
+}
+// The first form for a whole warp, with one answer for all its lanes.
 __device__ __forceinline__ bool bounded_wait_warp(uint64_t* bar, uint32_t parity,
                                                   volatile int* failed) {
   return __all_sync(kFull, bounded_wait(bar, parity, failed));
@@ -245,6 +259,16 @@ __device__ __forceinline__ void tmem_wait_ld(float2 (&v)[8]) {
                  "+f"(v[7].y)::"memory");
 }
 
+// Two fp32 products in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 ra, rb, rd;\n"
+      " mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n"
+      " mul.rn.f32x2 rd, ra, rb;\n mov.b64 {%0, %1}, rd;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 // Two fp32 FMAs in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
