@@ -101,6 +101,23 @@ __device__ __forceinline__ uint32_t team_min(uint32_t v, uint32_t* red) {
   return ~team_max<W>(~v, red);
 }
 
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Exchanges of a sorting network: the larger key (with its 4-bit tag) to place a.
+__device__ __forceinline__ void order2(uint32_t& ka, uint32_t& ta, uint32_t& kb, uint32_t& tb) {
+  const bool swap = kb > ka;  // equal keys stay: they are in order of their tags
+  const uint32_t k0 = max(ka, kb), k1 = min(ka, kb);
+  const uint32_t t0 = swap ? tb : ta, t1 = swap ? ta : tb;
+  ka = k0;
+  kb = k1;
+  ta = t0;
+  tb = t1;
+}
+
 template <typename T>
 __device__ __forceinline__ float load_logit(const T* p) {
   if constexpr (std::is_same<T, float>::value)
@@ -109,8 +126,17 @@ __device__ __forceinline__ float load_logit(const T* p) {
     return __uint_as_float(uint32_t(__ldg(reinterpret_cast<const uint16_t*>(p))) << 16);
 }
 
-__device__ __forceinline__ float sigmoid_exact(float x) {
-  return __fdiv_rn(1.0f, 1.0f + expf(-x));  // the selection key: correctly rounded division
+// 1 / (1 + exp(-x)), with a correctly rounded reciprocal: it is part of the
+// selection key, so its last bit can decide.
+__device__ __forceinline__ float sigmoid_exact(float x) { return __frcp_rn(1.0f + expf(-x)); }
+// The same without the reciprocal's branch for extreme exponents, for 1 <= y <
+// 2^126: an approximation within an ulp and one correction with the exact
+// remainder give the correctly rounded reciprocal (Markstein, "IA-64 and
+// Elementary Functions"; compared with __frcp_rn for every float of that range).
+__device__ __forceinline__ float rcp_mid(float y) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(y));
+  return __fmaf_rn(r, __fmaf_rn(-y, r, 1.0f), r);
 }
 
 // Floats to integers with the same order (-0 and +0 alike); 0 means "cannot be chosen".
@@ -142,20 +168,43 @@ struct TokenScores {
       bad |= !(x[j] < INFINITY);  // NaN or +inf
       mx = fmaxf(mx, x[j]);
     }
-    // one reduction for both: a bad value makes the maximum +inf
-    mx = team_reduce<W>(bad ? INFINITY : mx, red, OpMax());
-    live = active && mx < INFINITY;
-    m = mx > -INFINITY ? mx : 0.0f;
-    float total = 0.0f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if (!live) x[j] = -INFINITY;
-      if constexpr (SIG)
-        s[j] = x[j] > -INFINITY ? sigmoid_exact(x[j]) : 0.0f;
+    if (SIG && W == 1) {
+      bad = __any_sync(kFull, bad);
+      live = active && !bad;
+      m = 0.0f;
+    } else {
+      // one reduction for both: a bad value makes the maximum +inf
+      mx = bad ? INFINITY : mx;
+      if constexpr (W == 1)
+        mx = warp_max(mx);
       else
-        s[j] = x[j] > -INFINITY ? expf(x[j] - m) : 0.0f;
-      total += s[j];
+        mx = team_reduce<W>(mx, red, OpMax());
+      live = active && mx < INFINITY;
+      m = mx > -INFINITY ? mx : 0.0f;
     }
+    float total = 0.0f;
+    if constexpr (SIG) {
+      bool far = false;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (!live) x[j] = -INFINITY;
+        const float y = 1.0f + expf(-x[j]);
+        far |= y >= 0x1p126f && x[j] > -INFINITY;
+        s[j] = x[j] > -INFINITY ? rcp_mid(y) : 0.0f;
+      }
+      if (far) {  // logits below about -87
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] = x[j] > -INFINITY ? sigmoid_exact(x[j]) : 0.0f;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (!live) x[j] = -INFINITY;
+        s[j] = x[j] > -INFINITY ? expf(x[j] - m) : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) total += s[j];
     total = team_reduce<W>(total, red, OpSum());
     inv_total = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
     inv = SIG ? inv_total : 1.0f;
@@ -186,6 +235,7 @@ mp_k_route(const RouteArgs p) {
   __shared__ uint32_t redu[kRouteWarps];
   __shared__ float stage[W == 1 ? kRouteWarps * 256 : 1];
   __shared__ double dred[kRouteWarps];
+  __shared__ int sm_chosen[kRouteWarps][MP_MAX_TOPK];
   __shared__ int s_routed;
   __shared__ int s_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -222,14 +272,53 @@ mp_k_route(const RouteArgs p) {
       }
       key[j] = x[j] > -INFINITY && k > -INFINITY ? order_key(k) : 0u;
     }
+    int mine = -1;  // lane k of the (first) warp: the k-th choice
+    bool any = false;
+    if constexpr (W == 1 && V <= 8) {
+      // Each lane sorts its keys once (odd-even transposition: neighbours only,
+      // so equal keys keep their order), then K rounds take the largest head;
+      // among equal heads the lowest expert.  Against searching each lane's keys
+      // again in every round this is fewer instructions, which is what bounds
+      // the kernel.
+      uint32_t tag[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) tag[j] = j;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = i & 1; j + 1 < V; j += 2) order2(key[j], tag[j], key[j + 1], tag[j + 1]);
+      uint32_t tags = 0;  // 4 bits each, the head's lowest
+#pragma unroll
+      for (int j = 0; j < V; ++j) tags |= tag[j] << (4 * j);
+      int* chosen = sm_chosen[warp];
+      int k = 0;
+      for (; k < K; ++k) {
+        const uint32_t top = __reduce_max_sync(kFull, key[0]);
+        if (top == 0) break;
+        bool won = key[0] == top;
+        const uint32_t e = (tags & 15u) * kWarp + lane;
+        const unsigned heads = __ballot_sync(kFull, won);
+        if (heads & (heads - 1)) {  // (the whole warp is here: the ballot is the same for all)
+          const uint32_t lowest = __reduce_min_sync(kFull, won ? e : 0xffffffffu);
+          won = won && e == lowest;
+        }
+        if (won) chosen[k] = int(e);
+#pragma unroll
+        for (int j = 0; j + 1 < V; ++j) key[j] = won ? key[j + 1] : key[j];
+        key[V - 1] = won ? 0u : key[V - 1];
+        tags = won ? tags >> 4 : tags;
+      }
+      __syncwarp();
+      if (lane < k) mine = chosen[lane];
+      __syncwarp();
+      any = k > 0;
+    } else {
     // K rounds: the largest key, among equals the lowest expert
     uint32_t best = 0;
     int bestj = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j)
       if (key[j] > best) { best = key[j]; bestj = j; }
-    int mine = -1;  // lane k of the (first) warp: the k-th choice
-    bool any = false;
     for (int k = 0; k < K; ++k) {
       const uint32_t top = team_max<W>(best, redu);
       if (top == 0) break;
@@ -245,6 +334,7 @@ mp_k_route(const RouteArgs p) {
           if (key[j] > best) { best = key[j]; bestj = j; }
         }
       }
+    }
     }
     if (W == 1 || warp == 0) {
       float w = mine >= 0 ? sc.score_of(load_logit(row + mine)) : 0.0f;
