@@ -9,6 +9,7 @@ library or a CPU tensor raises at once.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -437,17 +438,25 @@ def mp_dispatch_ll_quant(R, N, K, E, H, qformat, rank_major, x, topk_idx, num_to
 
 
 def _arr(t, name, dtype, numel):
-    """The device pointer of a dense CUDA tensor of this type with room for `numel` elements."""
+    """The device address of a dense CUDA tensor of this type with room for `numel` elements."""
     if t is None:
         return None
-    p = _dev(t, name)
-    if t.dtype is not dtype:
-        raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
-    if t.numel() < numel:
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() < numel:
+        _dev(t, name)
+        if t.dtype is not dtype:
+            raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
         raise ValueError("%s holds %d elements, %d are needed" % (name, t.numel(), numel))
-    return p
+    return t.data_ptr()
 
 
+def _raw_stream(stream):
+    """The stream's handle; the current device's current one costs no stream object."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+@functools.lru_cache(maxsize=None)
 def mp_route_workspace_size(R: int, N: int, E: int) -> int:
     return int(lib().mp_route_workspace_size(R, N, E))
 
@@ -474,7 +483,7 @@ def mp_route(R, N, K, E, scoring, logits, bias, active, normalize, scale, loss_c
         _arr(balance_loss, "balance_loss", torch.float32, R),
         _arr(dev_err, "dev_err", torch.int32, 1),
         _arr(workspace, "workspace", torch.uint8, mp_route_workspace_size(R, N, E)),
-        _stream(stream))
+        _raw_stream(stream))
 
 
 def mp_route_backward(R, N, K, E, scoring, logits, active, normalize, scale, loss_coef, topk_idx,
@@ -491,7 +500,7 @@ def mp_route_backward(R, N, K, E, scoring, logits, active, normalize, scale, los
         _arr(num_routed, "num_routed", torch.int32, R),
         _arr(d_balance_loss, "d_balance_loss", torch.float32, R),
         _arr(d_logits, "d_logits", torch.bfloat16 if dtype == MP_BF16 else torch.float32,
-             R * N * E), _stream(stream))
+             R * N * E), _raw_stream(stream))
 
 
 _F8 = torch.float8_e4m3fn
@@ -508,7 +517,7 @@ def mp_expert_matmul_e4m3(E, rows, N, K, a, a_scales, w, w_scales, expert_offset
         _arr(w_scales, "w_scales", torch.float32, E * -(-N // SCALE_BLOCK) * (K // SCALE_BLOCK)),
         _arr(expert_offsets, "expert_offsets", torch.int32, E + 1),
         _arr(out, "out", torch.bfloat16, rows * N), _arr(dev_err, "dev_err", torch.int32, 1),
-        _stream(stream))
+        _raw_stream(stream))
 
 
 def mp_expert_matmul_dgrad_e4m3(E, rows, N, K, dy, dy_scales, w, w_scales, expert_offsets, dx,
@@ -521,7 +530,7 @@ def mp_expert_matmul_dgrad_e4m3(E, rows, N, K, dy, dy_scales, w, w_scales, exper
         _arr(w_scales, "w_scales", torch.float32, E * -(-N // SCALE_BLOCK) * (K // SCALE_BLOCK)),
         _arr(expert_offsets, "expert_offsets", torch.int32, E + 1),
         _arr(dx, "dx", torch.bfloat16, rows * K), _arr(dev_err, "dev_err", torch.int32, 1),
-        _stream(stream))
+        _raw_stream(stream))
 
 
 def mp_expert_matmul_wgrad_e4m3(E, rows, N, K, dy, dy_scales, a, a_scales, expert_offsets, dw,
@@ -534,7 +543,7 @@ def mp_expert_matmul_wgrad_e4m3(E, rows, N, K, dy, dy_scales, a, a_scales, exper
         _arr(a_scales, "a_scales", torch.float32, rows * (K // SCALE_BLOCK)),
         _arr(expert_offsets, "expert_offsets", torch.int32, E + 1),
         _arr(dw, "dw", torch.bfloat16, E * N * K), _arr(dev_err, "dev_err", torch.int32, 1),
-        _stream(stream))
+        _raw_stream(stream))
 
 
 def mp_swiglu_e4m3(rows, I, gate_up, row_weights, num_rows, out, out_scales, stream=None) -> int:
@@ -545,7 +554,7 @@ def mp_swiglu_e4m3(rows, I, gate_up, row_weights, num_rows, out, out_scales, str
         _arr(row_weights, "row_weights", torch.float32, rows),
         _arr(num_rows, "num_rows", torch.int32, 1), _arr(out, "out", _F8, rows * I),
         _arr(out_scales, "out_scales", torch.float32, rows * (I // SCALE_BLOCK)),
-        _stream(stream))
+        _raw_stream(stream))
 
 
 def mp_swiglu_backward_e4m3(rows, I, gate_up, row_weights, d_out, num_rows, d_gate_up,
@@ -557,4 +566,4 @@ def mp_swiglu_backward_e4m3(rows, I, gate_up, row_weights, d_out, num_rows, d_ga
         _arr(d_out, "d_out", torch.bfloat16, rows * I), _arr(num_rows, "num_rows", torch.int32, 1),
         _arr(d_gate_up, "d_gate_up", _F8, rows * 2 * I),
         _arr(d_gate_up_scales, "d_gate_up_scales", torch.float32, rows * (2 * I // SCALE_BLOCK)),
-        _arr(d_row_weights, "d_row_weights", torch.float32, rows), _stream(stream))
+        _arr(d_row_weights, "d_row_weights", torch.float32, rows), _raw_stream(stream))

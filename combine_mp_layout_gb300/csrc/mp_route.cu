@@ -234,7 +234,6 @@ mp_k_route(const RouteArgs p) {
   __shared__ float red[kRouteWarps];
   __shared__ uint32_t redu[kRouteWarps];
   __shared__ float stage[W == 1 ? kRouteWarps * 256 : 1];
-  __shared__ double dred[kRouteWarps];
   __shared__ int sm_chosen[kRouteWarps][MP_MAX_TOPK];
   __shared__ int s_routed;
   __shared__ int s_last;
@@ -398,26 +397,22 @@ mp_k_route(const RouteArgs p) {
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  double sum = 0.0;
+  const int T_ = __ldcg(p.ws_routed + rank);
+  const float unfix = 1.0f / p.fix;
+  float sum = 0.0f;  // a fixed order again: thread, warp, block
   for (int e = threadIdx.x; e < E; e += kRouteThreads) {
     const int c = __ldcg(gc + e);
     const unsigned long long f = __ldcg(gm + e);
     p.counts[int64_t(rank) * E + e] = c;
-    sum += double(c) * double(f);
+    sum += float(c) * (float(f) * unfix);
     gc[e] = 0;
     gm[e] = 0;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  if (lane == 0) dred[warp] = sum;
-  __syncthreads();
+  sum = team_reduce<kRouteWarps>(sum, red, OpSum());
   if (threadIdx.x == 0) {
-    double all = 0.0;
-    for (int w = 0; w < kRouteWarps; ++w) all += dred[w];
-    const int T_ = __ldcg(p.ws_routed + rank);
-    const double T2 = double(T_ > 0 ? T_ : 1) * double(T_ > 0 ? T_ : 1);
+    const float tokens = float(T_ > 0 ? T_ : 1);
     p.routed[rank] = T_;
-    p.loss[rank] = float(double(p.loss_coef) * E / (double(K) * T2) * (all / double(p.fix)));
+    p.loss[rank] = p.loss_coef * float(E) / float(K) * (sum / tokens / tokens);
     p.ws_routed[rank] = 0;
     p.ws_done[rank] = 0;
   }
