@@ -179,15 +179,17 @@ struct Ring {
   }
 };
 
-// Every warp's end: nothing of the block is in use after it.
+// Every warp's end: nothing of the block (or cluster) is in use after it.
+template <bool SPLIT>
 __device__ __forceinline__ void block_end() {
   __syncwarp();
   tcgen05_fence_before();
-  __syncthreads();
+  if constexpr (SPLIT) cluster_sync_all(); else __syncthreads();
   tcgen05_fence_after();
 }
 
-template <bool DGRAD>
+// SPLIT: one tile per cluster, each of its blocks a part of the reduction.
+template <bool DGRAD, bool SPLIT>
 __global__ void __launch_bounds__(kMMThreads, 1)
 mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
                    const __grid_constant__ CUtensorMap map_short,
@@ -213,10 +215,14 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
   const uint32_t tmem = tail->tmem;
   const int ncol = (p.out_cols + kBN - 1) / kBN;
   const int tiles = pre[p.E] * ncol;  // below 2^31: the C ABI checks
-  const int first = blockIdx.x, step = gridDim.x;
+  const int parts = SPLIT ? int(cluster_size()) : 1, part = SPLIT ? int(cluster_rank()) : 0;
+  const int first = blockIdx.x / parts, step = SPLIT ? tiles : gridDim.x;
+  // the reduction blocks of this block's tiles
+  const int kb_lo = SPLIT ? p.red_blocks * part / parts : 0;
+  const int kb_hi = SPLIT ? p.red_blocks * (part + 1) / parts : p.red_blocks;
   // steps of this block: every tile's reduction blocks, one after the other
-  const int64_t steps =
-      tiles > first ? int64_t((tiles - first + step - 1) / step) * p.red_blocks : 0;
+  const int64_t count = tiles > first ? (tiles - first + step - 1) / step : 0;
+  const int64_t steps = count * (kb_hi - kb_lo);
   volatile int* failed = &tail->failed;
 
   // The sums need more registers than a twelfth of the file: the four warps
@@ -233,7 +239,7 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
         const Tile tl = tile_at(p, pre, ncol, t);
         const int boxes = (tl.nrows + kShortBox - 1) / kShortBox;
         const uint32_t bytes = uint32_t(boxes) * kShortBox * kBK + kStageW;
-        for (int kb = 0; kb < p.red_blocks; ++kb, s.next(p.stages)) {
+        for (int kb = kb_lo; kb < kb_hi; ++kb, s.next(p.stages)) {
           if (s.round > 0 && !bounded_wait_idle(&tail->done[s.slot], (s.round - 1) & 1u, failed)) {
             ok = false;
             break;
@@ -288,15 +294,16 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
     // ahead of the one in use: a row's scales lie red_blocks apart, so every
     // load is a trip to L2.
     const int half = warp - 2;
-    const bool vec = p.red_blocks % 4 == 0 && (reinterpret_cast<uintptr_t>(p.a_scales) & 15) == 0;
+    const bool vec = p.red_blocks % 4 == 0 && kb_lo % 4 == 0 && kb_hi % 4 == 0 &&
+                     (reinterpret_cast<uintptr_t>(p.a_scales) & 15) == 0;
     Ring s;
     // a slot's old scales are used up when the step two after theirs, which took
     // their accumulator over, is done: `behind` is that step
     Ring behind;
     behind.slot = 2;
-    int count = 0;
+    int made = 0;
     bool ok = true;
-    for (int t = first; t < tiles && ok; t += step, ++count) {
+    for (int t = first; t < tiles && ok; t += step, ++made) {
       const Tile tl = tile_at(p, pre, ncol, t);
       const float* src[4];
 #pragma unroll
@@ -308,7 +315,7 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
       auto load4 = [&](int kb) {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          wahead[u] = kb + u < p.red_blocks ? __ldg(sw + int64_t(kb + u) * p.ws_red) : 0.0f;
+          wahead[u] = kb + u < kb_hi ? __ldg(sw + int64_t(kb + u) * p.ws_red) : 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (vec) {
@@ -320,21 +327,21 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
           } else {
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-              ahead[i][u] = kb + u < p.red_blocks ? __ldg(src[i] + kb + u) : 0.0f;
+              ahead[i][u] = kb + u < kb_hi ? __ldg(src[i] + kb + u) : 0.0f;
           }
         }
       };
-      load4(0);
-      for (int kb0 = 0; kb0 < p.red_blocks && ok; kb0 += 4) {
+      load4(kb_lo);
+      for (int kb0 = kb_lo; kb0 < kb_hi && ok; kb0 += 4) {
         float v[4][4];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[u][i] = ahead[i][u] * wahead[u];
-        if (kb0 + 4 < p.red_blocks) load4(kb0 + 4);
+        if (kb0 + 4 < kb_hi) load4(kb0 + 4);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          if (kb0 + u < p.red_blocks && ok) {
+          if (kb0 + u < kb_hi && ok) {
             if (s.round > 0) {
               ok = bounded_wait_idle_warp(&tail->done[behind.slot], behind.round & 1u, failed);
               behind.next(p.stages);
@@ -342,8 +349,8 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
             if (ok) {
               // (a tile's place is overwritten kTileRing tiles later, and at most
               // as many steps as there are stages are prepared ahead)
-              if (kb0 + u == 0 && half == 0 && lane == 0)
-                tail->tile[count % kTileRing] = make_int4(tl.row0, tl.nrows, tl.col0, 0);
+              if (kb0 + u == kb_lo && half == 0 && lane == 0)
+                tail->tile[made % kTileRing] = make_int4(tl.row0, tl.nrows, tl.col0, 0);
 #pragma unroll
               for (int i = 0; i < 4; ++i) tail->scale[s.slot][half][lane + i * 32] = v[u][i];
               __syncwarp();
@@ -355,7 +362,8 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
       }
     }
   }
-  block_end();
+  if constexpr (SPLIT) cluster_sync_all();  // (the parts are being joined)
+  block_end<SPLIT>();
   if (warp == 1) tmem_dealloc<false>(tmem, 2 * kBN);
   if (threadIdx.x == 0 && tail->failed) raise_error(p.dev_err, MP_ERR_TIMEOUT);
   } else {
@@ -375,17 +383,17 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
     hand_back();  // both accumulators are free at the start
     hand_back();
     uint32_t src = tmem + col + (uint32_t(q) << 21);
-    const int64_t count = steps / p.red_blocks;
+    int4 tl = make_int4(0, 0, 0, 0);
     for (int64_t i = 0; i < count; ++i) {
       float2 acc[kCols / 2];
 #pragma unroll
       for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
       bool ok = true, some = false;
-      for (int kb = 0; kb < p.red_blocks; ++kb, s.next(p.stages), src ^= kBN) {
+      for (int kb = kb_lo; kb < kb_hi; ++kb, s.next(p.stages), src ^= kBN) {
         ok = bounded_wait_warp(&tail->done[s.slot], s.round & 1u, failed);
         if (!ok) break;
         tcgen05_fence_after();
-        if (kb == 0) some = q * 32 < tail->tile[i % kTileRing].y;
+        if (kb == kb_lo) some = q * 32 < tail->tile[i % kTileRing].y;
         if (some) {
           const float sc = tail->scale[s.slot][col >> 7][lrow];
           const float2 s2 = make_float2(sc, sc);
@@ -409,8 +417,17 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
         }
       }
       if (!ok) break;
-      const int4 tl = tail->tile[i % kTileRing];
-      if (lrow < tl.y) {
+      tl = tail->tile[i % kTileRing];
+      if (SPLIT) {
+        // fp32 sums into the stages, which are done with: [4 channels][row]
+        float4* mine = reinterpret_cast<float4*>(stages) + (col >> 2) * kBM + lrow;
+        if (lrow < tl.y) {
+#pragma unroll
+          for (int c = 0; c < kCols / 4; ++c)
+            mine[c * kBM] = make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x,
+                                        acc[2 * c + 1].y);
+        }
+      } else if (lrow < tl.y) {
         uint16_t* dst =
             p.out + int64_t(tl.x + lrow) * p.out_cols + tl.z + col;
         const int left = p.out_cols - (tl.z + col);  // a multiple of 16 (or <= 0)
@@ -432,17 +449,151 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
         }
       }
     }
-    block_end();
+    if constexpr (SPLIT) {
+      cluster_sync_all();
+      // the parts in ascending order: four channels of a row per thread and turn
+      const int quads = tl.y * (kBN / 4);
+      for (int i = part * kEpiWarps * 32 + int(threadIdx.x) - kEpiFirst * 32; i < quads;
+           i += parts * kEpiWarps * 32) {
+        const int row = i / (kBN / 4), c4 = i % (kBN / 4);
+        const float4* at = reinterpret_cast<const float4*>(stages) + c4 * kBM + row;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int z = 0; z < parts; ++z) {
+          const float4 v = ld_cluster_f4(map_to_rank(at, z));
+          sum.x += v.x;
+          sum.y += v.y;
+          sum.z += v.z;
+          sum.w += v.w;
+        }
+        if (tl.z + c4 * 4 < p.out_cols) {
+          uint2 o;
+          o.x = pack_bf16x2_rn(sum.x, sum.y);
+          o.y = pack_bf16x2_rn(sum.z, sum.w);
+          *reinterpret_cast<uint2*>(p.out + int64_t(tl.x + row) * p.out_cols + tl.z + c4 * 4) = o;
+        }
+      }
+    }
+    block_end<SPLIT>();
   }
 }
 
-template <bool DGRAD>
-cudaError_t launch_mm(MMArgs p, const void* a, const void* w, int K, int red, cudaStream_t st) {
-  CUtensorMap mr, ms, mw;
-  if (!make_map_2d(&mr, a, 1, uint64_t(red), uint64_t(p.rows), kBK, kBM) ||
-      !make_map_2d(&ms, a, 1, uint64_t(red), uint64_t(p.rows), kBK, kShortBox) ||
-      !make_map_2d(&mw, w, 1, uint64_t(K), uint64_t(p.E) * p.w_rows, kBK, DGRAD ? kBK : kBN))
-    return cudaErrorInvalidValue;
+// ---------------------------------------------------------------------------
+// A few rows in all (one token, or one token's experts): the weights' bytes are
+// the whole cost, and the tiles above spend longer on their pipeline's start
+// than on the bytes.  A block takes 16 channels of one expert and up to eight
+// rows, its warps every eighth scale block of the reduction.  The products are
+// mma.m16n8k32 on registers: which channels of a scale block meet in one MMA is
+// free, as long as both operands agree, so a thread's operands are the 16 bytes
+// that it loads.  Each block sum (fp32) is scaled and added up in fp32, the
+// warps' sums are joined in a fixed order.
+// ---------------------------------------------------------------------------
+constexpr int kVecRows = 8;
+constexpr int kVecWarps = 8;
+constexpr int kVecAhead = 4;  // scale blocks whose loads are in flight per warp
+
+__device__ __forceinline__ void mma_e4m3_16x8x32(float (&c)[4], uint32_t a0, uint32_t a1,
+                                                 uint32_t a2, uint32_t a3, uint32_t b0,
+                                                 uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// grid (channels / 16, rows): the block of row r works if r is its expert's first.
+__global__ void __launch_bounds__(kVecWarps * 32)
+mp_k_expert_matvec(const MMArgs p, const unsigned char* __restrict__ a,
+                   const unsigned char* __restrict__ w) {
+  __shared__ float part[kVecWarps][kVecRows][16];
+  __shared__ int mine[2];  // expert, rows
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row0 = blockIdx.y;
+  int e = 0, nrows = p.rows;
+  if (p.expert_offsets != nullptr) {
+    if (threadIdx.x == 0) mine[1] = 0;
+    __syncthreads();
+    int bad = 0;
+    for (int i = threadIdx.x; i < p.E; i += kVecWarps * 32) {
+      const int lo = __ldg(p.expert_offsets + i), hi = __ldg(p.expert_offsets + i + 1);
+      if (lo < 0 || hi < lo) bad |= MP_ERR_INVALID_ARG;
+      if (hi > p.rows) bad |= MP_ERR_CAPACITY;
+      if (lo == row0 && hi > lo) {
+        mine[0] = i;
+        mine[1] = min(hi, p.rows) - lo;
+      }
+    }
+    if (bad && blockIdx.x == 0 && blockIdx.y == 0) raise_error(p.dev_err, bad);
+    if (__syncthreads_or(bad & MP_ERR_INVALID_ARG)) return;
+    e = mine[0];
+    nrows = mine[1];
+  } else if (row0 != 0) {
+    return;
+  }
+  if (nrows <= 0) return;
+  const int n0 = blockIdx.x * 16;
+  const int g = lane >> 2, t = lane & 3;
+  const int64_t K = int64_t(p.red_blocks) * kBK;
+  const unsigned char* w0 = w + (int64_t(e) * p.w_rows + n0 + g) * K + t * 16;
+  const unsigned char* w1 = w0 + 8 * K;
+  const unsigned char* x = a + (row0 + min(g, nrows - 1)) * K + t * 16;
+  const float* sw = p.w_scales + e * p.ws_expert + int64_t(n0 >> 7) * p.ws_out;
+  const float* sa0 = p.a_scales + int64_t(row0 + min(2 * t, nrows - 1)) * p.red_blocks;
+  const float* sa1 = p.a_scales + int64_t(row0 + min(2 * t + 1, nrows - 1)) * p.red_blocks;
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int kb0 = warp; kb0 < p.red_blocks; kb0 += kVecWarps * kVecAhead) {
+    Words<4> va[kVecAhead][2], vb[kVecAhead][2];
+    uint4 vx[kVecAhead][2];
+    float s0[kVecAhead], s1[kVecAhead];
+#pragma unroll
+    for (int u = 0; u < kVecAhead; ++u) {
+      const int kb = kb0 + u * kVecWarps;
+      if (kb < p.red_blocks) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int64_t at = int64_t(kb) * kBK + h * 64;
+          va[u][h] = ld_stream_w<4>(reinterpret_cast<const Words<4>*>(w0 + at));
+          vb[u][h] = ld_stream_w<4>(reinterpret_cast<const Words<4>*>(w1 + at));
+          vx[u][h] = __ldg(reinterpret_cast<const uint4*>(x + at));
+        }
+        const float s = __ldg(sw + int64_t(kb) * p.ws_red);
+        s0[u] = s * __ldg(sa0 + kb);
+        s1[u] = s * __ldg(sa1 + kb);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kVecAhead; ++u) {
+      if (kb0 + u * kVecWarps < p.red_blocks) {
+        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 b = vx[u][h];
+          mma_e4m3_16x8x32(c, va[u][h].w[0], vb[u][h].w[0], va[u][h].w[1], vb[u][h].w[1], b.x, b.y);
+          mma_e4m3_16x8x32(c, va[u][h].w[2], vb[u][h].w[2], va[u][h].w[3], vb[u][h].w[3], b.z, b.w);
+        }
+        sum[0] = fmaf(c[0], s0[u], sum[0]);
+        sum[1] = fmaf(c[1], s1[u], sum[1]);
+        sum[2] = fmaf(c[2], s0[u], sum[2]);
+        sum[3] = fmaf(c[3], s1[u], sum[3]);
+      }
+    }
+  }
+  part[warp][2 * t][g] = sum[0];
+  part[warp][2 * t + 1][g] = sum[1];
+  part[warp][2 * t][g + 8] = sum[2];
+  part[warp][2 * t + 1][g + 8] = sum[3];
+  __syncthreads();
+  const int row = threadIdx.x >> 4, ch = threadIdx.x & 15;
+  if (row < nrows) {
+    float all = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kVecWarps; ++i) all += part[i][row][ch];
+    p.out[int64_t(row0 + row) * p.out_cols + n0 + ch] = uint16_t(pack_bf16x2_rn(all, 0.0f));
+  }
+}
+
+template <bool DGRAD, bool SPLIT>
+cudaError_t launch_mm_as(MMArgs p, const CUtensorMap& mr, const CUtensorMap& ms,
+                         const CUtensorMap& mw, int blocks, int parts, cudaStream_t st) {
   p.stages = kMaxStages;
   while (mm_smem_bytes(p.E, p.stages) > size_t(kMaxSmem)) --p.stages;
   const int smem = int(mm_smem_bytes(p.E, p.stages));
@@ -451,17 +602,44 @@ cudaError_t launch_mm(MMArgs p, const void* a, const void* w, int K, int red, cu
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || configured_smem[dev] < smem) {
-    e = cudaFuncSetAttribute(mp_k_expert_matmul<DGRAD>,
+    e = cudaFuncSetAttribute(mp_k_expert_matmul<DGRAD, SPLIT>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured_smem[dev] = smem;
   }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(blocks));
+  cfg.blockDim = dim3(kMMThreads);
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(parts);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = SPLIT ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, mp_k_expert_matmul<DGRAD, SPLIT>, mr, ms, mw, p);
+}
+
+template <bool DGRAD>
+cudaError_t launch_mm(const MMArgs& p, const void* a, const void* w, int K, int red,
+                      cudaStream_t st) {
+  CUtensorMap mr, ms, mw;
+  if (!make_map_2d(&mr, a, 1, uint64_t(red), uint64_t(p.rows), kBK, kBM) ||
+      !make_map_2d(&ms, a, 1, uint64_t(red), uint64_t(p.rows), kBK, kShortBox) ||
+      !make_map_2d(&mw, w, 1, uint64_t(K), uint64_t(p.E) * p.w_rows, kBK, DGRAD ? kBK : kBN))
+    return cudaErrorInvalidValue;
   // at most one short tile per expert
   const int64_t row_tiles = std::min<int64_t>(p.rows, int64_t(p.rows) / kBM + p.E);
   const int64_t tiles = row_tiles * ((p.out_cols + kBN - 1) / kBN);
-  mp_k_expert_matmul<DGRAD><<<unsigned(std::min<int64_t>(tiles, sm_count())), kMMThreads,
-                              size_t(smem), st>>>(mr, ms, mw, p);
-  return cudaGetLastError();
+  const int sms = sm_count();
+  // too few tiles for the GPU: up to eight blocks (one cluster) share each
+  int parts = 1;
+  while (parts < 8 && tiles * parts * 2 <= sms && p.red_blocks >= parts * 4) parts *= 2;
+  if (parts > 1)
+    return launch_mm_as<DGRAD, true>(p, mr, ms, mw, int(tiles) * parts, parts, st);
+  return launch_mm_as<DGRAD, false>(p, mr, ms, mw, int(std::min<int64_t>(tiles, sms)), 1, st);
 }
 
 }  // namespace
@@ -488,6 +666,12 @@ cudaError_t launch_expert_matmul(int E, int rows, int N, int K, bool dgrad, cons
   p.out = static_cast<uint16_t*>(out);
   p.out32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   p.dev_err = dev_err;
+  if (!dgrad && rows <= kVecRows) {
+    mp_k_expert_matvec<<<dim3(unsigned(N / 16), unsigned(expert_offsets ? rows : 1)),
+                         kVecWarps * 32, 0, st>>>(p, static_cast<const unsigned char*>(a),
+                                                  static_cast<const unsigned char*>(w));
+    return cudaGetLastError();
+  }
   return dgrad ? launch_mm<true>(p, a, w, K, red, st) : launch_mm<false>(p, a, w, K, red, st);
 }
 

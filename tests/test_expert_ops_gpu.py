@@ -415,6 +415,37 @@ def test_wgrad(counts, N, K, slack, exact):
         lo += n
 
 
+@pytest.mark.parametrize("kind", ["fwd", "dgrad"])
+@pytest.mark.parametrize("counts,N,K,slack", [
+    ([2, 0, 3, 1, 0, 2], 272, 384, 0), ([0, 8], 16, 2048, 1), ([9], 512, 1152, 0),
+    ([4, 60, 2], 256, 640, 0), ([130], 128, 2176, 0)])
+def test_matmul_few_rows(kind, counts, N, K, slack):
+    """The forms for few rows: row products, and reductions split over blocks."""
+    test_matmul(kind, counts, N, K, slack, True)
+    test_matmul(kind, counts, N, K, slack, False)
+
+
+@pytest.mark.parametrize("rows", [1, 8, 9, 40, 300])
+def test_matmul_block_sums_are_fp32(rows):
+    """Within one scale block 448 * 448 cancels and 2^-5 stays: every partial sum has at most
+    23 significant bits, so fp32 sums in any order give it exactly; sums kept in fewer bits
+    would not."""
+    N, K = 256, 256
+    a = torch.zeros((rows, K), device=DEV)
+    w = torch.zeros((1, N, K), device=DEV)
+    a[:, 3], a[:, 77], a[:, 40] = 448.0, 448.0, 0.125
+    w[:, :, 3], w[:, :, 77], w[:, :, 40] = 448.0, -448.0, 0.25
+    a[:, 128 + 5], w[:, :, 128 + 5] = 1.0, 2.0
+    out = zeros((rows, N), torch.bfloat16)
+    err = zeros(1, torch.int32)
+    B.check(B.mp_expert_matmul_e4m3(1, rows, N, K, a.to(torch.float8_e4m3fn),
+                                    torch.ones((rows, 2), device=DEV),
+                                    w.to(torch.float8_e4m3fn), torch.ones((1, 2, 2), device=DEV),
+                                    None, out, err))
+    torch.cuda.synchronize()
+    assert bool((out == 2.03125).all())
+
+
 def test_matmul_dense_without_offsets_and_gradient_identity():
     """E = 1 without offsets is the dense product; <dy, a w^T> = <dy w, a> = <dy^T a, w>."""
     g = gen(13)
