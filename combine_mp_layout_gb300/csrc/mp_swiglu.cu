@@ -27,6 +27,7 @@ namespace {
 constexpr int kSwWarps = 4;
 constexpr int kCPL = 16;                  // channels per lane
 constexpr int kSpan = kCPL * kWarp;       // channels per warp and step
+constexpr int kBlocksPerSM = 64;          // of a full grid; larger problems loop
 
 struct SwigluArgs {
   int rows, I;
@@ -39,10 +40,10 @@ struct SwigluArgs {
   float* d_row_weights;      // [rows] or NULL
 };
 
-// 16 bf16 channels of one lane (32-byte loads where the base allows).
+// 16 bf16 channels of one lane, as their eight words (32-byte loads where the
+// base allows).
 template <bool A32>
-__device__ __forceinline__ void load16(const uint16_t* p, float (&f)[kCPL]) {
-  uint32_t w[8];
+__device__ __forceinline__ void load16(const uint16_t* p, uint32_t (&w)[8]) {
   if constexpr (A32) {
     const Words<8> v = ld_stream_w<8>(reinterpret_cast<const Words<8>*>(p));
 #pragma unroll
@@ -56,43 +57,47 @@ __device__ __forceinline__ void load16(const uint16_t* p, float (&f)[kCPL]) {
       w[4 + i] = b.w[i];
     }
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    f[2 * i] = bf16_lo(w[i]);
-    f[2 * i + 1] = bf16_hi(w[i]);
-  }
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+
+// 1 / (1 + exp(-x)) of two channels from the fast exponential and reciprocal:
+// a few fp32 ulps, far below the e4m3 rounding that follows.
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float2 t = mul2(x, make_float2(-kLog2e, -kLog2e));
+  float2 e, r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = add2(e, make_float2(1.0f, 1.0f));
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+  return r;
 }
 
-// 1 / (1 + exp(-x)) from the fast exponential and reciprocal: a few fp32 ulps,
-// far below the e4m3 rounding that follows.
-__device__ __forceinline__ float sigmoid_fast(float x) {
-  return __fdividef(1.0f, 1.0f + __expf(-x));
-}
-
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+__device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) {
   uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a.y), "f"(a.x));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(b.y), "f"(b.x));
   return uint32_t(lo) | (uint32_t(hi) << 16);
 }
 
 // Quantises the lane's 16 values (its block's other values in the seven lanes
 // beside it) and stores codes and scale.  Every lane of the warp calls it.
-__device__ __forceinline__ void quantise_store(const float (&z)[kCPL], bool valid,
+__device__ __forceinline__ void quantise_store(const float2 (&z)[kCPL / 2], bool valid,
                                                unsigned char* codes, float* scale) {
   float amax = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kCPL; ++i) amax = fmaxf(amax, fabsf(z[i]));
+  for (int i = 0; i < kCPL / 2; ++i) amax = fmaxf(amax, fmaxf(fabsf(z[i].x), fabsf(z[i].y)));
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
   float sc = amax * (1.0f / 448.0f);
   if (!(sc >= 0x1p-126f)) sc = 1.0f;
   const float inv = sc < INFINITY ? __fdiv_rn(1.0f, sc) : 0.0f;
   if (!valid) return;
+  const float2 inv2 = make_float2(inv, inv);
   Words<4> q;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    q.w[i] = e4m3x4(z[4 * i] * inv, z[4 * i + 1] * inv, z[4 * i + 2] * inv, z[4 * i + 3] * inv);
+  for (int i = 0; i < 4; ++i) q.w[i] = e4m3x4(mul2(z[2 * i], inv2), mul2(z[2 * i + 1], inv2));
   st_stream_w<4>(reinterpret_cast<Words<4>*>(codes), q);
   if ((threadIdx.x & 7) == 0) *scale = sc;
 }
@@ -115,75 +120,104 @@ mp_k_swiglu(const SwigluArgs p) {
     const int64_t row = unit / spans;
     const int ch = int(unit - row * spans) * kSpan + lane * kCPL;
     const bool valid = ch < p.I;
-    float g[kCPL], u[kCPL];
+    uint32_t g[kCPL / 2] = {}, u[kCPL / 2] = {};
     if (valid) {
       const uint16_t* src = p.gate_up + row * 2 * p.I + ch;
       load16<A32>(src, g);
       load16<A32>(src + p.I, u);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kCPL; ++i) g[i] = u[i] = 0.0f;
     }
     const float w = p.row_weights != nullptr ? __ldg(p.row_weights + row) : 1.0f;
+    const float2 w2 = make_float2(w, w);
+    float2 z[kCPL / 2];
 #pragma unroll
-    for (int i = 0; i < kCPL; ++i) g[i] = g[i] * sigmoid_fast(g[i]) * u[i] * w;
-    quantise_store(g, valid, p.out + row * p.I + ch, p.out_scales + row * (p.I / 128) + ch / 128);
+    for (int i = 0; i < kCPL / 2; ++i) {
+      const float2 gate = unpack2(g[i]);
+      z[i] = mul2(mul2(mul2(gate, sigmoid2(gate)), unpack2(u[i])), w2);
+    }
+    quantise_store(z, valid, p.out + row * p.I + ch, p.out_scales + row * (p.I / 128) + ch / 128);
   }
 }
 
-// A block per row: its warps take the row's spans in turn, and the row weight's
+// WPR warps (1, 2 or 4) per row take the row's spans in turn; the row weight's
 // gradient is added up in a fixed order (lanes, then warps).
-template <bool A32>
-__global__ void __launch_bounds__(kSwWarps * kWarp)
+template <bool A32, int WPR>
+__global__ void __launch_bounds__(kSwWarps * kWarp, 8)
 mp_k_swiglu_backward(const SwigluArgs p) {
   __shared__ float red[2][kSwWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kRows = kSwWarps / WPR;
   const int rows = live_rows(p);
   int flip = 0;
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, flip ^= 1) {
-    const float w = p.row_weights != nullptr ? __ldg(p.row_weights + row) : 1.0f;
-    float dw = 0.0f;
-    for (int c0 = warp * kSpan; c0 < p.I; c0 += kSwWarps * kSpan) {
+  for (int64_t r0 = int64_t(blockIdx.x) * kRows; r0 < rows;
+       r0 += int64_t(gridDim.x) * kRows, flip ^= 1) {
+    const int64_t row = r0 + warp / WPR;
+    const bool live = row < rows;
+    const float w = live && p.row_weights != nullptr ? __ldg(p.row_weights + row) : 1.0f;
+    const float2 w2 = make_float2(w, w), one = make_float2(1.0f, 1.0f);
+    float2 dw = make_float2(0.0f, 0.0f);
+    for (int c0 = (warp % WPR) * kSpan; live && c0 < p.I; c0 += WPR * kSpan) {
       const int ch = c0 + lane * kCPL;
       const bool valid = ch < p.I;
-      float g[kCPL], u[kCPL], d[kCPL];
+      uint32_t g[kCPL / 2] = {}, u[kCPL / 2] = {}, d[kCPL / 2] = {};
       if (valid) {
         const uint16_t* src = p.gate_up + row * 2 * p.I + ch;
         load16<A32>(src, g);
         load16<A32>(src + p.I, u);
         load16<A32>(p.d_out + row * p.I + ch, d);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kCPL; ++i) g[i] = u[i] = d[i] = 0.0f;
       }
+      float2 dg[kCPL / 2], du[kCPL / 2];
 #pragma unroll
-      for (int i = 0; i < kCPL; ++i) {
-        const float sig = sigmoid_fast(g[i]);
-        const float act = g[i] * sig;
-        dw += d[i] * act * u[i];
-        const float dd = d[i] * w;
-        const float du = dd * act;
-        g[i] = dd * u[i] * sig * (1.0f + g[i] * (1.0f - sig));
-        u[i] = du;
+      for (int i = 0; i < kCPL / 2; ++i) {
+        const float2 gate = unpack2(g[i]), up = unpack2(u[i]), dz = unpack2(d[i]);
+        const float2 sig = sigmoid2(gate);
+        const float2 act = mul2(gate, sig);
+        dw = fma2(mul2(dz, act), up, dw);
+        const float2 dd = mul2(dz, w2);
+        du[i] = mul2(dd, act);
+        // sig (1 + gate (1 - sig)) = sig + act (1 - sig)
+        const float2 slope = fma2(act, fma2(sig, make_float2(-1.0f, -1.0f), one), sig);
+        dg[i] = mul2(mul2(dd, up), slope);
       }
       unsigned char* codes = p.out + row * 2 * p.I + ch;
       float* scales = p.out_scales + row * (p.I / 64) + ch / 128;
-      quantise_store(g, valid, codes, scales);
-      quantise_store(u, valid, codes + p.I, scales + p.I / 128);
+      quantise_store(dg, valid, codes, scales);
+      quantise_store(du, valid, codes + p.I, scales + p.I / 128);
     }
     if (p.d_row_weights != nullptr) {
+      float sum = dw.x + dw.y;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dw += __shfl_xor_sync(kFull, dw, o);
-      if (lane == 0) red[flip][warp] = dw;
-      __syncthreads();  // (two buffers: one barrier per row is enough)
-      if (threadIdx.x == 0) {
-        float all = 0.0f;
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      if constexpr (WPR == 1) {
+        if (live && lane == 0) p.d_row_weights[row] = sum;
+      } else {
+        if (lane == 0) red[flip][warp] = sum;
+        __syncthreads();  // (two buffers: one barrier per turn is enough)
+        if (live && lane == 0 && warp % WPR == 0) {
+          float all = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kSwWarps; ++i) all += red[flip][i];
-        p.d_row_weights[row] = all;
+          for (int i = 0; i < WPR; ++i) all += red[flip][warp + i];
+          p.d_row_weights[row] = all;
+        }
       }
     }
   }
+}
+
+unsigned grid_for(int64_t blocks) {
+  return unsigned(std::min<int64_t>(blocks, int64_t(sm_count()) * kBlocksPerSM));
+}
+
+template <bool A32>
+cudaError_t launch_backward(const SwigluArgs& p, cudaStream_t st) {
+  const int spans = (p.I + kSpan - 1) / kSpan;
+  const int64_t rows = p.rows;
+  if (spans == 1)
+    mp_k_swiglu_backward<A32, 1><<<grid_for((rows + 3) / 4), kSwWarps * kWarp, 0, st>>>(p);
+  else if (spans == 2)
+    mp_k_swiglu_backward<A32, 2><<<grid_for((rows + 1) / 2), kSwWarps * kWarp, 0, st>>>(p);
+  else
+    mp_k_swiglu_backward<A32, 4><<<grid_for(rows), kSwWarps * kWarp, 0, st>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -197,12 +231,12 @@ cudaError_t launch_swiglu(int rows, int I, const void* gate_up, const float* row
   p.row_weights = row_weights; p.num_rows = num_rows;
   p.out = static_cast<unsigned char*>(out); p.out_scales = out_scales;
   const int64_t units = int64_t(rows) * ((I + kSpan - 1) / kSpan);
-  const int64_t blocks = std::min<int64_t>((units + kSwWarps - 1) / kSwWarps, 0x7fffffff);
+  const unsigned blocks = grid_for((units + kSwWarps - 1) / kSwWarps);
   const bool a32 = (reinterpret_cast<uintptr_t>(gate_up) & 31u) == 0;
   if (a32)
-    mp_k_swiglu<true><<<unsigned(blocks), kSwWarps * kWarp, 0, st>>>(p);
+    mp_k_swiglu<true><<<blocks, kSwWarps * kWarp, 0, st>>>(p);
   else
-    mp_k_swiglu<false><<<unsigned(blocks), kSwWarps * kWarp, 0, st>>>(p);
+    mp_k_swiglu<false><<<blocks, kSwWarps * kWarp, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -220,11 +254,7 @@ cudaError_t launch_swiglu_backward(int rows, int I, const void* gate_up, const f
   p.d_row_weights = d_row_weights;
   const bool a32 = ((reinterpret_cast<uintptr_t>(gate_up) | reinterpret_cast<uintptr_t>(d_out)) &
                     31u) == 0;
-  if (a32)
-    mp_k_swiglu_backward<true><<<unsigned(rows), kSwWarps * kWarp, 0, st>>>(p);
-  else
-    mp_k_swiglu_backward<false><<<unsigned(rows), kSwWarps * kWarp, 0, st>>>(p);
-  return cudaGetLastError();
+  return a32 ? launch_backward<true>(p, st) : launch_backward<false>(p, st);
 }
 
 }  // namespace mp
