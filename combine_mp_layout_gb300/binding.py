@@ -102,6 +102,8 @@ def lib() -> ctypes.CDLL:
         L.mp_expert_matmul_wgrad_e4m3.argtypes = [i32] * 4 + [P] * 8
         L.mp_swiglu_e4m3.argtypes = [i32] * 2 + [P] * 6
         L.mp_swiglu_backward_e4m3.argtypes = [i32] * 2 + [P] * 8
+        L.mp_ll_row_weights.argtypes = [i32] * 3 + [P, P, i64, P, P]
+        L.mp_ll_row_weights_backward.argtypes = [i32] * 3 + [P, i64, P, P, P]
         L.mp_dispatch_ll.argtypes = [i32] * 7 + [P] * 4 + [i64] + [P] * 8
         for f in ("mp_layout", "mp_dispatch", "mp_dispatch_offsets", "mp_dispatch_rows",
                   "mp_dispatch_rows_e4m3", "mp_dispatch_rows_mxfp8", "mp_dispatch_offsets_global",
@@ -115,7 +117,8 @@ def lib() -> ctypes.CDLL:
                   "mp_dispatch_ll", "mp_layout_dispatch", "mp_dispatch_ll_rows_quant",
                   "mp_dispatch_ll_quant", "mp_route", "mp_route_backward",
                   "mp_expert_matmul_e4m3", "mp_expert_matmul_dgrad_e4m3",
-                  "mp_expert_matmul_wgrad_e4m3", "mp_swiglu_e4m3", "mp_swiglu_backward_e4m3"):
+                  "mp_expert_matmul_wgrad_e4m3", "mp_swiglu_e4m3", "mp_swiglu_backward_e4m3",
+                  "mp_ll_row_weights", "mp_ll_row_weights_backward"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -567,3 +570,22 @@ def mp_swiglu_backward_e4m3(rows, I, gate_up, row_weights, d_out, num_rows, d_ga
         _arr(d_gate_up, "d_gate_up", _F8, rows * 2 * I),
         _arr(d_gate_up_scales, "d_gate_up_scales", torch.float32, rows * (2 * I // SCALE_BLOCK)),
         _arr(d_row_weights, "d_row_weights", torch.float32, rows), _raw_stream(stream))
+
+
+def mp_ll_row_weights(R, N, K, topk_weights, slot_row, recv_capacity, row_weights,
+                      stream=None) -> int:
+    """Routing weights of the low-latency slots at their receive rows."""
+    return lib().mp_ll_row_weights(
+        R, N, K, _arr(topk_weights, "topk_weights", torch.float32, R * N * K),
+        _arr(slot_row, "slot_row", torch.int32, R * N * K), int(recv_capacity),
+        _arr(row_weights, "row_weights", torch.float32, int(recv_capacity)),
+        _raw_stream(stream))
+
+
+def mp_ll_row_weights_backward(R, N, K, d_row_weights, rows, slot_row, d_topk_weights,
+                               stream=None) -> int:
+    """Gradients of the rows' weights back at their slots."""
+    return lib().mp_ll_row_weights_backward(
+        R, N, K, _arr(d_row_weights, "d_row_weights", torch.float32, int(rows)), int(rows),
+        _arr(slot_row, "slot_row", torch.int32, R * N * K),
+        _arr(d_topk_weights, "d_topk_weights", torch.float32, R * N * K), _raw_stream(stream))

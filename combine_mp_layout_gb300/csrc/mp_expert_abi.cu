@@ -169,4 +169,35 @@ int mp_swiglu_backward_e4m3(int rows, int I, const void* gate_up, const float* r
                                           reinterpret_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+int ll_row_weights(int R, int N, int K, const int32_t* slot_row, int64_t rows, bool back,
+                   const float* in, const float* in_slots, float* out, const float* out_slots,
+                   mp_stream_t stream) {
+  if (R < 1 || R > MP_MAX_RANKS || N < 0 || K < 1 || K > MP_MAX_TOPK || rows < 0 ||
+      int64_t(R) * N * K >= k31)
+    return MP_ERR_INVALID_ARG;
+  if (N > 0 && (!slot_row || !(back ? out_slots : in_slots))) return MP_ERR_INVALID_ARG;
+  if (rows > 0 && !(back ? in : out)) return MP_ERR_INVALID_ARG;
+  if (!aligned_to(slot_row, 4) || !aligned_to(in, 4) || !aligned_to(out, 4))
+    return MP_ERR_INVALID_ARG;
+  return status_of(launch_ll_row_weights(int64_t(R) * N * K, rows, back, slot_row, in, out,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+int mp_ll_row_weights(int R, int N, int K, const float* topk_weights, const int32_t* slot_row,
+                      int64_t recv_capacity, float* row_weights, mp_stream_t stream) {
+  return ll_row_weights(R, N, K, slot_row, recv_capacity, false, topk_weights, topk_weights,
+                        row_weights, nullptr, stream);
+}
+
+int mp_ll_row_weights_backward(int R, int N, int K, const float* d_row_weights, int64_t rows,
+                               const int32_t* slot_row, float* d_topk_weights,
+                               mp_stream_t stream) {
+  return ll_row_weights(R, N, K, slot_row, rows, true, d_row_weights, nullptr, d_topk_weights,
+                        d_topk_weights, stream);
+}
+
 }  // extern "C"

@@ -240,4 +240,8 @@ cudaError_t launch_swiglu_backward(int rows, int I, const void* gate_up, const f
                                    float* d_gate_up_scales, float* d_row_weights,
                                    cudaStream_t stream);
 
+// Weights of the low-latency layout's slots to their rows, or gradients back.
+cudaError_t launch_ll_row_weights(int64_t slots, int64_t rows, bool back, const int32_t* slot_row,
+                                  const float* in, float* out, cudaStream_t stream);
+
 }  // namespace mp

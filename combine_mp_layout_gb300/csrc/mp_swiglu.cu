@@ -203,6 +203,22 @@ mp_k_swiglu_backward(const SwigluArgs p) {
   }
 }
 
+// A thread per (token, slot): its weight to the row that the slot was given, or
+// (BACK) the row's gradient back to the slot.
+template <bool BACK>
+__global__ void __launch_bounds__(256)
+mp_k_ll_row_weights(int64_t slots, int64_t rows, const int32_t* __restrict__ slot_row,
+                    const float* __restrict__ in, float* __restrict__ out) {
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= slots) return;
+  const int row = __ldg(slot_row + i);
+  const bool placed = row >= 0 && row < rows;
+  if constexpr (BACK)
+    out[i] = placed ? __ldg(in + row) : 0.0f;
+  else if (placed)
+    out[row] = __ldg(in + i);
+}
+
 unsigned grid_for(int64_t blocks) {
   return unsigned(std::min<int64_t>(blocks, int64_t(sm_count()) * kBlocksPerSM));
 }
@@ -255,6 +271,17 @@ cudaError_t launch_swiglu_backward(int rows, int I, const void* gate_up, const f
   const bool a32 = ((reinterpret_cast<uintptr_t>(gate_up) | reinterpret_cast<uintptr_t>(d_out)) &
                     31u) == 0;
   return a32 ? launch_backward<true>(p, st) : launch_backward<false>(p, st);
+}
+
+cudaError_t launch_ll_row_weights(int64_t slots, int64_t rows, bool back, const int32_t* slot_row,
+                                  const float* in, float* out, cudaStream_t st) {
+  if (slots == 0) return cudaSuccess;
+  const unsigned blocks = unsigned((slots + 255) / 256);
+  if (back)
+    mp_k_ll_row_weights<true><<<blocks, 256, 0, st>>>(slots, rows, slot_row, in, out);
+  else
+    mp_k_ll_row_weights<false><<<blocks, 256, 0, st>>>(slots, rows, slot_row, in, out);
+  return cudaGetLastError();
 }
 
 }  // namespace mp

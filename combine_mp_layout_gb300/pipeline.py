@@ -3,7 +3,9 @@ device memory and streams only; every computation is a library kernel).
 
 ``EPPlan`` owns the device buffers of one (R, N, K, E, H, dtype) problem and
 runs mp_layout -> mp_dispatch -> mp_combine on them; ``RSVPlan`` does the same
-for mp_reducescatterv / mp_allgatherv.
+for mp_reducescatterv / mp_allgatherv; ``MoELayerPlan`` for a whole expert layer
+(router, low-latency e4m3 dispatch, the experts' gated products, combine) and its
+gradient.
 """
 from __future__ import annotations
 
@@ -164,3 +166,136 @@ class RSVPlan:
 
     def allgatherv(self, stream=None) -> int:
         return B.mp_allgatherv(self.R, self.H * 2, self.sizes, self.shards, self.ag_out, stream)
+
+
+class MoELayerPlan:
+    """One expert layer: tokens x [R][N][H] and router logits [R][N][E] in, bf16 [R][N][H] out.
+
+    Expert e computes w_down[e] (silu(g) * u), (g, u) = w_gate_up[e] x, on e4m3 rows; its
+    weights are e4m3 with one fp32 scale per 128 x 128 block: w_gate_up [E][2I][H] (the gate's
+    channels first) and w_down [E][H][I].  ``forward`` leaves what ``backward`` needs in the
+    plan's buffers.
+    """
+
+    def __init__(self, R: int, N: int, K: int, E: int, H: int, I: int, scoring: str = "softmax",
+                 normalize: bool = True, scale: float = 1.0, loss_coef: float = 0.01,
+                 logits_dtype=torch.float32, recv_capacity: int | None = None, train: bool = True,
+                 device="cuda"):
+        if scoring not in ("softmax", "sigmoid"):
+            raise ValueError("scoring must be softmax or sigmoid")
+        if H % B.SCALE_BLOCK or I % B.SCALE_BLOCK:
+            raise ValueError("H and I must be multiples of %d" % B.SCALE_BLOCK)
+        self.R, self.N, self.K, self.E, self.H, self.I = R, N, K, E, H, I
+        self.scoring = B.MP_SOFTMAX if scoring == "softmax" else B.MP_SIGMOID
+        self.normalize, self.scale, self.loss_coef = normalize, scale, loss_coef
+        dev = self.device = torch.device(device)
+        self.cap = cap = R * N * K if recv_capacity is None else int(recv_capacity)
+        ws = B.mp_route_workspace_size(R, N, E)
+        if ws == 0:
+            raise ValueError("invalid problem shape R=%d N=%d E=%d" % (R, N, E))
+
+        def buf(shape, dtype):
+            return torch.zeros(shape, dtype=dtype, device=dev)
+        f32, bf16, f8, nb = torch.float32, torch.bfloat16, torch.float8_e4m3fn, B.SCALE_BLOCK
+        self.workspace = buf(ws, torch.uint8)
+        self.dev_err = _i32(1, dev)
+        # router
+        self.topk_idx, self.topk_weights = _i32((R, N, K), dev), buf((R, N, K), f32)
+        self.num_tokens_per_expert, self.num_routed = _i32((R, E), dev), _i32(R, dev)
+        self.balance_loss = buf(R, f32)
+        # expert-major rows
+        self.expert_offsets, self.expert_src_offsets = _i32(E + 1, dev), _i32((E, R), dev)
+        self.recv_src_token, self.slot_row = _i32(max(cap, 1), dev), _i32((R, N, K), dev)
+        self.recv_x, self.recv_scales = buf((cap, H), f8), buf((cap, H // nb), f32)
+        self.row_weights = buf(cap, f32)
+        # experts
+        self.gate_up = buf((cap, 2 * I), bf16)
+        self.z, self.z_scales = buf((cap, I), f8), buf((cap, I // nb), f32)
+        self.y = buf((cap, H), bf16)
+        self.ones = torch.ones((R, N, K), dtype=f32, device=dev)
+        self.out = buf((R, N, H), bf16)
+        if train:
+            self.dy, self.dy_scales = buf((cap, H), f8), buf((cap, H // nb), f32)
+            self.dz = buf((cap, I), bf16)
+            self.d_gate_up = buf((cap, 2 * I), f8)
+            self.d_gate_up_scales = buf((cap, 2 * I // nb), f32)
+            self.d_row_weights = buf(cap, f32)
+            self.d_rows = buf((cap, H), bf16)
+            self.d_x = buf((R, N, H), bf16)
+            self.d_w_gate_up, self.d_w_down = buf((E, 2 * I, H), bf16), buf((E, H, I), bf16)
+            self.d_topk_weights = buf((R, N, K), f32)
+            self.d_logits = buf((R, N, E), logits_dtype)
+
+    @property
+    def _num_rows(self):
+        return self.expert_offsets[self.E:]
+
+    def forward(self, x, logits, w_gate_up, w_gate_up_scales, w_down, w_down_scales, bias=None,
+                active=None, stream=None):
+        """The layer's output (self.out); self.balance_loss holds the loss per rank."""
+        R, N, K, E, H, I, cap = (self.R, self.N, self.K, self.E, self.H, self.I, self.cap)
+        B.check(B.mp_route(R, N, K, E, self.scoring, logits, bias, active, self.normalize,
+                           self.scale, self.loss_coef, self.topk_idx, self.topk_weights,
+                           self.num_tokens_per_expert, self.num_routed, self.balance_loss,
+                           self.dev_err, self.workspace, stream), "mp_route")
+        # (small batches: the dispatch that counts for itself is one kernel)
+        counts = self.num_tokens_per_expert if R * N * K > 16384 else None
+        B.check(B.mp_dispatch_ll_quant(R, N, K, E, H, B.MP_Q_E4M3, 0, x, self.topk_idx, counts,
+                                       cap, self.expert_offsets, self.expert_src_offsets,
+                                       self.recv_src_token, self.slot_row, self.recv_x,
+                                       self.recv_scales, self.dev_err, stream),
+                "mp_dispatch_ll_quant")
+        B.check(B.mp_ll_row_weights(R, N, K, self.topk_weights, self.slot_row, cap,
+                                    self.row_weights, stream), "mp_ll_row_weights")
+        B.check(B.mp_expert_matmul_e4m3(E, cap, 2 * I, H, self.recv_x, self.recv_scales, w_gate_up,
+                                        w_gate_up_scales, self.expert_offsets, self.gate_up,
+                                        self.dev_err, stream), "mp_expert_matmul_e4m3")
+        B.check(B.mp_swiglu_e4m3(cap, I, self.gate_up, self.row_weights, self._num_rows, self.z,
+                                 self.z_scales, stream), "mp_swiglu_e4m3")
+        B.check(B.mp_expert_matmul_e4m3(E, cap, H, I, self.z, self.z_scales, w_down, w_down_scales,
+                                        self.expert_offsets, self.y, self.dev_err, stream),
+                "mp_expert_matmul_e4m3")
+        B.check(B.mp_combine_ll(R, N, K, H, self.y, cap, self.slot_row, self.ones, self.out,
+                                self.dev_err, stream), "mp_combine_ll")
+        return self.out
+
+    def backward(self, d_out, logits, w_gate_up, w_gate_up_scales, w_down, w_down_scales,
+                 d_balance_loss=None, active=None, stream=None):
+        """Gradients of a forward pass, from the output's (and the losses'): d_x, d_logits,
+        d_w_gate_up, d_w_down of the plan."""
+        R, N, K, E, H, I, cap = (self.R, self.N, self.K, self.E, self.H, self.I, self.cap)
+        B.check(B.mp_dispatch_ll_rows_quant(R, N, K, H, B.MP_Q_E4M3, d_out, self.slot_row, cap,
+                                            self.dy, self.dy_scales, stream),
+                "mp_dispatch_ll_rows_quant")
+        B.check(B.mp_expert_matmul_dgrad_e4m3(E, cap, H, I, self.dy, self.dy_scales, w_down,
+                                              w_down_scales, self.expert_offsets, self.dz,
+                                              self.dev_err, stream), "mp_expert_matmul_dgrad_e4m3")
+        B.check(B.mp_expert_matmul_wgrad_e4m3(E, cap, H, I, self.dy, self.dy_scales, self.z,
+                                              self.z_scales, self.expert_offsets, self.d_w_down,
+                                              self.dev_err, stream), "mp_expert_matmul_wgrad_e4m3")
+        B.check(B.mp_swiglu_backward_e4m3(cap, I, self.gate_up, self.row_weights, self.dz,
+                                          self._num_rows, self.d_gate_up, self.d_gate_up_scales,
+                                          self.d_row_weights, stream), "mp_swiglu_backward_e4m3")
+        B.check(B.mp_expert_matmul_wgrad_e4m3(E, cap, 2 * I, H, self.d_gate_up,
+                                              self.d_gate_up_scales, self.recv_x,
+                                              self.recv_scales, self.expert_offsets,
+                                              self.d_w_gate_up, self.dev_err, stream),
+                "mp_expert_matmul_wgrad_e4m3")
+        B.check(B.mp_expert_matmul_dgrad_e4m3(E, cap, 2 * I, H, self.d_gate_up,
+                                              self.d_gate_up_scales, w_gate_up, w_gate_up_scales,
+                                              self.expert_offsets, self.d_rows, self.dev_err,
+                                              stream), "mp_expert_matmul_dgrad_e4m3")
+        B.check(B.mp_combine_ll(R, N, K, H, self.d_rows, cap, self.slot_row, self.ones, self.d_x,
+                                self.dev_err, stream), "mp_combine_ll")
+        B.check(B.mp_ll_row_weights_backward(R, N, K, self.d_row_weights, cap, self.slot_row,
+                                             self.d_topk_weights, stream),
+                "mp_ll_row_weights_backward")
+        B.check(B.mp_route_backward(R, N, K, E, self.scoring, logits, active, self.normalize,
+                                    self.scale, self.loss_coef, self.topk_idx,
+                                    self.d_topk_weights, self.num_tokens_per_expert,
+                                    self.num_routed, d_balance_loss, self.d_logits, stream),
+                "mp_route_backward")
+        return self.d_x, self.d_logits, self.d_w_gate_up, self.d_w_down
+
+    def device_error(self) -> int:
+        return int(self.dev_err.item())

@@ -642,7 +642,13 @@ int mp_dispatch_ll_quant(int R, int N, int K, int E, int H, int qformat, int ran
  * low-latency dispatch, each with its gradient.  No counterpart in the pages;
  * a layer is
  *   mp_route -> mp_dispatch_ll_quant (MP_Q_E4M3) -> mp_expert_matmul_e4m3
- *   -> mp_swiglu_e4m3 -> mp_expert_matmul_e4m3 -> mp_combine_ll.
+ *   -> mp_swiglu_e4m3 (with mp_ll_row_weights) -> mp_expert_matmul_e4m3
+ *   -> mp_combine_ll (weights 1),
+ * and its gradient
+ *   mp_dispatch_ll_rows_quant of the output's gradient -> mp_expert_matmul_dgrad_e4m3
+ *   -> mp_swiglu_backward_e4m3 -> mp_expert_matmul_dgrad_e4m3 -> mp_combine_ll,
+ *   mp_expert_matmul_wgrad_e4m3 for both weights, and
+ *   mp_ll_row_weights_backward -> mp_route_backward.
  */
 
 /* Score functions of the router. */
@@ -801,6 +807,23 @@ int mp_swiglu_e4m3(int rows, int I, const void *gate_up, const float *row_weight
 int mp_swiglu_backward_e4m3(int rows, int I, const void *gate_up, const float *row_weights,
                             const void *d_out, const int32_t *num_rows, void *d_gate_up,
                             float *d_gate_up_scales, float *d_row_weights, mp_stream_t stream);
+
+/*
+ * mp_ll_row_weights -- the routing weights of the low-latency layout's slots at
+ * the rows they were given, for mp_swiglu_e4m3:
+ *   row_weights[slot_row[s][t][k]] = topk_weights[s][t][k]
+ * for entries in [0, recv_capacity); other rows are not written.
+ * mp_ll_row_weights_backward -- the way back for mp_route_backward:
+ *   d_topk_weights[s][t][k] = d_row_weights[slot_row[s][t][k]], 0 for entries
+ * outside [0, rows).
+ * Checks: 1 <= R <= 32, N >= 0, 1 <= K <= 32, R*N*K < 2^31, recv_capacity and
+ *   rows >= 0, non-NULL buffers where entries or rows exist, 4-byte alignment.
+ */
+int mp_ll_row_weights(int R, int N, int K, const float *topk_weights, const int32_t *slot_row,
+                      int64_t recv_capacity, float *row_weights, mp_stream_t stream);
+int mp_ll_row_weights_backward(int R, int N, int K, const float *d_row_weights, int64_t rows,
+                               const int32_t *slot_row, float *d_topk_weights,
+                               mp_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -114,6 +114,19 @@ def test_swiglu_rejects(L, bad):
                                      a["sc"], a["dw"], _p(0)) == B.MP_ERR_INVALID_ARG
 
 
+@no_gpu
+@pytest.mark.parametrize("bad", [dict(R=0), dict(R=33), dict(N=-1), dict(K=0), dict(K=33),
+                                 dict(cap=-1), dict(w=_p(0)), dict(slots=_p(0)), dict(rows=_p(0)),
+                                 dict(w=_p(FAKE + 2)), dict(slots=_p(FAKE + 1)),
+                                 dict(R=32, N=2 ** 25, K=2)])
+def test_row_weights_reject(L, bad):
+    a = dict(dict(R=2, N=8, K=2, cap=16, w=_p(), slots=_p(), rows=_p()), **bad)
+    assert L.mp_ll_row_weights(a["R"], a["N"], a["K"], a["w"], a["slots"], a["cap"], a["rows"],
+                               _p(0)) == B.MP_ERR_INVALID_ARG
+    assert L.mp_ll_row_weights_backward(a["R"], a["N"], a["K"], a["rows"], a["cap"], a["slots"],
+                                        a["w"], _p(0)) == B.MP_ERR_INVALID_ARG
+
+
 def test_binding_refuses_cpu_tensors(L):
     t = torch.zeros(8)
     with pytest.raises(TypeError):

@@ -692,3 +692,78 @@ def test_swiglu_rows_past_32_bit_offsets():
     g, u, s, _ = swiglu_ref(x[-1:], I, None)
     check_quantised(out[-1:], sc[-1:], g * s * u)
     assert bool((sc[:-1] == 1.0).all())
+
+
+# ------------------------------------------------------------------ the layer
+
+@pytest.mark.parametrize("scoring,N", [("softmax", 64), ("sigmoid", 37)])
+def test_moe_layer_forward_and_backward(scoring, N):
+    """The whole layer against 64 bits on unquantised rows.  e4m3 rounds each value of a row
+    with a relative error of at most 2^-4, about uniform: 2^-4 / sqrt(3) in the 2-norm, once
+    for the tokens and once for the activation (forward), and for the gradients once more for
+    each quantised factor: within 2^-4 * sqrt(2), and 2^-4 * sqrt(4)."""
+    from combine_mp_layout_gb300.moe_layer import quantise_weights
+    from combine_mp_layout_gb300.pipeline import MoELayerPlan
+    R, K, E, H, I = 2, 2, 8, 256, 384
+    g = gen(31)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=g, device=DEV)
+    x, d_out = rand(R, N, H).bfloat16(), rand(R, N, H).bfloat16()
+    logits, d_loss = rand(R, N, E) * 1.5, rand(R)
+    active = (torch.rand((R, N), generator=g, device=DEV) < 0.9).to(torch.uint8)
+    bias = rand(E) * 0.1 if scoring == "sigmoid" else None
+    wg, wd = quantise_weights(rand(E, 2 * I, H) / 16), quantise_weights(rand(E, H, I) / 16)
+    plan = MoELayerPlan(R, N, K, E, H, I, scoring=scoring, scale=1.5, loss_coef=0.1)
+    plan.forward(x, logits, *wg, *wd, bias=bias, active=active)
+    plan.backward(d_out, logits, *wg, *wd, d_balance_loss=d_loss, active=active)
+    torch.cuda.synchronize()
+    assert plan.device_error() == 0
+    # the same layer in 64 bits, with the kernel's choice of experts
+    xd = x.double().requires_grad_(True)
+    ld = logits.double().requires_grad_(True)
+    wgd = weights_ref(*wg).requires_grad_(True)
+    wdd = weights_ref(*wd).requires_grad_(True)
+    mode = B.MP_SOFTMAX if scoring == "softmax" else B.MP_SIGMOID
+    lost = ~active.bool()[..., None]
+    masked = torch.where(lost, torch.full_like(ld, -math.inf), ld)
+    _, w, loss = objective_ref(masked, plan.topk_idx, plan.num_tokens_per_expert, plan.num_routed,
+                               mode, True, 1.5, 0.1, zeros((R, N, K)), zeros(R), K)
+    out = torch.zeros((R, N, H), dtype=torch.float64, device=DEV)
+    for k in range(K):
+        e = plan.topk_idx[..., k].long()
+        on = (e >= 0)[..., None]
+        ec = e.clamp(min=0)
+        gu = torch.einsum("rnh,rnih->rni", xd, wgd[ec])
+        a, u = gu.split(I, -1)
+        z = a * torch.sigmoid(a) * u * w[..., k:k + 1]
+        out = out + torch.where(on, torch.einsum("rni,rnhi->rnh", z, wdd[ec]), 0.0)
+    assert torch.allclose(plan.balance_loss.double(), loss, rtol=1e-4)
+
+    def off(got, want):
+        return float((got.double() - want).norm() / want.norm())
+    assert off(plan.out, out.detach()) <= 2.0 ** -4 * math.sqrt(2)
+    total = (out * d_out.double()).sum() + (loss * d_loss.double()).sum()
+    dx, dlog, dwg, dwd = torch.autograd.grad(total, (xd, ld, wgd, wdd))
+    for got, want in ((plan.d_x, dx), (plan.d_w_gate_up, dwg), (plan.d_w_down, dwd)):
+        assert off(got, want) <= 2.0 ** -3
+    live = active.bool()
+    assert float(plan.d_logits[~live].abs().max()) == 0.0
+    assert off(plan.d_logits[live], dlog[live]) <= 2.0 ** -3
+
+
+def test_row_weights_and_back():
+    R, N, K, cap = 2, 50, 3, 200
+    g = gen(32)
+    w = torch.rand((R, N, K), generator=g, device=DEV)
+    slots = torch.randperm(R * N * K, generator=g, device=DEV).to(torch.int32).view(R, N, K)
+    slots[0, 3, 1] = -1
+    rows, back = zeros(cap) - 7, zeros((R, N, K)) - 7
+    B.check(B.mp_ll_row_weights(R, N, K, w, slots, cap, rows))
+    B.check(B.mp_ll_row_weights_backward(R, N, K, rows, cap, slots, back))
+    torch.cuda.synchronize()
+    placed = (slots >= 0) & (slots < cap)
+    want = zeros(cap) - 7
+    want[slots[placed].long()] = w[placed]
+    assert torch.equal(rows, want)
+    assert torch.equal(back, torch.where(placed, w, 0.0))
