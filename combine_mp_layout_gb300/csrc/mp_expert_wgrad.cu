@@ -5,11 +5,15 @@
 //                 (sd[r][n/128] * dy[r][n]) * (sa[r][k/128] * a[r][k])
 //
 // Here the scales change with every step of the reduction, so they cannot be
-// taken out of the tensor core's sum: the rows are dequantised on their way
-// into shared memory.  Each value (e4m3, 4 significant bits, times its fp32
-// scale) is rounded once to bf16 (8 significant bits: an error of at most
-// 2^-8 of the value, where e4m3 itself carries up to 2^-4), the products are
-// exact and summed in fp32 in TMEM over all rows of the expert.
+// taken out of the tensor core's sum: the rows are dequantised to f16 on their
+// way into shared memory.  A code is exact in f16; its scale is divided by a
+// power of two near the largest scale that its channel block has in the expert
+// (so that f16's range does for any scales: full precision down to 2^-19 of the
+// largest) and rounded to f16, and so is their product: 2^-11 each, where the
+// code itself carries up to 2^-4.  Products are exact, sums over the rows fp32
+// in TMEM; the powers of two are put back in fp32 before the one rounding to
+// bf16.  (Against dequantising in fp32 and rounding to bf16 this is eight times
+// as exact and two instructions per pair of values instead of five.)
 //
 // A pair of blocks (cta_group::2) works on 256 x 256 weights: each block
 // dequantises the 128 dy channels of its half of M and the 128 a channels of
@@ -21,8 +25,9 @@
 //
 // Warps of a block: sixteen convert (global memory to registers some stages
 // ahead, across tiles too, then to shared memory), four write finished tiles,
-// one (in the first block) issues the MMAs, and one hands each converted stage
-// over to the tensor core's proxy.  The hand-over is its own because a proxy
+// one (in the first block) issues the MMAs, three look up the largest scales of
+// the tiles to come, and one hands each converted stage over to the tensor
+// core's proxy.  The hand-over is its own because a proxy
 // fence waits for the loads that its thread has in flight: in the converting
 // warps it made every stage as long as a load.
 #include <algorithm>
@@ -47,7 +52,9 @@ constexpr int kWStage = 2 * kWOperand;
 constexpr int kConvWarps = 16;
 constexpr int kPer = kWRows / (kConvWarps * 4);  // rows of each operand per thread and stage
 constexpr int kAhead = 3;           // stages whose global loads are in flight
-constexpr int kWThreads = (kConvWarps + 4 + 2) * 32;  // 4 epilogue warps, MMAs, hand-over
+constexpr int kMmaWarp = kConvWarps + 4, kHandWarp = kMmaWarp + 1, kNormWarp = kMmaWarp + 2;
+constexpr int kWThreads = (kNormWarp + 3) * 32;
+constexpr int kNorms = 4;           // tiles whose powers of two are kept
 constexpr int kLbo = kWRows * 128;  // 64 bf16 channels (128 bytes) of all of a stage's rows
 
 struct WgradArgs {
@@ -64,6 +71,9 @@ struct WgradArgs {
 
 struct WgradTail {
   uint64_t conv[kWStages];          // a block's half of a stage is written
+  uint64_t nfull[kNorms], nempty[kNorms];
+  // powers of two of dy (this block's channels) and a (both blocks'), and back
+  float mul[kNorms][3], back[kNorms][3];
   uint64_t full[kWStages], empty[kWStages], tfull[2], tempty[2];
   uint32_t tmem;
   int failed;
@@ -93,10 +103,10 @@ __device__ __forceinline__ WTile wtile_at(const WgradArgs& p, int t) {
   return w;
 }
 
-// 16 e4m3 values times s, rounded to bf16: 8 words.
+// 16 e4m3 values times s in f16: 8 words.
 __device__ __forceinline__ void dequant16(const uint4& v, float s, uint32_t (&o)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  const float2 s2 = make_float2(s, s);
+  const __half2 s2 = __half2half2(__float2half_rn(s));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t h0, h1;  // f16 pairs: every e4m3 value is exact in f16
@@ -104,10 +114,10 @@ __device__ __forceinline__ void dequant16(const uint4& v, float s, uint32_t (&o)
         " cvt.rn.f16x2.e4m3x2 %0, lo;\n cvt.rn.f16x2.e4m3x2 %1, hi;\n}"
         : "=r"(h0), "=r"(h1)
         : "r"(w[i]));
-    const float2 f0 = mul2(__half22float2(*reinterpret_cast<__half2*>(&h0)), s2);
-    const float2 f1 = mul2(__half22float2(*reinterpret_cast<__half2*>(&h1)), s2);
-    o[2 * i] = pack_bf16x2_rn(f0.x, f0.y);
-    o[2 * i + 1] = pack_bf16x2_rn(f1.x, f1.y);
+    const __half2 p0 = __hmul2(*reinterpret_cast<__half2*>(&h0), s2);
+    const __half2 p1 = __hmul2(*reinterpret_cast<__half2*>(&h1), s2);
+    o[2 * i] = *reinterpret_cast<const uint32_t*>(&p0);
+    o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&p1);
   }
 }
 
@@ -133,6 +143,10 @@ mp_k_expert_wgrad(const WgradArgs p) {
       mbar_init(&tail->full[i], 2);
       mbar_init(&tail->empty[i], 1);
     }
+    for (int i = 0; i < kNorms; ++i) {
+      mbar_init(&tail->nfull[i], 3);
+      mbar_init(&tail->nempty[i], 4);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tail->tfull[i], 1);
       mbar_init(&tail->tempty[i], 2 * 4);
@@ -140,7 +154,7 @@ mp_k_expert_wgrad(const WgradArgs p) {
     tail->failed = 0;
     mbar_init_fence();
   }
-  if (warp == kConvWarps + 4) tmem_alloc<true>(&tail->tmem, 512);
+  if (warp == kMmaWarp) tmem_alloc<true>(&tail->tmem, 512);
   if (p.expert_offsets != nullptr && blockIdx.x == 0) {
     int bad = 0;
     for (int e = threadIdx.x; e < p.E; e += kWThreads) {
@@ -175,8 +189,11 @@ mp_k_expert_wgrad(const WgradArgs p) {
     const float *psd = p.dy_scales, *psa = p.a_scales;
     uint4 v[kAhead][2 * kPer];
     float s[kAhead][2 * kPer];
+    float m[kAhead][2];  // the powers of two of the stage's tile
     bool have[kAhead];
-    auto load = [&](uint4 (&v)[2 * kPer], float (&s)[2 * kPer], bool& have) {
+    float md = 0.0f, ma = 0.0f;
+    uint32_t seen = 0;  // tiles with rows so far
+    auto load = [&](uint4 (&v)[2 * kPer], float (&s)[2 * kPer], float (&m)[2], bool& have) {
       if (row0 >= end) {  // on to the next tile with rows
         WTile w;
         do {
@@ -195,10 +212,17 @@ mp_k_expert_wgrad(const WgradArgs p) {
           pa = p.a + k + c * 16;
           psd = p.dy_scales + n / 128;
           psa = p.a_scales + k / 128;
+          const int slot = seen % kNorms;
+          more = bounded_wait_warp(&tail->nfull[slot], (seen / kNorms) & 1u, failed);
+          md = tail->mul[slot][0];
+          ma = tail->mul[slot][1 + rank];
+          ++seen;
         }
       }
       have = more;
       if (!more) return;
+      m[0] = md;
+      m[1] = ma;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int row = row0 + r + i * (kWRows / kPer);
@@ -213,7 +237,7 @@ mp_k_expert_wgrad(const WgradArgs p) {
       row0 += kWRows;
     };
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) load(v[i], s[i], have[i]);
+    for (int i = 0; i < kAhead; ++i) load(v[i], s[i], m[i], have[i]);
     int slot = 0;
     uint32_t round = 0;
     bool ok = true;
@@ -227,14 +251,14 @@ mp_k_expert_wgrad(const WgradArgs p) {
         uint32_t o[8];
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-          dequant16(v[i][j], s[i][j], o);
+          dequant16(v[i][j], s[i][j] * m[i][0], o);
           store16(td, r + j * (kWRows / kPer), c, o);
-          dequant16(v[i][kPer + j], s[i][kPer + j], o);
+          dequant16(v[i][kPer + j], s[i][kPer + j] * m[i][1], o);
           store16(td + kWOperand, r + j * (kWRows / kPer), c, o);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&tail->conv[slot]);
-        load(v[i], s[i], have[i]);
+        load(v[i], s[i], m[i], have[i]);
         if (++slot == kWStages) {
           slot = 0;
           ++round;
@@ -251,6 +275,14 @@ mp_k_expert_wgrad(const WgradArgs p) {
       const uint32_t buf = nt & 1u;
       if (some && !bounded_wait_idle_warp(&tail->tfull[buf], (nt >> 1) & 1u, failed)) break;
       tcgen05_fence_after();
+      float2 bd = make_float2(0.0f, 0.0f), ba0 = bd, ba1 = bd;  // powers of two to put back
+      if (some) {
+        const int norm = nt % kNorms;
+        if (!bounded_wait_warp(&tail->nfull[norm], (nt / kNorms) & 1u, failed)) break;
+        bd = make_float2(tail->back[norm][0], tail->back[norm][0]);
+        ba0 = make_float2(tail->back[norm][1], tail->back[norm][1]);
+        ba1 = make_float2(tail->back[norm][2], tail->back[norm][2]);
+      }
       const int n = w.n0 + rank * kWC + q * 32 + lane;
       uint16_t* dst = p.dw + (int64_t(w.e) * p.N + n) * p.K + w.k0;
 #pragma unroll
@@ -266,7 +298,10 @@ mp_k_expert_wgrad(const WgradArgs p) {
         if (n < p.N && w.k0 + c * 16 < p.K) {
           Words<8> o;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o.w[j] = pack_bf16x2_rn(v[j].x, v[j].y);
+          for (int j = 0; j < 8; ++j) {
+            const float2 t2 = mul2(mul2(v[j], bd), c < kWC / 16 ? ba0 : ba1);
+            o.w[j] = pack_bf16x2_rn(t2.x, t2.y);
+          }
           if (p.out32) {
             st_stream_w<8>(reinterpret_cast<Words<8>*>(dst + c * 16), o);
           } else {
@@ -279,11 +314,14 @@ mp_k_expert_wgrad(const WgradArgs p) {
       if (some) {
         tcgen05_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_first(&tail->tempty[buf], rank);
+        if (lane == 0) {
+          mbar_arrive_first(&tail->tempty[buf], rank);
+          mbar_arrive(&tail->nempty[nt % kNorms]);
+        }
         ++nt;
       }
     }
-  } else if (warp == kConvWarps + 5) {
+  } else if (warp == kHandWarp) {
     // ---- each stage that this block's warps have written, on to the products
     if (elect_one()) {
       int slot = 0;
@@ -304,9 +342,51 @@ mp_k_expert_wgrad(const WgradArgs p) {
         }
       }
     }
+  } else if (warp >= kNormWarp) {
+    // ---- the power of two of a channel block in the tiles to come: of dy's, or
+    // of one of the two of a.  Scaled by it the block's largest finite scale of
+    // the expert's rows lies in [2^5, 2^6): times 448 it is within f16.
+    const int which = warp - kNormWarp;
+    uint32_t seen = 0;
+    for (int t = first; t < tiles; t += stride) {
+      const WTile w = wtile_at(p, t);
+      if (w.lo == w.hi) continue;
+      const int slot = seen % kNorms;
+      const float* src;
+      int ld;
+      if (which == 0) {
+        src = p.dy_scales + min(w.n0 + rank * kWC, p.N - kWC) / 128;
+        ld = p.N / 128;
+      } else {
+        src = p.a_scales + min(w.k0 + (which - 1) * kWC, p.K - kWC) / 128;
+        ld = p.K / 128;
+      }
+      float top = 0.0f;
+      for (int r0 = w.lo; r0 < w.hi; r0 += 256) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          x[i] = fabsf(__ldg(src + int64_t(min(r0 + i * 32 + lane, w.hi - 1)) * ld));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i] < INFINITY ? x[i] : 0.0f);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      const int ex = max(int(__float_as_uint(top) >> 23) - 127, -121);
+      if (seen >= kNorms &&
+          !bounded_wait_idle_warp(&tail->nempty[slot], (seen / kNorms - 1) & 1u, failed))
+        break;
+      if (lane == 0) {
+        tail->mul[slot][which] = __uint_as_float(uint32_t(132 - ex) << 23);   // 2^(5 - ex)
+        tail->back[slot][which] = __uint_as_float(uint32_t(122 + ex) << 23);  // 2^(ex - 5)
+        mbar_arrive(&tail->nfull[slot]);
+      }
+      __syncwarp();
+      ++seen;
+    }
   } else if (rank == 0 && elect_one()) {
     // ---- products: four K = 16 MMAs a stage into the tile's accumulator
-    constexpr uint32_t idesc = mma_idesc_bf16(2 * kWC, 2 * kWC, true, true);
+    constexpr uint32_t idesc = mma_idesc_f16(2 * kWC, 2 * kWC, true, true);
     uint32_t nt = 0;
     int slot = 0;
     uint32_t round = 0;
@@ -326,7 +406,7 @@ mp_k_expert_wgrad(const WgradArgs p) {
         const uint64_t da = smem_desc_sw128(sd + kWOperand, kLbo, 1024);
 #pragma unroll
         for (int k = 0; k < kWRows / 16; ++k)
-          mma_bf16_pair(tmem + buf * 256, dd + ((k * 16 * 128) >> 4), da + ((k * 16 * 128) >> 4),
+          mma_f16_pair(tmem + buf * 256, dd + ((k * 16 * 128) >> 4), da + ((k * 16 * 128) >> 4),
                         idesc, step > 0 || k > 0);
         mma_commit<true>(&tail->empty[slot]);
         if (++slot == kWStages) {
@@ -347,7 +427,7 @@ mp_k_expert_wgrad(const WgradArgs p) {
   tcgen05_fence_before();
   cluster_sync_all();  // nothing of either block is in use any more
   tcgen05_fence_after();
-  if (warp == kConvWarps + 4) tmem_dealloc<true>(tmem, 512);
+  if (warp == kMmaWarp) tmem_dealloc<true>(tmem, 512);
   if (threadIdx.x == 0 && tail->failed) raise_error(p.dev_err, MP_ERR_TIMEOUT);
 }
 

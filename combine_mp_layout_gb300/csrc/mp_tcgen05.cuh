@@ -216,8 +216,8 @@ __host__ __device__ constexpr uint32_t mma_idesc(int m, int n, uint32_t a_fmt, u
 __host__ __device__ constexpr uint32_t mma_idesc_f8(int m, int n, bool a_mn, bool b_mn) {
   return mma_idesc(m, n, 0u, 0u, a_mn, b_mn);  // e4m3 x e4m3
 }
-__host__ __device__ constexpr uint32_t mma_idesc_bf16(int m, int n, bool a_mn, bool b_mn) {
-  return mma_idesc(m, n, 1u, 1u, a_mn, b_mn);  // bf16 x bf16
+__host__ __device__ constexpr uint32_t mma_idesc_f16(int m, int n, bool a_mn, bool b_mn) {
+  return mma_idesc(m, n, 0u, 0u, a_mn, b_mn);  // f16 x f16 (kind::f16)
 }
 
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -229,7 +229,7 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
       : "memory");
 }
 // Pair only: M = 256 rows in two blocks.
-__device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_f16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                               bool accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"

@@ -759,9 +759,11 @@ int mp_expert_matmul_dgrad_e4m3(int E, int rows, int N, int K, const void *dy,
  * mp_expert_matmul_wgrad_e4m3 -- the gradient of the weights:
  *   dw[e][n][k] = bf16( sum over the rows r of expert e of
  *                       (dy_scales[r][n/128] * dy[r][n]) * (a_scales[r][k/128] * a[r][k]) )
- * each factor rounded to bf16 (8 significant bits; an e4m3 code has 4), the
- * products exact, the sum over rows in fp32.  Experts without rows get zeros
- * (so do, here, those whose offsets decrease; a negative offset counts as 0).
+ * each factor held in f16 (with a power of two per channel block and expert that
+ * makes its range do: a relative error of at most 2^-10 for scales down to 2^-19
+ * of the block's largest), the products exact, the sum over rows in fp32.
+ * Experts without rows get zeros (so do, here, those whose offsets decrease; a
+ * negative offset counts as 0).
  *   out  dw              bf16 [E][N][K]
  * Checks and device errors as mp_expert_matmul_e4m3, with N % 128 == 0 and
  *   E * (N/128) * ceil(K/256) < 2^31.
