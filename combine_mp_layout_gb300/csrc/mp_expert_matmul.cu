@@ -626,9 +626,9 @@ template <bool DGRAD>
 cudaError_t launch_mm(const MMArgs& p, const void* a, const void* w, int K, int red,
                       cudaStream_t st) {
   CUtensorMap mr, ms, mw;
-  if (!make_map_2d(&mr, a, 1, uint64_t(red), uint64_t(p.rows), kBK, kBM) ||
-      !make_map_2d(&ms, a, 1, uint64_t(red), uint64_t(p.rows), kBK, kShortBox) ||
-      !make_map_2d(&mw, w, 1, uint64_t(K), uint64_t(p.E) * p.w_rows, kBK, DGRAD ? kBK : kBN))
+  if (!make_map_bytes(&mr, a, uint64_t(red), uint64_t(p.rows), kBK, kBM) ||
+      !make_map_bytes(&ms, a, uint64_t(red), uint64_t(p.rows), kBK, kShortBox) ||
+      !make_map_bytes(&mw, w, uint64_t(K), uint64_t(p.E) * p.w_rows, kBK, DGRAD ? kBK : kBN))
     return cudaErrorInvalidValue;
   // at most one short tile per expert
   const int64_t row_tiles = std::min<int64_t>(p.rows, int64_t(p.rows) / kBM + p.E);

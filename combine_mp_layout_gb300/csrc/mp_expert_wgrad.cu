@@ -23,9 +23,11 @@
 // much again for the same products.  Both operands are MN-major: a row of
 // channels stays a row in shared memory, nothing is transposed.
 //
-// Warps of a block: sixteen convert (global memory to registers some stages
-// ahead, across tiles too, then to shared memory), four write finished tiles,
-// one (in the first block) issues the MMAs, three look up the largest scales of
+// Warps of a block: one loads rows and scales as they are (TMA, a ring of raw
+// stages: with loads to registers the lines that an SM can have on their way,
+// half of them for a scale each, set the pace), sixteen convert from there,
+// four write finished tiles, one (in the first block) issues the MMAs, three
+// look up the largest scales of
 // the tiles to come, and one hands each converted stage over to the tensor
 // core's proxy.  The hand-over is its own because a proxy
 // fence waits for the loads that its thread has in flight: in the converting
@@ -46,16 +48,19 @@ namespace {
 
 constexpr int kWC = 128;            // dy and a channels per block: one scale block each
 constexpr int kWRows = 64;          // rows per stage: four K = 16 steps of kind::f16
-constexpr int kWStages = 6;
+constexpr int kWStages = 5;
 constexpr int kWOperand = kWRows * kWC * 2;
 constexpr int kWStage = 2 * kWOperand;
 constexpr int kConvWarps = 16;
-constexpr int kPer = kWRows / (kConvWarps * 4);  // rows of each operand per thread and stage
-constexpr int kAhead = 3;           // stages whose global loads are in flight
-constexpr int kMmaWarp = kConvWarps + 4, kHandWarp = kMmaWarp + 1, kNormWarp = kMmaWarp + 2;
-constexpr int kWThreads = (kNormWarp + 3) * 32;
+constexpr int kRaw = 3;             // raw stages: dy and a codes, then their scales
+constexpr int kRawCodes = kWRows * kWC;
+constexpr int kRawScales = kWRows * 16;  // four scales of a row: one TMA box is 16 bytes wide
+constexpr int kRawStage = 2 * (kRawCodes + kRawScales);
+constexpr int kMmaWarp = kConvWarps + 4, kHandWarp = kMmaWarp + 1, kNormWarp = kMmaWarp + 2,
+              kLoadWarp = kNormWarp + 3;
+constexpr int kWThreads = (kLoadWarp + 1) * 32;
 constexpr int kNorms = 4;           // tiles whose powers of two are kept
-constexpr int kLbo = kWRows * 128;  // 64 bf16 channels (128 bytes) of all of a stage's rows
+constexpr int kLbo = kWRows * 128;  // 64 f16 channels (128 bytes) of all of a stage's rows
 
 struct WgradArgs {
   int E, rows, N, K;
@@ -67,9 +72,11 @@ struct WgradArgs {
   uint16_t* dw;
   int32_t* dev_err;
   int out32;                        // dw is 32-byte aligned
+  int tma_scales;                   // both scale arrays can be loaded by TMA
 };
 
 struct WgradTail {
+  uint64_t raw[kRaw], rawfree[kRaw];
   uint64_t conv[kWStages];          // a block's half of a stage is written
   uint64_t nfull[kNorms], nempty[kNorms];
   // powers of two of dy (this block's channels) and a (both blocks'), and back
@@ -78,7 +85,8 @@ struct WgradTail {
   uint32_t tmem;
   int failed;
 };
-constexpr size_t kWSmem = size_t(kWStages) * kWStage + sizeof(WgradTail);
+constexpr size_t kWSmem =
+    size_t(kWStages) * kWStage + size_t(kRaw) * kRawStage + sizeof(WgradTail);
 
 struct WTile {
   int e, lo, hi, n0, k0;  // n0, k0: of the pair
@@ -132,9 +140,13 @@ __device__ __forceinline__ void store16(unsigned char* tile, int r, int c, const
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
-mp_k_expert_wgrad(const WgradArgs p) {
+mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
+                  const __grid_constant__ CUtensorMap map_a,
+                  const __grid_constant__ CUtensorMap map_sd,
+                  const __grid_constant__ CUtensorMap map_sa, const WgradArgs p) {
   extern __shared__ __align__(1024) unsigned char stages[];
-  WgradTail* tail = reinterpret_cast<WgradTail*>(stages + size_t(kWStages) * kWStage);
+  unsigned char* raws = stages + size_t(kWStages) * kWStage;
+  WgradTail* tail = reinterpret_cast<WgradTail*>(raws + size_t(kRaw) * kRawStage);
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const int rank = int(cluster_rank());
   if (threadIdx.x == 0) {
@@ -142,6 +154,10 @@ mp_k_expert_wgrad(const WgradArgs p) {
       mbar_init(&tail->conv[i], kConvWarps);
       mbar_init(&tail->full[i], 2);
       mbar_init(&tail->empty[i], 1);
+    }
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(&tail->raw[i], 1);
+      mbar_init(&tail->rawfree[i], kConvWarps);
     }
     for (int i = 0; i < kNorms; ++i) {
       mbar_init(&tail->nfull[i], 3);
@@ -173,92 +189,66 @@ mp_k_expert_wgrad(const WgradArgs p) {
   volatile int* failed = &tail->failed;
 
   if (warp < kConvWarps) {
-    // ---- rows from global memory, dequantised, into the ring of stages.  A
-    // thread has 16 channels of kPer of a stage's rows of each operand.  There are
-    // no branches in a stage: rows past the expert's last one are read as
-    // the last one, with scale 0, and channels past the matrix as its last block
-    // (nothing of theirs is stored).  (With a branch around each load the
-    // warps, not the products, set the pace: 1,540 clocks a stage.)
+    // ---- raw rows, dequantised, into the ring of stages.  A thread has 16
+    // channels of one row of each operand.  Rows past the expert's last one (of
+    // another expert) count as zeros.  Eight neighbouring lanes have four chunks
+    // of rows r and r ^ 5, whose places differ by both swizzles: no two of them
+    // read or write the same 16-byte bank.
     const int c = (lane & 3) | ((lane >> 1) & 4);
-    const int r = warp * 4 + ((lane >> 2) & 1) + ((lane >> 3) & 2);
+    const int r = (warp >> 1) * 8 + (((warp & 1) + ((lane >> 3) & 2)) ^ (((lane >> 2) & 1) * 5));
     const int nb = p.N / 128, kb = p.K / 128;
-    // where the next loads come from: rows row0 .. of the expert ending at `end`
-    int t = first - stride, row0 = 0, end = 0;
-    bool more = true;
-    const unsigned char *pd = p.dy, *pa = p.a;
-    const float *psd = p.dy_scales, *psa = p.a_scales;
-    uint4 v[kAhead][2 * kPer];
-    float s[kAhead][2 * kPer];
-    float m[kAhead][2];  // the powers of two of the stage's tile
-    bool have[kAhead];
-    float md = 0.0f, ma = 0.0f;
     uint32_t seen = 0;  // tiles with rows so far
-    auto load = [&](uint4 (&v)[2 * kPer], float (&s)[2 * kPer], float (&m)[2], bool& have) {
-      if (row0 >= end) {  // on to the next tile with rows
-        WTile w;
-        do {
-          t += stride;
-          if (t >= tiles) {
-            more = false;
-            break;
-          }
-          w = wtile_at(p, t);
-        } while (w.lo == w.hi);
-        if (more) {
-          row0 = w.lo;
-          end = w.hi;
-          const int n = min(w.n0 + rank * kWC, p.N - kWC), k = min(w.k0 + rank * kWC, p.K - kWC);
-          pd = p.dy + n + c * 16;
-          pa = p.a + k + c * 16;
-          psd = p.dy_scales + n / 128;
-          psa = p.a_scales + k / 128;
-          const int slot = seen % kNorms;
-          more = bounded_wait_warp(&tail->nfull[slot], (seen / kNorms) & 1u, failed);
-          md = tail->mul[slot][0];
-          ma = tail->mul[slot][1 + rank];
-          ++seen;
-        }
-      }
-      have = more;
-      if (!more) return;
-      m[0] = md;
-      m[1] = ma;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int row = row0 + r + i * (kWRows / kPer);
-        const int64_t at = min(row, end - 1);
-        v[i] = __ldg(reinterpret_cast<const uint4*>(pd + at * p.N));
-        v[kPer + i] = __ldg(reinterpret_cast<const uint4*>(pa + at * p.K));
-        const float sd = __ldg(psd + at * nb);
-        const float sk = __ldg(psa + at * kb);
-        s[i] = row < end ? sd : 0.0f;
-        s[kPer + i] = row < end ? sk : 0.0f;
-      }
-      row0 += kWRows;
-    };
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) load(v[i], s[i], m[i], have[i]);
-    int slot = 0;
-    uint32_t round = 0;
+    int slot = 0, rs = 0;
+    uint32_t round = 0, rround = 0;
     bool ok = true;
-    while (ok) {
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        ok = ok && have[i];
-        if (ok && round > 0) ok = bounded_wait_warp(&tail->empty[slot], (round - 1) & 1u, failed);
+    for (int t = first; t < tiles && ok; t += stride) {
+      const WTile w = wtile_at(p, t);
+      if (w.lo == w.hi) continue;
+      const int nblk = min(w.n0 + rank * kWC, p.N - kWC) / 128;
+      const int kblk = min(w.k0 + rank * kWC, p.K - kWC) / 128;
+      const int norm = seen % kNorms;
+      ok = bounded_wait_warp(&tail->nfull[norm], (seen / kNorms) & 1u, failed);
+      if (!ok) break;
+      const float md = tail->mul[norm][0], ma = tail->mul[norm][1 + rank];
+      ++seen;
+      for (int row0 = w.lo; row0 < w.hi; row0 += kWRows) {
+        ok = bounded_wait_warp(&tail->raw[rs], rround & 1u, failed);
         if (!ok) break;
-        unsigned char* td = stages + slot * kWStage;
-        uint32_t o[8];
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          dequant16(v[i][j], s[i][j] * m[i][0], o);
-          store16(td, r + j * (kWRows / kPer), c, o);
-          dequant16(v[i][kPer + j], s[i][kPer + j] * m[i][1], o);
-          store16(td + kWOperand, r + j * (kWRows / kPer), c, o);
+        const unsigned char* src = raws + rs * kRawStage;
+        const int at = r * 128 + ((c ^ (r & 7)) << 4);
+        uint4 vd = *reinterpret_cast<const uint4*>(src + at);
+        uint4 va = *reinterpret_cast<const uint4*>(src + kRawCodes + at);
+        float sd, sa;
+        const int row = row0 + r;
+        if (p.tma_scales) {
+          const float* sc = reinterpret_cast<const float*>(src + 2 * kRawCodes) + r * 4;
+          sd = sc[nblk & 3];
+          sa = sc[kWRows * 4 + (kblk & 3)];
+        } else {
+          const int64_t in = min(row, w.hi - 1);
+          sd = __ldg(p.dy_scales + in * nb + nblk);
+          sa = __ldg(p.a_scales + in * kb + kblk);
+        }
+        if (row0 + kWRows > w.hi && row >= w.hi) {
+          vd = va = make_uint4(0, 0, 0, 0);
+          sd = sa = 0.0f;
         }
         __syncwarp();
+        if (lane == 0) mbar_arrive(&tail->rawfree[rs]);  // (the values are in registers)
+        if (++rs == kRaw) {
+          rs = 0;
+          ++rround;
+        }
+        uint32_t od[8], oa[8];
+        dequant16(vd, sd * md, od);
+        dequant16(va, sa * ma, oa);
+        if (round > 0) ok = bounded_wait_warp(&tail->empty[slot], (round - 1) & 1u, failed);
+        if (!ok) break;
+        unsigned char* dst = stages + slot * kWStage;
+        store16(dst, r, c, od);
+        store16(dst + kWOperand, r, c, oa);
+        __syncwarp();
         if (lane == 0) mbar_arrive(&tail->conv[slot]);
-        load(v[i], s[i], m[i], have[i]);
         if (++slot == kWStages) {
           slot = 0;
           ++round;
@@ -339,6 +329,42 @@ mp_k_expert_wgrad(const WgradArgs p) {
             slot = 0;
             ++round;
           }
+        }
+      }
+    }
+  } else if (warp == kLoadWarp) {
+    // ---- rows and scales as they are, some stages ahead of the conversion
+    if (elect_one()) {
+      int rs = 0;
+      uint32_t rround = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += stride) {
+        const WTile w = wtile_at(p, t);
+        const int n = min(w.n0 + rank * kWC, p.N - kWC), k = min(w.k0 + rank * kWC, p.K - kWC);
+        for (int row0 = w.lo; row0 < w.hi; row0 += kWRows) {
+          if (rround > 0) ok = bounded_wait_idle(&tail->rawfree[rs], (rround - 1) & 1u, failed);
+          if (!ok) break;
+          unsigned char* dst = raws + rs * kRawStage;
+          uint64_t* bar = &tail->raw[rs];
+          mbar_arrive_expect_tx(bar, p.tma_scales ? kRawStage : 2 * kRawCodes);
+          tma_load_2d(dst, &map_dy, n, row0, bar);
+          tma_load_2d(dst + kRawCodes, &map_a, k, row0, bar);
+          if (p.tma_scales) {
+            tma_load_2d(dst + 2 * kRawCodes, &map_sd, (n / 128) & ~3, row0, bar);
+            tma_load_2d(dst + 2 * kRawCodes + kRawScales, &map_sa, (k / 128) & ~3, row0, bar);
+          }
+          if (++rs == kRaw) {
+            rs = 0;
+            ++rround;
+          }
+        }
+      }
+      // every load has landed and been used before the block may end
+      for (int i = 0; i < kRaw; ++i) {
+        if (rround > 0) bounded_wait_idle(&tail->rawfree[rs], (rround - 1) & 1u, failed);
+        if (++rs == kRaw) {
+          rs = 0;
+          ++rround;
         }
       }
     }
@@ -446,6 +472,7 @@ cudaError_t launch_expert_wgrad(int E, int rows, int N, int K, const void* dy,
   p.expert_offsets = expert_offsets;
   p.dw = static_cast<uint16_t*>(dw);
   p.dev_err = dev_err;
+  p.tma_scales = 0;
   static thread_local int configured[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -460,7 +487,21 @@ cudaError_t launch_expert_wgrad(int E, int rows, int N, int K, const void* dy,
   const int64_t tiles = int64_t(E) * ((N + 2 * kWC - 1) / (2 * kWC)) *
                         ((K + 2 * kWC - 1) / (2 * kWC));  // below 2^31: the C ABI checks
   const int pairs = int(std::min<int64_t>(tiles, sm_count() / 2));
-  mp_k_expert_wgrad<<<2 * pairs, kWThreads, kWSmem, st>>>(p);
+  CUtensorMap mdy = {}, ma = {}, msd = {}, msa = {};
+  if (rows > 0) {
+    const int nb = N / 128, kb = K / 128;
+    // TMA wants rows of whole 16 bytes, and a base aligned to them
+    p.tma_scales = nb % 4 == 0 && kb % 4 == 0 &&
+                   ((reinterpret_cast<uintptr_t>(dy_scales) |
+                     reinterpret_cast<uintptr_t>(a_scales)) & 15u) == 0;
+    if (!make_map_bytes(&mdy, dy, uint64_t(N), uint64_t(rows), kWC, kWRows) ||
+        !make_map_bytes(&ma, a, uint64_t(K), uint64_t(rows), kWC, kWRows))
+      return cudaErrorInvalidValue;
+    if (p.tma_scales && (!make_map_f32(&msd, dy_scales, uint64_t(nb), uint64_t(rows), 4, kWRows) ||
+                         !make_map_f32(&msa, a_scales, uint64_t(kb), uint64_t(rows), 4, kWRows)))
+      return cudaErrorInvalidValue;
+  }
+  mp_k_expert_wgrad<<<2 * pairs, kWThreads, kWSmem, st>>>(mdy, ma, msd, msa, p);
   return cudaGetLastError();
 }
 

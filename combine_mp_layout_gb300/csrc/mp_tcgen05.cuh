@@ -12,8 +12,8 @@ namespace mp {
 
 // ---------------------------------------------------------------------------
 // Host: a 2-D tensor map over a dense row-major array (inner extent `cols`
-// elements of `elem` bytes), loaded in boxes of box_cols x box_rows with the
-// 128-byte swizzle.  Elements outside the array read as zero.
+// elements of `elem` bytes), loaded in boxes of box_cols x box_rows.  Elements
+// outside the array read as zero.
 // ---------------------------------------------------------------------------
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -33,19 +33,30 @@ inline EncodeTiledFn encode_tiled() {
   return fn;
 }
 
-inline bool make_map_2d(CUtensorMap* map, const void* base, int elem, uint64_t cols,
-                        uint64_t rows, uint32_t box_cols, uint32_t box_rows) {
+inline bool encode_map_2d(CUtensorMap* map, const void* base, CUtensorMapDataType type, int elem,
+                          uint64_t cols, uint64_t rows, uint32_t box_cols, uint32_t box_rows,
+                          CUtensorMapSwizzle swizzle) {
   const EncodeTiledFn fn = encode_tiled();
   if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {cols * uint64_t(elem)};
   const cuuint32_t box[2] = {box_cols, box_rows};
   const cuuint32_t step[2] = {1, 1};
-  return fn(map,
-            elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-            const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Bytes (e4m3 codes), with the 128-byte swizzle.
+inline bool make_map_bytes(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                           uint32_t box_cols, uint32_t box_rows) {
+  return encode_map_2d(map, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, cols, rows, box_cols, box_rows,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// fp32 values (scales), as they are.
+inline bool make_map_f32(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                         uint32_t box_cols, uint32_t box_rows) {
+  return encode_map_2d(map, base, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, cols, rows, box_cols,
+                       box_rows, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 // ---------------------------------------------------------------------------
