@@ -91,6 +91,16 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
+__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Bounded wait on an mbarrier phase by one thread (2^26 attempts of some 20
 // clocks, about a second); false, with the failure noted in the block's flag,
 // when it gives up.  Every role of a block that waits for another one gives up
@@ -125,10 +135,15 @@ __device__ __forceinline__ bool bounded_wait_idle_warp(uint64_t* bar, uint32_t p
                                                        volatile int* failed) {
   return __all_sync(kFull, bounded_wait_idle(bar, parity, failed));
 }
-// The first form for a whole warp, with one answer for all its lanes.
+// The first form for a whole warp.  The vote in the loop makes the answer, and
+// so the loop itself, the same for all lanes in the compiler's eyes too: the
+// branches after it need no reconvergence.
 __device__ __forceinline__ bool bounded_wait_warp(uint64_t* bar, uint32_t parity,
                                                   volatile int* failed) {
-  return __all_sync(kFull, bounded_wait(bar, parity, failed));
+  for (uint32_t n = 0; n < (1u << 25); ++n)
+    if (__all_sync(kFull, try_wait(bar, parity))) return true;
+  *failed = 1;
+  return false;
 }
 
 __device__ __forceinline__ void tcgen05_fence_before() {
