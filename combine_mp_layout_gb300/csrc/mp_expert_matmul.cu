@@ -43,7 +43,10 @@ constexpr int kMMThreads = (kEpiFirst + kEpiWarps) * 32;
 constexpr int kCols = kBN * 4 / kEpiWarps;  // channels per warp, of 32 rows
 constexpr int kTileRing = 8;         // tiles whose place is kept for the epilogue
 constexpr int kBandRows = 2048;      // rows per band of the tile order
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 4;
+constexpr int kMaxParts = 4;         // blocks that share a tile's reduction: one cluster (of
+                                     // eight, too few fit beside each other: 25 us against
+                                     // 14.5 us for 32 rows x 4096 x 7168)
 constexpr int kMaxSmem = 232448;     // bytes of shared memory a block may have
 
 struct MMArgs {
@@ -457,13 +460,17 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
            i += parts * kEpiWarps * 32) {
         const int row = i / (kBN / 4), c4 = i % (kBN / 4);
         const float4* at = reinterpret_cast<const float4*>(stages) + c4 * kBM + row;
-        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int z = 0; z < parts; ++z) {
-          const float4 v = ld_cluster_f4(map_to_rank(at, z));
-          sum.x += v.x;
-          sum.y += v.y;
-          sum.z += v.z;
-          sum.w += v.w;
+        float4 v[kMaxParts];  // all on their way before the first is needed
+#pragma unroll
+        for (int z = 0; z < kMaxParts; ++z)
+          v[z] = z < parts ? ld_cluster_f4(map_to_rank(at, z)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float4 sum = v[0];
+#pragma unroll
+        for (int z = 1; z < kMaxParts; ++z) {
+          sum.x += v[z].x;
+          sum.y += v[z].y;
+          sum.z += v[z].z;
+          sum.w += v[z].w;
         }
         if (tl.z + c4 * 4 < p.out_cols) {
           uint2 o;
@@ -481,13 +488,14 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
 // A few rows in all (one token, or one token's experts): the weights' bytes are
 // the whole cost, and the tiles above spend longer on their pipeline's start
 // than on the bytes.  A block takes 16 channels of one expert and up to eight
-// rows, its warps every eighth scale block of the reduction.  The products are
+// rows (the MMA's columns), its warps every eighth scale block of the reduction.  The products are
 // mma.m16n8k32 on registers: which channels of a scale block meet in one MMA is
 // free, as long as both operands agree, so a thread's operands are the 16 bytes
 // that it loads.  Each block sum (fp32) is scaled and added up in fp32, the
 // warps' sums are joined in a fixed order.
 // ---------------------------------------------------------------------------
-constexpr int kVecRows = 8;
+constexpr int kVecRows = 8;   // columns of the MMA
+constexpr int kVecMost = 4;   // rows up to which the launcher takes this form
 constexpr int kVecWarps = 8;
 constexpr int kVecAhead = 4;  // scale blocks whose loads are in flight per warp
 
@@ -634,9 +642,10 @@ cudaError_t launch_mm(const MMArgs& p, const void* a, const void* w, int K, int 
   const int64_t row_tiles = std::min<int64_t>(p.rows, int64_t(p.rows) / kBM + p.E);
   const int64_t tiles = row_tiles * ((p.out_cols + kBN - 1) / kBN);
   const int sms = sm_count();
-  // too few tiles for the GPU: up to eight blocks (one cluster) share each
+  // too few tiles for the GPU: up to four blocks (one cluster) share each (nine
+  // rows x 4096 x 7168: 12.5 us, 25.8 us with a block per tile)
   int parts = 1;
-  while (parts < 8 && tiles * parts * 2 <= sms && p.red_blocks >= parts * 4) parts *= 2;
+  while (parts < kMaxParts && tiles * parts * 2 <= sms && p.red_blocks >= parts * 4) parts *= 2;
   if (parts > 1)
     return launch_mm_as<DGRAD, true>(p, mr, ms, mw, int(tiles) * parts, parts, st);
   return launch_mm_as<DGRAD, false>(p, mr, ms, mw, int(std::min<int64_t>(tiles, sms)), 1, st);
@@ -666,7 +675,10 @@ cudaError_t launch_expert_matmul(int E, int rows, int N, int K, bool dgrad, cons
   p.out = static_cast<uint16_t*>(out);
   p.out32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   p.dev_err = dev_err;
-  if (!dgrad && rows <= kVecRows) {
+  // one expert's few rows (4096 x 7168 in the row form, and as tiles: one row 9.4
+  // and 11.5 us, four 10.9 and 12.4 us, eight 14.7 and 12.5 us; eight rows of
+  // seven experts 67 and 38 us)
+  if (!dgrad && rows <= kVecMost && (E == 1 || rows == 1)) {
     mp_k_expert_matvec<<<dim3(unsigned(N / 16), unsigned(expert_offsets ? rows : 1)),
                          kVecWarps * 32, 0, st>>>(p, static_cast<const unsigned char*>(a),
                                                   static_cast<const unsigned char*>(w));
