@@ -48,11 +48,11 @@ namespace {
 
 constexpr int kWC = 128;            // dy and a channels per block: one scale block each
 constexpr int kWRows = 64;          // rows per stage: four K = 16 steps of kind::f16
-constexpr int kWStages = 5;
+constexpr int kWStages = 4;
 constexpr int kWOperand = kWRows * kWC * 2;
 constexpr int kWStage = 2 * kWOperand;
 constexpr int kConvWarps = 16;
-constexpr int kRaw = 3;             // raw stages: dy and a codes, then their scales
+constexpr int kRaw = 5;             // raw stages: dy and a codes, then their scales
 constexpr int kRawCodes = kWRows * kWC;
 constexpr int kRawScales = kWRows * 16;  // four scales of a row: one TMA box is 16 bytes wide
 constexpr int kRawStage = 2 * (kRawCodes + kRawScales);
@@ -151,13 +151,13 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
   const int rank = int(cluster_rank());
   if (threadIdx.x == 0) {
     for (int i = 0; i < kWStages; ++i) {
-      mbar_init(&tail->conv[i], kConvWarps);
+      mbar_init(&tail->conv[i], kConvWarps / 2);
       mbar_init(&tail->full[i], 2);
       mbar_init(&tail->empty[i], 1);
     }
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(&tail->raw[i], 1);
-      mbar_init(&tail->rawfree[i], kConvWarps);
+      mbar_init(&tail->rawfree[i], kConvWarps / 2);
     }
     for (int i = 0; i < kNorms; ++i) {
       mbar_init(&tail->nfull[i], 3);
@@ -189,16 +189,19 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
   volatile int* failed = &tail->failed;
 
   if (warp < kConvWarps) {
-    // ---- raw rows, dequantised, into the ring of stages.  A thread has 16
-    // channels of one row of each operand.  Rows past the expert's last one (of
-    // another expert) count as zeros.  Eight neighbouring lanes have four chunks
-    // of rows r and r ^ 5, whose places differ by both swizzles: no two of them
-    // read or write the same 16-byte bank.
+    // ---- raw rows, dequantised, into the ring of stages.  The warps are two
+    // groups that take alternate stages, a thread with 16 channels of rows r and
+    // r + 32 of each operand: what a stage costs in waits and arrivals is spread
+    // over two stages' time.  Rows past the expert's last one (of another expert)
+    // count as zeros.  Eight neighbouring lanes have four chunks of rows r and
+    // r ^ 5, whose places differ by both swizzles: no two of them read or write
+    // the same 16-byte bank.
+    const int group = warp & 1, gw = warp >> 1;
     const int c = (lane & 3) | ((lane >> 1) & 4);
-    const int r = (warp >> 1) * 8 + (((warp & 1) + ((lane >> 3) & 2)) ^ (((lane >> 2) & 1) * 5));
+    const int r = (gw >> 1) * 8 + (((gw & 1) + ((lane >> 3) & 2)) ^ (((lane >> 2) & 1) * 5));
     const int nb = p.N / 128, kb = p.K / 128;
     uint32_t seen = 0;  // tiles with rows so far
-    int slot = 0, rs = 0;
+    int slot = 0, rs = 0, turn = 0;
     uint32_t round = 0, rround = 0;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += stride) {
@@ -211,44 +214,54 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
       if (!ok) break;
       const float md = tail->mul[norm][0], ma = tail->mul[norm][1 + rank];
       ++seen;
-      for (int row0 = w.lo; row0 < w.hi; row0 += kWRows) {
-        ok = bounded_wait_warp(&tail->raw[rs], rround & 1u, failed);
-        if (!ok) break;
-        const unsigned char* src = raws + rs * kRawStage;
-        const int at = r * 128 + ((c ^ (r & 7)) << 4);
-        uint4 vd = *reinterpret_cast<const uint4*>(src + at);
-        uint4 va = *reinterpret_cast<const uint4*>(src + kRawCodes + at);
-        float sd, sa;
-        const int row = row0 + r;
-        if (p.tma_scales) {
-          const float* sc = reinterpret_cast<const float*>(src + 2 * kRawCodes) + r * 4;
-          sd = sc[nblk & 3];
-          sa = sc[kWRows * 4 + (kblk & 3)];
-        } else {
-          const int64_t in = min(row, w.hi - 1);
-          sd = __ldg(p.dy_scales + in * nb + nblk);
-          sa = __ldg(p.a_scales + in * kb + kblk);
+      for (int row0 = w.lo; row0 < w.hi; row0 += kWRows, turn ^= 1) {
+        if (turn == group) {
+          ok = bounded_wait_warp(&tail->raw[rs], rround & 1u, failed);
+          if (!ok) break;
+          const unsigned char* src = raws + rs * kRawStage;
+          uint4 vd[2], va[2];
+          float sd[2], sa[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int at = (r + 32 * i) * 128 + ((c ^ (r & 7)) << 4);
+            vd[i] = *reinterpret_cast<const uint4*>(src + at);
+            va[i] = *reinterpret_cast<const uint4*>(src + kRawCodes + at);
+            const int row = row0 + r + 32 * i;
+            if (p.tma_scales) {
+              const float* sc = reinterpret_cast<const float*>(src + 2 * kRawCodes) + (r + 32 * i) * 4;
+              sd[i] = sc[nblk & 3];
+              sa[i] = sc[kWRows * 4 + (kblk & 3)];
+            } else {
+              const int64_t in = min(row, w.hi - 1);
+              sd[i] = __ldg(p.dy_scales + in * nb + nblk);
+              sa[i] = __ldg(p.a_scales + in * kb + kblk);
+            }
+            if (row0 + kWRows > w.hi && row >= w.hi) {
+              vd[i] = va[i] = make_uint4(0, 0, 0, 0);
+              sd[i] = sa[i] = 0.0f;
+            }
+          }
+          if (round > 0) ok = bounded_wait_warp(&tail->empty[slot], (round - 1) & 1u, failed);
+          if (!ok) break;
+          unsigned char* dst = stages + slot * kWStage;
+          uint32_t o[8];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            dequant16(vd[i], sd[i] * md, o);
+            store16(dst, r + 32 * i, c, o);
+            dequant16(va[i], sa[i] * ma, o);
+            store16(dst + kWOperand, r + 32 * i, c, o);
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&tail->rawfree[rs]);
+            mbar_arrive(&tail->conv[slot]);
+          }
         }
-        if (row0 + kWRows > w.hi && row >= w.hi) {
-          vd = va = make_uint4(0, 0, 0, 0);
-          sd = sa = 0.0f;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tail->rawfree[rs]);  // (the values are in registers)
         if (++rs == kRaw) {
           rs = 0;
           ++rround;
         }
-        uint32_t od[8], oa[8];
-        dequant16(vd, sd * md, od);
-        dequant16(va, sa * ma, oa);
-        if (round > 0) ok = bounded_wait_warp(&tail->empty[slot], (round - 1) & 1u, failed);
-        if (!ok) break;
-        unsigned char* dst = stages + slot * kWStage;
-        store16(dst, r, c, od);
-        store16(dst + kWOperand, r, c, oa);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tail->conv[slot]);
         if (++slot == kWStages) {
           slot = 0;
           ++round;
