@@ -258,6 +258,30 @@ static inline cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim
   return cudaGetLastError();
 }
 
+// A kernel whose first step is pdl_wait_prior_grid(), launched with programmatic
+// stream serialization: its launch is prepared while the kernel ahead of it on
+// the stream still runs.  `cluster`: blocks per cluster, 0 where the kernel says.
+template <typename... KArgs, typename... Args>
+static inline cudaError_t launch_waiting(void (*kernel)(KArgs...), dim3 grid, dim3 block,
+                                         size_t smem, cudaStream_t stream, unsigned cluster,
+                                         Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 // Bounded spin for the decoupled lookback: about a second at most (2^20
 // polls, back-off capped at ~1 us), then the caller reports MP_ERR_TIMEOUT.
 constexpr uint32_t kSpinLimit = 1u << 20;

@@ -213,6 +213,7 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc<false>(&tail->tmem, 2 * kBN);
+  pdl_wait_prior_grid();  // (nothing of the above touches global memory)
   tile_prefix(p, pre, tail->scan);
   tcgen05_fence_after();
   const uint32_t tmem = tail->tmem;
@@ -516,6 +517,7 @@ mp_k_expert_matvec(const MMArgs p, const unsigned char* __restrict__ a,
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row0 = blockIdx.y;
   int e = 0, nrows = p.rows;
+  pdl_wait_prior_grid();
   if (p.expert_offsets != nullptr) {
     if (threadIdx.x == 0) mine[1] = 0;
     __syncthreads();
@@ -602,19 +604,8 @@ cudaError_t launch_mm_as(MMArgs p, const CUtensorMap& mr, const CUtensorMap& ms,
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured_smem[dev] = smem;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(blocks));
-  cfg.blockDim = dim3(kMMThreads);
-  cfg.dynamicSmemBytes = size_t(smem);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(parts);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = SPLIT ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, mp_k_expert_matmul<DGRAD, SPLIT>, mr, ms, mw, p);
+  return launch_waiting(mp_k_expert_matmul<DGRAD, SPLIT>, dim3(unsigned(blocks)), dim3(kMMThreads),
+                        size_t(smem), st, SPLIT ? unsigned(parts) : 0u, mr, ms, mw, p);
 }
 
 template <bool DGRAD>
@@ -665,10 +656,10 @@ cudaError_t launch_expert_matmul(int E, int rows, int N, int K, bool dgrad, cons
   // one expert's few rows (4096 x 7168 in this form, and as tiles: one row 7.5 and
   // 11.5 us, eight 8.5 and 12.4 us; but eight rows of seven experts 49 and 38 us)
   if (!dgrad && rows <= kVecRows && (E == 1 || rows == 1)) {
-    mp_k_expert_matvec<<<dim3(unsigned(N / 16), unsigned(expert_offsets ? rows : 1)),
-                         kVecWarps * 32, 0, st>>>(p, static_cast<const unsigned char*>(a),
-                                                  static_cast<const unsigned char*>(w));
-    return cudaGetLastError();
+    return launch_waiting(mp_k_expert_matvec,
+                          dim3(unsigned(N / 16), unsigned(expert_offsets ? rows : 1)),
+                          dim3(kVecWarps * 32), 0, st, 0, p, static_cast<const unsigned char*>(a),
+                          static_cast<const unsigned char*>(w));
   }
   return dgrad ? launch_mm<true>(p, a, w, K, red, st) : launch_mm<false>(p, a, w, K, red, st);
 }

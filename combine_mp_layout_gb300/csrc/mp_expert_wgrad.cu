@@ -175,6 +175,7 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
     mbar_init_fence();
   }
   if (warp == kMmaWarp) tmem_alloc<true>(&tail->tmem, 512);
+  pdl_wait_prior_grid();  // (nothing of the above touches global memory)
   if (p.expert_offsets != nullptr && blockIdx.x == 0) {
     int bad = 0;
     for (int e = threadIdx.x; e < p.E; e += kWThreads) {
@@ -518,8 +519,8 @@ cudaError_t launch_expert_wgrad(int E, int rows, int N, int K, const void* dy,
                          !make_map_f32(&msa, a_scales, uint64_t(kb), uint64_t(rows), 4, kWRows)))
       return cudaErrorInvalidValue;
   }
-  mp_k_expert_wgrad<<<2 * pairs, kWThreads, kWSmem, st>>>(mdy, ma, msd, msa, p);
-  return cudaGetLastError();
+  return launch_waiting(mp_k_expert_wgrad, dim3(unsigned(2 * pairs)), dim3(kWThreads), kWSmem, st, 0,
+                        mdy, ma, msd, msa, p);
 }
 
 }  // namespace mp

@@ -248,6 +248,7 @@ mp_k_route(const RouteArgs p) {
   const int team = threadIdx.x / kTeam;
   const int rank = blockIdx.y;
   const int E = p.E, K = p.K;
+  pdl_wait_prior_grid();
   for (int e = threadIdx.x; e < E; e += kRouteThreads) sm_count_[e] = 0;
   if (threadIdx.x == 0) s_routed = 0;
   __syncthreads();
@@ -443,6 +444,7 @@ mp_k_route_backward(const RouteArgs p) {
   const int rank = blockIdx.y;
   const int E = p.E, K = p.K;
   float* g = sm_g + team * E;
+  pdl_wait_prior_grid();
   for (int e = t; e < E; e += kTeam) g[e] = 0.0f;
   float c[V];  // the share's gradient, the same for every routed token of the rank
   {
@@ -542,13 +544,11 @@ cudaError_t launch_route_as(const RouteArgs& p, bool backward, cudaStream_t st) 
   const int64_t need = (int64_t(p.N) + kTeams - 1) / kTeams;
   const int64_t most = std::max<int64_t>(1, int64_t(sm_count()) * (W == 1 ? 4 : 2) / p.R);
   const dim3 grid(unsigned(std::max<int64_t>(1, std::min(need, most))), unsigned(p.R));
-  if (backward) {
-    const size_t smem = size_t(kTeams) * p.E * 4;
-    mp_k_route_backward<T, V, W, SIG><<<grid, kRouteThreads, smem, st>>>(p);
-  } else {
-    mp_k_route<T, V, W, SIG><<<grid, kRouteThreads, size_t(p.E) * 4, st>>>(p);
-  }
-  return cudaGetLastError();
+  if (backward)
+    return launch_waiting(mp_k_route_backward<T, V, W, SIG>, grid, dim3(kRouteThreads),
+                          size_t(kTeams) * p.E * 4, st, 0, p);
+  return launch_waiting(mp_k_route<T, V, W, SIG>, grid, dim3(kRouteThreads), size_t(p.E) * 4, st,
+                        0, p);
 }
 
 template <typename T, bool SIG>

@@ -115,6 +115,7 @@ __device__ __forceinline__ int live_rows(const SwigluArgs& p) {
 template <bool A32>
 __global__ void __launch_bounds__(kSwWarps * kWarp)
 mp_k_swiglu(const SwigluArgs p) {
+  pdl_wait_prior_grid();
   const int lane = threadIdx.x & 31;
   const int spans = (p.I + kSpan - 1) / kSpan;
   const int64_t units = int64_t(live_rows(p)) * spans;
@@ -147,6 +148,7 @@ mp_k_swiglu(const SwigluArgs p) {
 template <bool A32, int WPR>
 __global__ void __launch_bounds__(kSwWarps * kWarp, 8)
 mp_k_swiglu_backward(const SwigluArgs p) {
+  pdl_wait_prior_grid();
   __shared__ float red[2][kSwWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kRows = kSwWarps / WPR;
@@ -213,6 +215,7 @@ template <bool BACK>
 __global__ void __launch_bounds__(256)
 mp_k_ll_row_weights(int64_t slots, int64_t rows, const int32_t* __restrict__ slot_row,
                     const float* __restrict__ in, float* __restrict__ out) {
+  pdl_wait_prior_grid();
   const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (i >= slots) return;
   const int row = __ldg(slot_row + i);
@@ -231,13 +234,14 @@ template <bool A32>
 cudaError_t launch_backward(const SwigluArgs& p, cudaStream_t st) {
   const int spans = (p.I + kSpan - 1) / kSpan;
   const int64_t rows = p.rows;
+  const dim3 block(kSwWarps * kWarp);
   if (spans == 1)
-    mp_k_swiglu_backward<A32, 1><<<grid_for((rows + 3) / 4), kSwWarps * kWarp, 0, st>>>(p);
-  else if (spans == 2)
-    mp_k_swiglu_backward<A32, 2><<<grid_for((rows + 1) / 2), kSwWarps * kWarp, 0, st>>>(p);
-  else
-    mp_k_swiglu_backward<A32, 4><<<grid_for(rows), kSwWarps * kWarp, 0, st>>>(p);
-  return cudaGetLastError();
+    return launch_waiting(mp_k_swiglu_backward<A32, 1>, dim3(grid_for((rows + 3) / 4)), block, 0, st,
+                          0, p);
+  if (spans == 2)
+    return launch_waiting(mp_k_swiglu_backward<A32, 2>, dim3(grid_for((rows + 1) / 2)), block, 0, st,
+                          0, p);
+  return launch_waiting(mp_k_swiglu_backward<A32, 4>, dim3(grid_for(rows)), block, 0, st, 0, p);
 }
 
 }  // namespace
@@ -253,11 +257,8 @@ cudaError_t launch_swiglu(int rows, int I, const void* gate_up, const float* row
   const int64_t units = int64_t(rows) * ((I + kSpan - 1) / kSpan);
   const unsigned blocks = grid_for((units + kSwWarps - 1) / kSwWarps);
   const bool a32 = (reinterpret_cast<uintptr_t>(gate_up) & 31u) == 0;
-  if (a32)
-    mp_k_swiglu<true><<<blocks, kSwWarps * kWarp, 0, st>>>(p);
-  else
-    mp_k_swiglu<false><<<blocks, kSwWarps * kWarp, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_waiting(a32 ? mp_k_swiglu<true> : mp_k_swiglu<false>, dim3(blocks),
+                        dim3(kSwWarps * kWarp), 0, st, 0, p);
 }
 
 cudaError_t launch_swiglu_backward(int rows, int I, const void* gate_up, const float* row_weights,
@@ -281,11 +282,8 @@ cudaError_t launch_ll_row_weights(int64_t slots, int64_t rows, bool back, const 
                                   const float* in, float* out, cudaStream_t st) {
   if (slots == 0) return cudaSuccess;
   const unsigned blocks = unsigned((slots + 255) / 256);
-  if (back)
-    mp_k_ll_row_weights<true><<<blocks, 256, 0, st>>>(slots, rows, slot_row, in, out);
-  else
-    mp_k_ll_row_weights<false><<<blocks, 256, 0, st>>>(slots, rows, slot_row, in, out);
-  return cudaGetLastError();
+  return launch_waiting(back ? mp_k_ll_row_weights<true> : mp_k_ll_row_weights<false>,
+                        dim3(blocks), dim3(256), 0, st, 0, slots, rows, slot_row, in, out);
 }
 
 }  // namespace mp
