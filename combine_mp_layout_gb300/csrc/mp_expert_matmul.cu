@@ -17,8 +17,8 @@
 // owns the lane: with the weights there and the rows as columns, reading a scale
 // per column from shared memory took as long as the products.
 //
-// Warps of a block: one loads (TMA, a ring of stages), one issues the MMAs, two work out the scales of the next steps, the
-// others add up the block sums.
+// Warps of a block: one loads (TMA, a ring of stages), one issues the MMAs, two
+// work out the scales of the next steps, the others add up the block sums.
 #include <algorithm>
 #include <cstdint>
 #include <cuda.h>
@@ -233,143 +233,144 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
   // before them give theirs up (128 * 96 + 256 * 200 is less than the launch's
   // 384 * 168).  Each side has its own end, which keeps the two budgets apart.
   if (warp < kEpiFirst) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-  if (warp == 0) {
-    // ---- loads: one lane keeps the ring of stages full
-    if (elect_one()) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    if (warp == 0) {
+      // ---- loads: one lane keeps the ring of stages full
+      if (elect_one()) {
+        Ring s;
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += step) {
+          const Tile tl = tile_at(p, pre, ncol, t);
+          const int boxes = (tl.nrows + kShortBox - 1) / kShortBox;
+          const uint32_t bytes = uint32_t(boxes) * kShortBox * kBK + kStageW;
+          for (int kb = kb_lo; kb < kb_hi; ++kb, s.next(p.stages)) {
+            if (s.round > 0 &&
+                !bounded_wait_idle(&tail->done[s.slot], (s.round - 1) & 1u, failed)) {
+              ok = false;
+              break;
+            }
+            unsigned char* sr = stages + size_t(s.slot) * kStage;
+            unsigned char* sw = sr + kStageR;
+            uint64_t* ready = &tail->ready[s.slot];
+            mbar_arrive_expect_tx(ready, bytes);
+            if (boxes == kBM / kShortBox) {
+              tma_load_2d(sr, &map_rows, kb * kBK, tl.row0, ready);
+            } else {
+              for (int i = 0; i < boxes; ++i)
+                tma_load_2d(sr + i * kShortBox * kBK, &map_short, kb * kBK,
+                            tl.row0 + i * kShortBox, ready);
+            }
+            if constexpr (DGRAD) {
+#pragma unroll
+              for (int c = 0; c < kBN / 128; ++c)
+                tma_load_2d(sw + c * 128 * kBK, &map_w, tl.col0 + c * 128,
+                            tl.e * p.w_rows + kb * kBK, ready);
+            } else {
+              tma_load_2d(sw, &map_w, kb * kBK, tl.e * p.w_rows + tl.col0, ready);
+            }
+          }
+        }
+        // every load has landed and been used before the block may end
+        for (int i = 0; i < p.stages; ++i, s.next(p.stages))
+          if (s.round > 0) bounded_wait(&tail->done[s.slot], (s.round - 1) & 1u, failed);
+      }
+    } else if (warp == 1) {
+      // ---- products: one lane issues the MMAs of a stage into one of two accumulators
+      if (elect_one()) {
+        constexpr uint32_t idesc = mma_idesc_f8(kBM, kBN, /*a_mn=*/false, /*b_mn=*/DGRAD);
+        Ring s;
+        uint32_t acc = tmem;
+        for (int64_t i = 0; i < steps; ++i, s.next(p.stages), acc ^= kBN) {
+          if (!bounded_wait(&tail->ready[s.slot], s.round & 1u, failed)) break;
+          tcgen05_fence_after();
+          const uint32_t sr = smem_addr(stages + size_t(s.slot) * kStage);
+          const uint64_t dr = smem_desc_sw128(sr, 16, 1024);
+          const uint64_t dw = smem_desc_sw128(sr + kStageR, DGRAD ? 128 * kBK : 16, 1024);
+#pragma unroll
+          for (int k = 0; k < kBK / 32; ++k)
+            mma_f8(acc, dr + ((k * 32) >> 4),
+                   dw + (DGRAD ? ((k * 32 * 128) >> 4) : ((k * 32) >> 4)), idesc, k > 0);
+          mma_commit<false>(&tail->done[s.slot]);
+        }
+      }
+    } else {
+      // ---- scales of the next steps: row times weight scale, this warp for one
+      // half of the channels.  Four steps are loaded at a time, one such group
+      // ahead of the one in use: a row's scales lie red_blocks apart, so every
+      // load is a trip to L2.
+      const int half = warp - 2;
+      const bool vec = p.red_blocks % 4 == 0 && kb_lo % 4 == 0 && kb_hi % 4 == 0 &&
+                       (reinterpret_cast<uintptr_t>(p.a_scales) & 15) == 0;
       Ring s;
+      // a slot's old scales are used up when the step two after theirs, which took
+      // their accumulator over, is done: `behind` is that step
+      Ring behind;
+      behind.slot = 2;
+      int made = 0;
       bool ok = true;
-      for (int t = first; t < tiles && ok; t += step) {
+      for (int t = first; t < tiles && ok; t += step, ++made) {
         const Tile tl = tile_at(p, pre, ncol, t);
-        const int boxes = (tl.nrows + kShortBox - 1) / kShortBox;
-        const uint32_t bytes = uint32_t(boxes) * kShortBox * kBK + kStageW;
-        for (int kb = kb_lo; kb < kb_hi; ++kb, s.next(p.stages)) {
-          if (s.round > 0 && !bounded_wait_idle(&tail->done[s.slot], (s.round - 1) & 1u, failed)) {
-            ok = false;
-            break;
-          }
-          unsigned char* sr = stages + size_t(s.slot) * kStage;
-          unsigned char* sw = sr + kStageR;
-          uint64_t* ready = &tail->ready[s.slot];
-          mbar_arrive_expect_tx(ready, bytes);
-          if (boxes == kBM / kShortBox) {
-            tma_load_2d(sr, &map_rows, kb * kBK, tl.row0, ready);
-          } else {
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d(sr + i * kShortBox * kBK, &map_short, kb * kBK,
-                          tl.row0 + i * kShortBox, ready);
-          }
-          if constexpr (DGRAD) {
+        const float* src[4];
 #pragma unroll
-            for (int c = 0; c < kBN / 128; ++c)
-              tma_load_2d(sw + c * 128 * kBK, &map_w, tl.col0 + c * 128,
-                          tl.e * p.w_rows + kb * kBK, ready);
-          } else {
-            tma_load_2d(sw, &map_w, kb * kBK, tl.e * p.w_rows + tl.col0, ready);
-          }
-        }
-      }
-      // every load has landed and been used before the block may end
-      for (int i = 0; i < p.stages; ++i, s.next(p.stages))
-        if (s.round > 0) bounded_wait(&tail->done[s.slot], (s.round - 1) & 1u, failed);
-    }
-  } else if (warp == 1) {
-    // ---- products: one lane issues the MMAs of a stage into one of two accumulators
-    if (elect_one()) {
-      constexpr uint32_t idesc = mma_idesc_f8(kBM, kBN, /*a_mn=*/false, /*b_mn=*/DGRAD);
-      Ring s;
-      uint32_t acc = tmem;
-      for (int64_t i = 0; i < steps; ++i, s.next(p.stages), acc ^= kBN) {
-        if (!bounded_wait(&tail->ready[s.slot], s.round & 1u, failed)) break;
-        tcgen05_fence_after();
-        const uint32_t sr = smem_addr(stages + size_t(s.slot) * kStage);
-        const uint64_t dr = smem_desc_sw128(sr, 16, 1024);
-        const uint64_t dw = smem_desc_sw128(sr + kStageR, DGRAD ? 128 * kBK : 16, 1024);
+        for (int i = 0; i < 4; ++i)
+          src[i] = p.a_scales + int64_t(tl.row0 + min(lane + i * 32, tl.nrows - 1)) * p.red_blocks;
+        const int cb = min((tl.col0 >> 7) + half, (p.out_cols - 1) >> 7);
+        const float* sw = p.w_scales + tl.e * p.ws_expert + int64_t(cb) * p.ws_out;
+        float ahead[4][4], wahead[4];
+        auto load4 = [&](int kb) {
 #pragma unroll
-        for (int k = 0; k < kBK / 32; ++k)
-          mma_f8(acc, dr + ((k * 32) >> 4),
-                       dw + (DGRAD ? ((k * 32 * 128) >> 4) : ((k * 32) >> 4)), idesc, k > 0);
-        mma_commit<false>(&tail->done[s.slot]);
-      }
-    }
-  } else {
-    // ---- scales of the next steps: row times weight scale, this warp for one
-    // half of the channels.  Four steps are loaded at a time, one such group
-    // ahead of the one in use: a row's scales lie red_blocks apart, so every
-    // load is a trip to L2.
-    const int half = warp - 2;
-    const bool vec = p.red_blocks % 4 == 0 && kb_lo % 4 == 0 && kb_hi % 4 == 0 &&
-                     (reinterpret_cast<uintptr_t>(p.a_scales) & 15) == 0;
-    Ring s;
-    // a slot's old scales are used up when the step two after theirs, which took
-    // their accumulator over, is done: `behind` is that step
-    Ring behind;
-    behind.slot = 2;
-    int made = 0;
-    bool ok = true;
-    for (int t = first; t < tiles && ok; t += step, ++made) {
-      const Tile tl = tile_at(p, pre, ncol, t);
-      const float* src[4];
+          for (int u = 0; u < 4; ++u)
+            wahead[u] = kb + u < kb_hi ? __ldg(sw + int64_t(kb + u) * p.ws_red) : 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        src[i] = p.a_scales + int64_t(tl.row0 + min(lane + i * 32, tl.nrows - 1)) * p.red_blocks;
-      const int cb = min((tl.col0 >> 7) + half, (p.out_cols - 1) >> 7);
-      const float* sw = p.w_scales + tl.e * p.ws_expert + int64_t(cb) * p.ws_out;
-      float ahead[4][4], wahead[4];
-      auto load4 = [&](int kb) {
+          for (int i = 0; i < 4; ++i) {
+            if (vec) {
+              const float4 v = __ldg(reinterpret_cast<const float4*>(src[i] + kb));
+              ahead[i][0] = v.x;
+              ahead[i][1] = v.y;
+              ahead[i][2] = v.z;
+              ahead[i][3] = v.w;
+            } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          wahead[u] = kb + u < kb_hi ? __ldg(sw + int64_t(kb + u) * p.ws_red) : 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (vec) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(src[i] + kb));
-            ahead[i][0] = v.x;
-            ahead[i][1] = v.y;
-            ahead[i][2] = v.z;
-            ahead[i][3] = v.w;
-          } else {
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              ahead[i][u] = kb + u < kb_hi ? __ldg(src[i] + kb + u) : 0.0f;
-          }
-        }
-      };
-      load4(kb_lo);
-      for (int kb0 = kb_lo; kb0 < kb_hi && ok; kb0 += 4) {
-        float v[4][4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[u][i] = ahead[i][u] * wahead[u];
-        if (kb0 + 4 < kb_hi) load4(kb0 + 4);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if (kb0 + u < kb_hi && ok) {
-            if (s.round > 0) {
-              ok = bounded_wait_idle_warp(&tail->done[behind.slot], behind.round & 1u, failed);
-              behind.next(p.stages);
+              for (int u = 0; u < 4; ++u)
+                ahead[i][u] = kb + u < kb_hi ? __ldg(src[i] + kb + u) : 0.0f;
             }
-            if (ok) {
-              // (a tile's place is overwritten kTileRing tiles later, and at most
-              // as many steps as there are stages are prepared ahead)
-              if (kb0 + u == kb_lo && half == 0 && lane == 0)
-                tail->tile[made % kTileRing] = make_int4(tl.row0, tl.nrows, tl.col0, 0);
+          }
+        };
+        load4(kb_lo);
+        for (int kb0 = kb_lo; kb0 < kb_hi && ok; kb0 += 4) {
+          float v[4][4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) tail->scale[s.slot][half][lane + i * 32] = v[u][i];
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&tail->ready[s.slot]);
-              s.next(p.stages);
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[u][i] = ahead[i][u] * wahead[u];
+          if (kb0 + 4 < kb_hi) load4(kb0 + 4);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if (kb0 + u < kb_hi && ok) {
+              if (s.round > 0) {
+                ok = bounded_wait_idle_warp(&tail->done[behind.slot], behind.round & 1u, failed);
+                behind.next(p.stages);
+              }
+              if (ok) {
+                // (a tile's place is overwritten kTileRing tiles later, and at most
+                // as many steps as there are stages are prepared ahead)
+                if (kb0 + u == kb_lo && half == 0 && lane == 0)
+                  tail->tile[made % kTileRing] = make_int4(tl.row0, tl.nrows, tl.col0, 0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tail->scale[s.slot][half][lane + i * 32] = v[u][i];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tail->ready[s.slot]);
+                s.next(p.stages);
+              }
             }
           }
         }
       }
     }
-  }
-  if constexpr (SPLIT) cluster_sync_all();  // (the parts are being joined)
-  block_end<SPLIT>();
-  if (warp == 1) tmem_dealloc<false>(tmem, 2 * kBN);
-  if (threadIdx.x == 0 && tail->failed) raise_error(p.dev_err, MP_ERR_TIMEOUT);
+    if constexpr (SPLIT) cluster_sync_all();  // (the parts are being joined)
+    block_end<SPLIT>();
+    if (warp == 1) tmem_dealloc<false>(tmem, 2 * kBN);
+    if (threadIdx.x == 0 && tail->failed) raise_error(p.dev_err, MP_ERR_TIMEOUT);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---- block sums from TMEM into fp32 registers, then bf16 rows
@@ -464,7 +465,8 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
         float4 v[kMaxParts];  // all on their way before the first is needed
 #pragma unroll
         for (int z = 0; z < kMaxParts; ++z)
-          v[z] = z < parts ? ld_cluster_f4(map_to_rank(at, z)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          v[z] = z < parts ? ld_cluster_f4(map_to_rank(at, z))
+                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         float4 sum = v[0];
 #pragma unroll
         for (int z = 1; z < kMaxParts; ++z) {

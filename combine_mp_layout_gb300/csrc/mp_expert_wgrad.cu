@@ -233,7 +233,8 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
             va[i] = *reinterpret_cast<const uint4*>(src + kRawCodes + at);
             const int row = row0 + r + 32 * i;
             if (p.tma_scales) {
-              const float* sc = reinterpret_cast<const float*>(src + 2 * kRawCodes) + (r + 32 * i) * 4;
+              const float* sc =
+                  reinterpret_cast<const float*>(src + 2 * kRawCodes) + (r + 32 * i) * 4;
               sd[i] = sc[nblk & 3];
               sa[i] = sc[kWRows * 4 + (kblk & 3)];
             } else {
@@ -519,8 +520,8 @@ cudaError_t launch_expert_wgrad(int E, int rows, int N, int K, const void* dy,
                          !make_map_f32(&msa, a_scales, uint64_t(kb), uint64_t(rows), 4, kWRows)))
       return cudaErrorInvalidValue;
   }
-  return launch_waiting(mp_k_expert_wgrad, dim3(unsigned(2 * pairs)), dim3(kWThreads), kWSmem, st, 0,
-                        mdy, ma, msd, msa, p);
+  return launch_waiting(mp_k_expert_wgrad, dim3(unsigned(2 * pairs)), dim3(kWThreads), kWSmem, st,
+                        0, mdy, ma, msd, msa, p);
 }
 
 }  // namespace mp

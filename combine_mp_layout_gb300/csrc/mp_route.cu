@@ -455,7 +455,8 @@ mp_k_route_backward(const RouteArgs p) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int e = j * kTeam + t;
-      c[j] = e < E && p.d_loss != nullptr ? f * float(__ldg(p.counts + int64_t(rank) * E + e)) : 0.0f;
+      c[j] = e < E && p.d_loss != nullptr ? f * float(__ldg(p.counts + int64_t(rank) * E + e))
+                                           : 0.0f;
     }
   }
   if constexpr (W > 1) __syncthreads(); else __syncwarp();

@@ -62,7 +62,9 @@ __device__ __forceinline__ void load16(const uint16_t* p, uint32_t (&w)[8]) {
     }
   }
 }
-__device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  return make_float2(bf16_lo(w), bf16_hi(w));
+}
 
 // 1 / (1 + exp(-x)) of two channels from the fast exponential and reciprocal:
 // a few fp32 ulps, far below the e4m3 rounding that follows.
@@ -236,11 +238,11 @@ cudaError_t launch_backward(const SwigluArgs& p, cudaStream_t st) {
   const int64_t rows = p.rows;
   const dim3 block(kSwWarps * kWarp);
   if (spans == 1)
-    return launch_waiting(mp_k_swiglu_backward<A32, 1>, dim3(grid_for((rows + 3) / 4)), block, 0, st,
-                          0, p);
+    return launch_waiting(mp_k_swiglu_backward<A32, 1>, dim3(grid_for((rows + 3) / 4)), block, 0,
+                          st, 0, p);
   if (spans == 2)
-    return launch_waiting(mp_k_swiglu_backward<A32, 2>, dim3(grid_for((rows + 1) / 2)), block, 0, st,
-                          0, p);
+    return launch_waiting(mp_k_swiglu_backward<A32, 2>, dim3(grid_for((rows + 1) / 2)), block, 0,
+                          st, 0, p);
   return launch_waiting(mp_k_swiglu_backward<A32, 4>, dim3(grid_for(rows)), block, 0, st, 0, p);
 }
 

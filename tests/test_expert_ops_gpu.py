@@ -801,3 +801,98 @@ def test_row_weights_and_back():
     want[slots[placed].long()] = w[placed]
     assert torch.equal(rows, want)
     assert torch.equal(back, torch.where(placed, w, 0.0))
+
+
+# ------------------------------------------------------------------ guard regions
+
+class Guarded:
+    """A buffer between two guard regions of 4 KB; `intact` after the calls."""
+
+    def __init__(self, shape, dtype):
+        n = math.prod(shape) * torch.empty(0, dtype=dtype).element_size()
+        self.raw = torch.full((4096 + n + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+        self.n = n
+        self.t = self.raw[4096:4096 + n].view(dtype).view(shape)
+
+    def intact(self):
+        return bool((self.raw[:4096] == 0x5A).all()) and bool((self.raw[4096 + self.n:] == 0x5A).all())
+
+
+@pytest.mark.parametrize("counts,N,K", [([1], 144, 384), ([5, 0, 130], 272, 128), ([40], 16, 640),
+                                        ([129, 3], 400, 256)])
+def test_products_write_only_their_outputs(counts, N, K):
+    g = gen(41)
+    E, rows = len(counts), sum(counts)
+    n128 = -(-N // 128) * 128
+    a, sa = codes((rows, K), g, False), scales((rows, K // 128), g, False)
+    dy, sd = codes((rows, n128), g, False), scales((rows, n128 // 128), g, False)
+    w, sw = codes((E, N, K), g, False), scales((E, n128 // 128, K // 128), g, False)
+    w2 = codes((E, n128, K), g, False)
+    out, dx = Guarded((rows, N), torch.bfloat16), Guarded((rows, K), torch.bfloat16)
+    dw, err = Guarded((E, n128, K), torch.bfloat16), Guarded((1,), torch.int32)
+    err.t.zero_()
+    off = offsets(counts)
+    B.check(B.mp_expert_matmul_e4m3(E, rows, N, K, a, sa, w, sw, off, out.t, err.t))
+    B.check(B.mp_expert_matmul_dgrad_e4m3(E, rows, n128, K, dy, sd, w2, sw, off, dx.t, err.t))
+    B.check(B.mp_expert_matmul_wgrad_e4m3(E, rows, n128, K, dy, sd, a, sa, off, dw.t, err.t))
+    torch.cuda.synchronize()
+    assert int(err.t) == 0
+    assert all(b.intact() for b in (out, dx, dw, err))
+
+
+@pytest.mark.parametrize("R,N,E,K", [(1, 1, 1, 1), (3, 29, 70, 5), (2, 11, 1500, 32)])
+def test_router_and_activation_write_only_their_outputs(R, N, E, K):
+    g = gen(42)
+    logits = torch.randn((R, N, E), generator=g, device=DEV)
+    f32, i32 = torch.float32, torch.int32
+    ids, w, counts = Guarded((R, N, K), i32), Guarded((R, N, K), f32), Guarded((R, E), i32)
+    routed, loss, err = Guarded((R,), i32), Guarded((R,), f32), Guarded((1,), i32)
+    ws, d = Guarded((B.mp_route_workspace_size(R, N, E),), torch.uint8), Guarded((R, N, E), f32)
+    ws.t.zero_()
+    err.t.zero_()
+    B.check(B.mp_route(R, N, K, E, B.MP_SIGMOID, logits, None, None, True, 1.0, 0.1, ids.t, w.t,
+                       counts.t, routed.t, loss.t, err.t, ws.t))
+    B.check(B.mp_route_backward(R, N, K, E, B.MP_SIGMOID, logits, None, True, 1.0, 0.1, ids.t,
+                                torch.ones_like(w.t), counts.t, routed.t, torch.ones_like(loss.t),
+                                d.t))
+    rows, I = 3 * R, 128 * (1 + N % 7)
+    x = torch.randn((rows, 2 * I), generator=g, device=DEV).bfloat16()
+    f8 = torch.float8_e4m3fn
+    out, sc = Guarded((rows, I), f8), Guarded((rows, I // 128), f32)
+    dg, dsc = Guarded((rows, 2 * I), f8), Guarded((rows, 2 * I // 128), f32)
+    dw = Guarded((rows,), f32)
+    B.check(B.mp_swiglu_e4m3(rows, I, x, None, None, out.t, sc.t))
+    B.check(B.mp_swiglu_backward_e4m3(rows, I, x, None, x[:, :I].contiguous(), None, dg.t, dsc.t,
+                                      dw.t))
+    torch.cuda.synchronize()
+    assert all(b.intact() for b in (ids, w, counts, routed, loss, err, ws, d, out, sc, dg, dsc, dw))
+
+
+def test_products_repeat_bit_for_bit_and_in_a_graph():
+    """No order of blocks changes a bit, and the calls can be captured."""
+    g = gen(43)
+    E, rows, N, K = 3, 333, 512, 1024
+    a, sa = codes((rows, K), g, False), scales((rows, K // 128), g, False)
+    dy, sd = codes((rows, N), g, False), scales((rows, N // 128), g, False)
+    w, sw = codes((E, N, K), g, False), scales((E, N // 128, K // 128), g, False)
+    off, err = offsets([100, 33, 200]), zeros(1, torch.int32)
+    outs = [zeros((rows, N), torch.bfloat16), zeros((rows, K), torch.bfloat16),
+            zeros((E, N, K), torch.bfloat16)]
+
+    def calls():
+        B.check(B.mp_expert_matmul_e4m3(E, rows, N, K, a, sa, w, sw, off, outs[0], err))
+        B.check(B.mp_expert_matmul_dgrad_e4m3(E, rows, N, K, dy, sd, w, sw, off, outs[1], err))
+        B.check(B.mp_expert_matmul_wgrad_e4m3(E, rows, N, K, dy, sd, a, sa, off, outs[2], err))
+    calls()
+    torch.cuda.synchronize()
+    first = [o.clone() for o in outs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, f) for o, f in zip(outs, first))
+    assert int(err) == 0
