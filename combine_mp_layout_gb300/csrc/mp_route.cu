@@ -14,8 +14,8 @@
 // A warp (up to 1,024 experts) or a block of eight warps (beyond) holds one
 // token's logits in registers, V per thread, so they are read once.
 //
-// Measured at 8 x 4,096 tokens, 256 experts, top-8, sigmoid: forward 45 us, gradient
-// 28 us (10 and 14 us of memory traffic are in them at most); 8 tokens of 64 experts
+// Measured at 8 x 4,096 tokens, 256 experts, top-8, sigmoid: forward 34 us, gradient
+// 27 us (10 and 14 us of memory traffic are in them at most); 8 tokens of 64 experts
 // 5.4 us.  The forward pass is bound by instructions: exponential and reciprocal of
 // every score, then sort and rounds (integer compares and selects run at half rate:
 // that pipe is 63% active); about 10 us are launch, block sums and the ranks' ends.
@@ -25,6 +25,7 @@
 // the global sums as fixed-point integers with as many fraction bits as 2^63 /
 // (N + 1) leaves.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -41,6 +42,11 @@ namespace {
 
 constexpr int kRouteWarps = 8;
 constexpr int kRouteThreads = kRouteWarps * kWarp;
+// Up to how many choices candidates are tried first.  8 x 4,096 tokens of 256
+// experts: 8 choices 34 us against 44 us by rounds, 16 38 and 55, 20 50 and 60, but
+// 32 choices 87 and 76 us (nearly all lanes' largest count, and more than 32 keys
+// reach the least of them).
+constexpr int kCandidateTopk = 20;
 
 struct RouteArgs {
   int R, N, K, E;
@@ -230,6 +236,153 @@ __device__ __forceinline__ void load_token(const T* row, int E, int t, float (&x
   }
 }
 
+// Choosing the K largest keys, among equal ones the lowest expert.  A key of -inf
+// is never chosen; the choices are fewer than K if there are no more.
+//
+// A warp per token.  The K-th of the lanes' largest keys is no larger than the K-th
+// of all keys, so the choices are among those that reach it, a few more than K when
+// few lanes hold two of them.  Each of these goes to a lane, in the experts' order,
+// and counts those before it.  Returns the number of choices, or -1 if there are
+// more than 32 candidates.
+template <int V>
+__device__ __forceinline__ int choose_candidates(const float (&key)[V], int K, int lane,
+                                                 float* sm_key, int* sm_expert, int* chosen) {
+  float m = key[0];
+#pragma unroll
+  for (int j = 1; j < V; ++j) m = fmaxf(m, key[j]);
+  float least = -INFINITY;
+  for (int k = 0; k < K; ++k) {  // (equal ones leave together: the bound is lower then)
+    least = warp_max(m);
+    m = m == least ? -INFINITY : m;
+  }
+  least = fmaxf(least, -FLT_MAX);  // -inf is no candidate
+  sm_key[lane] = -INFINITY;
+  __syncwarp();
+  const unsigned below = (1u << lane) - 1u;
+  int c = 0;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const bool in = key[j] >= least;
+    const unsigned b = __ballot_sync(kFull, in);
+    const int at = c + __popc(b & below);
+    if (in && at < kWarp) {
+      sm_key[at] = key[j];
+      sm_expert[at] = j * kWarp + lane;
+    }
+    c += __popc(b);
+  }
+  __syncwarp();
+  if (c > kWarp) return -1;
+  const float k = sm_key[lane];
+  int place = 0;
+  for (int q = 0; q < c; q += 4) {  // (keys past c are -inf)
+    const float4 o = *reinterpret_cast<const float4*>(sm_key + q);
+    place += int(o.x > k) + int(o.y > k) + int(o.z > k) + int(o.w > k);
+  }
+  const unsigned taken = __reduce_or_sync(kFull, lane < c ? 1u << place : 0u);
+  if (__popc(taken) != c) {  // equal keys share a place: the lower expert first
+    for (int q = 0; q < c; ++q) place += int(q < lane && sm_key[q] == k);
+  }
+  if (lane < c && place < K) chosen[place] = sm_expert[lane];
+  return min(c, K);
+}
+
+// The largest of a team's keys that are left (0: none), searched again in the lane
+// that lost one.
+template <int V, int W>
+struct Searched {
+  uint32_t (&key)[V];
+  const int t;
+  uint32_t best = 0;
+  int bestj = 0;
+  __device__ __forceinline__ Searched(uint32_t (&k)[V], int thread) : key(k), t(thread) {
+    search(-1);
+  }
+  __device__ __forceinline__ void search(int gone) {
+    best = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (j == gone) key[j] = 0;
+      if (key[j] > best) { best = key[j]; bestj = j; }
+    }
+  }
+  // the expert, or -1; the same in every thread
+  __device__ __forceinline__ int next(uint32_t* red) {
+    const uint32_t top = team_max<W>(best, red);
+    if (top == 0) return -1;
+    const uint32_t own = uint32_t(bestj * (W * kWarp) + t);
+    const uint32_t e = team_min<W>(best == top ? own : 0xffffffffu, red);
+    if (best == top && own == e) search(bestj);
+    return int(e);
+  }
+};
+
+// A warp per token, in K rounds: for any K and any ties.
+template <int V>
+__device__ __forceinline__ int choose_rounds(const float (&value)[V], int K, int lane,
+                                             int* chosen) {
+  uint32_t key[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) key[j] = value[j] > -INFINITY ? order_key(value[j]) : 0u;
+  int k = 0;
+  if constexpr (V <= 8) {
+    // Each lane sorts its keys once (odd-even transposition: neighbours only, so
+    // equal keys keep their order), then K rounds take the largest head.  Against
+    // searching each lane's keys again in every round this is fewer instructions.
+    uint32_t tag[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) tag[j] = j;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = i & 1; j + 1 < V; j += 2) order2(key[j], tag[j], key[j + 1], tag[j + 1]);
+    uint32_t tags = 0;  // 4 bits each, the head's lowest
+#pragma unroll
+    for (int j = 0; j < V; ++j) tags |= tag[j] << (4 * j);
+    for (; k < K; ++k) {
+      const uint32_t top = __reduce_max_sync(kFull, key[0]);
+      if (top == 0) break;
+      bool won = key[0] == top;
+      const uint32_t e = (tags & 15u) * kWarp + lane;
+      const unsigned heads = __ballot_sync(kFull, won);
+      if (heads & (heads - 1)) {  // (the whole warp is here: the ballot is the same for all)
+        const uint32_t lowest = __reduce_min_sync(kFull, won ? e : 0xffffffffu);
+        won = won && e == lowest;
+      }
+      if (won) chosen[k] = int(e);
+#pragma unroll
+      for (int j = 0; j + 1 < V; ++j) key[j] = won ? key[j + 1] : key[j];
+      key[V - 1] = won ? 0u : key[V - 1];
+      tags = won ? tags >> 4 : tags;
+    }
+  } else {
+    Searched<V, 1> rest(key, lane);
+    for (; k < K; ++k) {
+      const int e = rest.next(nullptr);
+      if (e < 0) break;
+      if (lane == 0) chosen[k] = e;
+    }
+  }
+  return k;
+}
+
+// A block per token: thread k of the first warp gets the k-th choice.
+template <int V, int W>
+__device__ __forceinline__ bool choose_in_block(const float (&value)[V], int K, int t,
+                                                uint32_t* red, int& mine) {
+  uint32_t key[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) key[j] = value[j] > -INFINITY ? order_key(value[j]) : 0u;
+  Searched<V, W> rest(key, t);
+  int k = 0;
+  for (; k < K; ++k) {
+    const int e = rest.next(red);
+    if (e < 0) break;
+    if (t == k) mine = e;
+  }
+  return k > 0;
+}
+
 // grid (blocks per rank, R).  W = 1: a warp per token; W = 8: a block per token.
 template <typename T, int V, int W, bool SIG>
 __global__ void __launch_bounds__(kRouteThreads)
@@ -240,7 +393,9 @@ mp_k_route(const RouteArgs p) {
   __shared__ float red[kRouteWarps];
   __shared__ uint32_t redu[kRouteWarps];
   __shared__ float stage[W == 1 ? kRouteWarps * 256 : 1];
-  __shared__ int sm_chosen[kRouteWarps][MP_MAX_TOPK];
+  __shared__ int sm_chosen[W == 1 ? kRouteWarps : 1][MP_MAX_TOPK];
+  __shared__ __align__(16) float sm_key[W == 1 ? kRouteWarps : 1][kWarp];
+  __shared__ int sm_expert[W == 1 ? kRouteWarps : 1][kWarp];
   __shared__ int s_routed;
   __shared__ int s_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -268,79 +423,30 @@ mp_k_route(const RouteArgs p) {
     sc.compute(x, active, red);
     if (active && !sc.live && t == 0) raise_error(p.dev_err, MP_ERR_BAD_VALUE);
 
-    uint32_t key[V];
+    float key[V];  // -inf where the expert cannot be chosen
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      float k = x[j];
+      key[j] = x[j];
       if constexpr (SIG) {
         const int e = j * kTeam + t;
-        k = sc.s[j] + (p.bias != nullptr && e < E ? __ldg(p.bias + e) : 0.0f);
+        const float k = sc.s[j] + (p.bias != nullptr && e < E ? __ldg(p.bias + e) : 0.0f);
+        key[j] = x[j] > -INFINITY && k > -INFINITY ? k : -INFINITY;
       }
-      key[j] = x[j] > -INFINITY && k > -INFINITY ? order_key(k) : 0u;
     }
     int mine = -1;  // lane k of the (first) warp: the k-th choice
-    bool any = false;
-    if constexpr (W == 1 && V <= 8) {
-      // Each lane sorts its keys once (odd-even transposition: neighbours only,
-      // so equal keys keep their order), then K rounds take the largest head;
-      // among equal heads the lowest expert.  Against searching each lane's keys
-      // again in every round this is fewer instructions, which is what bounds
-      // the kernel.
-      uint32_t tag[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) tag[j] = j;
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int j = i & 1; j + 1 < V; j += 2) order2(key[j], tag[j], key[j + 1], tag[j + 1]);
-      uint32_t tags = 0;  // 4 bits each, the head's lowest
-#pragma unroll
-      for (int j = 0; j < V; ++j) tags |= tag[j] << (4 * j);
+    bool any;
+    if constexpr (W == 1) {
       int* chosen = sm_chosen[warp];
-      int k = 0;
-      for (; k < K; ++k) {
-        const uint32_t top = __reduce_max_sync(kFull, key[0]);
-        if (top == 0) break;
-        bool won = key[0] == top;
-        const uint32_t e = (tags & 15u) * kWarp + lane;
-        const unsigned heads = __ballot_sync(kFull, won);
-        if (heads & (heads - 1)) {  // (the whole warp is here: the ballot is the same for all)
-          const uint32_t lowest = __reduce_min_sync(kFull, won ? e : 0xffffffffu);
-          won = won && e == lowest;
-        }
-        if (won) chosen[k] = int(e);
-#pragma unroll
-        for (int j = 0; j + 1 < V; ++j) key[j] = won ? key[j + 1] : key[j];
-        key[V - 1] = won ? 0u : key[V - 1];
-        tags = won ? tags >> 4 : tags;
-      }
+      int n = -1;
+      if (V > 1 && K <= kCandidateTopk)
+        n = choose_candidates<V>(key, K, lane, sm_key[warp], sm_expert[warp], chosen);
+      if (n < 0) n = choose_rounds<V>(key, K, lane, chosen);
       __syncwarp();
-      if (lane < k) mine = chosen[lane];
+      if (lane < n) mine = chosen[lane];
       __syncwarp();
-      any = k > 0;
+      any = n > 0;
     } else {
-    // K rounds: the largest key, among equals the lowest expert
-    uint32_t best = 0;
-    int bestj = 0;
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (key[j] > best) { best = key[j]; bestj = j; }
-    for (int k = 0; k < K; ++k) {
-      const uint32_t top = team_max<W>(best, redu);
-      if (top == 0) break;
-      any = true;
-      const uint32_t e = team_min<W>(best == top ? uint32_t(bestj * kTeam + t) : 0xffffffffu, redu);
-      if (t == k) mine = int(e);
-      if (best == top && uint32_t(bestj * kTeam + t) == e) {
-        best = 0;
-        const int gone = bestj;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          if (j == gone) key[j] = 0;
-          if (key[j] > best) { best = key[j]; bestj = j; }
-        }
-      }
-    }
+      any = choose_in_block<V, W>(key, K, t, redu, mine);
     }
     if (W == 1 || warp == 0) {
       float w = mine >= 0 ? sc.score_of(load_logit(row + mine)) : 0.0f;

@@ -161,6 +161,44 @@ def test_route(R, N, E, K, scoring, dtype, masked, normalize):
         assert torch.equal(got[k], again[k]), k
 
 
+@pytest.mark.parametrize("E,K", [(33, 1), (64, 6), (64, 20), (64, 21), (100, 20), (256, 8),
+                                 (256, 16), (256, 20), (256, 32), (500, 8), (1024, 8), (1000, 20),
+                                 (1024, 32)])
+def test_route_selection_with_many_equal_keys(E, K):
+    """Rows of few distinct values, from all equal to nearly all different, and rows with their
+    largest keys all in a few lanes: the choices are a stable sort's."""
+    g = gen(5)
+    rows = []
+    for levels in (1, 2, 3, 5, 9, 17, 33, 65, 129, 4097):
+        x = torch.randint(0, levels, (40, E), generator=g, device=DEV).float() - levels // 2
+        rows.append(x * 0.0 if levels == 2 else x / 8)     # (-0 and +0 among them)
+    x = torch.randn((120, E), generator=g, device=DEV)
+    e = torch.arange(E, device=DEV)
+    for i in range(120):                                   # experts e % 32 in one to eight lanes
+        x[i, e % 32 < 1 + i % 8] += 20.0 if i < 60 else 0.5
+    x[torch.rand(x.shape, generator=g, device=DEV) < 0.3] = -math.inf
+    rows.append(x)
+    few = torch.full((40, E), -math.inf, device=DEV)       # fewer experts than choices
+    for i in range(40):
+        few[i, torch.randperm(E, generator=g, device=DEV)[:i % (K + 2)]] = float(i % 3)
+    rows.append(few)
+    x = torch.cat(rows)[None].contiguous()
+    key = torch.where(torch.isnan(x), -math.inf, x)
+    val, order = torch.sort(key + 0.0, dim=-1, descending=True, stable=True)
+    want = torch.where(val[..., :K] > -math.inf, order[..., :K], -1)
+    got = run_route(x, K, B.MP_SOFTMAX)
+    assert torch.equal(got["ids"].long(), want)
+    # sigmoid of 0 everywhere: the bias alone decides, and -inf in it forbids an expert
+    bias = torch.randint(-2, 3, (E,), generator=g, device=DEV).float()
+    bias[torch.rand(E, generator=g, device=DEV) < 0.2] = -math.inf
+    y = torch.where(x > -math.inf, 0.0, x)
+    key = torch.where(y > -math.inf, 0.5 + bias, -math.inf)
+    val, order = torch.sort(key, dim=-1, descending=True, stable=True)
+    want = torch.where(val[..., :K] > -math.inf, order[..., :K], -1)
+    got = run_route(y, K, B.MP_SIGMOID, bias=bias)
+    assert torch.equal(got["ids"].long(), want)
+
+
 def test_route_ties_extremes_and_dead_rows():
     """Equal logits go to the lower expert; the type's lowest value is an ordinary logit, -inf
     never chosen; rows of nothing, of NaN and of +inf are routed nowhere."""
