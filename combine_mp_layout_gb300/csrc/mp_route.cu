@@ -14,11 +14,12 @@
 // A warp (up to 1,024 experts) or a block of eight warps (beyond) holds one
 // token's logits in registers, V per thread, so they are read once.
 //
-// Measured at 8 x 4,096 tokens, 256 experts, top-8, sigmoid: forward 34 us, gradient
+// Measured at 8 x 4,096 tokens, 256 experts, top-8, sigmoid: forward 31 us, gradient
 // 27 us (10 and 14 us of memory traffic are in them at most); 8 tokens of 64 experts
-// 5.4 us.  The forward pass is bound by instructions: exponential and reciprocal of
-// every score, then sort and rounds (integer compares and selects run at half rate:
-// that pipe is 63% active); about 10 us are launch, block sums and the ranks' ends.
+// 5.2 us.  The forward pass is bound by instructions, about 770 per token and warp
+// (71% of the issue slots taken): exponential and reciprocal of every score, the
+// candidates' compares and ballots; about 8 us are launch, block sums and the ranks'
+// ends.
 //
 // The sums over tokens are order-free and so the same on every run: counts are
 // integers, and each block's share sums (fp32, added in a fixed order) enter
@@ -138,6 +139,14 @@ __device__ __forceinline__ float load_logit(const T* p) {
     return __uint_as_float(uint32_t(__ldg(reinterpret_cast<const uint16_t*>(p))) << 16);
 }
 
+template <typename T>
+__device__ __forceinline__ void store_grad(T* p, float v) {
+  if constexpr (std::is_same<T, float>::value)
+    *p = v;
+  else
+    *p = __float2bfloat16_rn(v);
+}
+
 // 1 / (1 + exp(-x)), with a correctly rounded reciprocal: it is part of the
 // selection key, so its last bit can decide.
 __device__ __forceinline__ float sigmoid_exact(float x) { return __frcp_rn(1.0f + expf(-x)); }
@@ -171,7 +180,9 @@ struct TokenScores {
     return x > -INFINITY ? expf(x - m) * inv_total : 0.0f;
   }
 
-  // x: the token's logits, -inf past the last expert
+  // x: the token's logits, -inf past the last expert.  LEFT_OUT: the caller leaves a
+  // token out that is not live; its scores are not to be used.
+  template <bool LEFT_OUT>
   __device__ __forceinline__ void compute(float (&x)[V], bool active, float* red) {
     bool bad = false;
     float mx = -INFINITY;
@@ -199,10 +210,10 @@ struct TokenScores {
       bool far = false;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        if (!live) x[j] = -INFINITY;
-        const float y = 1.0f + expf(-x[j]);
-        far |= y >= 0x1p126f && x[j] > -INFINITY;
-        s[j] = x[j] > -INFINITY ? rcp_mid(y) : 0.0f;
+        if (!LEFT_OUT && !live) x[j] = -INFINITY;
+        const float y = 1.0f + expf(-x[j]);  // +inf: the score is 0
+        s[j] = y < 0x1p126f ? rcp_mid(y) : 0.0f;
+        far |= y >= 0x1p126f && y < INFINITY;
       }
       if (far) {  // logits below about -87
 #pragma unroll
@@ -211,7 +222,7 @@ struct TokenScores {
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        if (!live) x[j] = -INFINITY;
+        if (!LEFT_OUT && !live) x[j] = -INFINITY;
         s[j] = x[j] > -INFINITY ? expf(x[j] - m) : 0.0f;
       }
     }
@@ -229,6 +240,11 @@ struct TokenScores {
 
 template <typename T, int V, int W>
 __device__ __forceinline__ void load_token(const T* row, int E, int t, float (&x)[V]) {
+  if (E == V * W * kWarp) {  // (no comparison per logit then)
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = load_logit(row + j * (W * kWarp) + t);
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int e = j * (W * kWarp) + t;
@@ -242,11 +258,12 @@ __device__ __forceinline__ void load_token(const T* row, int E, int t, float (&x
 // A warp per token.  The K-th of the lanes' largest keys is no larger than the K-th
 // of all keys, so the choices are among those that reach it, a few more than K when
 // few lanes hold two of them.  Each of these goes to a lane, in the experts' order,
-// and counts those before it.  Returns the number of choices, or -1 if there are
-// more than 32 candidates.
+// and counts those before it.  A choice is an expert and its score.  Returns the
+// number of choices, or -1 if there are more than 32 candidates.
 template <int V>
-__device__ __forceinline__ int choose_candidates(const float (&key)[V], int K, int lane,
-                                                 float* sm_key, int* sm_expert, int* chosen) {
+__device__ __forceinline__ int choose_candidates(const float (&key)[V],
+                                                 const float (&score)[V], int K, int lane,
+                                                 float* sm_key, int2* sm_choice, int2* chosen) {
   float m = key[0];
 #pragma unroll
   for (int j = 1; j < V; ++j) m = fmaxf(m, key[j]);
@@ -267,7 +284,7 @@ __device__ __forceinline__ int choose_candidates(const float (&key)[V], int K, i
     const int at = c + __popc(b & below);
     if (in && at < kWarp) {
       sm_key[at] = key[j];
-      sm_expert[at] = j * kWarp + lane;
+      sm_choice[at] = make_int2(j * kWarp + lane, __float_as_int(score[j]));
     }
     c += __popc(b);
   }
@@ -283,7 +300,7 @@ __device__ __forceinline__ int choose_candidates(const float (&key)[V], int K, i
   if (__popc(taken) != c) {  // equal keys share a place: the lower expert first
     for (int q = 0; q < c; ++q) place += int(q < lane && sm_key[q] == k);
   }
-  if (lane < c && place < K) chosen[place] = sm_expert[lane];
+  if (lane < c && place < K) chosen[place] = sm_choice[lane];
   return min(c, K);
 }
 
@@ -317,10 +334,10 @@ struct Searched {
   }
 };
 
-// A warp per token, in K rounds: for any K and any ties.
+// A warp per token, in K rounds: for any K and any ties.  The experts alone.
 template <int V>
 __device__ __forceinline__ int choose_rounds(const float (&value)[V], int K, int lane,
-                                             int* chosen) {
+                                             int2* chosen) {
   uint32_t key[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) key[j] = value[j] > -INFINITY ? order_key(value[j]) : 0u;
@@ -349,7 +366,7 @@ __device__ __forceinline__ int choose_rounds(const float (&value)[V], int K, int
         const uint32_t lowest = __reduce_min_sync(kFull, won ? e : 0xffffffffu);
         won = won && e == lowest;
       }
-      if (won) chosen[k] = int(e);
+      if (won) chosen[k].x = int(e);
 #pragma unroll
       for (int j = 0; j + 1 < V; ++j) key[j] = won ? key[j + 1] : key[j];
       key[V - 1] = won ? 0u : key[V - 1];
@@ -360,7 +377,7 @@ __device__ __forceinline__ int choose_rounds(const float (&value)[V], int K, int
     for (; k < K; ++k) {
       const int e = rest.next(nullptr);
       if (e < 0) break;
-      if (lane == 0) chosen[k] = e;
+      if (lane == 0) chosen[k].x = e;
     }
   }
   return k;
@@ -383,9 +400,15 @@ __device__ __forceinline__ bool choose_in_block(const float (&value)[V], int K, 
   return k > 0;
 }
 
+// Blocks per SM that the registers are to allow.  With a warp per token of 1,024
+// experts two blocks and a few spilled registers (forward 97 us for 8 x 4,096 tokens,
+// top-8, sigmoid, gradient 93 us) beat one block without (147 and 144 us); with up to
+// 256 experts four (80 registers and three blocks: forward 39 us against 31).
+constexpr int route_blocks(int V, int W) { return V <= 8 ? 4 : V == 16 || W == 1 ? 2 : 1; }
+
 // grid (blocks per rank, R).  W = 1: a warp per token; W = 8: a block per token.
 template <typename T, int V, int W, bool SIG>
-__global__ void __launch_bounds__(kRouteThreads)
+__global__ void __launch_bounds__(kRouteThreads, route_blocks(V, W))
 mp_k_route(const RouteArgs p) {
   constexpr int kTeam = W * kWarp;
   constexpr int kTeams = kRouteWarps / W;
@@ -393,9 +416,10 @@ mp_k_route(const RouteArgs p) {
   __shared__ float red[kRouteWarps];
   __shared__ uint32_t redu[kRouteWarps];
   __shared__ float stage[W == 1 ? kRouteWarps * 256 : 1];
-  __shared__ int sm_chosen[W == 1 ? kRouteWarps : 1][MP_MAX_TOPK];
+  __shared__ int2 sm_chosen[W == 1 ? kRouteWarps : 1][MP_MAX_TOPK];
   __shared__ __align__(16) float sm_key[W == 1 ? kRouteWarps : 1][kWarp];
-  __shared__ int sm_expert[W == 1 ? kRouteWarps : 1][kWarp];
+  __shared__ int2 sm_choice[W == 1 ? kRouteWarps : 1][kWarp];
+  __shared__ float sm_bias[W == 1 && SIG ? V * kWarp : 1];
   __shared__ int s_routed;
   __shared__ int s_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -405,6 +429,10 @@ mp_k_route(const RouteArgs p) {
   const int E = p.E, K = p.K;
   pdl_wait_prior_grid();
   for (int e = threadIdx.x; e < E; e += kRouteThreads) sm_count_[e] = 0;
+  if constexpr (W == 1 && SIG) {
+    for (int e = threadIdx.x; e < V * kWarp; e += kRouteThreads)
+      sm_bias[e] = p.bias != nullptr && e < E ? __ldg(p.bias + e) : 0.0f;
+  }
   if (threadIdx.x == 0) s_routed = 0;
   __syncthreads();
 
@@ -420,8 +448,15 @@ mp_k_route(const RouteArgs p) {
     load_token<T, V, W>(row, E, t, x);
     TokenScores<T, V, W, SIG> sc;
     const bool active = p.active == nullptr || p.active[tok] != 0;
-    sc.compute(x, active, red);
+    sc.template compute<W == 1>(x, active, red);
     if (active && !sc.live && t == 0) raise_error(p.dev_err, MP_ERR_BAD_VALUE);
+    if (W == 1 && !sc.live) {
+      if (lane < K) {
+        p.topk_idx[tok * K + lane] = -1;
+        p.topk_weights[tok * K + lane] = 0.0f;
+      }
+      continue;
+    }
 
     float key[V];  // -inf where the expert cannot be chosen
 #pragma unroll
@@ -429,27 +464,34 @@ mp_k_route(const RouteArgs p) {
       key[j] = x[j];
       if constexpr (SIG) {
         const int e = j * kTeam + t;
-        const float k = sc.s[j] + (p.bias != nullptr && e < E ? __ldg(p.bias + e) : 0.0f);
+        const float b = W == 1 ? sm_bias[W == 1 ? e : 0]
+                               : p.bias != nullptr && e < E ? __ldg(p.bias + e) : 0.0f;
+        const float k = sc.s[j] + b;
         key[j] = x[j] > -INFINITY && k > -INFINITY ? k : -INFINITY;
       }
     }
     int mine = -1;  // lane k of the (first) warp: the k-th choice
+    float w = 0.0f;  // its score
     bool any;
     if constexpr (W == 1) {
-      int* chosen = sm_chosen[warp];
+      int2* chosen = sm_chosen[warp];
       int n = -1;
       if (V > 1 && K <= kCandidateTopk)
-        n = choose_candidates<V>(key, K, lane, sm_key[warp], sm_expert[warp], chosen);
-      if (n < 0) n = choose_rounds<V>(key, K, lane, chosen);
+        n = choose_candidates<V>(key, sc.s, K, lane, sm_key[warp], sm_choice[warp], chosen);
+      const bool scored = n >= 0;
+      if (!scored) n = choose_rounds<V>(key, K, lane, chosen);
       __syncwarp();
-      if (lane < n) mine = chosen[lane];
+      if (lane < n) {
+        mine = chosen[lane].x;
+        w = scored ? __int_as_float(chosen[lane].y) : sc.score_of(load_logit(row + mine));
+      }
       __syncwarp();
       any = n > 0;
     } else {
       any = choose_in_block<V, W>(key, K, t, redu, mine);
+      if (warp == 0 && mine >= 0) w = sc.score_of(load_logit(row + mine));
     }
     if (W == 1 || warp == 0) {
-      float w = mine >= 0 ? sc.score_of(load_logit(row + mine)) : 0.0f;
       if (p.normalize) {
         float total = w;
 #pragma unroll
@@ -537,7 +579,7 @@ mp_k_route(const RouteArgs p) {
 //   sigmoid: dl_e = s_e (1 - s_e) ((c_e - sum_j p_j c_j) / sum_j s_j + g_e)
 //   g_k = scale * dw_k, or scale / S * (dw_k - sum_j dw_j s_j / S), S = sum of the chosen s.
 template <typename T, int V, int W, bool SIG>
-__global__ void __launch_bounds__(kRouteThreads)
+__global__ void __launch_bounds__(kRouteThreads, route_blocks(V, W))
 mp_k_route_backward(const RouteArgs p) {
   constexpr int kTeam = W * kWarp;
   constexpr int kTeams = kRouteWarps / W;
@@ -570,11 +612,12 @@ mp_k_route_backward(const RouteArgs p) {
   for (int n = blockIdx.x * kTeams + team; n < p.N; n += gridDim.x * kTeams) {
     const int64_t tok = int64_t(rank) * p.N + n;
     const T* row = static_cast<const T*>(p.logits) + tok * E;
+    T* row_out = static_cast<T*>(p.d_logits) + tok * E;
     float x[V];
     load_token<T, V, W>(row, E, t, x);
     TokenScores<T, V, W, SIG> sc;
     const bool active = p.active == nullptr || p.active[tok] != 0;
-    sc.compute(x, active, red);
+    sc.template compute<false>(x, active, red);
 
     int id = -1;
     bool any;
@@ -624,7 +667,6 @@ mp_k_route_backward(const RouteArgs p) {
     dot = team_reduce<W>(dot, red, OpSum());  // (for W > 1 its barriers follow every read of g)
     if constexpr (W == 1) __syncwarp();
     if ((W == 1 || warp == 0) && id >= 0) g[id] = 0.0f;  // cleared for the next token
-    T* out = static_cast<T*>(p.d_logits) + tok * E;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int e = j * kTeam + t;
@@ -633,12 +675,7 @@ mp_k_route_backward(const RouteArgs p) {
         d = sc.s[j] * (1.0f - sc.s[j]) * (h[j] + ((any ? c[j] : 0.0f) - dot) * sc.inv);
       else
         d = sc.s[j] * (h[j] - dot);
-      if (e < E) {
-        if constexpr (std::is_same<T, float>::value)
-          out[e] = d;
-        else
-          out[e] = __float2bfloat16_rn(d);
-      }
+      if (e < E) store_grad(row_out + e, d);
     }
     if constexpr (W == 1) __syncwarp(); else __syncthreads();
   }
