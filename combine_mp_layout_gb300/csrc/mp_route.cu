@@ -15,7 +15,7 @@
 // token's logits in registers, V per thread, so they are read once.
 //
 // Measured at 8 x 4,096 tokens, 256 experts, top-8, sigmoid: forward 31 us, gradient
-// 27 us (10 and 14 us of memory traffic are in them at most); 8 tokens of 64 experts
+// 26 us (10 and 14 us of memory traffic are in them at most); 8 tokens of 64 experts
 // 5.2 us.  The forward pass is bound by instructions, about 770 per token and warp
 // (71% of the issue slots taken): exponential and reciprocal of every score, the
 // candidates' compares and ballots; about 8 us are launch, block sums and the ranks'
@@ -401,8 +401,8 @@ __device__ __forceinline__ bool choose_in_block(const float (&value)[V], int K, 
 }
 
 // Blocks per SM that the registers are to allow.  With a warp per token of 1,024
-// experts two blocks and a few spilled registers (forward 97 us for 8 x 4,096 tokens,
-// top-8, sigmoid, gradient 93 us) beat one block without (147 and 144 us); with up to
+// experts two blocks and a few spilled registers (forward 96 us for 8 x 4,096 tokens,
+// top-8, sigmoid, gradient 87 us) beat one block without (147 and 144 us); with up to
 // 256 experts four (80 registers and three blocks: forward 39 us against 31).
 constexpr int route_blocks(int V, int W) { return V <= 8 ? 4 : V == 16 || W == 1 ? 2 : 1; }
 
@@ -617,19 +617,25 @@ mp_k_route_backward(const RouteArgs p) {
     load_token<T, V, W>(row, E, t, x);
     TokenScores<T, V, W, SIG> sc;
     const bool active = p.active == nullptr || p.active[tok] != 0;
+    // what the chosen ones' gradients need is on its way while the scores are computed
+    int id = -1;
+    float d = 0.0f, chosen_x = -INFINITY;
+    if ((W == 1 || warp == 0) && lane < K) {
+      id = __ldg(p.topk_idx + tok * K + lane);
+      if (p.d_weights != nullptr) d = __ldg(p.d_weights + tok * K + lane) * p.scale;
+      if (uint32_t(id) >= uint32_t(E)) id = -1;
+      if (id >= 0) chosen_x = load_logit(row + id);
+    }
     sc.template compute<false>(x, active, red);
 
-    int id = -1;
     bool any;
     if (W == 1 || warp == 0) {
-      if (lane < K) id = __ldg(p.topk_idx + tok * K + lane);
-      if (uint32_t(id) >= uint32_t(E)) id = -1;
       any = __any_sync(kFull, id >= 0);
-      float s = 0.0f, d = 0.0f;
-      if (id >= 0 && sc.live) {
-        s = sc.score_of(load_logit(row + id));
-        if (p.d_weights != nullptr) d = __ldg(p.d_weights + tok * K + lane) * p.scale;
-      }
+      float s = 0.0f;
+      if (id >= 0 && sc.live)
+        s = sc.score_of(chosen_x);
+      else
+        d = 0.0f;
       if (p.normalize) {
         float total = s, dot = d * s;
 #pragma unroll
@@ -684,9 +690,11 @@ mp_k_route_backward(const RouteArgs p) {
 template <typename T, int V, int W, bool SIG>
 cudaError_t launch_route_as(const RouteArgs& p, bool backward, cudaStream_t st) {
   constexpr int kTeams = kRouteWarps / W;
-  // enough blocks to fill the GPU a few times over, spread over the ranks
+  // As many blocks as are resident at a time, spread over the ranks.  (Up to 256
+  // experts, forward: four per SM 19 us for 8 x 4,096 tokens of 64, three 20, six 23: a
+  // block's sums at its end cost more than the tokens that it takes over.)
   const int64_t need = (int64_t(p.N) + kTeams - 1) / kTeams;
-  const int64_t most = std::max<int64_t>(1, int64_t(sm_count()) * (W == 1 ? 4 : 2) / p.R);
+  const int64_t most = std::max<int64_t>(1, int64_t(sm_count()) * (W > 1 || V == 32 ? 2 : 4) / p.R);
   const dim3 grid(unsigned(std::max<int64_t>(1, std::min(need, most))), unsigned(p.R));
   if (backward)
     return launch_waiting(mp_k_route_backward<T, V, W, SIG>, grid, dim3(kRouteThreads),
