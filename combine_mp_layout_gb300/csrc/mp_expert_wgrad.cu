@@ -165,7 +165,7 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
     }
     for (int i = 0; i < kNorms; ++i) {
       mbar_init(&tail->nfull[i], 3);
-      mbar_init(&tail->nempty[i], 4);
+      mbar_init(&tail->nempty[i], 4 + kConvWarps);  // every warp that reads the slot
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tail->tfull[i], 1);
@@ -218,6 +218,10 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
       ok = bounded_wait_warp(&tail->nfull[norm], (seen / kNorms) & 1u, failed);
       if (!ok) break;
       const float md = tail->mul[norm][0], ma = tail->mul[norm][1 + rank];
+      // Given back by either group: one without a stage in this tile is waited for by
+      // nothing else, and would find the barrier a phase further.
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tail->nempty[norm]);
       ++seen;
       for (int row0 = w.lo; row0 < w.hi; row0 += kWRows, turn ^= 1) {
         if (turn == group) {
