@@ -761,7 +761,8 @@ int mp_expert_matmul_dgrad_e4m3(int E, int rows, int N, int K, const void *dy,
  *                       (dy_scales[r][n/128] * dy[r][n]) * (a_scales[r][k/128] * a[r][k]) )
  * each factor held in f16 (with a power of two per channel block and expert that
  * makes its range do: a relative error of at most 2^-10 for scales down to 2^-19
- * of the block's largest), the products exact, the sum over rows in fp32.
+ * of the block's largest, blocks of nothing but zeros aside), the products exact,
+ * the sum over rows in fp32.
  * Experts without rows get zeros (so do, here, those whose offsets decrease; a
  * negative offset counts as 0).
  *   out  dw              bf16 [E][N][K]

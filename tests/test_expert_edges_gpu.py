@@ -35,3 +35,70 @@ def test_wgrad_many_tiles_of_one_stage():
     want = wgrad_ref(counts, dy, sd, a, sa).float().bfloat16()
     for _ in range(3):
         assert torch.equal(wgrad(counts, dy, sd, a, sa), want)
+
+
+def wgrad_tolerance(counts, dy, sd, a, sa, want):
+    """Both factors in f16 with a relative error of at most 2^-10, fp32 sums, one rounding to
+    bf16 (as in test_wgrad of the operators' tests)."""
+    size = wgrad_ref(counts, dy.float().abs(), sd, a.float().abs(), sa)
+    n = torch.tensor(counts, device=DEV, dtype=torch.float64)[:, None, None]
+    return (2.0 ** -9 + 2.0 ** -18 + n * 2 * 2.0 ** -24) * size + 2.0 ** -8 * want.abs()
+
+
+@pytest.mark.parametrize("N,K", [(256, 384), (512, 1024)])  # scales by loads, and by TMA
+@pytest.mark.parametrize("dy_exp,a_exp", [(-28, 0), (-45, 3), (0, -30), (-60, -40), (20, 0)])
+@pytest.mark.parametrize("share", [0.02, 0.6])
+def test_wgrad_blocks_of_zeros_cost_the_others_nothing(N, K, dy_exp, a_exp, share):
+    """Quantisers give a block of zeros scale 1, whatever the scales beside it are; a row of a
+    token without a gradient (padding, a masked loss) is all such blocks.  The other rows' scales
+    here lie within 2^5 of one another, so their factors keep their relative error."""
+    g = gen(52)
+    counts = [300, 0, 40, 1, 700, 33]
+    rows = sum(counts)
+    dy, sd = codes((rows, N), g, False), scales((rows, N // 128), g, False) * 2.0 ** dy_exp
+    a, sa = codes((rows, K), g, False), scales((rows, K // 128), g, False) * 2.0 ** a_exp
+
+    def clear(c, s):  # a share of the blocks, at least one per column, -0 codes among them
+        z = torch.rand(s.shape, generator=g, device=DEV) < share
+        z[7] = True
+        z[301] = z[310:330] = True
+        c = c.float().view(rows, -1, 128)
+        sign = torch.randint(0, 2, c.shape, generator=g, device=DEV) * -0.0
+        return (torch.where(z[..., None], sign, c).view(rows, -1).to(torch.float8_e4m3fn),
+                torch.where(z, 1.0, s))
+    dy, sd = clear(dy, sd)
+    a, sa = clear(a, sa)
+    want = wgrad_ref(counts, dy, sd, a, sa)
+    got = wgrad(counts, dy, sd, a, sa).double()
+    assert bool(((got - want).abs() <= wgrad_tolerance(counts, dy, sd, a, sa, want)).all())
+
+
+def test_wgrad_all_zero_rows_and_scales_without_bound():
+    """Blocks of zeros only, with the largest finite scale and with scale 0."""
+    N, K, rows = 256, 256, 80
+    zero = zeros((rows, N), torch.float8_e4m3fn)
+    one = torch.full((rows, K), 1.5, device=DEV).to(torch.float8_e4m3fn)
+    for s in (0.0, 1e-30, 1.0, torch.finfo(torch.float32).max):
+        sd = torch.full((rows, 2), s, device=DEV)
+        assert float(wgrad([rows], zero, sd, one, torch.ones_like(sd)).abs().max()) == 0.0
+    sd[3], dy = 2.0 ** -120, zero.clone()
+    dy[3] = 2.0
+    got = wgrad([rows], dy, sd, one, torch.ones_like(sd))
+    assert bool((got == 3.0 * 2.0 ** -120).all())
+
+
+def test_wgrad_infinite_and_nan_scales_stay_in_their_channel_block():
+    g = gen(53)
+    counts, N, K = [90, 70], 512, 512
+    rows = sum(counts)
+    dy, sd = codes((rows, N), g, True), scales((rows, N // 128), g, True) * 2.0 ** -40
+    a, sa = codes((rows, K), g, True), scales((rows, K // 128), g, True)
+    dy[5], sd[5] = 0.0, 1.0
+    dy[120], sd[120] = 0.0, 1.0
+    clean = wgrad(counts, dy, sd, a, sa)
+    sd[11, 1], sa[20, 2], sd[130, 3] = torch.inf, torch.nan, -torch.inf
+    got = wgrad(counts, dy, sd, a, sa)
+    hit = torch.zeros((2, N, K), dtype=torch.bool, device=DEV)
+    hit[0, 128:256] = hit[0, :, 256:384] = hit[1, 384:] = True
+    assert not bool(got[hit].isfinite().any())
+    assert torch.equal(got[~hit], clean[~hit])
