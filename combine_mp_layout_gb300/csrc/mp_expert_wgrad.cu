@@ -88,7 +88,7 @@ struct WgradTail {
   // powers of two of this block's dy and a channels, and the limits of their scales
   // times these
   struct __align__(16) Norm { float dy, a; __half most_dy, most_a; } norm[kNorms];
-  float back[kNorms][3];            // put back: dy's, and those of both blocks' a
+  int back[kNorms][3];              // exponents to put back: dy's, and both blocks' a's
   int2 queue[3][2 * kWarp];         // rows whose codes are to be looked at, their scales
   uint64_t full[kWStages], empty[kWStages], tfull[2], tempty[2];
   uint32_t tmem;
@@ -380,13 +380,21 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
       const uint32_t buf = nt & 1u;
       if (some && !bounded_wait_idle_warp(&tail->tfull[buf], (nt >> 1) & 1u, failed)) break;
       tcgen05_fence_after();
-      float2 bd = make_float2(0.0f, 0.0f), ba0 = bd, ba1 = bd;  // powers of two to put back
+      // The powers of two to put back, in two factors of the same sign of exponent: one
+      // after the other, dy's and a's could leave fp32's range on the way to a sum that
+      // lies within it.
+      float2 back[2][2] = {};
       if (some) {
         const int norm = nt % kNorms;
         if (!bounded_wait_warp(&tail->nfull[norm], (nt / kNorms) & 1u, failed)) break;
-        bd = make_float2(tail->back[norm][0], tail->back[norm][0]);
-        ba0 = make_float2(tail->back[norm][1], tail->back[norm][1]);
-        ba1 = make_float2(tail->back[norm][2], tail->back[norm][2]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int ex = tail->back[norm][0] + tail->back[norm][1 + h];  // -252 to 244
+          const float f = __uint_as_float(uint32_t(127 + (ex >> 1)) << 23);
+          const float g = __uint_as_float(uint32_t(127 + ex - (ex >> 1)) << 23);
+          back[h][0] = make_float2(f, f);
+          back[h][1] = make_float2(g, g);
+        }
       }
       const int n = w.n0 + rank * kWC + q * 32 + lane;
       uint16_t* dst = p.dw + (int64_t(w.e) * p.N + n) * p.K + w.k0;
@@ -404,7 +412,7 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
           Words<8> o;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float2 t2 = mul2(mul2(v[j], bd), c < kWC / 16 ? ba0 : ba1);
+            const float2 t2 = mul2(mul2(v[j], back[c / (kWC / 16)][0]), back[c / (kWC / 16)][1]);
             o.w[j] = pack_bf16x2_rn(t2.x, t2.y);
           }
           if (p.out32) {
@@ -551,7 +559,7 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
           tail->norm[slot].a = mul;
           tail->norm[slot].most_a = most;
         }
-        tail->back[slot][which] = __uint_as_float(uint32_t(122 + ex) << 23);  // 2^(ex - 5)
+        tail->back[slot][which] = ex - 5;
         mbar_arrive(&tail->nfull[slot]);
       }
       __syncwarp();

@@ -102,3 +102,18 @@ def test_wgrad_infinite_and_nan_scales_stay_in_their_channel_block():
     hit[0, 128:256] = hit[0, :, 256:384] = hit[1, 384:] = True
     assert not bool(got[hit].isfinite().any())
     assert torch.equal(got[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("dy_exp,a_exp", [(120, -120), (-120, 120), (100, -90), (-124, 60),
+                                          (60, -124), (126, -126)])
+def test_wgrad_products_of_far_scales(dy_exp, a_exp):
+    """Scales whose products are ordinary numbers, each one near an end of fp32's range: small
+    whole codes, so every sum is exact."""
+    g = gen(54)
+    counts, N, K = [70, 33], 256, 256
+    rows = sum(counts)
+    dy, a = codes((rows, N), g, True), codes((rows, K), g, True)
+    sd = torch.full((rows, 2), 2.0 ** dy_exp, device=DEV)
+    sa = torch.full((rows, 2), 2.0 ** a_exp, device=DEV)
+    want = wgrad_ref(counts, dy, sd, a, sa).float().bfloat16()
+    assert torch.equal(wgrad(counts, dy, sd, a, sa), want)
