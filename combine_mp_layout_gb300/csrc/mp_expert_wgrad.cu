@@ -79,6 +79,7 @@ struct WgradArgs {
   int32_t* dev_err;
   int out32;                        // dw is 32-byte aligned
   int tma_scales;                   // both scale arrays can be loaded by TMA
+  int patience;                     // of the waits
 };
 
 struct WgradTail {
@@ -154,7 +155,8 @@ __device__ __forceinline__ __half2 limited(float lo, float hi, __half2 most) {
   uint32_t r;
   asm("min.NaN.xorsign.abs.f16x2 %0, %1, %2;"
       : "=r"(r)
-      : "r"(*reinterpret_cast<const uint32_t*>(&s)), "r"(*reinterpret_cast<const uint32_t*>(&most)));
+      : "r"(*reinterpret_cast<const uint32_t*>(&s)),
+        "r"(*reinterpret_cast<const uint32_t*>(&most)));
   return *reinterpret_cast<const __half2*>(&r);
 }
 
@@ -304,12 +306,12 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
       const int nblk = min(w.n0 + rank * kWC, p.N - kWC) / 128;
       const int kblk = min(w.k0 + rank * kWC, p.K - kWC) / 128;
       const int norm = seen % kNorms;
-      ok = bounded_wait_warp(&tail->nfull[norm], (seen / kNorms) & 1u, failed);
+      ok = bounded_wait_warp(&tail->nfull[norm], (seen / kNorms) & 1u, failed, p.patience);
       if (!ok) break;
       ++seen;
       for (int row0 = w.lo; row0 < w.hi; row0 += kWRows, turn ^= 1) {
         if (turn == group) {
-          ok = bounded_wait_warp(&tail->raw[rs], rround & 1u, failed);
+          ok = bounded_wait_warp(&tail->raw[rs], rround & 1u, failed, p.patience);
           if (!ok) break;
           const unsigned char* src = raws + rs * kRawStage;
           uint4 vd[2], va[2];
@@ -335,7 +337,8 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
               sd[i] = sa[i] = 0.0f;
             }
           }
-          if (round > 0) ok = bounded_wait_warp(&tail->empty[slot], (round - 1) & 1u, failed);
+          if (round > 0)
+            ok = bounded_wait_warp(&tail->empty[slot], (round - 1) & 1u, failed, p.patience);
           if (!ok) break;
           unsigned char* dst = stages + slot * kWStage;
           uint32_t o[8];
@@ -378,7 +381,8 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
       const WTile w = wtile_at(p, t);
       const bool some = w.hi > w.lo;
       const uint32_t buf = nt & 1u;
-      if (some && !bounded_wait_idle_warp(&tail->tfull[buf], (nt >> 1) & 1u, failed)) break;
+      if (some && !bounded_wait_idle_warp(&tail->tfull[buf], (nt >> 1) & 1u, failed, p.patience))
+        break;
       tcgen05_fence_after();
       // The powers of two to put back, in two factors of the same sign of exponent: one
       // after the other, dy's and a's could leave fp32's range on the way to a sum that
@@ -386,7 +390,7 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
       float2 back[2][2] = {};
       if (some) {
         const int norm = nt % kNorms;
-        if (!bounded_wait_warp(&tail->nfull[norm], (nt / kNorms) & 1u, failed)) break;
+        if (!bounded_wait_warp(&tail->nfull[norm], (nt / kNorms) & 1u, failed, p.patience)) break;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int ex = tail->back[norm][0] + tail->back[norm][1 + h];  // -252 to 244
@@ -444,7 +448,7 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
         const WTile w = wtile_at(p, t);
         const int steps = (w.hi - w.lo + kWRows - 1) / kWRows;
         for (int step = 0; step < steps; ++step) {
-          ok = bounded_wait(&tail->conv[slot], round & 1u, failed);
+          ok = bounded_wait(&tail->conv[slot], round & 1u, failed, p.patience);
           if (!ok) break;
           fence_proxy_async_smem();
           mbar_arrive_first(&tail->full[slot], rank);
@@ -465,7 +469,8 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
         const WTile w = wtile_at(p, t);
         const int n = min(w.n0 + rank * kWC, p.N - kWC), k = min(w.k0 + rank * kWC, p.K - kWC);
         for (int row0 = w.lo; row0 < w.hi; row0 += kWRows) {
-          if (rround > 0) ok = bounded_wait_idle(&tail->rawfree[rs], (rround - 1) & 1u, failed);
+          if (rround > 0)
+            ok = bounded_wait_idle(&tail->rawfree[rs], (rround - 1) & 1u, failed, p.patience);
           if (!ok) break;
           unsigned char* dst = raws + rs * kRawStage;
           uint64_t* bar = &tail->raw[rs];
@@ -484,7 +489,8 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
       }
       // every load has landed and been used before the block may end
       for (int i = 0; i < kRaw; ++i) {
-        if (rround > 0) bounded_wait_idle(&tail->rawfree[rs], (rround - 1) & 1u, failed);
+        if (rround > 0)
+          bounded_wait_idle(&tail->rawfree[rs], (rround - 1) & 1u, failed, p.patience);
         if (++rs == kRaw) {
           rs = 0;
           ++rround;
@@ -546,7 +552,8 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
       }
       const int ex = max(int(__float_as_uint(top) >> 23) - 127, -121);
       if (seen >= kNorms &&
-          !bounded_wait_idle_warp(&tail->nempty[slot], (seen / kNorms - 1) & 1u, failed))
+          !bounded_wait_idle_warp(&tail->nempty[slot], (seen / kNorms - 1) & 1u, failed,
+                                  p.patience))
         break;
       if (lane == 0) {
         const float mul = __uint_as_float(uint32_t(132 - ex) << 23);          // 2^(5 - ex)
@@ -577,9 +584,9 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
       const int steps = (w.hi - w.lo + kWRows - 1) / kWRows;
       if (steps == 0) continue;
       const uint32_t buf = nt & 1u;
-      if (nt >= 2) ok = bounded_wait(&tail->tempty[buf], ((nt >> 1) - 1) & 1u, failed);
+      if (nt >= 2) ok = bounded_wait(&tail->tempty[buf], ((nt >> 1) - 1) & 1u, failed, p.patience);
       for (int step = 0; step < steps && ok; ++step) {
-        ok = bounded_wait(&tail->full[slot], round & 1u, failed);
+        ok = bounded_wait(&tail->full[slot], round & 1u, failed, p.patience);
         if (!ok) break;
         tcgen05_fence_after();
         const uint32_t sd = smem_addr(stages + slot * kWStage);
@@ -601,7 +608,7 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
     // the last products finish before TMEM is given back
     const int last = slot > 0 ? slot - 1 : kWStages - 1;
     if (slot > 0 || round > 0)
-      bounded_wait(&tail->empty[last], (slot > 0 ? round : round - 1) & 1u, failed);
+      bounded_wait(&tail->empty[last], (slot > 0 ? round : round - 1) & 1u, failed, p.patience);
   }
 
   __syncwarp();
@@ -628,6 +635,9 @@ cudaError_t launch_expert_wgrad(int E, int rows, int N, int K, const void* dy,
   p.dw = static_cast<uint16_t*>(dw);
   p.dev_err = dev_err;
   p.tma_scales = 0;
+  // Roles wait for whole tiles and for the look over a whole expert's scales: 2^21 rows
+  // take 20 ms of products and, if all of them are zeros to look at, about 0.1 s.
+  p.patience = 1 + rows / (1 << 21);
   static thread_local int configured[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

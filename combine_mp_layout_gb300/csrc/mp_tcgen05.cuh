@@ -106,18 +106,22 @@ __device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
 // when it gives up.  Every role of a block that waits for another one gives up
 // by itself.  The loop is three instructions: whatever else it does is added
 // to the time from one role to the next, which the products wait for.
+// `patience`, here and below: how many times as long, where what is waited for
+// takes longer the larger the problem is.
 __device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity,
-                                             volatile int* failed) {
+                                             volatile int* failed, int patience = 1) {
   uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .u32 n;\n mov.u32 n, 0;\n"
-      "$MP_TRY_%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " @p bra $MP_END_%=;\n add.u32 n, n, 1;\n setp.lt.u32 p, n, 67108864;\n"
-      " @p bra $MP_TRY_%=;\n setp.ne.u32 p, n, n;\n"
-      "$MP_END_%=:\n selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
+  do {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+        "$MP_TRY_%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " @p bra $MP_END_%=;\n add.u32 n, n, 1;\n setp.lt.u32 p, n, 67108864;\n"
+        " @p bra $MP_TRY_%=;\n setp.ne.u32 p, n, n;\n"
+        "$MP_END_%=:\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+  } while (!ok && --patience > 0);
   if (!ok) *failed = 1;
   return ok != 0;
 }
@@ -125,23 +129,27 @@ __device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity,
 // between attempts (up to 1 us each), so that they take no issue slots and no
 // turns at the barrier unit from those that are waited for.
 __device__ __forceinline__ bool bounded_wait_idle(uint64_t* bar, uint32_t parity,
-                                                  volatile int* failed) {
-  for (uint32_t n = 0; n < kSpinLimit; ++n)
-    if (mbar_try_wait(bar, parity)) return true;
+                                                  volatile int* failed, int patience = 1) {
+  do {
+    for (uint32_t n = 0; n < kSpinLimit; ++n)
+      if (mbar_try_wait(bar, parity)) return true;
+  } while (--patience > 0);
   *failed = 1;
   return false;
 }
 __device__ __forceinline__ bool bounded_wait_idle_warp(uint64_t* bar, uint32_t parity,
-                                                       volatile int* failed) {
-  return __all_sync(kFull, bounded_wait_idle(bar, parity, failed));
+                                                       volatile int* failed, int patience = 1) {
+  return __all_sync(kFull, bounded_wait_idle(bar, parity, failed, patience));
 }
 // The first form for a whole warp.  The vote in the loop makes the answer, and
 // so the loop itself, the same for all lanes in the compiler's eyes too: the
 // branches after it need no reconvergence.
 __device__ __forceinline__ bool bounded_wait_warp(uint64_t* bar, uint32_t parity,
-                                                  volatile int* failed) {
-  for (uint32_t n = 0; n < (1u << 25); ++n)
-    if (__all_sync(kFull, try_wait(bar, parity))) return true;
+                                                  volatile int* failed, int patience = 1) {
+  do {
+    for (uint32_t n = 0; n < (1u << 25); ++n)
+      if (__all_sync(kFull, try_wait(bar, parity))) return true;
+  } while (--patience > 0);
   *failed = 1;
   return false;
 }

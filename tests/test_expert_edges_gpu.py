@@ -117,3 +117,24 @@ def test_wgrad_products_of_far_scales(dy_exp, a_exp):
     sa = torch.full((rows, 2), 2.0 ** a_exp, device=DEV)
     want = wgrad_ref(counts, dy, sd, a, sa).float().bfloat16()
     assert torch.equal(wgrad(counts, dy, sd, a, sa), want)
+
+
+@pytest.mark.parametrize("rows,dy_exp", [(400_000_000, 0), (60_000_000, -30)])
+def test_wgrad_of_one_expert_with_very_many_rows(rows, dy_exp):
+    """Seconds of work in one tile: no wait for it gives up.  All rows are zeros but for three
+    (scale 1 for the others: with small scales beside it each row's codes have to be looked at)."""
+    need = rows * 2 * (128 + 4) + (2 << 30)
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < need:
+        pytest.skip("needs %d GB of free device memory" % (need >> 30))
+    g = gen(55)
+    at = torch.tensor([0, rows // 3, rows - 1], device=DEV)
+    dy, a = (torch.zeros((rows, 128), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+             for _ in range(2))
+    sd, sa = (torch.ones((rows, 1), device=DEV) for _ in range(2))
+    few = [codes((3, 128), g, True), codes((3, 128), g, True)]
+    dy.view(torch.uint8)[at], a.view(torch.uint8)[at] = (t.view(torch.uint8) for t in few)
+    sd[at] = 2.0 ** dy_exp
+    got = wgrad([rows], dy, sd, a, sa)[0]
+    want = (few[0].double() * 2.0 ** dy_exp).t() @ few[1].double()
+    assert torch.equal(got, want.float().bfloat16())
