@@ -8,14 +8,16 @@
 // taken out of the tensor core's sum: the rows are dequantised to f16 on their
 // way into shared memory.  A code is exact in f16; its scale is divided by a
 // power of two near the largest scale that its channel block has in the expert
-// (so that f16's range does for any scales: full precision down to 2^-19 of the
-// largest) and rounded to f16, and so is their product: 2^-11 each, where the
-// code itself carries up to 2^-4.  Blocks whose codes are all zero do not count
-// for the largest: quantisers give them scale 1, which beside a gradient's small
-// scales would leave these no bits.  Products are exact, sums over the rows fp32
-// in TMEM; the powers of two are put back in fp32 before the one rounding to
-// bf16.  (Against dequantising in fp32 and rounding to bf16 this is eight times
-// as exact and two instructions per pair of values instead of five.)
+// and rounded to f16, and so is their product: 2^-11 each, where the code itself
+// carries up to 2^-4.  That holds within f16's normal range: for every code at
+// scales down to 2^-10 of the largest, for codes from 1 up down to 2^-19; below it
+// the error is half a step of f16's subnormals, 2^-30 of the largest scale.
+// Blocks whose codes are all zero do not count for the largest: quantisers give
+// them scale 1, which beside a gradient's small scales would leave these no bits.
+// Products are exact, sums over the rows fp32 in TMEM; the powers of two are put
+// back in fp32 before the one rounding to bf16.  (Against dequantising in fp32 and
+// rounding to bf16 this is eight times as exact and two instructions per pair of
+// values instead of five.)
 //
 // A pair of blocks (cta_group::2) works on 256 x 256 weights: each block
 // dequantises the 128 dy channels of its half of M and the 128 a channels of

@@ -175,6 +175,10 @@ class MoELayerPlan:
     weights are e4m3 with one fp32 scale per 128 x 128 block: w_gate_up [E][2I][H] (the gate's
     channels first) and w_down [E][H][I].  ``forward`` leaves what ``backward`` needs in the
     plan's buffers.
+
+    The weights' gradients are sums in fp32 of products of e4m3 rows held in f16: relative to
+    the largest scale of their 128 channels in the expert's rows, so rows whose scale is
+    below 2^-19 of it lose bits and below 2^-30 are lost (``mp_expert_matmul_wgrad_e4m3``).
     """
 
     def __init__(self, R: int, N: int, K: int, E: int, H: int, I: int, scoring: str = "softmax",

@@ -759,10 +759,14 @@ int mp_expert_matmul_dgrad_e4m3(int E, int rows, int N, int K, const void *dy,
  * mp_expert_matmul_wgrad_e4m3 -- the gradient of the weights:
  *   dw[e][n][k] = bf16( sum over the rows r of expert e of
  *                       (dy_scales[r][n/128] * dy[r][n]) * (a_scales[r][k/128] * a[r][k]) )
- * each factor held in f16 (with a power of two per channel block and expert that
- * makes its range do: a relative error of at most 2^-10 for scales down to 2^-19
- * of the block's largest, blocks of nothing but zeros aside), the products exact,
- * the sum over rows in fp32.
+ * the products exact, the sum over rows in fp32.  Each factor is held in f16, as
+ * its scale's ratio to a power of two near s, the largest finite scale that its
+ * 128 channels have in the rows of the expert (blocks of nothing but zeros aside):
+ * off by at most 2^-10 of its value (2^-11 for the scale, 2^-11 for the product)
+ * plus 2^-30 s, which only products below 2^-19 s feel; a scale below 2^-19 s is
+ * itself off by up to 2^-30 s, times the code.  So every code keeps its 2^-10 at
+ * scales down to 2^-10 s and codes of 1 and more at scales down to 2^-19 s; a row
+ * whose scale lies below about 2^-30 s is lost, whatever the other factor's is.
  * Experts without rows get zeros (so do, here, those whose offsets decrease; a
  * negative offset counts as 0).
  *   out  dw              bf16 [E][N][K]

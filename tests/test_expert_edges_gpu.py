@@ -138,3 +138,35 @@ def test_wgrad_of_one_expert_with_very_many_rows(rows, dy_exp):
     got = wgrad([rows], dy, sd, a, sa)[0]
     want = (few[0].double() * 2.0 ** dy_exp).t() @ few[1].double()
     assert torch.equal(got, want.float().bfloat16())
+
+
+def test_wgrad_small_codes_at_small_scales():
+    """A factor is off by at most 2^-10 of its value (two roundings of 2^-11, and 2^-22 for
+    their product), 2^-30 of the largest scale for its product, and as much times the code
+    where the scale is below 2^-19 of the largest: both only below f16's normal range.  Each
+    expert has one row that sets the largest scale (its other factor is zero) and one to look at."""
+    U11 = 2.0 ** -11
+    code = torch.tensor([2.0 ** -9, 2.0 ** -6, 9 * 2.0 ** -9, 0.125, 1.0, 1.875, 13.0, 448.0],
+                        device=DEV)
+    ratio = [1.99, 1.37, 1.0, 0.7] + [f * 2.0 ** -k for k in (9, 10, 14, 18, 19, 22, 27, 31)
+                                      for f in (1.0, 1.1, 1.37, 1.93)]
+    E, N, K = len(ratio), 128, 128
+    dy = torch.zeros((E, 2, N), device=DEV)
+    dy[:, 0, 5] = 448.0
+    dy[:, 1] = code.repeat(N // 8)
+    s = torch.ones((E, 2, 1), device=DEV)
+    s[:, 1, 0] = torch.tensor(ratio, device=DEV)
+    a = torch.zeros((E, 2, K), device=DEV)
+    a[:, 1] = 1.0
+    f8 = torch.float8_e4m3fn
+    got = wgrad([2] * E, dy.view(-1, N).to(f8), s.view(-1, 1), a.view(-1, K).to(f8),
+                torch.ones((2 * E, 1), device=DEV)).double()
+    scale, c = s[:, 1].double(), dy[:, 1].to(f8).double()
+    top = s.double().amax(1)
+    want = scale * c
+    err = want * (2 * U11 + U11 * U11)
+    err = torch.where(scale * c < 2.0 ** -18 * top, err + 2.0 ** -30 * top, err)
+    err = torch.where(scale < 2.0 ** -18 * top, err + 2.0 ** -30 * top * c * (1 + U11), err)
+    # one term, so the sum is exact, and rounding to bf16 keeps the order
+    low, high = ((want + d).float().bfloat16().double()[..., None] for d in (-err, err))
+    assert bool(((low <= got) & (got <= high)).all())
