@@ -441,7 +441,8 @@ mp_k_route(const RouteArgs p) {
   for (int j = 0; j < V; ++j) mass[j] = 0.0f;
   int routed = 0;
 
-  for (int n = blockIdx.x * kTeams + team; n < p.N; n += gridDim.x * kTeams) {
+  // (unsigned: the index after the last token may lie past 2^31)
+  for (uint32_t n = blockIdx.x * kTeams + team; n < uint32_t(p.N); n += gridDim.x * kTeams) {
     const int64_t tok = int64_t(rank) * p.N + n;
     const T* row = static_cast<const T*>(p.logits) + tok * E;
     float x[V];
@@ -609,7 +610,7 @@ mp_k_route_backward(const RouteArgs p) {
   }
   if constexpr (W > 1) __syncthreads(); else __syncwarp();
 
-  for (int n = blockIdx.x * kTeams + team; n < p.N; n += gridDim.x * kTeams) {
+  for (uint32_t n = blockIdx.x * kTeams + team; n < uint32_t(p.N); n += gridDim.x * kTeams) {
     const int64_t tok = int64_t(rank) * p.N + n;
     const T* row = static_cast<const T*>(p.logits) + tok * E;
     T* row_out = static_cast<T*>(p.d_logits) + tok * E;

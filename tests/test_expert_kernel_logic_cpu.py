@@ -1,7 +1,12 @@
 """Logic of the expert layer's kernels that can be followed without a GPU, taken from their
-source: the hand-over of shared-memory slots between warps."""
+source: the hand-over of shared-memory slots between warps, and loops at the ends of their
+index types."""
 import os
 import re
+import shutil
+import subprocess
+
+import pytest
 
 from combine_mp_layout_gb300 import _build
 
@@ -63,3 +68,64 @@ def test_wgrad_late_warp_never_misses_a_phase():
                 known.add(s)
                 todo.append(s)
     assert (tiles, tiles, tiles) in known
+
+
+def run_loop(tmp_path, header, index, names, limit, turns):
+    """Runs one of the kernels' loops on the CPU (its `for (...)` as it stands, with the given
+    values for what it names): every index lies in [0, limit), and there are so many of them."""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    values = "\n".join("  %s = %s;" % kv for kv in names.items())
+    text = """#include <cstdint>
+#include <cstdio>
+struct Dim { unsigned x, y; };
+struct Args { int N, I; };
+int main() {
+  Dim blockIdx = {}, gridDim = {};
+  Args p = {};
+  (void)blockIdx; (void)gridDim; (void)p;
+%s
+  long long turns = 0;
+  for (%s) {
+    if ((long long)(%s) < 0 || (long long)(%s) >= %dLL) { std::puts("index out of range"); return 1; }
+    if (++turns > %dLL) { std::puts("does not end"); return 1; }
+  }
+  std::printf("%%lld\\n", turns);
+  return 0;
+}
+""" % (values, header, index, index, limit, turns + 2)
+    src, exe = tmp_path / "loop.cpp", tmp_path / "loop"
+    src.write_text(text)
+    subprocess.run([cxx, "-O1", "-fwrapv", str(src), "-o", str(exe)], check=True,
+                   capture_output=True, text=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, (header, names, r.stdout)
+    assert int(r.stdout) == turns, (header, names)
+
+
+def loops(text, containing):
+    """What stands in the parentheses of the `for` loops that name `containing`."""
+    found = []
+    for m in re.finditer(r"\bfor \(", text):
+        end, depth = m.end(), 1
+        while depth:
+            depth += {"(": 1, ")": -1}.get(text[end], 0)
+            end += 1
+        found.append(" ".join(text[m.end():end - 1].split()))
+    return [h for h in found if containing in h]
+
+
+@pytest.mark.parametrize("N", [0, 1, 4863, 2 ** 31 - 4864, 2 ** 31 - 4000, 2 ** 31 - 1])
+def test_router_token_loops_stay_within_the_tokens(tmp_path, N):
+    """Up to the largest number of tokens that is accepted, for the first and the last warp."""
+    heads = loops(source("mp_route.cu"), "gridDim.x * kTeams")
+    assert len(heads) == 2
+    blocks, teams = 608, 8
+    for header in heads:
+        for block, team in ((0, 0), (blocks - 1, teams - 1)):
+            at = block * teams + team
+            run_loop(tmp_path, header, "n",
+                     {"blockIdx.x": block, "gridDim.x": blocks, "p.N": N,
+                      "const int kTeams": teams, "const int team": team},
+                     N, max(0, -(-(N - at) // (blocks * teams))))
