@@ -119,14 +119,15 @@ __global__ void __launch_bounds__(kSwWarps * kWarp)
 mp_k_swiglu(const SwigluArgs p) {
   pdl_wait_prior_grid();
   const int lane = threadIdx.x & 31;
-  const int spans = (p.I + kSpan - 1) / kSpan;
+  const int spans = (p.I - 1) / kSpan + 1;
   const int64_t units = int64_t(live_rows(p)) * spans;
   const int64_t nw = int64_t(gridDim.x) * kSwWarps;
   for (int64_t unit = int64_t(blockIdx.x) * kSwWarps + (threadIdx.x >> 5); unit < units;
        unit += nw) {
     const int64_t row = unit / spans;
-    const int ch = int(unit - row * spans) * kSpan + lane * kCPL;
-    const bool valid = ch < p.I;
+    // (unsigned, here and below: the channels after a row's last may lie past 2^31)
+    const uint32_t ch = uint32_t(unit - row * spans) * kSpan + lane * kCPL;
+    const bool valid = ch < uint32_t(p.I);
     uint32_t g[kCPL / 2] = {}, u[kCPL / 2] = {};
     if (valid) {
       const uint16_t* src = p.gate_up + row * 2 * p.I + ch;
@@ -163,9 +164,9 @@ mp_k_swiglu_backward(const SwigluArgs p) {
     const float w = live && p.row_weights != nullptr ? __ldg(p.row_weights + row) : 1.0f;
     const float2 w2 = make_float2(w, w), one = make_float2(1.0f, 1.0f);
     float2 dw = make_float2(0.0f, 0.0f);
-    for (int c0 = (warp % WPR) * kSpan; live && c0 < p.I; c0 += WPR * kSpan) {
-      const int ch = c0 + lane * kCPL;
-      const bool valid = ch < p.I;
+    for (uint32_t c0 = (warp % WPR) * kSpan; live && c0 < uint32_t(p.I); c0 += WPR * kSpan) {
+      const uint32_t ch = c0 + lane * kCPL;
+      const bool valid = ch < uint32_t(p.I);
       uint32_t g[kCPL / 2] = {}, u[kCPL / 2] = {}, d[kCPL / 2] = {};
       if (valid) {
         const uint16_t* src = p.gate_up + row * 2 * p.I + ch;
@@ -234,7 +235,7 @@ unsigned grid_for(int64_t blocks) {
 
 template <bool A32>
 cudaError_t launch_backward(const SwigluArgs& p, cudaStream_t st) {
-  const int spans = (p.I + kSpan - 1) / kSpan;
+  const int spans = (p.I - 1) / kSpan + 1;
   const int64_t rows = p.rows;
   const dim3 block(kSwWarps * kWarp);
   if (spans == 1)
@@ -256,7 +257,7 @@ cudaError_t launch_swiglu(int rows, int I, const void* gate_up, const float* row
   p.gate_up = static_cast<const uint16_t*>(gate_up);
   p.row_weights = row_weights; p.num_rows = num_rows;
   p.out = static_cast<unsigned char*>(out); p.out_scales = out_scales;
-  const int64_t units = int64_t(rows) * ((I + kSpan - 1) / kSpan);
+  const int64_t units = int64_t(rows) * ((I - 1) / kSpan + 1);
   const unsigned blocks = grid_for((units + kSwWarps - 1) / kSwWarps);
   const bool a32 = (reinterpret_cast<uintptr_t>(gate_up) & 31u) == 0;
   return launch_waiting(a32 ? mp_k_swiglu<true> : mp_k_swiglu<false>, dim3(blocks),

@@ -70,38 +70,44 @@ def test_wgrad_late_warp_never_misses_a_phase():
     assert (tiles, tiles, tiles) in known
 
 
-def run_loop(tmp_path, header, index, names, limit, turns):
-    """Runs one of the kernels' loops on the CPU (its `for (...)` as it stands, with the given
-    values for what it names): every index lies in [0, limit), and there are so many of them."""
+def run_c(tmp_path, body):
+    """What a C++ program with this main prints; integers wrap around as on the GPU."""
     cxx = shutil.which("g++") or shutil.which("c++")
     if cxx is None:
         pytest.skip("no C++ compiler")
-    values = "\n".join("  %s = %s;" % kv for kv in names.items())
-    text = """#include <cstdint>
+    src, exe = tmp_path / "a.cpp", tmp_path / "a"
+    src.write_text("""#include <cstdint>
 #include <cstdio>
 struct Dim { unsigned x, y; };
-struct Args { int N, I; };
+struct Args { int N, I, K, E, rows, out_cols; };
 int main() {
   Dim blockIdx = {}, gridDim = {};
   Args p = {};
   (void)blockIdx; (void)gridDim; (void)p;
 %s
-  long long turns = 0;
-  for (%s) {
-    if ((long long)(%s) < 0 || (long long)(%s) >= %dLL) { std::puts("index out of range"); return 1; }
-    if (++turns > %dLL) { std::puts("does not end"); return 1; }
-  }
-  std::printf("%%lld\\n", turns);
-  return 0;
 }
-""" % (values, header, index, index, limit, turns + 2)
-    src, exe = tmp_path / "loop.cpp", tmp_path / "loop"
-    src.write_text(text)
+""" % body)
     subprocess.run([cxx, "-O1", "-fwrapv", str(src), "-o", str(exe)], check=True,
                    capture_output=True, text=True)
-    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
-    assert r.returncode == 0, (header, names, r.stdout)
-    assert int(r.stdout) == turns, (header, names)
+    return subprocess.run([str(exe)], check=True, capture_output=True, text=True,
+                          timeout=60).stdout
+
+
+def assignments(names):
+    return "\n".join("  %s = %s;" % kv for kv in names.items())
+
+
+def run_loop(tmp_path, header, index, names, limit, turns):
+    """Runs one of the kernels' loops on the CPU (its `for (...)` as it stands, with the given
+    values for what it names): every index lies in [0, limit), and there are so many of them."""
+    out = run_c(tmp_path, assignments(names) + """
+  long long turns = 0;
+  for (%s) {
+    if ((long long)(%s) < 0 || (long long)(%s) >= %dLL) { std::puts("out of range"); return 0; }
+    if (++turns > %dLL) { std::puts("does not end"); return 0; }
+  }
+  std::printf("%%lld", turns);""" % (header, index, index, limit, turns + 2))
+    assert out.strip() == str(turns), (header, names, out)
 
 
 def loops(text, containing):
@@ -129,3 +135,60 @@ def test_router_token_loops_stay_within_the_tokens(tmp_path, N):
                      {"blockIdx.x": block, "gridDim.x": blocks, "p.N": N,
                       "const int kTeams": teams, "const int team": team},
                      N, max(0, -(-(N - at) // (blocks * teams))))
+
+
+LONGEST = 2 ** 31 - 128
+
+
+def statement(text, pattern):
+    """The one statement that matches, as it stands."""
+    found = set(" ".join(m.split()) for m in re.findall(pattern + r"[^;]*;", text))
+    assert len(found) == 1, (pattern, found)
+    return found.pop()
+
+
+@pytest.mark.parametrize("I", [128, 512, 640, 2 ** 30, LONGEST - 1024, LONGEST])
+def test_activation_channels_stay_within_the_row(tmp_path, I):
+    """Up to the largest inner size that is accepted."""
+    text = source("mp_swiglu.cu")
+    forward, backward = text[:text.index("mp_k_swiglu_backward(")], text[
+        text.index("mp_k_swiglu_backward("):]
+    spans = statement(forward, r"const int spans = ")
+    names = {"p.I": I, "const int kSpan": 512, "const int kCPL": 16}
+    assert int(run_c(tmp_path, assignments(names) + """
+  %s
+  std::printf("%%d", spans);""" % spans)) == -(-I // 512)
+    for host in re.findall(r"int64_t\(rows\) \* (\([^;]*\));", text):
+        assert int(run_c(tmp_path, assignments(dict(names, **{"const int I": I})) + """
+  std::printf("%%lld", (long long)(%s));""" % host)) == -(-I // 512)
+    # the forward kernel's last span of a row: the lanes that have channels
+    left = I - (-(-I // 512) - 1) * 512
+    assert int(run_c(tmp_path, assignments(names) + """
+  const int64_t row = 3;
+  %s
+  const int64_t unit = row * spans + spans - 1;
+  int lanes = 0;
+  for (int lane = 0; lane < 32; ++lane) {
+    %s
+    %s
+    lanes += valid;
+  }
+  std::printf("%%d", lanes);""" % (spans, statement(forward, r"const (?:int|uint32_t) ch = "),
+                                 statement(forward, r"const bool valid = ")))) == left // 16
+    # the gradient's walk over a row
+    heads = loops(backward, "WPR * kSpan")
+    assert len(heads) == 1
+    for warp in (0, 3):
+        run_loop(tmp_path, heads[0], "c0",
+                 dict(names, **{"const int warp": warp, "const int WPR": 4, "const bool live": 1}),
+                 I, max(0, -(-(I - warp * 512) // 2048)))
+    at = (I - 1) // 512 * 512
+    assert int(run_c(tmp_path, assignments(dict(names, **{"const unsigned c0": at})) + """
+  int lanes = 0;
+  for (int lane = 0; lane < 32; ++lane) {
+    %s
+    %s
+    lanes += valid;
+  }
+  std::printf("%%d", lanes);""" % (statement(backward, r"const (?:int|uint32_t) ch = "),
+                                 statement(backward, r"const bool valid = ")))) == left // 16
