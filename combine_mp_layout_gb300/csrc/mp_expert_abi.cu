@@ -41,6 +41,7 @@ bool matmul_args_ok(int E, int rows, int N, int K, const void* a, const float* a
                     const int32_t* dev_err) {
   if (E < 1 || E > MP_MAX_EXPERTS || rows < 0 || N < 1 || K < 1) return false;
   if (K % MP_SCALE_BLOCK != 0 || int64_t(E) * N >= k31) return false;
+  if (rows > INT32_MAX - 1024) return false;  // a tile's last row index stays an int
   if (!dev_err || (!expert_offsets && E != 1)) return false;
   if (rows > 0 && (!a || !a_scales)) return false;
   if ((rows > 0 || w_always) && (!w || !w_scales)) return false;
@@ -51,10 +52,9 @@ bool matmul_args_ok(int E, int rows, int N, int K, const void* a, const float* a
 }
 
 // Row tiles of 64 rows or more, at most one short one per expert, times column
-// tiles of 256 channels; a tile's last row index stays an int.
+// tiles of 256 channels.
 bool tiles_ok(int E, int rows, int cols) {
-  return rows <= INT32_MAX - 1024 &&
-         (int64_t(rows) / 64 + E) * ((int64_t(cols) + 255) / 256) < k31;
+  return (int64_t(rows) / 64 + E) * ((int64_t(cols) + 255) / 256) < k31;
 }
 
 }  // namespace

@@ -1,14 +1,16 @@
 """Logic of the expert layer's kernels that can be followed without a GPU, taken from their
 source: the hand-over of shared-memory slots between warps, and loops at the ends of their
 index types."""
+import ctypes
 import os
 import re
 import shutil
 import subprocess
 
 import pytest
+import torch
 
-from combine_mp_layout_gb300 import _build
+from combine_mp_layout_gb300 import _build, binding as B
 
 
 def source(name):
@@ -192,3 +194,15 @@ def test_activation_channels_stay_within_the_row(tmp_path, I):
   }
   std::printf("%%d", lanes);""" % (statement(backward, r"const (?:int|uint32_t) ch = "),
                                  statement(backward, r"const bool valid = ")))) == left // 16
+
+
+@pytest.mark.skipif(torch.cuda.is_available(),
+                    reason="fake-pointer argument checks run only on a host without a visible GPU")
+@pytest.mark.parametrize("call", ["mp_expert_matmul_e4m3", "mp_expert_matmul_dgrad_e4m3",
+                                  "mp_expert_matmul_wgrad_e4m3"])
+@pytest.mark.parametrize("rows", [2 ** 31 - 1024, 2 ** 31 - 1])
+def test_products_refuse_rows_whose_tiles_pass_32_bits(call, rows):
+    _build.build()
+    p = ctypes.c_void_p(0x10000)  # never dereferenced
+    assert getattr(B.lib(), call)(1, rows, 128, 128, p, p, p, p, None, p, p,
+                                  None) == B.MP_ERR_INVALID_ARG
