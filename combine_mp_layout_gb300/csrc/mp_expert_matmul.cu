@@ -217,7 +217,7 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
   tile_prefix(p, pre, tail->scan);
   tcgen05_fence_after();
   const uint32_t tmem = tail->tmem;
-  const int ncol = (p.out_cols + kBN - 1) / kBN;
+  const int ncol = ceil_div(p.out_cols, kBN);
   const int tiles = pre[p.E] * ncol;  // below 2^31: the C ABI checks
   const int parts = SPLIT ? int(cluster_size()) : 1, part = SPLIT ? int(cluster_rank()) : 0;
   const int first = blockIdx.x / parts, step = SPLIT ? tiles : gridDim.x;
@@ -620,7 +620,7 @@ cudaError_t launch_mm(const MMArgs& p, const void* a, const void* w, int K, int 
     return cudaErrorInvalidValue;
   // at most one short tile per expert
   const int64_t row_tiles = std::min<int64_t>(p.rows, int64_t(p.rows) / kBM + p.E);
-  const int64_t tiles = row_tiles * ((p.out_cols + kBN - 1) / kBN);
+  const int64_t tiles = row_tiles * ceil_div(p.out_cols, kBN);
   const int sms = sm_count();
   // too few tiles for the GPU: up to four blocks (one cluster) share each (nine
   // rows x 4096 x 7168: 12.5 us, 25.8 us with a block per tile)
@@ -639,7 +639,7 @@ cudaError_t launch_expert_matmul(int E, int rows, int N, int K, bool dgrad, cons
                                  cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
   const int red = dgrad ? N : K, cols = dgrad ? K : N;
-  const int kb = K / MP_SCALE_BLOCK, nb = (N + MP_SCALE_BLOCK - 1) / MP_SCALE_BLOCK;
+  const int kb = K / MP_SCALE_BLOCK, nb = ceil_div(N, MP_SCALE_BLOCK);
   MMArgs p;
   p.E = E;
   p.rows = rows;

@@ -107,7 +107,7 @@ struct WTile {
 // Experts ascending, then n, with k fastest: the tiles running at one time
 // share the rows of an expert.
 __device__ __forceinline__ WTile wtile_at(const WgradArgs& p, int t) {
-  const int kt = (p.K + 2 * kWC - 1) / (2 * kWC), nt = (p.N + 2 * kWC - 1) / (2 * kWC);
+  const int kt = ceil_div(p.K, 2 * kWC), nt = ceil_div(p.N, 2 * kWC);
   WTile w;
   w.e = t / (kt * nt);
   const int rem = t - w.e * (kt * nt);
@@ -282,7 +282,7 @@ mp_k_expert_wgrad(const __grid_constant__ CUtensorMap map_dy,
   cluster_sync_all();  // both blocks' mbarriers and TMEM are ready
   tcgen05_fence_after();
   const uint32_t tmem = tail->tmem;
-  const int tiles = p.E * ((p.N + 2 * kWC - 1) / (2 * kWC)) * ((p.K + 2 * kWC - 1) / (2 * kWC));
+  const int tiles = p.E * ceil_div(p.N, 2 * kWC) * ceil_div(p.K, 2 * kWC);
   const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
   volatile int* failed = &tail->failed;
 
@@ -651,8 +651,8 @@ cudaError_t launch_expert_wgrad(int E, int rows, int N, int K, const void* dy,
     if (dev >= 0 && dev < 64) configured[dev] = 1;
   }
   p.out32 = (reinterpret_cast<uintptr_t>(dw) & 31u) == 0;
-  const int64_t tiles = int64_t(E) * ((N + 2 * kWC - 1) / (2 * kWC)) *
-                        ((K + 2 * kWC - 1) / (2 * kWC));  // below 2^31: the C ABI checks
+  // below 2^31: the C ABI checks
+  const int64_t tiles = int64_t(E) * ceil_div(N, 2 * kWC) * ceil_div(K, 2 * kWC);
   const int pairs = int(std::min<int64_t>(tiles, sm_count() / 2));
   CUtensorMap mdy = {}, ma = {}, msd = {}, msa = {};
   if (rows > 0) {

@@ -7,6 +7,9 @@
 
 namespace mp {
 
+// a / b rounded up, for a >= 0: no sum on the way passes a.
+__host__ __device__ constexpr int ceil_div(int a, int b) { return a / b + (a % b != 0); }
+
 // SM count of the current device (cached per device).
 int sm_count();
 

@@ -206,3 +206,29 @@ def test_products_refuse_rows_whose_tiles_pass_32_bits(call, rows):
     p = ctypes.c_void_p(0x10000)  # never dereferenced
     assert getattr(B.lib(), call)(1, rows, 128, 128, p, p, p, p, None, p, p,
                                   None) == B.MP_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("n", [128, 256, 272, 7168, 2 ** 31 - 384, 2 ** 31 - 256, 2 ** 31 - 128,
+                               2 ** 31 - 16])
+def test_products_column_tiles_of_the_largest_sizes(tmp_path, n):
+    """The numbers of column tiles and of scale blocks, as the kernels and launchers work them
+    out, for output channels up to the largest that are accepted."""
+    helper = re.search(r"constexpr int ceil_div\(int a, int b\) (\{[^}]*\})",
+                       source("mp_internal.h"))
+    names = {"p.out_cols": n, "p.N": n, "p.K": n, "p.E": 1, "const int N": n, "const int K": n,
+             "const int E": 1, "const int kBN": 256, "const int kWC": 128,
+             "const int MP_SCALE_BLOCK": 128, "const int64_t row_tiles": 1}
+    if helper:
+        names["const auto ceil_div"] = "[](int a, int b) " + helper.group(1)
+
+    def value(text, pattern, name):
+        return int(run_c(tmp_path, assignments(names) + """
+  %s
+  std::printf("%%lld", (long long)%s);""" % (statement(text, pattern), name)))
+    mm, wg = source("mp_expert_matmul.cu"), source("mp_expert_wgrad.cu")
+    tiles = -(-n // 256)
+    assert value(mm, r"const int ncol = ", "ncol") == tiles
+    assert value(mm, r"const int64_t tiles = ", "tiles") == tiles
+    assert value(mm, r"const int kb = ", "nb") == -(-n // 128)
+    assert value(wg, r"const int kt = ", "kt") == tiles
+    assert value(wg, r"const int kt = ", "nt") == tiles
