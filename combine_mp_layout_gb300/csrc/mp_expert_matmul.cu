@@ -596,15 +596,17 @@ cudaError_t launch_mm_as(MMArgs p, const CUtensorMap& mr, const CUtensorMap& ms,
   p.stages = kMaxStages;
   while (mm_smem_bytes(p.E, p.stages) > size_t(kMaxSmem)) --p.stages;
   const int smem = int(mm_smem_bytes(p.E, p.stages));
-  static thread_local int configured_smem[64] = {0};
+  // The limit belongs to the function on the device, and so to all threads: always the
+  // most that a block may have, whatever this call needs, so that none lowers another's.
+  static thread_local bool configured[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || configured_smem[dev] < smem) {
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
     e = cudaFuncSetAttribute(mp_k_expert_matmul<DGRAD, SPLIT>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) configured_smem[dev] = smem;
+    if (dev >= 0 && dev < 64) configured[dev] = true;
   }
   return launch_waiting(mp_k_expert_matmul<DGRAD, SPLIT>, dim3(unsigned(blocks)), dim3(kMMThreads),
                         size_t(smem), st, SPLIT ? unsigned(parts) : 0u, mr, ms, mw, p);

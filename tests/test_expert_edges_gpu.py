@@ -1,4 +1,6 @@
 """The expert layer's operators at the edges of what they accept, against 64-bit forms."""
+from concurrent.futures import ThreadPoolExecutor
+
 import numpy as np
 import pytest
 import torch
@@ -170,3 +172,43 @@ def test_wgrad_small_codes_at_small_scales():
     # one term, so the sum is exact, and rounding to bf16 keeps the order
     low, high = ((want + d).float().bfloat16().double()[..., None] for d in (-err, err))
     assert bool(((low <= got) & (got <= high)).all())
+
+
+@pytest.mark.parametrize("kind", ["fwd", "dgrad"])
+@pytest.mark.parametrize("rows,N", [(64, 128), (8192, 512)])  # split reductions, whole tiles
+def test_products_of_many_and_few_experts_from_two_threads(kind, rows, N):
+    """The shared memory of a call grows with its experts; threads whose calls alternate do not
+    take it from each other."""
+    K = 2048
+    err = zeros(1, torch.int32)
+    f = B.mp_expert_matmul_e4m3 if kind == "fwd" else B.mp_expert_matmul_dgrad_e4m3
+    src, dst = (K, N) if kind == "fwd" else (N, K)
+
+    def prepared(E):
+        g = gen(56)
+        counts = np.zeros(E, np.int64)
+        counts[[0, E - 1]] = [rows - 3, 3]
+        a, sa = codes((rows, src), g, True), scales((rows, src // 128), g, True)
+        w = torch.zeros((E, N, K), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+        w[[0, E - 1]] = codes((2, N, K), g, True)
+        sw = scales((E, N // 128, K // 128), g, True)
+        ws = w[[0, E - 1]].double() * sw[[0, E - 1]].double().repeat_interleave(
+            128, 1).repeat_interleave(128, 2)
+        if kind == "fwd":
+            ws = ws.transpose(1, 2)
+        ad, off = rows_ref(a, sa), offsets(counts)
+        want = torch.cat([ad[:-3] @ ws[0], ad[-3:] @ ws[1]]).float().bfloat16()
+        torch.cuda.synchronize()
+
+        def call():
+            out = zeros((rows, dst), torch.bfloat16)
+            status = f(E, rows, N, K, a, sa, w, sw, off, out, err)
+            torch.cuda.synchronize()
+            return status, torch.equal(out, want)
+        return call
+    many, few = prepared(4000), prepared(2)
+    with ThreadPoolExecutor(1) as one, ThreadPoolExecutor(1) as other:
+        for _ in range(3):
+            assert one.submit(many).result() == (B.MP_OK, True)
+            assert other.submit(few).result() == (B.MP_OK, True)
+    assert int(err) == 0
