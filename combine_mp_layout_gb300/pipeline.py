@@ -238,6 +238,8 @@ class MoELayerPlan:
                 active=None, stream=None):
         """The layer's output (self.out); self.balance_loss holds the loss per rank."""
         R, N, K, E, H, I, cap = (self.R, self.N, self.K, self.E, self.H, self.I, self.cap)
+        # (the dispatches read what stands at an address, whatever it is)
+        B._arr(x, "x", torch.bfloat16, R * N * H)
         B.check(B.mp_route(R, N, K, E, self.scoring, logits, bias, active, self.normalize,
                            self.scale, self.loss_coef, self.topk_idx, self.topk_weights,
                            self.num_tokens_per_expert, self.num_routed, self.balance_loss,
@@ -268,6 +270,7 @@ class MoELayerPlan:
         """Gradients of a forward pass, from the output's (and the losses'): d_x, d_logits,
         d_w_gate_up, d_w_down of the plan."""
         R, N, K, E, H, I, cap = (self.R, self.N, self.K, self.E, self.H, self.I, self.cap)
+        B._arr(d_out, "d_out", torch.bfloat16, R * N * H)
         B.check(B.mp_dispatch_ll_rows_quant(R, N, K, H, B.MP_Q_E4M3, d_out, self.slot_row, cap,
                                             self.dy, self.dy_scales, stream),
                 "mp_dispatch_ll_rows_quant")
