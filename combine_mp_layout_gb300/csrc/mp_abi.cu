@@ -3,6 +3,7 @@
 // no synchronisation, no state kept between calls.
 #include <cstdint>
 #include <cuda_runtime.h>
+#include <mutex>
 
 #include "../../include/mp_layout.h"
 #include "mp_common.cuh"
@@ -20,6 +21,27 @@ int sm_count() {
     n = 1;
   if (dev >= 0 && dev < 64) cached[dev] = n;
   return n;
+}
+
+cudaError_t raise_smem_limit(const void* kernel, int dev, int smem) {
+  struct Limit {
+    const void* kernel;
+    int dev, smem;
+  };
+  static std::mutex lock;
+  static Limit limits[1024];  // kernels of this library times devices: never full
+  static int used = 0;
+  std::lock_guard<std::mutex> hold(lock);
+  int i = 0;
+  while (i < used && (limits[i].kernel != kernel || limits[i].dev != dev)) ++i;
+  if (i < used && limits[i].smem >= smem) return cudaSuccess;
+  if (i == 1024) return cudaErrorInvalidValue;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  limits[i] = {kernel, dev, smem};
+  if (i == used) ++used;
+  return cudaSuccess;
 }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -907,8 +907,8 @@ static cudaError_t dispatch_copy_tma(int R, int64_t tokens, int64_t row_bytes, c
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (configured[dev] < int(smem)) {
-    cudaError_t e = cudaFuncSetAttribute(mp_k_dispatch_tma,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    cudaError_t e =
+        raise_smem_limit(reinterpret_cast<const void*>(mp_k_dispatch_tma), dev, int(smem));
     if (e != cudaSuccess) return e;
     configured[dev] = int(smem);
   }
@@ -1766,7 +1766,7 @@ static cudaError_t ll_dispatch_fused_nw(LLFusedArgs a, cudaStream_t stream) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (smem > 48 * 1024 && configured[dev] < int(smem)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        raise_smem_limit(reinterpret_cast<const void*>(kernel), dev, int(smem));
     if (e != cudaSuccess) return e;
     configured[dev] = int(smem);
   }
@@ -2217,7 +2217,7 @@ static cudaError_t layout_dispatch_fused_nw(HTFusedArgs a, cudaStream_t stream) 
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (smem > 48 * 1024 && configured[dev] < int(smem)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        raise_smem_limit(reinterpret_cast<const void*>(kernel), dev, int(smem));
     if (e != cudaSuccess) return e;
     configured[dev] = int(smem);
   }

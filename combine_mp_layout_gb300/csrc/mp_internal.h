@@ -13,6 +13,10 @@ __host__ __device__ constexpr int ceil_div(int a, int b) { return a / b + (a % b
 // SM count of the current device (cached per device).
 int sm_count();
 
+// Lets a kernel have `smem` bytes of dynamic shared memory on device `dev`.  That
+// limit is the function's, for all host threads of the process: it is only raised.
+cudaError_t raise_smem_limit(const void* kernel, int dev, int smem);
+
 // Host-side argument checks of mp_dispatch (MP_OK or MP_ERR_INVALID_ARG):
 // the receive-offset scan's arguments without its workspace, and the row
 // copy's.

@@ -1389,8 +1389,7 @@ cudaError_t launch_layout(int R, int N, int K, int E, const int32_t* topk_idx,
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && configured_smem[dev] < int(smem) && smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(mp_k_layout, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(smem));
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(mp_k_layout), dev, int(smem));
     if (e != cudaSuccess) return e;
     configured_smem[dev] = int(smem);
   }
@@ -1424,8 +1423,7 @@ cudaError_t launch_scan(int R, int N, int K, int E, const int32_t* topk_idx,
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && configured_smem[dev] < int(smem) && smem > 32 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(mp_k_scan, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(smem));
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(mp_k_scan), dev, int(smem));
     if (e != cudaSuccess) return e;
     configured_smem[dev] = int(smem);
   }
@@ -1478,8 +1476,7 @@ cudaError_t launch_layout_cluster(int R, int N, int K, int E, const int32_t* top
   }
   if (ready[dev][v] < 0) return cudaErrorNotSupported;
   if (smem > 48 * 1024 && configured_smem[dev][v] < int(smem)) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
-        cudaSuccess)
+    if (raise_smem_limit(reinterpret_cast<const void*>(kernel), dev, int(smem)) != cudaSuccess)
       return cudaErrorNotSupported;
     configured_smem[dev][v] = int(smem);
   }
@@ -1550,8 +1547,7 @@ cudaError_t launch_layout_scan(int R, int N, int K, int E, const int32_t* topk_i
   const int variant = (meta ? 2 : 0) + lookback;
   static thread_local int configured[64][4] = {};
   if (smem > 48 * 1024 && configured[dev][variant] < int(smem)) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(smem));
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kernel), dev, int(smem));
     if (e != cudaSuccess) return cudaErrorNotSupported;
     configured[dev][variant] = int(smem);
   }
@@ -1597,8 +1593,8 @@ static cudaError_t ll_offsets(int R, int N, int K, int E, const int32_t* topk_id
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (smem > 48 * 1024 && configured[dev] < int(smem)) {
-    cudaError_t e = cudaFuncSetAttribute(mp_k_ll_offsets<RANK_MAJOR>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    cudaError_t e = raise_smem_limit(
+        reinterpret_cast<const void*>(mp_k_ll_offsets<RANK_MAJOR>), dev, int(smem));
     if (e != cudaSuccess) return e;
     configured[dev] = int(smem);
   }

@@ -237,3 +237,37 @@ def test_activation_scales_are_the_rounded_quotients():
     B.check(B.mp_swiglu_backward_e4m3(rows, I, x, w, u, None, dg, dsc, None))
     du = (u.float() * w[:, None]) * 32
     assert torch.equal(dsc[:, I // 128:], scale_of(du))
+
+
+def test_layouts_of_many_and_fewer_experts_from_two_threads():
+    """The same for the layout kernels that the layer stands on: more than 48 KB of shared
+    memory in both threads, more of it in one."""
+    R, N, K = 2, 300, 32
+
+    def prepared(E):
+        g = gen(58)
+        idx = torch.randint(0, E, (R, N, K), generator=g, device=DEV, dtype=torch.int32)
+        want = torch.stack([torch.bincount(idx[r].flatten().long(), minlength=E) for r in range(R)])
+        i32 = torch.int32
+        per_rank, per_expert = zeros((R, R), i32), zeros((R, E), i32)
+        mask, err = zeros((R, N), i32), zeros(1, i32)
+        ws = zeros(B.mp_workspace_size(R, N, E), torch.uint8)
+        off, src = zeros(E + 1, i32), zeros((E, R), i32)
+        token, slot = zeros(R * N * K, i32), zeros((R, N, K), i32)
+        torch.cuda.synchronize()
+
+        def call():
+            status = [B.mp_layout(R, N, K, E, idx, per_rank, per_expert, mask, err, ws),
+                      B.mp_dispatch_ll_offsets(R, N, K, E, idx, per_expert, R * N * K, off, src,
+                                               token, slot, err)]
+            torch.cuda.synchronize()
+            assert int(err) == 0 and torch.equal(per_expert.long(), want)
+            assert torch.equal(off[1:].long(), want.sum(0).cumsum(0))
+            return status
+        return call
+    for fewer in (4200, 6000):
+        many, few = prepared(8192), prepared(fewer)
+        with ThreadPoolExecutor(1) as one, ThreadPoolExecutor(1) as other:
+            for _ in range(3):
+                assert one.submit(many).result() == [B.MP_OK] * 2
+                assert other.submit(few).result() == [B.MP_OK] * 2
