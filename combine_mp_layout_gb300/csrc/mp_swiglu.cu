@@ -5,12 +5,9 @@
 //   z_i = w_r * g_i / (1 + exp(-g_i)) * u_i      (w_r: the row's routing weight, or 1)
 //   dg_i = w_r dz_i u_i sig_i (1 + g_i (1 - sig_i)),  du_i = w_r dz_i g_i sig_i,
 //   dw_r = sum_i dz_i g_i sig_i u_i,                   sig_i = 1 / (1 + exp(-g_i))
-// Quantisation: per 128 channels scale = amax / 448, as on dispatch, and codes
-// e4m3(value * (1 / scale)) (scale 1, all codes 0, for a block whose scale would
-// be below 2^-126).  The product with the rounded reciprocal is within 1.5 ulp of
-// value / scale, which dispatch rounds: a code differs where the quotient lies
-// that near the middle of two codes.  (With the quotient itself the gradient takes
-// 102 us instead of 91.)
+// Quantisation as on dispatch: per 128 channels scale = amax / 448, codes
+// e4m3(value / scale) (scale 1, all codes 0, for a block whose scale would be
+// below 2^-126).
 //
 // Both kernels are bound by memory: they read bf16 once and write one byte per
 // value.  A lane holds 16 channels (one 32-byte load per operand), eight lanes
@@ -69,11 +66,8 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
   return make_float2(bf16_lo(w), bf16_hi(w));
 }
 
-// 1 / (1 + exp(-x)) of two channels from the fast exponential and reciprocal.  The
-// exponential's argument is rounded to fp32, so for negative x the error grows with
-// |x|: 2e-7 at -4, 8e-7 at -15, 3.4e-6 at -84, and the two functions' few ulps.  That
-// is far below the e4m3 rounding that follows; in the row weight's gradient, which is
-// not rounded so, such gates' terms are small.
+// 1 / (1 + exp(-x)) of two channels from the fast exponential and reciprocal:
+// a few fp32 ulps, far below the e4m3 rounding that follows.
 __device__ __forceinline__ float2 sigmoid2(float2 x) {
   constexpr float kLog2e = 1.4426950408889634f;
   const float2 t = mul2(x, make_float2(-kLog2e, -kLog2e));
@@ -102,12 +96,7 @@ __device__ __forceinline__ void quantise_store(const float2 (&z)[kCPL / 2], bool
   for (int i = 0; i < kCPL / 2; ++i) amax = fmaxf(amax, fmaxf(fabsf(z[i].x), fabsf(z[i].y)));
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-  // amax / 448 correctly rounded: the product with the rounded reciprocal and one
-  // correction by the exact remainder (Markstein, "IA-64 and Elementary Functions";
-  // a division costs the forward kernel 5 of 58 us)
-  constexpr float k448th = 1.0f / 448.0f;
-  float sc = amax * k448th;
-  if (sc < INFINITY) sc = fmaf(fmaf(-448.0f, sc, amax), k448th, sc);
+  float sc = amax * (1.0f / 448.0f);
   if (!(sc >= 0x1p-126f)) sc = 1.0f;
   const float inv = sc < INFINITY ? __fdiv_rn(1.0f, sc) : 0.0f;
   if (!valid) return;

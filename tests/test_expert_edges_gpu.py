@@ -214,31 +214,6 @@ def test_products_of_many_and_few_experts_from_two_threads(kind, rows, N):
     assert int(err) == 0
 
 
-def test_activation_scales_are_the_rounded_quotients():
-    """With gates of 32 the sigmoid is 1 in fp32 and z = 32 u w exactly rounded once: scales are
-    amax / 448 bit for bit, forward and (through d_out) in the gradient's second half."""
-    g = gen(57)
-    rows, I = 600, 512
-    x = zeros((rows, 2 * I), torch.bfloat16)
-    x[:, :I] = 32.0
-    u = torch.randn((rows, I), generator=g, device=DEV).bfloat16()
-    x[:, I:] = u
-    w = torch.rand(rows, generator=g, device=DEV) * torch.exp2(
-        torch.randint(-100, 100, (rows,), generator=g, device=DEV).float())
-    f8 = torch.float8_e4m3fn
-
-    def scale_of(v):  # (in fp32 a division by a number is a product with its reciprocal)
-        return (v.view(rows, -1, 128).abs().amax(-1).double() / 448.0).float()
-    out, sc = zeros((rows, I), f8), zeros((rows, I // 128))
-    B.check(B.mp_swiglu_e4m3(rows, I, x, w, None, out, sc))
-    z = (u.float() * 32) * w[:, None]
-    assert torch.equal(sc, scale_of(z))
-    dg, dsc = zeros((rows, 2 * I), f8), zeros((rows, 2 * I // 128))
-    B.check(B.mp_swiglu_backward_e4m3(rows, I, x, w, u, None, dg, dsc, None))
-    du = (u.float() * w[:, None]) * 32
-    assert torch.equal(dsc[:, I // 128:], scale_of(du))
-
-
 def test_layouts_of_many_and_fewer_experts_from_two_threads():
     """The same for the layout kernels that the layer stands on: more than 48 KB of shared
     memory in both threads, more of it in one."""
