@@ -246,3 +246,29 @@ def test_layouts_of_many_and_fewer_experts_from_two_threads():
             for _ in range(3):
                 assert one.submit(many).result() == [B.MP_OK] * 2
                 assert other.submit(few).result() == [B.MP_OK] * 2
+
+
+def test_activation_scales_and_codes_are_as_near_as_stated():
+    """With gates of 32 the sigmoid is 1 in fp32 and z = 32 u w is rounded once, so z is known:
+    scales within one ulp (2^-23) of amax / 448, and each code that of a value within 1.5 ulp (at
+    most 1.5 * 2^-23 of it) of z / scale."""
+    g = gen(57)
+    rows, I = 600, 512
+    x = zeros((rows, 2 * I), torch.bfloat16)
+    x[:, :I] = 32.0
+    u = torch.randn((rows, I), generator=g, device=DEV).bfloat16()
+    x[:, I:] = u
+    w = torch.rand(rows, generator=g, device=DEV) * torch.exp2(
+        torch.randint(-100, 100, (rows,), generator=g, device=DEV).float())
+    f8 = torch.float8_e4m3fn
+    out, sc = zeros((rows, I), f8), zeros((rows, I // 128))
+    B.check(B.mp_swiglu_e4m3(rows, I, x, w, None, out, sc))
+    z = ((u.float() * 32) * w[:, None]).double().view(rows, -1, 128)
+    want = z.abs().amax(-1) / 448
+    assert bool(((sc.double() - want).abs() <= 2.0 ** -23 * want).all())
+    q = (z / sc.double()[..., None]).view(rows, I).abs()
+    low, high = ((q * (1 + d * 1.5 * 2.0 ** -23)).clamp(max=448.0).float().to(f8).double()
+                 for d in (-1, 1))
+    got = out.double().abs()
+    assert bool(((low <= got) & (got <= high)).all())
+    assert bool((out.double().sign() * z.view(rows, I).sign() >= 0).all())
