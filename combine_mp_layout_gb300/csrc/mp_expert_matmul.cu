@@ -495,8 +495,8 @@ mp_k_expert_matmul(const __grid_constant__ CUtensorMap map_rows,
 // mma.m16n8k32 on registers: which channels of a scale block meet in one MMA is
 // free, as long as both operands agree, so a thread's operands are the 16 bytes
 // that it loads.  Each block sum (fp32) is scaled and added up in fp32, the
-// warps' sums are joined in a fixed order.  One row of 4096 x 7168: 6.8 us, 4.3
-// TB/s of weights.
+// warps' sums are joined in a fixed order.  One row of 4096 x 7168: 6.4 to 8.0 us from
+// run to run, 3.7 to 4.6 TB/s of weights.
 // ---------------------------------------------------------------------------
 constexpr int kVecRows = 8;   // columns of the MMA, rows that the launcher gives it
 constexpr int kVecWarps = 8;
@@ -657,8 +657,8 @@ cudaError_t launch_expert_matmul(int E, int rows, int N, int K, bool dgrad, cons
   p.out = static_cast<uint16_t*>(out);
   p.out32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   p.dev_err = dev_err;
-  // one expert's few rows (4096 x 7168 in this form, and as tiles: one row 7.5 and
-  // 11.5 us, eight 8.5 and 12.4 us; but eight rows of seven experts 49 and 38 us)
+  // one expert's few rows (4096 x 7168 in this form, and as tiles, in one run: one row
+  // 7.5 and 11.5 us, eight 8.5 and 12.4 us; but eight rows of seven experts 49 and 38 us)
   if (!dgrad && rows <= kVecRows && (E == 1 || rows == 1)) {
     return launch_waiting(mp_k_expert_matvec,
                           dim3(unsigned(N / 16), unsigned(expert_offsets ? rows : 1)),

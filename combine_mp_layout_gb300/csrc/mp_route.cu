@@ -14,12 +14,13 @@
 // A warp (up to 1,024 experts) or a block of eight warps (beyond) holds one
 // token's logits in registers, V per thread, so they are read once.
 //
-// Measured at 8 x 4,096 tokens, 256 experts, top-8, sigmoid: forward 31 us, gradient
-// 26 us (10 and 14 us of memory traffic are in them at most); 8 tokens of 64 experts
-// 5.2 us.  The forward pass is bound by instructions, about 770 per token and warp
-// (71% of the issue slots taken): exponential and reciprocal of every score, the
-// candidates' compares and ballots; about 8 us are launch, block sums and the ranks'
-// ends.
+// Measured at 8 x 4,096 tokens, 256 experts, top-8, sigmoid: forward 31.6 us, gradient
+// 25.6 us (10 and 14 us of memory traffic are in them at most); 8 tokens of 64 experts
+// 5.3 us; with a block per token, 2,048, 4,096 and 8,192 experts, forward 510, 673 and
+// 1,585 us, gradient 308, 419 and 1,099 us.  The forward pass is bound by
+// instructions, about 770 per token and warp (71% of the issue slots taken):
+// exponential and reciprocal of every score, the candidates' compares and ballots;
+// about 8 us are launch, block sums and the ranks' ends.
 //
 // The sums over tokens are order-free and so the same on every run: counts are
 // integers, and each block's share sums (fp32, added in a fixed order) enter
@@ -44,9 +45,10 @@ namespace {
 constexpr int kRouteWarps = 8;
 constexpr int kRouteThreads = kRouteWarps * kWarp;
 // Up to how many choices candidates are tried first.  8 x 4,096 tokens of 256
-// experts: 8 choices 34 us against 44 us by rounds, 16 38 and 55, 20 50 and 60, but
-// 32 choices 87 and 76 us (nearly all lanes' largest count, and more than 32 keys
-// reach the least of them).
+// experts, both ways side by side: 8 choices 34 us against 44 us by rounds, 16 38 and
+// 55, 20 50 and 60, but 32 choices 87 and 76 us (nearly all lanes' largest count, and
+// more than 32 keys reach the least of them).  Later steps shortened what both share:
+// 8 choices take 31.6 us now.
 constexpr int kCandidateTopk = 20;
 
 struct RouteArgs {

@@ -674,7 +674,10 @@ size_t mp_route_workspace_size(int R, int N, int E);
  * Scores of a token: softmax of its logits, or 1 / (1 + exp(-logit)); 0 for a
  * logit of -inf, which is never chosen.  The K largest logits (MP_SOFTMAX) or
  * scores + bias (MP_SIGMOID) are chosen in descending order, among equals the
- * lower expert first; an expert whose sum is -inf or NaN is not chosen.
+ * lower expert first; an expert whose sum is -inf or NaN is not chosen.  All experts
+ * compete: a choice of groups of experts first, and of experts within those, is not
+ * covered (logits masked to -inf outside the groups give its choice, but leave the
+ * shares of the loss without those experts).
  * Weight: scale * score, divided by the sum of the chosen scores with
  * normalize != 0 (0 if that sum is 0).  Share p: score / sum of all scores.
  * With T = num_routed[r] and c = num_tokens_per_expert[r]:
