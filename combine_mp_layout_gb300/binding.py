@@ -102,6 +102,11 @@ def lib() -> ctypes.CDLL:
         L.mp_expert_matmul_wgrad_e4m3.argtypes = [i32] * 4 + [P] * 8
         L.mp_swiglu_e4m3.argtypes = [i32] * 2 + [P] * 6
         L.mp_swiglu_backward_e4m3.argtypes = [i32] * 2 + [P] * 8
+        L.mp_expert_matmul_bf16.argtypes = [i32] * 4 + [P] * 6
+        L.mp_expert_matmul_dgrad_bf16.argtypes = [i32] * 4 + [P] * 6
+        L.mp_expert_matmul_wgrad_bf16.argtypes = [i32] * 4 + [P] * 3 + [i32] * 2 + [P] * 3
+        L.mp_swiglu_bf16.argtypes = [i32] * 2 + [P] * 5
+        L.mp_swiglu_backward_bf16.argtypes = [i32] * 2 + [P] * 7
         L.mp_ll_row_weights.argtypes = [i32] * 3 + [P, P, i64, P, P]
         L.mp_ll_row_weights_backward.argtypes = [i32] * 3 + [P, i64, P, P, P]
         L.mp_dispatch_ll.argtypes = [i32] * 7 + [P] * 4 + [i64] + [P] * 8
@@ -118,6 +123,8 @@ def lib() -> ctypes.CDLL:
                   "mp_dispatch_ll_quant", "mp_route", "mp_route_backward",
                   "mp_expert_matmul_e4m3", "mp_expert_matmul_dgrad_e4m3",
                   "mp_expert_matmul_wgrad_e4m3", "mp_swiglu_e4m3", "mp_swiglu_backward_e4m3",
+                  "mp_expert_matmul_bf16", "mp_expert_matmul_dgrad_bf16",
+                  "mp_expert_matmul_wgrad_bf16", "mp_swiglu_bf16", "mp_swiglu_backward_bf16",
                   "mp_ll_row_weights", "mp_ll_row_weights_backward"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
@@ -569,6 +576,61 @@ def mp_swiglu_backward_e4m3(rows, I, gate_up, row_weights, d_out, num_rows, d_ga
         _arr(d_out, "d_out", torch.bfloat16, rows * I), _arr(num_rows, "num_rows", torch.int32, 1),
         _arr(d_gate_up, "d_gate_up", _F8, rows * 2 * I),
         _arr(d_gate_up_scales, "d_gate_up_scales", torch.float32, rows * (2 * I // SCALE_BLOCK)),
+        _arr(d_row_weights, "d_row_weights", torch.float32, rows), _raw_stream(stream))
+
+
+def mp_expert_matmul_bf16(E, rows, N, K, a, w, expert_offsets, out, dev_err, stream=None) -> int:
+    """out[r] = a[r] w[e]^T for the rows of every expert, all bf16."""
+    return lib().mp_expert_matmul_bf16(
+        E, rows, N, K, _arr(a, "a", torch.bfloat16, rows * K),
+        _arr(w, "w", torch.bfloat16, E * N * K),
+        _arr(expert_offsets, "expert_offsets", torch.int32, E + 1),
+        _arr(out, "out", torch.bfloat16, rows * N), _arr(dev_err, "dev_err", torch.int32, 1),
+        _raw_stream(stream))
+
+
+def mp_expert_matmul_dgrad_bf16(E, rows, N, K, dy, w, expert_offsets, dx, dev_err,
+                                stream=None) -> int:
+    """dx[r] = dy[r] w[e]: the gradient of the rows, with the weights as they are stored."""
+    return lib().mp_expert_matmul_dgrad_bf16(
+        E, rows, N, K, _arr(dy, "dy", torch.bfloat16, rows * N),
+        _arr(w, "w", torch.bfloat16, E * N * K),
+        _arr(expert_offsets, "expert_offsets", torch.int32, E + 1),
+        _arr(dx, "dx", torch.bfloat16, rows * K), _arr(dev_err, "dev_err", torch.int32, 1),
+        _raw_stream(stream))
+
+
+def mp_expert_matmul_wgrad_bf16(E, rows, N, K, dy, a, expert_offsets, accumulate, dw, dev_err,
+                                stream=None) -> int:
+    """dw[e] = dy^T a over the rows of every expert, in dw's type (bf16 or fp32); with
+    accumulate (fp32 only) added to what dw holds."""
+    f32 = dw is not None and dw.dtype is torch.float32
+    return lib().mp_expert_matmul_wgrad_bf16(
+        E, rows, N, K, _arr(dy, "dy", torch.bfloat16, rows * N),
+        _arr(a, "a", torch.bfloat16, rows * K),
+        _arr(expert_offsets, "expert_offsets", torch.int32, E + 1),
+        MP_FP32 if f32 else MP_BF16, int(bool(accumulate)),
+        _arr(dw, "dw", torch.float32 if f32 else torch.bfloat16, E * N * K),
+        _arr(dev_err, "dev_err", torch.int32, 1), _raw_stream(stream))
+
+
+def mp_swiglu_bf16(rows, I, gate_up, row_weights, num_rows, out, stream=None) -> int:
+    """row_weights * silu(gate) * up of bf16 [rows][2I], in bf16."""
+    return lib().mp_swiglu_bf16(
+        rows, I, _arr(gate_up, "gate_up", torch.bfloat16, rows * 2 * I),
+        _arr(row_weights, "row_weights", torch.float32, rows),
+        _arr(num_rows, "num_rows", torch.int32, 1),
+        _arr(out, "out", torch.bfloat16, rows * I), _raw_stream(stream))
+
+
+def mp_swiglu_backward_bf16(rows, I, gate_up, row_weights, d_out, num_rows, d_gate_up,
+                            d_row_weights, stream=None) -> int:
+    """The gradient of mp_swiglu_bf16: d_gate_up bf16, d_row_weights fp32."""
+    return lib().mp_swiglu_backward_bf16(
+        rows, I, _arr(gate_up, "gate_up", torch.bfloat16, rows * 2 * I),
+        _arr(row_weights, "row_weights", torch.float32, rows),
+        _arr(d_out, "d_out", torch.bfloat16, rows * I), _arr(num_rows, "num_rows", torch.int32, 1),
+        _arr(d_gate_up, "d_gate_up", torch.bfloat16, rows * 2 * I),
         _arr(d_row_weights, "d_row_weights", torch.float32, rows), _raw_stream(stream))
 
 

@@ -1,0 +1,329 @@
+// mp_expert_wgrad_bf16.cu -- the gradient of the experts' weights from bf16 rows
+// (sm_103a: TMA, tcgen05 on pairs of blocks, TMEM).
+//
+//   dw[e][n][k] (+)= sum over the rows r of expert e of dy[r][n] * a[r][k]
+//
+// Products are exact, sums over the rows fp32 in TMEM; then one rounding to bf16,
+// or none (fp32, optionally added to what stands there: one fp32 addition).
+//
+// A pair of blocks (cta_group::2) works on 256 x 256 weights, 64 rows per stage:
+// each block loads its 128 dy channels (M) and its half of the a channels (N), 32
+// KB for 512 clocks of MMA.  Both operands are MN-major: a row of channels stays a
+// row in shared memory, nothing is transposed.
+//
+// An expert's last stage may reach into the next expert's rows (or past the array,
+// where the loads give zeros).  These rows must not count, whatever they hold, so
+// a warp of each block overwrites them with zeros in shared memory, up to the next
+// multiple of 16; steps of 16 rows behind that are not issued.
+//
+// Warps of a block: one loads, one (of the pair's first block) issues the MMAs,
+// one clears, four write finished tiles while the next one's products run.
+#include <algorithm>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "mp_pair16.cuh"
+
+namespace mp {
+
+namespace {
+
+constexpr int kWC = 128;                      // dy and a channels per block
+constexpr int kWRows = 64;                    // rows per stage: four K = 16 steps
+constexpr int kWOperand = kWRows * kWC * 2;
+constexpr int kWStage = 2 * kWOperand;
+constexpr int kChunk = kWRows * 128;          // 64 channels (128 bytes) of a stage's rows
+constexpr int kWStages = 6;
+constexpr int kEpiWarps = 4;
+constexpr int kClearWarp = 2, kEpiFirst = 3;
+constexpr int kWThreads = (kEpiFirst + kEpiWarps) * 32;
+
+struct WArgs {
+  int E, rows, N, K;
+  const int32_t* expert_offsets;
+  void* dw;
+  int32_t* dev_err;
+  int out32;       // rows of dw are 32-byte aligned
+  int accumulate;  // fp32: add to dw
+  int patience;    // of the waits for whole tiles
+};
+
+struct WTail {
+  uint64_t full[kWStages], empty[kWStages];  // full: of the pair's first block
+  uint64_t last[kWStages];                   // this block's loads of a stage to be cleared
+  uint64_t tfull[2], tempty[2];
+  uint32_t tmem;
+  int failed;
+};
+constexpr size_t kWSmem = size_t(kWStages) * kWStage + sizeof(WTail);
+
+struct WTile {
+  int e, lo, hi, n0, k0;  // n0, k0: of the pair
+  __device__ __forceinline__ int steps() const { return (hi - lo + kWRows - 1) / kWRows; }
+  // rows of the last stage, 0 if it is a whole one
+  __device__ __forceinline__ int rest() const { return (hi - lo) % kWRows; }
+};
+
+// Experts ascending, then n, with k fastest: the tiles running at one time
+// share the rows of an expert.
+__device__ __forceinline__ WTile wtile_at(const WArgs& p, int t) {
+  const int kt = ceil_div(p.K, 2 * kWC), nt = ceil_div(p.N, 2 * kWC);
+  WTile w;
+  w.e = t / (kt * nt);
+  const int rem = t - w.e * (kt * nt);
+  w.n0 = (rem / kt) * 2 * kWC;
+  w.k0 = (rem % kt) * 2 * kWC;
+  rows_of(p.expert_offsets, p.rows, w.e, w.lo, w.hi);
+  return w;
+}
+
+// Half of a tile's a channels: whole MMA steps of 32 for the pair.
+__device__ __forceinline__ int half_cols(const WArgs& p, const WTile& w) {
+  return min(2 * kWC, (p.K - w.k0 + 31) & ~31) / 2;
+}
+
+template <bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
+mp_k_expert_wgrad_bf16(const __grid_constant__ CUtensorMap map_dy,
+                       const __grid_constant__ CUtensorMap map_a, const WArgs p) {
+  extern __shared__ __align__(1024) unsigned char stages[];
+  WTail* tail = reinterpret_cast<WTail*>(stages + size_t(kWStages) * kWStage);
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  const int rank = int(cluster_rank());
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWStages; ++i) {
+      mbar_init(&tail->full[i], 2);
+      mbar_init(&tail->empty[i], 1);
+      mbar_init(&tail->last[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tail->tfull[i], 1);
+      mbar_init(&tail->tempty[i], 2 * kEpiWarps);
+    }
+    tail->failed = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_alloc<true>(&tail->tmem, 512);
+  pdl_wait_prior_grid();  // (nothing of the above touches global memory)
+  if (blockIdx.x == 0) {
+    int bad = 0;
+    for (int e = threadIdx.x; e < p.E; e += kWThreads)
+      bad |= offset_errors(p.expert_offsets, p.rows, e);
+    if (bad) raise_error(p.dev_err, bad);
+  }
+  __syncthreads();
+  cluster_sync_all();  // both blocks' barriers and TMEM are ready
+  tcgen05_fence_after();
+  const uint32_t tmem = tail->tmem;
+  const int tiles = p.E * ceil_div(p.N, 2 * kWC) * ceil_div(p.K, 2 * kWC);
+  const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+  volatile int* failed = &tail->failed;
+
+  if (warp == 0) {
+    // ---- loads: one lane keeps the ring of stages full
+    if (elect_one()) {
+      RingAt s;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += stride) {
+        const WTile w = wtile_at(p, t);
+        const int half = half_cols(p, w);
+        const int n = w.n0 + rank * kWC, k = w.k0 + rank * half;
+        const uint32_t bytes = uint32_t(kWOperand + (half > 64 ? kWOperand : kChunk));
+        const int steps = w.steps(), rest = w.rest();
+        for (int i = 0; i < steps; ++i, s.next(kWStages)) {
+          if (s.round > 0 &&
+              !bounded_wait_idle(&tail->empty[s.slot], (s.round - 1) & 1u, failed)) {
+            ok = false;
+            break;
+          }
+          unsigned char* dst = stages + size_t(s.slot) * kWStage;
+          const int row = w.lo + i * kWRows;
+          // a stage to be cleared goes to this block's clearing warp first
+          const bool whole = rest == 0 || i + 1 < steps;
+          const uint32_t bar = whole ? map_to_rank(&tail->full[s.slot], 0)
+                                     : map_to_rank(&tail->last[s.slot], uint32_t(rank));
+          arrive_expect_at(bar, bytes);
+          tma_load_2d_pair(dst, &map_dy, n, row, bar);
+          tma_load_2d_pair(dst + kChunk, &map_dy, n + 64, row, bar);
+          tma_load_2d_pair(dst + kWOperand, &map_a, k, row, bar);
+          if (half > 64) tma_load_2d_pair(dst + kWOperand + kChunk, &map_a, k + 64, row, bar);
+        }
+      }
+      // every load has landed and been used before the block may end
+      for (int i = 0; i < kWStages; ++i, s.next(kWStages))
+        if (s.round > 0) bounded_wait_idle(&tail->empty[s.slot], (s.round - 1) & 1u, failed);
+    }
+  } else if (warp == 1) {
+    // ---- products
+    if (rank == 0 && elect_one()) {
+      RingAt s;
+      uint32_t nt = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += stride) {
+        const WTile w = wtile_at(p, t);
+        const int steps = w.steps(), rest = w.rest();
+        if (steps == 0) continue;
+        const uint32_t idesc = mma_idesc_bf16(2 * kWC, 2 * half_cols(p, w), true, true);
+        const uint32_t buf = nt & 1u;
+        if (nt >= 2)
+          ok = bounded_wait(&tail->tempty[buf], ((nt >> 1) - 1) & 1u, failed, p.patience);
+        for (int i = 0; i < steps && ok; ++i) {
+          ok = bounded_wait(&tail->full[s.slot], s.round & 1u, failed);
+          if (!ok) break;
+          tcgen05_fence_after();
+          const uint32_t sd = smem_addr(stages + size_t(s.slot) * kWStage);
+          const uint64_t dd = smem_desc_sw128(sd, kChunk, 1024);
+          const uint64_t da = smem_desc_sw128(sd + kWOperand, kChunk, 1024);
+          const int rows = rest == 0 || i + 1 < steps ? kWRows : rest;
+#pragma unroll
+          for (int k = 0; k < kWRows / 16; ++k)
+            if (k * 16 < rows)
+              mma_f16_pair(tmem + buf * 256, dd + ((k * 16 * 128) >> 4),
+                           da + ((k * 16 * 128) >> 4), idesc, i > 0 || k > 0);
+          commit_to_pair(&tail->empty[s.slot], 0);
+          s.next(kWStages);
+        }
+        if (ok) commit_to_pair(&tail->tfull[buf], 0);
+        ++nt;
+      }
+    }
+  } else if (warp == kClearWarp) {
+    // ---- rows of another expert behind a tile's last one, to zeros
+    int slot = 0;
+    uint32_t phase = 0;  // bit i: parity of the next wait for last[i]
+    for (int t = first; t < tiles; t += stride) {
+      const WTile w = wtile_at(p, t);
+      const int steps = w.steps(), rest = w.rest();
+      if (steps == 0) continue;
+      const int at = (slot + steps - 1) % kWStages;
+      slot = (slot + steps) % kWStages;
+      if (rest == 0) continue;
+      if (!bounded_wait_idle_warp(&tail->last[at], (phase >> at) & 1u, failed, p.patience)) break;
+      phase ^= 1u << at;
+      unsigned char* dst = stages + size_t(at) * kWStage;
+      const int some = (-rest) & 15;  // rows to clear: 128 bytes of each of four chunks
+      for (int i = lane; i < some * 32; i += 32)
+        *reinterpret_cast<uint4*>(dst + (i & 3) * kChunk + (rest + (i >> 5)) * 128 +
+                                  ((i >> 2) & 7) * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_at(map_to_rank(&tail->full[at], 0));
+    }
+  } else {
+    // ---- accumulators to weights' gradients; an expert without rows gets zeros
+    const int q = warp & 3;  // the TMEM lanes this warp may read: 32 q ..
+    uint32_t nt = 0;  // tiles with products so far
+    for (int t = first; t < tiles; t += stride) {
+      const WTile w = wtile_at(p, t);
+      const bool some = w.hi > w.lo;
+      if (!some && F32 && p.accumulate) continue;
+      const uint32_t buf = nt & 1u;
+      if (some && !bounded_wait_idle_warp(&tail->tfull[buf], (nt >> 1) & 1u, failed, p.patience))
+        break;
+      tcgen05_fence_after();
+      const int n = w.n0 + rank * kWC + q * 32 + lane;
+      const int64_t at = (int64_t(w.e) * p.N + n) * p.K + w.k0;
+      const int cols = min(2 * kWC, p.K - w.k0);  // a multiple of 8
+      for (int c = 0; c < cols; c += 16) {
+        float2 v[8];
+        if (some) {
+          tmem_ld_x16(tmem + buf * 256 + c + (uint32_t(q) << 21), v);
+          tmem_wait_ld(v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = make_float2(0.0f, 0.0f);
+        }
+        if (n < p.N) {
+          if constexpr (F32) {
+            float* dst = static_cast<float*>(p.dw) + at + c;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // 8 columns: 32 bytes
+              if (c + h * 8 >= cols) break;
+              float4* d = reinterpret_cast<float4*>(dst + h * 8);
+              float2* x = v + h * 4;
+              if (p.accumulate) {
+                const float4 o0 = d[0], o1 = d[1];
+                x[0] = add2(make_float2(o0.x, o0.y), x[0]);
+                x[1] = add2(make_float2(o0.z, o0.w), x[1]);
+                x[2] = add2(make_float2(o1.x, o1.y), x[2]);
+                x[3] = add2(make_float2(o1.z, o1.w), x[3]);
+              }
+              if (p.out32) {
+                Words<8> o;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  o.w[2 * j] = __float_as_uint(x[j].x);
+                  o.w[2 * j + 1] = __float_as_uint(x[j].y);
+                }
+                st_stream_w<8>(reinterpret_cast<Words<8>*>(d), o);
+              } else {
+                d[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+                d[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+              }
+            }
+          } else {
+            uint16_t* dst = static_cast<uint16_t*>(p.dw) + at + c;
+            Words<8> o;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o.w[j] = pack_bf16x2_rn(v[j].x, v[j].y);
+            if (p.out32 && c + 16 <= cols) {
+              st_stream_w<8>(reinterpret_cast<Words<8>*>(dst), o);
+            } else {
+              uint4* d = reinterpret_cast<uint4*>(dst);
+              d[0] = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
+              if (c + 16 <= cols) d[1] = make_uint4(o.w[4], o.w[5], o.w[6], o.w[7]);
+            }
+          }
+        }
+      }
+      if (some) {
+        tcgen05_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at(map_to_rank(&tail->tempty[buf], 0));
+        ++nt;
+      }
+    }
+  }
+
+  __syncwarp();
+  tcgen05_fence_before();
+  cluster_sync_all();  // nothing of either block is in use any more
+  tcgen05_fence_after();
+  if (warp == 1) tmem_dealloc<true>(tmem, 512);
+  if (threadIdx.x == 0 && tail->failed) raise_error(p.dev_err, MP_ERR_TIMEOUT);
+}
+
+template <bool F32>
+cudaError_t launch_wgrad(const WArgs& p, const CUtensorMap& mdy, const CUtensorMap& ma,
+                         cudaStream_t st) {
+  static thread_local bool configured[64] = {};
+  const cudaError_t e = allow_smem(mp_k_expert_wgrad_bf16<F32>, configured);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = int64_t(p.E) * ceil_div(p.N, 2 * kWC) * ceil_div(p.K, 2 * kWC);
+  const int pairs = int(std::min<int64_t>(tiles, sm_count() / 2));
+  return launch_waiting(mp_k_expert_wgrad_bf16<F32>, dim3(unsigned(2 * pairs)), dim3(kWThreads),
+                        kWSmem, st, 0, mdy, ma, p);
+}
+
+}  // namespace
+
+cudaError_t launch_expert_wgrad_bf16(int E, int rows, int N, int K, const void* dy, const void* a,
+                                     const int32_t* expert_offsets, bool f32, bool accumulate,
+                                     void* dw, int32_t* dev_err, cudaStream_t st) {
+  WArgs p = {};
+  p.E = E; p.rows = rows; p.N = N; p.K = K;
+  p.expert_offsets = expert_offsets;
+  p.dw = dw;
+  p.dev_err = dev_err;
+  p.out32 = (reinterpret_cast<uintptr_t>(dw) & 31u) == 0 && (f32 || K % 16 == 0);
+  p.accumulate = accumulate;
+  p.patience = 1 + rows / (1 << 20);
+  CUtensorMap mdy = {}, ma = {};
+  if (rows > 0 && (!make_map_bf16(&mdy, dy, uint64_t(N), uint64_t(rows), 64, kWRows) ||
+                   !make_map_bf16(&ma, a, uint64_t(K), uint64_t(rows), 64, kWRows)))
+    return cudaErrorInvalidValue;
+  return f32 ? launch_wgrad<true>(p, mdy, ma, st) : launch_wgrad<false>(p, mdy, ma, st);
+}
+
+}  // namespace mp

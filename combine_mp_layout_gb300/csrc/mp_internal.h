@@ -247,6 +247,23 @@ cudaError_t launch_swiglu_backward(int rows, int I, const void* gate_up, const f
                                    float* d_gate_up_scales, float* d_row_weights,
                                    cudaStream_t stream);
 
+// The same products on bf16 rows with bf16 weights; the weights' gradient in bf16,
+// or in fp32 and then, with accumulate, added to dw.
+cudaError_t launch_expert_matmul_bf16(int E, int rows, int N, int K, bool dgrad, const void* a,
+                                      const void* w, const int32_t* expert_offsets, void* out,
+                                      int32_t* dev_err, cudaStream_t stream);
+cudaError_t launch_expert_wgrad_bf16(int E, int rows, int N, int K, const void* dy, const void* a,
+                                     const int32_t* expert_offsets, bool f32, bool accumulate,
+                                     void* dw, int32_t* dev_err, cudaStream_t stream);
+
+// The gated activation on bf16 rows, and its gradient.
+cudaError_t launch_swiglu_bf16(int rows, int I, const void* gate_up, const float* row_weights,
+                               const int32_t* num_rows, void* out, cudaStream_t stream);
+cudaError_t launch_swiglu_backward_bf16(int rows, int I, const void* gate_up,
+                                        const float* row_weights, const void* d_out,
+                                        const int32_t* num_rows, void* d_gate_up,
+                                        float* d_row_weights, cudaStream_t stream);
+
 // Weights of the low-latency layout's slots to their rows, or gradients back.
 cudaError_t launch_ll_row_weights(int64_t slots, int64_t rows, bool back, const int32_t* slot_row,
                                   const float* in, float* out, cudaStream_t stream);

@@ -822,6 +822,89 @@ int mp_swiglu_backward_e4m3(int rows, int I, const void *gate_up, const float *r
                             float *d_gate_up_scales, float *d_row_weights, mp_stream_t stream);
 
 /*
+ * mp_expert_matmul_bf16 -- each expert's product with its weights on bf16 rows, as
+ * the bf16 dispatches (mp_dispatch_ll with MP_BF16) leave them:
+ *   out[r][n] = bf16( sum over k of a[r][k] * w[e][n][k] )
+ * for the rows expert_offsets[e] <= r < expert_offsets[e+1] of every expert e;
+ * products exact, sums fp32, one rounding.
+ *   in   a               bf16 [rows][K]
+ *   in   w               bf16 [E][N][K]
+ *   in   expert_offsets  int32 [E+1], or NULL for E == 1 (all rows)
+ *   out  out             bf16 [rows][N]; rows of no expert are not written
+ * Checks: 1 <= E <= 8192, rows >= 0, N and K multiples of 8 (both > 0), rows, N, K
+ *   <= 2^31 - 1025, N*K < 2^39, (rows/256 + E) * ceil(N/256) < 2^31 - 4096,
+ *   non-NULL buffers (a and out when rows == 0), a, w and out 16-byte aligned.
+ * Device errors: MP_ERR_CAPACITY (an offset past `rows`; it is cut off there),
+ *   MP_ERR_INVALID_ARG (offsets that decrease or are negative; nothing is
+ *   written then), MP_ERR_TIMEOUT.
+ */
+int mp_expert_matmul_bf16(int E, int rows, int N, int K, const void *a, const void *w,
+                          const int32_t *expert_offsets, void *out, int32_t *dev_err,
+                          mp_stream_t stream);
+
+/*
+ * mp_expert_matmul_dgrad_bf16 -- the gradient of the rows, with the same weights as
+ * they are stored (no transposed copy):
+ *   dx[r][k] = bf16( sum over n of dy[r][n] * w[e][n][k] )
+ *   in   dy  bf16 [rows][N];  out  dx  bf16 [rows][K]
+ * Checks and device errors as mp_expert_matmul_bf16, with
+ *   (rows/256 + E) * ceil(K/256) < 2^31 - 4096.
+ */
+int mp_expert_matmul_dgrad_bf16(int E, int rows, int N, int K, const void *dy, const void *w,
+                                const int32_t *expert_offsets, void *dx, int32_t *dev_err,
+                                mp_stream_t stream);
+
+/*
+ * mp_expert_matmul_wgrad_bf16 -- the gradient of the weights:
+ *   g[e][n][k] = sum over the rows r of expert e of dy[r][n] * a[r][k]
+ * products exact, sums fp32; dw = bf16(g) (MP_BF16), dw = g (MP_FP32), or dw += g
+ * (MP_FP32 with accumulate != 0: one fp32 addition per weight, so that several
+ * batches' gradients add up in one array).  Experts without rows get zeros, or keep
+ * what they have with accumulate (so do, here, those whose offsets decrease; a
+ * negative offset counts as 0).  Rows of other experts, and rows of none, do not
+ * count whatever they hold.  Every call gives the same bits.
+ *   in   dy  bf16 [rows][N];  a  bf16 [rows][K]
+ *   out  dw  bf16 or fp32 [E][N][K]
+ * Checks: as mp_expert_matmul_bf16 (but of the tiles), dw_dtype MP_BF16 or MP_FP32,
+ *   accumulate 0 for MP_BF16, E * ceil(N/256) * ceil(K/256) < 2^31 - 4096.
+ * Device errors: MP_ERR_CAPACITY, MP_ERR_INVALID_ARG, MP_ERR_TIMEOUT as there.
+ */
+int mp_expert_matmul_wgrad_bf16(int E, int rows, int N, int K, const void *dy, const void *a,
+                                const int32_t *expert_offsets, int dw_dtype, int accumulate,
+                                void *dw, int32_t *dev_err, mp_stream_t stream);
+
+/*
+ * mp_swiglu_bf16 -- the gated activation between an expert's two bf16 products:
+ *   out[r][i] = bf16( w[r] * g / (1 + exp(-g)) * u ),
+ *   g = gate_up[r][i], u = gate_up[r][I + i],
+ * in fp32 (the exponential as in mp_swiglu_e4m3), one rounding.
+ *   in   gate_up      bf16 [rows][2I]: the gate's channels, then the up ones
+ *   in   row_weights  fp32 [rows], or NULL for 1 (see mp_swiglu_e4m3)
+ *   in   num_rows     int32 [1] on the device: rows in use, or NULL for all
+ *   out  out          bf16 [rows][I]; rows past num_rows are not written
+ * Checks: rows >= 0, I > 0, I % 8 == 0, I <= 2^31 - 4097, non-NULL buffers when
+ *   rows > 0, gate_up and out 16-byte aligned.  No device errors (num_rows is cut
+ *   to [0, rows]).
+ */
+int mp_swiglu_bf16(int rows, int I, const void *gate_up, const float *row_weights,
+                   const int32_t *num_rows, void *out, mp_stream_t stream);
+
+/*
+ * mp_swiglu_backward_bf16 -- its gradient:
+ *   with s = 1 / (1 + exp(-g)) and d = w[r] * d_out[r][i]:
+ *   d_gate_up[r][i] = bf16( d * u * s * (1 + g * (1 - s)) ),
+ *   d_gate_up[r][I + i] = bf16( d * g * s ),
+ *   d_row_weights[r] = sum over i of d_out[r][i] * g * s * u   (fp32, fixed order)
+ *   in   d_out          bf16 [rows][I]
+ *   out  d_gate_up      bf16 [rows][2I]
+ *   out  d_row_weights  fp32 [rows], or NULL
+ * Checks as mp_swiglu_bf16, d_out and d_gate_up 16-byte aligned too.
+ */
+int mp_swiglu_backward_bf16(int rows, int I, const void *gate_up, const float *row_weights,
+                            const void *d_out, const int32_t *num_rows, void *d_gate_up,
+                            float *d_row_weights, mp_stream_t stream);
+
+/*
  * mp_ll_row_weights -- the routing weights of the low-latency layout's slots at
  * the rows they were given, for mp_swiglu_e4m3:
  *   row_weights[slot_row[s][t][k]] = topk_weights[s][t][k]

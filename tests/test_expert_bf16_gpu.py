@@ -1,0 +1,558 @@
+"""The expert layer's operators on bf16 rows (products with bf16 weights, their gradients, gated
+activation) against plain implementations in 64 bits.
+
+Tolerances (U = 2^-24, the unit roundoff of fp32; bf16 rounds by at most 2^-8 of a value):
+  * products: one bf16 rounding, plus fp32 sums of n terms: n * 2 U times the sum of the terms'
+    magnitudes (2 U per step: the tensor core may cut instead of round).  Over many outputs the
+    bf16 rounding is about uniform, so its 2-norm is at most 2^-8 / sqrt(3).  Small whole numbers
+    make every sum exact: bit-equal there.
+  * activation: the fast exponential and reciprocal and four products, 1e-5 of a value, and the
+    bf16 rounding (of a subnormal result: half of bf16's smallest step, 2^-134).
+"""
+import math
+from concurrent.futures import ThreadPoolExecutor
+
+import numpy as np
+import pytest
+import torch
+
+from combine_mp_layout_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DEV = "cuda"
+BF = torch.bfloat16
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def zeros(shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype, device=DEV)
+
+
+def values(shape, g, exact):
+    x = torch.randn(shape, generator=g, device=DEV)
+    return ((x * 1.2).round().clamp(-2, 2) if exact else x).to(BF)
+
+
+def offsets(counts, first=0):
+    return torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+                            + first).to(torch.int32).to(DEV)
+
+
+def rounded(y, dtype=BF):
+    """64-bit values that fp32 holds exactly, in the output's type."""
+    return y.to(torch.float32).to(dtype).double()
+
+
+class Guarded:
+    """A buffer between two guard regions of 4 KB; `intact` after the calls."""
+
+    def __init__(self, shape, dtype, fill=7.0):
+        n = math.prod(shape) * torch.empty(0, dtype=dtype).element_size()
+        self.raw = torch.full((4096 + n + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+        self.n = n
+        self.t = self.raw[4096:4096 + n].view(dtype).view(shape)
+        self.t.fill_(fill)
+
+    def intact(self):
+        return bool((self.raw[:4096] == 0x5A).all()) and bool((self.raw[4096 + self.n:] == 0x5A).all())
+
+
+# ------------------------------------------------------------------ products
+
+MM = [  # counts, N, K, slack rows at the end
+    ([1], 8, 8, 0),
+    ([1], 16, 72, 1),
+    ([3], 48, 256, 2),
+    ([0, 1, 127, 129, 0], 136, 392, 7),
+    ([128, 256, 5], 264, 64, 0),
+    ([31, 33, 64, 65], 512, 1024, 3),
+    ([1, 1, 0, 1, 1, 0, 1], 1024, 512, 0),
+    ([700], 640, 384, 0),
+    ([257, 0, 513], 256, 7168, 1),
+    ([1], 4096, 2048, 0),
+    ([2500], 384, 264, 0),
+    ([40] * 90, 520, 200, 0),
+]
+
+
+@pytest.mark.parametrize("exact", [True, False])
+@pytest.mark.parametrize("kind", ["fwd", "dgrad"])
+@pytest.mark.parametrize("counts,N,K,slack", MM)
+def test_matmul(kind, counts, N, K, slack, exact):
+    g = gen(11)
+    E, rows = len(counts), sum(counts) + slack
+    src, dst = (K, N) if kind == "fwd" else (N, K)
+    a, w = values((rows, src), g, exact), values((E, N, K), g, exact)
+    off, err = offsets(counts), zeros(1, torch.int32)
+    buf = Guarded((rows, dst), BF)
+    f = B.mp_expert_matmul_bf16 if kind == "fwd" else B.mp_expert_matmul_dgrad_bf16
+    B.check(f(E, rows, N, K, a, w, off, buf.t, err))
+    torch.cuda.synchronize()
+    assert int(err) == 0 and buf.intact()
+    out = buf.t
+    lo, se, sy = 0, 0.0, 0.0
+    for e, n in enumerate(counts):
+        x = a[lo:lo + n].double()
+        we = w[e].double().t() if kind == "fwd" else w[e].double()
+        y, got = x @ we, out[lo:lo + n].double()
+        if exact:
+            assert torch.equal(got, rounded(y))
+        else:
+            tol = 2.0 ** -8 * y.abs() + src * 2 * U * (x.abs() @ we.abs())
+            assert float(((got - y).abs() - tol).max() if n else 0.0) <= 0.0
+            se += float((got - y).square().sum())
+            sy += float(y.square().sum())
+        lo += n
+    if not exact and sum(counts) * dst >= 4096:
+        assert math.sqrt(se / sy) <= 2.0 ** -8 / math.sqrt(3) + 1e-4
+    assert bool((out[lo:] == 7.0).all())
+
+
+WG = [([1], 8, 8, 0), ([0, 1, 63, 65, 0], 136, 392, 7), ([64, 128, 5], 256, 264, 0),
+      ([300, 0, 411], 384, 640, 1), ([5, 70, 0, 0, 130, 64, 1, 2], 248, 1024, 0),
+      ([1500], 520, 1160, 0), ([7] * 300, 256, 296, 0)]
+
+
+@pytest.mark.parametrize("exact", [True, False])
+@pytest.mark.parametrize("out", ["bf16", "fp32", "add"])
+@pytest.mark.parametrize("counts,N,K,slack", WG)
+def test_wgrad(counts, N, K, slack, out, exact):
+    g = gen(12)
+    E, rows = len(counts), sum(counts) + slack
+    dy, a = values((rows, N), g, exact), values((rows, K), g, exact)
+    before = values((E, N, K), g, exact).float()
+    buf, err = Guarded((E, N, K), BF if out == "bf16" else torch.float32), zeros(1, torch.int32)
+    if out == "add":
+        buf.t.copy_(before)
+    B.check(B.mp_expert_matmul_wgrad_bf16(E, rows, N, K, dy, a, offsets(counts), out == "add",
+                                          buf.t, err))
+    torch.cuda.synchronize()
+    assert int(err) == 0 and buf.intact()
+    lo = 0
+    for e, n in enumerate(counts):
+        x, d = a[lo:lo + n].double(), dy[lo:lo + n].double()
+        y, got = d.t() @ x, buf.t[e].double()
+        size = d.abs().t() @ x.abs()
+        if out == "add":
+            y = y + before[e].double()
+        if exact:
+            assert torch.equal(got, rounded(y, buf.t.dtype))
+        else:
+            last = 2.0 ** -8 if out == "bf16" else U
+            tol = n * 2 * U * size + last * y.abs()
+            if out == "add":  # the sum is rounded, and then it plus what was there
+                tol = tol + U * size
+            assert float(((got - y).abs() - tol).max()) <= 0.0
+        lo += n
+
+
+@pytest.mark.parametrize("counts", [[63, 65], [1, 1, 130], [33, 0, 64, 96]])
+def test_wgrad_takes_no_row_of_another_expert(counts):
+    """Rows of NaN and infinity (in other experts, and past the last one) do not count."""
+    g = gen(13)
+    N, K, E = 264, 136, len(counts)
+    rows = sum(counts) + 3
+    dy, a = values((rows, N), g, True), values((rows, K), g, True)
+    off, err = offsets(counts), zeros(1, torch.int32)
+    lo = 0
+    for e, n in enumerate(counts):
+        d, x = torch.full_like(dy, math.nan), torch.full_like(a, math.inf)
+        d[lo:lo + n], x[lo:lo + n] = dy[lo:lo + n], a[lo:lo + n]
+        dw = zeros((E, N, K), BF)
+        B.check(B.mp_expert_matmul_wgrad_bf16(E, rows, N, K, d, x, off, False, dw, err))
+        torch.cuda.synchronize()
+        assert torch.equal(dw[e].double(), rounded(d[lo:lo + n].double().t() @ x[lo:lo + n].double()))
+        lo += n
+    assert int(err) == 0
+
+
+def test_dense_without_offsets_and_gradient_identity():
+    """E = 1 without offsets is the dense product; <dy, a w^T> = <dy w, a> = <dy^T a, w>."""
+    g = gen(14)
+    rows, N, K = 200, 248, 384
+    a, dy, w = values((rows, K), g, True), values((rows, N), g, True), values((1, N, K), g, True)
+    y, dx, dw = zeros((rows, N), BF), zeros((rows, K), BF), zeros((1, N, K))
+    err = zeros(1, torch.int32)
+    B.check(B.mp_expert_matmul_bf16(1, rows, N, K, a, w, None, y, err))
+    B.check(B.mp_expert_matmul_dgrad_bf16(1, rows, N, K, dy, w, None, dx, err))
+    B.check(B.mp_expert_matmul_wgrad_bf16(1, rows, N, K, dy, a, None, False, dw, err))
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    p = [y.double() * dy.double(), dx.double() * a.double(), dw.double() * w.double()]
+    v = [float(t.sum()) for t in p]
+    assert max(v) - min(v) <= 2 * 2.0 ** -8 * min(float(t.abs().sum()) for t in p)
+
+
+def test_gradients_against_differences():
+    """Whole numbers: moving one factor by h moves the product's sum by h times the gradient."""
+    g = gen(15)
+    counts, N, K = [5, 0, 9], 24, 40
+    rows, E = sum(counts), 3
+    a, dy, w = values((rows, K), g, True), values((rows, N), g, True), values((E, N, K), g, True)
+    off, err = offsets(counts), zeros(1, torch.int32)
+    dx, dw = zeros((rows, K), BF), zeros((E, N, K))
+    B.check(B.mp_expert_matmul_dgrad_bf16(E, rows, N, K, dy, w, off, dx, err))
+    B.check(B.mp_expert_matmul_wgrad_bf16(E, rows, N, K, dy, a, off, False, dw, err))
+
+    def objective(a, w):
+        y = zeros((rows, N), BF)
+        B.check(B.mp_expert_matmul_bf16(E, rows, N, K, a, w, off, y, err))
+        return float((y.double() * dy.double()).sum())
+    for r, k in ((0, 0), (4, 39), (5, 7), (13, 20)):
+        up, down = a.clone(), a.clone()
+        up[r, k] += 1
+        down[r, k] -= 1
+        assert (objective(up, w) - objective(down, w)) / 2 == float(dx[r, k])
+    for e, n, k in ((0, 0, 0), (0, 23, 39), (1, 3, 3), (2, 11, 17)):
+        up, down = w.clone(), w.clone()
+        up[e, n, k] += 1
+        down[e, n, k] -= 1
+        assert (objective(a, up) - objective(a, down)) / 2 == float(dw[e, n, k])
+    assert int(err) == 0
+
+
+def test_sums_are_fp32():
+    """Sums that cancel at 2^15 and leave 2^-8: no step of the sum has less than 24 bits."""
+    rows, N, K = 40, 256, 512
+    a, w = zeros((rows, K), BF), zeros((1, N, K), BF)
+    a[:, 0], a[:, 511], a[:, 100] = 256.0, -256.0, 2.0 ** -8
+    w[:] = 128.0
+    w[..., 100] = 1.0
+    y, err = zeros((rows, N), BF), zeros(1, torch.int32)
+    B.check(B.mp_expert_matmul_bf16(1, rows, N, K, a, w, None, y, err))
+    torch.cuda.synchronize()
+    assert bool((y == 2.0 ** -8).all())
+
+
+def test_reports_bad_offsets_and_stays_in_bounds():
+    g = gen(16)
+    rows, N, K, E = 100, 128, 128, 3
+    a, w = values((rows, K), g, True), values((E, N, K), g, True)
+    ref = a.double() @ w[0].double().t()
+    for off, bits in (([0, 50, 90, 130], B.MP_ERR_CAPACITY), ([0, 50, 40, 100], B.MP_ERR_INVALID_ARG),
+                      ([-5, 50, 60, 100], B.MP_ERR_INVALID_ARG)):
+        o = torch.tensor(off, dtype=torch.int32, device=DEV)
+        out, dx, dw = (Guarded((rows, N), BF), Guarded((rows, K), BF), Guarded((E, N, K), BF))
+        errs = [zeros(1, torch.int32) for _ in range(3)]
+        B.check(B.mp_expert_matmul_bf16(E, rows, N, K, a, w, o, out.t, errs[0]))
+        B.check(B.mp_expert_matmul_dgrad_bf16(E, rows, N, K, a, w, o, dx.t, errs[1]))
+        B.check(B.mp_expert_matmul_wgrad_bf16(E, rows, N, K, a, a, o, False, dw.t, errs[2]))
+        torch.cuda.synchronize()
+        assert all(int(e) & bits for e in errs)
+        assert out.intact() and dx.intact() and dw.intact()
+        if bits == B.MP_ERR_CAPACITY:
+            assert torch.equal(out.t[:50].double(), rounded(ref[:50]))
+        else:  # nothing is written
+            assert bool((out.t == 7.0).all()) and bool((dx.t == 7.0).all())
+
+
+def test_nan_and_infinity_stay_in_their_row():
+    g = gen(17)
+    rows, N, K = 140, 256, 256
+    a, w = values((rows, K), g, True), values((2, N, K), g, True)
+    off, err = offsets([70, 70]), zeros(1, torch.int32)
+    clean, dirty = zeros((rows, N), BF), zeros((rows, N), BF)
+    B.check(B.mp_expert_matmul_bf16(2, rows, N, K, a, w, off, clean, err))
+    a[69], a[70, 3] = math.nan, math.inf
+    B.check(B.mp_expert_matmul_bf16(2, rows, N, K, a, w, off, dirty, err))
+    torch.cuda.synchronize()
+    assert bool(dirty[69].isnan().all()) and not bool(dirty[70].isfinite().any())
+    keep = [r for r in range(rows) if r not in (69, 70)]
+    assert torch.equal(clean[keep], dirty[keep])
+    # weights of another expert do not reach a row either, at the end of an odd reduction
+    w2 = values((2, 40, K), g, True)
+    w2[1] = math.nan
+    dy, dx = values((rows, 40), g, True), zeros((rows, K), BF)
+    B.check(B.mp_expert_matmul_dgrad_bf16(2, rows, 40, K, dy, w2, off, dx, err))
+    torch.cuda.synchronize()
+    assert torch.equal(dx[:70].double(), rounded(dy[:70].double() @ w2[0].double()))
+    assert bool(dx[70:].isnan().all()) and int(err) == 0
+
+
+def test_rows_past_32_bit_offsets():
+    """Elements past 2^31 in the rows, in the output and in the weights."""
+    g = gen(18)
+    err = zeros(1, torch.int32)
+    for N, K in ((128, 7168), (7168, 128)):
+        rows = 300_000
+        off = torch.tensor([rows - 130, rows - 5, rows], dtype=torch.int32, device=DEV)
+        a = zeros((rows, K), BF)
+        a[-130:] = values((130, K), g, True)
+        w = values((2, N, K), g, True)
+        out = zeros((rows, N), BF)
+        B.check(B.mp_expert_matmul_bf16(2, rows, N, K, a, w, off, out, err))
+        ad, wd = a[-130:].double(), w.double()
+        y = torch.cat([ad[:125] @ wd[0].t(), ad[125:] @ wd[1].t()])
+        torch.cuda.synchronize()
+        assert torch.equal(out[-130:].double(), rounded(y))
+        assert float(out[:-130].abs().max()) == 0.0
+        if N == 128:
+            dy, dw = zeros((rows, N), BF), zeros((2, N, K))
+            dy[-130:] = values((130, N), g, True)
+            B.check(B.mp_expert_matmul_wgrad_bf16(2, rows, N, K, dy, a, off, False, dw, err))
+            torch.cuda.synchronize()
+            dd = dy[-130:].double()
+            assert torch.equal(dw[0].double(), dd[:125].t() @ ad[:125])
+            assert torch.equal(dw[1].double(), dd[125:].t() @ ad[125:])
+        del a, out
+    E, N, K = 600, 2048, 2048  # 2.5e9 weights
+    w = zeros((E, N, K), BF)
+    w[-1] = values((N, K), g, True)
+    a = values((3, K), g, True)
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    off[-1] = 3
+    for rows in (3, 3000):  # the rows that there is room for choose the form
+        room, out = zeros((rows, K), BF), zeros((rows, N), BF)
+        room[:3] = a
+        B.check(B.mp_expert_matmul_bf16(E, rows, N, K, room, w, off, out, err))
+        torch.cuda.synchronize()
+        assert torch.equal(out[:3].double(), rounded(a.double() @ w[-1].double().t()))
+    del w
+    dw = torch.full((E, N, K), 7.0, dtype=BF, device=DEV)
+    dy = values((3, N), g, True)
+    B.check(B.mp_expert_matmul_wgrad_bf16(E, 3, N, K, dy, a, off, False, dw, err))
+    torch.cuda.synchronize()
+    assert torch.equal(dw[-1].double(), rounded(dy.double().t() @ a.double()))
+    assert all(float(dw[e].abs().max()) == 0.0 for e in (0, 299, 598))
+    assert int(err) == 0
+
+
+def test_without_rows_and_many_experts():
+    g = gen(19)
+    err = zeros(1, torch.int32)
+    none, off = zeros((0, 128), BF), zeros(3, torch.int32)
+    dw, kept = torch.full((2, 128, 128), 7.0, dtype=BF, device=DEV), zeros((2, 128, 128)) + 7
+    B.check(B.mp_expert_matmul_wgrad_bf16(2, 0, 128, 128, none, none, off, False, dw, err))
+    B.check(B.mp_expert_matmul_wgrad_bf16(2, 0, 128, 128, none, none, off, True, kept, err))
+    w = values((2, 128, 128), g, True)
+    B.check(B.mp_expert_matmul_bf16(2, 0, 128, 128, none, w, off, none, err))
+    B.check(B.mp_expert_matmul_dgrad_bf16(2, 0, 128, 128, none, w, off, none, err))
+    E, N, K = 8192, 16, 136
+    counts = np.zeros(E, np.int64)
+    counts[[3, 4000, 8191]] = [2, 1, 130]
+    rows = int(counts.sum())
+    a, w = values((rows, K), g, True), values((E, N, K), g, True)
+    out = zeros((rows, N), BF)
+    B.check(B.mp_expert_matmul_bf16(E, rows, N, K, a, w, offsets(counts), out, err))
+    torch.cuda.synchronize()
+    assert int(err) == 0 and float(dw.abs().max()) == 0.0 and bool((kept == 7).all())
+    expert = torch.from_numpy(np.repeat(np.arange(E), counts)).to(DEV)
+    y = torch.einsum("rk,rnk->rn", a.double(), w[expert].double())
+    assert torch.equal(out.double(), rounded(y))
+
+
+def test_on_another_stream():
+    g = gen(20)
+    rows, N, K = 64, 256, 512
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        a, w = values((rows, K), g, True), values((1, N, K), g, True)
+        out, err = zeros((rows, N), BF), zeros(1, torch.int32)
+        B.check(B.mp_expert_matmul_bf16(1, rows, N, K, a, w, None, out, err))
+    side.synchronize()
+    assert torch.equal(out.double(), rounded(a.double() @ w[0].double().t()))
+
+
+@pytest.mark.parametrize("shift", [8, 16])  # elements: 16- and 32-byte aligned
+def test_other_alignments(shift):
+    g = gen(21)
+    counts, N, K = [3, 90], 272, 320
+    rows = sum(counts)
+
+    def moved(t):
+        flat = zeros(t.numel() + shift, t.dtype)
+        flat[shift:] = t.flatten()
+        return flat[shift:].view(t.shape)
+    a, w = moved(values((rows, K), g, True)), moved(values((2, N, K), g, True))
+    dy = moved(values((rows, N), g, True))
+    y, dx, dw = moved(zeros((rows, N), BF)), moved(zeros((rows, K), BF)), moved(zeros((2, N, K), BF))
+    dw32 = zeros(2 * N * K + 4)[4:].view(2, N, K)
+    off, err = offsets(counts), zeros(1, torch.int32)
+    B.check(B.mp_expert_matmul_bf16(2, rows, N, K, a, w, off, y, err))
+    B.check(B.mp_expert_matmul_dgrad_bf16(2, rows, N, K, dy, w, off, dx, err))
+    B.check(B.mp_expert_matmul_wgrad_bf16(2, rows, N, K, dy, a, off, False, dw, err))
+    B.check(B.mp_expert_matmul_wgrad_bf16(2, rows, N, K, dy, a, off, True, dw32, err))
+    torch.cuda.synchronize()
+    for e, s in enumerate((slice(0, 3), slice(3, 93))):
+        x, d, we = a[s].double(), dy[s].double(), w[e].double()
+        assert torch.equal(y[s].double(), rounded(x @ we.t()))
+        assert torch.equal(dx[s].double(), rounded(d @ we))
+        assert torch.equal(dw[e].double(), rounded(d.t() @ x))
+        assert torch.equal(dw32[e].double(), d.t() @ x)
+    assert int(err) == 0
+
+
+@pytest.mark.parametrize("rows", [64, 8192])  # split reductions, whole tiles
+def test_many_and_few_experts_from_two_threads(rows):
+    """The shared memory of a call grows with its experts; threads whose calls alternate do not
+    take it from each other."""
+    N, K = 512, 1024
+    err = zeros(1, torch.int32)
+
+    def prepared(E):
+        g = gen(22)
+        counts = np.zeros(E, np.int64)
+        counts[[0, E - 1]] = [rows - 3, 3]
+        a = values((rows, K), g, True)
+        w = zeros((E, N, K), BF)
+        w[[0, E - 1]] = values((2, N, K), g, True)
+        ad, off = a.double(), offsets(counts)
+        want = torch.cat([ad[:-3] @ w[0].double().t(), ad[-3:] @ w[E - 1].double().t()])
+        want = want.float().to(BF)
+        torch.cuda.synchronize()
+
+        def call():
+            out = zeros((rows, N), BF)
+            status = B.mp_expert_matmul_bf16(E, rows, N, K, a, w, off, out, err)
+            torch.cuda.synchronize()
+            return status, torch.equal(out, want)
+        return call
+    many, few = prepared(4000), prepared(2)
+    with ThreadPoolExecutor(1) as one, ThreadPoolExecutor(1) as other:
+        for _ in range(3):
+            assert one.submit(many).result() == (B.MP_OK, True)
+            assert other.submit(few).result() == (B.MP_OK, True)
+    assert int(err) == 0
+
+
+def test_products_repeat_bit_for_bit_and_in_a_graph():
+    """No order of blocks changes a bit, and the calls can be captured."""
+    g = gen(23)
+    E, rows, N, K = 3, 333, 512, 1024
+    a, dy, w = values((rows, K), g, False), values((rows, N), g, False), values((E, N, K), g, False)
+    off, err = offsets([100, 33, 200]), zeros(1, torch.int32)
+    outs = [zeros((rows, N), BF), zeros((rows, K), BF), zeros((E, N, K), BF), zeros((E, N, K)),
+            zeros((2, N), BF)]
+
+    def calls():
+        B.check(B.mp_expert_matmul_bf16(E, rows, N, K, a, w, off, outs[0], err))
+        B.check(B.mp_expert_matmul_dgrad_bf16(E, rows, N, K, dy, w, off, outs[1], err))
+        B.check(B.mp_expert_matmul_wgrad_bf16(E, rows, N, K, dy, a, off, False, outs[2], err))
+        B.check(B.mp_expert_matmul_wgrad_bf16(E, rows, N, K, dy, a, off, True, outs[3], err))
+        B.check(B.mp_expert_matmul_bf16(1, 2, N, K, a, w, None, outs[4], err))
+    calls()
+    torch.cuda.synchronize()
+    first = [o.clone() for o in outs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, f) for o, f in zip(outs, first))
+    assert int(err) == 0
+
+
+# ------------------------------------------------------------------ activation
+
+def gate_ref(x, I, w):
+    g, u = x.double().split(I, -1)
+    s = torch.sigmoid(g)
+    return g, u, s, (torch.ones(x.shape[0], device=DEV).double() if w is None else w.double())[:, None]
+
+
+def near(got, want):
+    tol = (2.0 ** -8 + 1e-5) * want.abs() + 2.0 ** -134
+    return float(((got.double() - want).abs() - tol).max() if want.numel() else 0.0) <= 0.0
+
+
+@pytest.mark.parametrize("shift", [0, 8])  # 8 elements: 16-byte but not 32-byte aligned
+@pytest.mark.parametrize("rows,I,weighted,used", [
+    (1, 8, False, None), (3, 640, True, None), (64, 2048, False, 40), (130, 520, True, 129),
+    (5, 136, True, 0), (257, 4096, True, None), (4, 4224, False, 9), (1001, 48, True, 900),
+    (9, 64, True, None), (300, 264, False, -3)])
+def test_swiglu_and_backward(rows, I, weighted, used, shift):
+    g = gen(31)
+
+    def bf16(n, size):
+        flat = zeros(n + shift, BF)
+        flat[shift:] = (torch.randn(n, generator=g, device=DEV) * size).to(BF)
+        return flat[shift:]
+    x, d = bf16(rows * 2 * I, 3.0).view(rows, 2 * I), bf16(rows * I, 0.5).view(rows, I)
+    w = torch.randn(rows, generator=g, device=DEV) if weighted else None
+    num = None if used is None else torch.tensor([used], dtype=torch.int32, device=DEV)
+    n = rows if used is None else min(max(used, 0), rows)
+    out, dg, dw = Guarded((rows, I), BF), Guarded((rows, 2 * I), BF), Guarded((rows,), torch.float32)
+    B.check(B.mp_swiglu_bf16(rows, I, x, w, num, out.t))
+    B.check(B.mp_swiglu_backward_bf16(rows, I, x, w, d, num, dg.t, dw.t))
+    torch.cuda.synchronize()
+    gg, u, s, ww = gate_ref(x, I, w)
+    dd = d.double()
+    assert near(out.t[:n], (gg * s * u * ww)[:n])
+    assert near(dg.t[:n], torch.cat([dd * ww * u * s * (1 + gg * (1 - s)), dd * ww * gg * s], -1)[:n])
+    terms = dd * gg * s * u
+    assert bool(((dw.t.double() - terms.sum(-1)).abs() <= 1e-5 * terms.abs().sum(-1))[:n].all())
+    for b in (out, dg, dw):
+        assert b.intact() and bool((b.t[n:] == 7.0).all())
+    first = [b.t.clone() for b in (out, dg, dw)]
+    B.check(B.mp_swiglu_bf16(rows, I, x, w, num, out.t))
+    B.check(B.mp_swiglu_backward_bf16(rows, I, x, w, d, num, dg.t, dw.t))
+    torch.cuda.synchronize()
+    assert all(torch.equal(b.t, f) for b, f in zip((out, dg, dw), first))
+    B.check(B.mp_swiglu_backward_bf16(rows, I, x, w, d, num, dg.t, None))
+    torch.cuda.synchronize()
+    assert torch.equal(dg.t, first[1])
+
+
+def test_swiglu_backward_against_differences():
+    g = gen(32)
+    rows, I = 6, 256
+    x = (torch.randn((rows, 2 * I), generator=g, device=DEV) * 2).to(BF)
+    d = torch.randn((rows, I), generator=g, device=DEV).to(BF)
+    w = torch.rand(rows, generator=g, device=DEV) + 0.5
+    dg, dw = zeros((rows, 2 * I), BF), zeros(rows)
+    B.check(B.mp_swiglu_backward_bf16(rows, I, x, w, d, None, dg, dw))
+    torch.cuda.synchronize()
+
+    def f(x, w):
+        a, u = x.split(I, -1)
+        return (a * torch.sigmoid(a) * u * w[:, None] * d.double()).sum(-1)
+    h = 1e-5
+    xd, wd = x.double(), w.double()
+    for c in (0, 1, 127, 128, 255, 256, 300, 511):
+        v = torch.zeros_like(xd)
+        v[:, c] = h
+        diff = (f(xd + v, wd) - f(xd - v, wd)) / (2 * h)
+        # a difference of sums: 2^-52 of them over h, 1e-7 with room
+        assert bool(((dg.double()[:, c] - diff).abs() <= (2.0 ** -8 + 1e-5) * diff.abs() + 1e-7).all())
+    diff = (f(xd, wd + h) - f(xd, wd - h)) / (2 * h)
+    assert bool(((dw.double() - diff).abs() <= 1e-4 * diff.abs() + 1e-4).all())
+
+
+def test_swiglu_extremes():
+    """Gates far out on both sides, infinities, NaN kept to its place."""
+    x = zeros((2, 512), BF)
+    x[0, :256] = torch.linspace(-80, 120, 256, device=DEV).to(BF)
+    x[0, 256:] = 1.5
+    x[1, :256], x[1, 256:] = 2.0, 1.0
+    x[1, 7], x[1, 8], x[1, 300] = math.nan, math.inf, -math.inf
+    out = zeros((2, 256), BF)
+    B.check(B.mp_swiglu_bf16(2, 256, x, None, None, out))
+    torch.cuda.synchronize()
+    g, u, s, _ = gate_ref(x, 256, None)
+    assert near(out[:1], (g * s * u)[:1])
+    assert bool(out[1, 7].isnan()) and int(out[1].isnan().sum()) == 1
+    assert float(out[1, 8]) == math.inf and float(out[1, 44]) == -math.inf
+
+
+def test_swiglu_past_32_bit_offsets():
+    rows, I = 66_000, 16_392   # 2 * rows * I is past 2^31; I not a multiple of 16
+    x = zeros((rows, 2 * I), BF)
+    x[-1] = torch.randn(2 * I, generator=gen(33), device=DEV).to(BF)
+    out, dg = zeros((rows, I), BF), zeros((rows, 2 * I), BF)
+    B.check(B.mp_swiglu_bf16(rows, I, x, None, None, out))
+    B.check(B.mp_swiglu_backward_bf16(rows, I, x, None, x[:, :I].contiguous(), None, dg, None))
+    torch.cuda.synchronize()
+    g, u, s, _ = gate_ref(x[-1:], I, None)
+    assert near(out[-1:], g * s * u) and float(out[:-1].abs().max()) == 0.0
+    assert near(dg[-1:], torch.cat([g * u * s * (1 + g * (1 - s)), g * g * s], -1))
+    assert float(dg[:-1].abs().max()) == 0.0
