@@ -30,6 +30,7 @@ MP_FP32 = 2
 MP_SOFTMAX = 0
 MP_SIGMOID = 1
 SCALE_BLOCK = 128
+MX_BLOCK = 32
 # formats of the low-latency dispatch's in-kernel quantisation
 MP_Q_E4M3 = 0
 MP_Q_MXFP8 = 1
@@ -105,6 +106,7 @@ def lib() -> ctypes.CDLL:
         L.mp_expert_matmul_bf16.argtypes = [i32] * 4 + [P] * 6
         L.mp_expert_matmul_dgrad_bf16.argtypes = [i32] * 4 + [P] * 6
         L.mp_expert_matmul_wgrad_bf16.argtypes = [i32] * 4 + [P] * 3 + [i32] * 2 + [P] * 3
+        L.mp_expert_matmul_mxfp4.argtypes = [i32] * 4 + [P] * 7
         L.mp_swiglu_bf16.argtypes = [i32] * 2 + [P] * 5
         L.mp_swiglu_backward_bf16.argtypes = [i32] * 2 + [P] * 7
         L.mp_ll_row_weights.argtypes = [i32] * 3 + [P, P, i64, P, P]
@@ -124,7 +126,8 @@ def lib() -> ctypes.CDLL:
                   "mp_expert_matmul_e4m3", "mp_expert_matmul_dgrad_e4m3",
                   "mp_expert_matmul_wgrad_e4m3", "mp_swiglu_e4m3", "mp_swiglu_backward_e4m3",
                   "mp_expert_matmul_bf16", "mp_expert_matmul_dgrad_bf16",
-                  "mp_expert_matmul_wgrad_bf16", "mp_swiglu_bf16", "mp_swiglu_backward_bf16",
+                  "mp_expert_matmul_wgrad_bf16", "mp_expert_matmul_mxfp4", "mp_swiglu_bf16",
+                  "mp_swiglu_backward_bf16",
                   "mp_ll_row_weights", "mp_ll_row_weights_backward"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
@@ -612,6 +615,19 @@ def mp_expert_matmul_wgrad_bf16(E, rows, N, K, dy, a, expert_offsets, accumulate
         MP_FP32 if f32 else MP_BF16, int(bool(accumulate)),
         _arr(dw, "dw", torch.float32 if f32 else torch.bfloat16, E * N * K),
         _arr(dev_err, "dev_err", torch.int32, 1), _raw_stream(stream))
+
+
+def mp_expert_matmul_mxfp4(E, rows, N, K, a, w, w_scales, expert_offsets, out, dev_err,
+                           stream=None) -> int:
+    """out[r] = a[r] w[e]^T on bf16 rows with MXFP4 weights: codes uint8 [E][N][K/2], two a byte,
+    and one UE8M0 scale byte per 32 channels [E][N][K/32]."""
+    return lib().mp_expert_matmul_mxfp4(
+        E, rows, N, K, _arr(a, "a", torch.bfloat16, rows * K),
+        _arr(w, "w", torch.uint8, E * N * (K // 2)),
+        _arr(w_scales, "w_scales", torch.uint8, E * N * (K // MX_BLOCK)),
+        _arr(expert_offsets, "expert_offsets", torch.int32, E + 1),
+        _arr(out, "out", torch.bfloat16, rows * N), _arr(dev_err, "dev_err", torch.int32, 1),
+        _raw_stream(stream))
 
 
 def mp_swiglu_bf16(rows, I, gate_up, row_weights, num_rows, out, stream=None) -> int:

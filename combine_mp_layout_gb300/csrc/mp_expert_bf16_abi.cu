@@ -1,5 +1,5 @@
 // mp_expert_bf16_abi.cu -- the C ABI of the expert layer's operators on bf16 rows
-// (products with bf16 weights, gated activation) declared in include/mp_layout.h:
+// (products with bf16 and 4-bit weights, gated activation) declared in include/mp_layout.h:
 // argument checks, then one launch per call.
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -79,6 +79,16 @@ int mp_expert_matmul_wgrad_bf16(int E, int rows, int N, int K, const void* dy, c
   return status_of(launch_expert_wgrad_bf16(E, rows, N, K, dy, a, expert_offsets,
                                             dw_dtype == MP_FP32, accumulate != 0, dw, dev_err,
                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int mp_expert_matmul_mxfp4(int E, int rows, int N, int K, const void* a, const void* w,
+                           const uint8_t* w_scales, const int32_t* expert_offsets, void* out,
+                           int32_t* dev_err, mp_stream_t stream) {
+  if (!product_args_ok(E, rows, N, K, a, w, true, expert_offsets, out, false, dev_err) ||
+      K % MP_MX_BLOCK != 0 || !w_scales || !tiles_ok(E, rows, N))
+    return MP_ERR_INVALID_ARG;
+  return status_of(launch_expert_matmul_mxfp4(E, rows, N, K, a, w, w_scales, expert_offsets, out,
+                                              dev_err, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int mp_swiglu_bf16(int rows, int I, const void* gate_up, const float* row_weights,

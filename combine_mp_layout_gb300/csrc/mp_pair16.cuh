@@ -3,6 +3,7 @@
 // the ragged rows lies.
 #pragma once
 
+#include <algorithm>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -134,6 +135,240 @@ __device__ __forceinline__ int offset_errors(const int32_t* offsets, int rows, i
   if (offsets == nullptr) return 0;
   const int lo = __ldg(offsets + e), hi = __ldg(offsets + e + 1);
   return (lo < 0 || hi < lo ? MP_ERR_INVALID_ARG : 0) | (hi > rows ? MP_ERR_CAPACITY : 0);
+}
+
+// ---------------------------------------------------------------------------
+// Tiles of the products on ragged rows: 256 output channels (the MMA's M side,
+// 128 per block) by up to 256 rows (its N side), 64 reduction steps per stage.
+// ---------------------------------------------------------------------------
+constexpr int kBC = 128;                  // channels per block: 256 per pair
+constexpr int kBR = 256;                  // most rows per tile
+constexpr int kUnit = 32;                 // rows that a tile is a multiple of
+constexpr int kBK = 64;                   // reduction steps per stage: 128 bytes
+constexpr int kStageC = kBC * kBK * 2;    // bytes of a stage: channels, then rows
+constexpr int kStageR = kBR / 2 * kBK * 2;
+constexpr int kStage = kStageC + kStageR;
+constexpr int kMaxParts = 4;              // pairs that share a tile's reduction: one cluster
+constexpr int kBandTiles = 8;             // row tiles per band of the tile order
+constexpr int kEpiWarps = 4;
+constexpr int kTurn = 16 * 32 * 2;        // bytes of 16 rows x 32 channels
+
+struct RaggedArgs {
+  int E, rows, out_cols, red;             // out_cols, red: N and K, or K and N
+  int stages;
+  int out32;                              // rows of out are 32-byte aligned
+  int patience;                           // of the waits for whole tiles
+  const int32_t* expert_offsets;          // [E + 1], or NULL: one expert with all rows
+  uint16_t* out;                          // bf16 [rows][out_cols]
+  int32_t* dev_err;
+};
+
+// Exclusive prefix over experts of their number of row tiles, into pre[0 .. E].
+// Offsets that are negative or decrease leave no tiles at all (overlapping
+// experts could make more of them than the launcher's check allows for).
+template <int THREADS>
+__device__ void tile_prefix(const RaggedArgs& p, int* pre, int* scan) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.E + THREADS - 1) / THREADS;
+  const int e0 = min(tid * per, p.E), e1 = min(e0 + per, p.E);
+  int sum = 0, bad = 0;
+  for (int e = e0; e < e1; ++e) {
+    int lo, hi;
+    rows_of(p.expert_offsets, p.rows, e, lo, hi);
+    pre[e] = (hi - lo + kBR - 1) / kBR;
+    sum += pre[e];
+    bad |= offset_errors(p.expert_offsets, p.rows, e);
+  }
+  if (bad && blockIdx.x == 0) raise_error(p.dev_err, bad);
+  bad = __syncthreads_or(bad & MP_ERR_INVALID_ARG);
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  int base = 0;
+  for (int w = 0; w < warp; ++w) base += scan[w];
+  int at = base + incl - sum;
+  for (int e = e0; e < e1; ++e) {
+    const int n = pre[e];
+    pre[e] = at;
+    at += n;
+  }
+  if (tid == THREADS - 1) pre[p.E] = bad ? 0 : base + incl;
+  __syncthreads();
+}
+
+struct Tile {
+  int e, row0, nrows, n, col0;  // n: nrows rounded up to whole units
+};
+
+// Tile t in the order: experts ascending; within an expert, bands of kBandTiles
+// row tiles, in a band channels slowest, so that the tiles running at one time
+// share few weight channels and a band's rows.
+__device__ __forceinline__ Tile tile_at(const RaggedArgs& p, const int* pre, int ncol, int t) {
+  int lo = 0, hi = p.E;  // pre[lo] * ncol <= t < pre[hi] * ncol
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] * ncol <= t) lo = mid; else hi = mid;
+  }
+  const int mt = pre[lo + 1] - pre[lo];
+  const int local = t - pre[lo] * ncol;
+  const int band = local / (kBandTiles * ncol);
+  const int rem = local - band * kBandTiles * ncol;
+  const int mb = min(kBandTiles, mt - band * kBandTiles);
+  const int m = band * kBandTiles + rem % mb;
+  int r0, r1;
+  rows_of(p.expert_offsets, p.rows, lo, r0, r1);
+  // the expert's rows in whole units, spread evenly over its tiles
+  const int units = (r1 - r0 + kUnit - 1) / kUnit;
+  const int u0 = int(int64_t(units) * m / mt), u1 = int(int64_t(units) * (m + 1) / mt);
+  Tile tile;
+  tile.e = lo;
+  tile.row0 = r0 + u0 * kUnit;
+  tile.n = (u1 - u0) * kUnit;
+  tile.nrows = min(tile.n, r1 - tile.row0);
+  tile.col0 = rem / mb * 2 * kBC;
+  return tile;
+}
+
+// Every warp's end: nothing of the cluster is in use after it.
+__device__ __forceinline__ void cluster_end() {
+  __syncwarp();
+  tcgen05_fence_before();
+  cluster_sync_all();
+  tcgen05_fence_after();
+}
+
+// A box of a tile's rows: half of them per block, in the smallest of four sizes.
+struct RowMaps {
+  CUtensorMap m[4];                       // 16, 32, 64 and 128 rows
+};
+inline bool make_row_maps(RowMaps* r, const void* a, int red, int rows) {
+  for (int i = 0; i < 4; ++i)
+    if (!make_map_bf16(&r->m[i], a, uint64_t(red), uint64_t(rows), kBK, 16u << i)) return false;
+  return true;
+}
+__device__ __forceinline__ int row_box(int half) {
+  return half > 64 ? 3 : half > 32 ? 2 : half > 16 ? 1 : 0;
+}
+
+// The products of one stage: four K = 16 steps.
+template <bool C_MN>
+__device__ __forceinline__ void stage_products(const unsigned char* stage, uint32_t acc,
+                                               uint32_t idesc, bool first) {
+  const uint32_t sc = smem_addr(stage);
+  const uint64_t dc = smem_desc_sw128(sc, C_MN ? kStageC / 2 : 16, 1024);
+  const uint64_t dr = smem_desc_sw128(sc + kStageC, 16, 1024);
+#pragma unroll
+  for (int k = 0; k < kBK / 16; ++k)
+    mma_f16_pair(acc, dc + (C_MN ? ((k * 16 * 128) >> 4) : ((k * 32) >> 4)),
+                 dr + ((k * 32) >> 4), idesc, !first || k > 0);
+}
+
+// A finished accumulator, this warp's 32 channels from `ch` on, to bf16 rows.
+// `src`: its TMEM lanes and first column; `turn`: 2 * kTurn bytes of its own, in
+// which 16 rows x 32 channels at a time are turned around.
+__device__ __forceinline__ void write_tile(const RaggedArgs& p, const Tile& tl, int ch,
+                                           uint32_t src, unsigned char* turn) {
+  const int lane = threadIdx.x & 31;
+  const int r = lane >> 1, h = (lane & 1) * 16;  // the row and channels that it stores
+  const int left = p.out_cols - (ch + h);        // a multiple of 8 (or <= 0)
+  uint16_t* dst = p.out + int64_t(tl.row0 + r) * p.out_cols + ch + h;
+  float2 v[2][8];
+  tmem_ld_x16(src, v[0]);
+  tmem_wait_ld(v[0]);
+  for (int c0 = 0; c0 < tl.n; c0 += 32) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {  // 16 rows; the next 16 on their way from TMEM
+      const int c = c0 + b * 16;
+      if (c + 16 < tl.n) tmem_ld_x16(src + c + 16, v[b ^ 1]);
+      uint16_t* tw = reinterpret_cast<uint16_t*>(turn + b * kTurn) + lane;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t two = pack_bf16x2_rn(v[b][j].x, v[b][j].y);
+        tw[(2 * j) * 32] = uint16_t(two);
+        tw[(2 * j + 1) * 32] = uint16_t(two >> 16);
+      }
+      __syncwarp();
+      if (c + r < tl.nrows) {
+        const uint4* tr = reinterpret_cast<const uint4*>(turn + b * kTurn + r * 64 + h * 2);
+        const uint4 x = tr[0], y = tr[1];
+        if (p.out32 && left >= 16) {
+          const Words<8> o = {{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}};
+          st_stream_w<8>(reinterpret_cast<Words<8>*>(dst + int64_t(c) * p.out_cols), o);
+        } else {
+          uint4* d = reinterpret_cast<uint4*>(dst + int64_t(c) * p.out_cols);
+          if (left >= 8) d[0] = x;
+          if (left >= 16) d[1] = y;
+        }
+      }
+      if (c + 16 < tl.n) tmem_wait_ld(v[b ^ 1]);
+    }
+  }
+}
+
+// fp32 sums of a part of the reduction into shared memory: [row][channel].
+__device__ __forceinline__ void store_part(const Tile& tl, int q, uint32_t src, void* stages) {
+  float* mine = reinterpret_cast<float*>(stages) + q * 32 + (threadIdx.x & 31);
+  for (int c = 0; c < tl.n; c += 16) {
+    float2 v[8];
+    tmem_ld_x16(src + c, v);
+    tmem_wait_ld(v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      mine[(c + 2 * j) * kBC] = v[j].x;
+      mine[(c + 2 * j + 1) * kBC] = v[j].y;
+    }
+  }
+}
+
+// The parts' sums in ascending order, rounded once: four channels of a row per
+// thread and turn, the rows spread over the blocks that hold the same channels.
+template <int THREADS>
+__device__ __forceinline__ void join_parts(const RaggedArgs& p, const Tile& tl, int rank, int part,
+                                           int parts, const void* stages) {
+  const int ch0 = tl.col0 + rank * kBC;
+  for (int i = part * THREADS + int(threadIdx.x); i < tl.nrows * (kBC / 4);
+       i += parts * THREADS) {
+    const int row = i / (kBC / 4), c4 = i % (kBC / 4) * 4;
+    const float* at = reinterpret_cast<const float*>(stages) + row * kBC + c4;
+    float4 v[kMaxParts];  // all on their way before the first is needed
+#pragma unroll
+    for (int z = 0; z < kMaxParts; ++z)
+      v[z] = z < parts ? ld_cluster_f4(map_to_rank(at, uint32_t(2 * z + rank)))
+                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float4 sum = v[0];
+#pragma unroll
+    for (int z = 1; z < kMaxParts; ++z) {
+      sum.x += v[z].x;
+      sum.y += v[z].y;
+      sum.z += v[z].z;
+      sum.w += v[z].w;
+    }
+    if (ch0 + c4 < p.out_cols) {
+      uint2 o;
+      o.x = pack_bf16x2_rn(sum.x, sum.y);
+      o.y = pack_bf16x2_rn(sum.z, sum.w);
+      *reinterpret_cast<uint2*>(p.out + int64_t(tl.row0 + row) * p.out_cols + ch0 + c4) = o;
+    }
+  }
+}
+
+// How many pairs share a tile's reduction: with few tiles, clusters of two or
+// four, while all of them run at once and each has `least` stages.
+inline int parts_for(int64_t tiles, int stages, int least) {
+  int parts = 1;
+  while (parts < kMaxParts && tiles * 2 * parts <= sm_count() / 2 && stages >= 2 * least * parts)
+    parts *= 2;
+  return parts;
+}
+// Row tiles times channel tiles, at most (one short row tile per expert).
+inline int64_t most_tiles(const RaggedArgs& p) {
+  const int64_t row_tiles = std::min<int64_t>(p.rows, int64_t(p.rows) / kBR + p.E);
+  return row_tiles * ceil_div(p.out_cols, 2 * kBC);
 }
 
 }  // namespace mp

@@ -874,6 +874,25 @@ int mp_expert_matmul_wgrad_bf16(int E, int rows, int N, int K, const void *dy, c
                                 void *dw, int32_t *dev_err, mp_stream_t stream);
 
 /*
+ * mp_expert_matmul_mxfp4 -- mp_expert_matmul_bf16 with 4-bit weights, as
+ * mp_allgatherv_mxfp4 (with R = 1, a weight's rows being the rows) quantises them:
+ *   out[r][n] = bf16( sum over k of a[r][k] * 2^(w_scales[e][n][k/32] - 127) * w[e][n][k] )
+ * The weights are exact in bf16, so are the products; sums fp32, one rounding.
+ *   in   a         bf16 [rows][K]
+ *   in   w         uint8 [E][N][K/2]: two e2m1 codes a byte, the even k in the low
+ *                  nibble (0, 1/2, 1, 3/2, 2, 3, 4, 6; bit 3 the sign)
+ *   in   w_scales  uint8 [E][N][K/32]: UE8M0, 255 makes its 32 weights NaN
+ *   out  out       bf16 [rows][N]; rows of no expert are not written
+ * A weight past bf16's largest number (from 2^128) is infinite.
+ * Checks and device errors as mp_expert_matmul_bf16, with K % 32 == 0 and w_scales
+ *   (of any alignment) not NULL.
+ */
+#define MP_MX_BLOCK 32
+int mp_expert_matmul_mxfp4(int E, int rows, int N, int K, const void *a, const void *w,
+                           const uint8_t *w_scales, const int32_t *expert_offsets, void *out,
+                           int32_t *dev_err, mp_stream_t stream);
+
+/*
  * mp_swiglu_bf16 -- the gated activation between an expert's two bf16 products:
  *   out[r][i] = bf16( w[r] * g / (1 + exp(-g)) * u ),
  *   g = gate_up[r][i], u = gate_up[r][I + i],

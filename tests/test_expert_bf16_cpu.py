@@ -58,6 +58,14 @@ def test_wgrad_rejects(L, bad):
 
 
 @no_gpu
+@pytest.mark.parametrize("bad", BAD[:-11] + BAD[-9:] + [dict(K=48), dict(K=72), dict(s=_p(0))])
+def test_mxfp4_rejects(L, bad):
+    a = dict(MM, s=_p(FAKE + 1), **bad) if "s" not in bad else dict(MM, **bad)
+    assert L.mp_expert_matmul_mxfp4(a["E"], a["rows"], a["N"], a["K"], a["a"], a["w"], a["s"],
+                                    a["off"], a["out"], a["err"], _p(0)) == B.MP_ERR_INVALID_ARG
+
+
+@no_gpu
 @pytest.mark.parametrize("bad", [
     dict(rows=-1), dict(I=0), dict(I=4), dict(I=20), dict(I=2 ** 31 - 4088), dict(x=_p(0)),
     dict(out=_p(0)), dict(x=_p(FAKE + 8)), dict(out=_p(FAKE + 8)), dict(w=_p(FAKE + 2)),

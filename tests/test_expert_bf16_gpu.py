@@ -556,3 +556,189 @@ def test_swiglu_past_32_bit_offsets():
     assert near(out[-1:], g * s * u) and float(out[:-1].abs().max()) == 0.0
     assert near(dg[-1:], torch.cat([g * u * s * (1 + g * (1 - s)), g * g * s], -1))
     assert float(dg[:-1].abs().max()) == 0.0
+
+
+# ------------------------------------------------------------------ 4-bit weights
+
+E2M1 = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+
+
+def fp4_weights(shape, g, low=126, high=128):
+    """Random codes and scale bytes (low to high), and the weights in 64 bits."""
+    E, N, K = shape
+    w = torch.randint(0, 256, (E, N, K // 2), generator=g, device=DEV, dtype=torch.uint8)
+    s = torch.randint(low, high + 1, (E, N, K // 32), generator=g, device=DEV, dtype=torch.uint8)
+    return w, s
+
+
+def fp4_ref(w, s):
+    table = torch.tensor(E2M1 + [-v for v in E2M1], dtype=torch.float64, device=DEV)
+    codes = torch.stack([w & 15, w >> 4], -1).flatten(-2).long()
+    return table[codes] * torch.exp2(s.double() - 127).repeat_interleave(32, -1)
+
+
+MX = [  # counts, N, K, slack rows at the end
+    ([1], 8, 32, 0),
+    ([1], 16, 96, 1),
+    ([3], 48, 256, 2),
+    ([0, 1, 127, 129, 0], 136, 416, 7),
+    ([128, 256, 5], 264, 64, 0),
+    ([31, 33, 64, 65], 512, 1024, 3),
+    ([1, 1, 0, 1, 1, 0, 1], 1024, 512, 0),
+    ([5, 0, 2, 8, 1], 520, 736, 0),
+    ([700], 640, 384, 0),
+    ([257, 0, 513], 256, 7168, 1),
+    ([1], 4096, 2048, 0),
+    ([4], 4096, 7168, 0),
+    ([40] * 90, 520, 224, 0),
+]
+
+
+@pytest.mark.parametrize("exact", [True, False])
+@pytest.mark.parametrize("counts,N,K,slack", MX)
+def test_mxfp4(counts, N, K, slack, exact):
+    g = gen(41)
+    E, rows = len(counts), sum(counts) + slack
+    a = values((rows, K), g, exact)
+    w, s = fp4_weights((E, N, K), g) if exact else fp4_weights((E, N, K), g, 110, 140)
+    ref = fp4_ref(w, s)
+    err, buf = zeros(1, torch.int32), Guarded((rows, N), BF)
+    B.check(B.mp_expert_matmul_mxfp4(E, rows, N, K, a, w, s, offsets(counts), buf.t, err))
+    torch.cuda.synchronize()
+    assert int(err) == 0 and buf.intact()
+    lo = 0
+    for e, n in enumerate(counts):
+        x, we = a[lo:lo + n].double(), ref[e].t()
+        y, got = x @ we, buf.t[lo:lo + n].double()
+        if exact:
+            assert torch.equal(got, rounded(y))
+        else:
+            tol = 2.0 ** -8 * y.abs() + K * 2 * U * (x.abs() @ we.abs())
+            assert float(((got - y).abs() - tol).max() if n else 0.0) <= 0.0
+        lo += n
+    assert bool((buf.t[lo:] == 7.0).all())
+
+
+@pytest.mark.parametrize("rows", [1, 5, 300])
+def test_mxfp4_scales_of_any_size(rows):
+    """One term per output: the weight itself, through all codes and scales that leave it finite
+    (6 * 2^125 is the largest), with a token that brings the product into range."""
+    N, K = 16, 32 * 253
+    w = torch.arange(16, dtype=torch.uint8, device=DEV)  # channel n: code n everywhere
+    w = (w | (w << 4))[:, None].expand(N, K // 2).contiguous()[None]
+    s = torch.arange(253, dtype=torch.uint8, device=DEV)[None].expand(N, 253).contiguous()[None]
+    err = zeros(1, torch.int32)
+    table = torch.tensor(E2M1 + [-v for v in E2M1], dtype=torch.float64, device=DEV)
+    for scale in (0, 1, 3, 60, 126, 127, 128, 129, 130, 200, 251, 252):
+        for factor in (2.0 ** (100 if scale < 127 else -100), 1.0):
+            a, out = zeros((rows, K), BF), zeros((rows, N), BF)
+            a[:, scale * 32 + 7] = factor
+            B.check(B.mp_expert_matmul_mxfp4(1, rows, N, K, a, w, s, None, out, err))
+            torch.cuda.synchronize()
+            want = rounded(table * 2.0 ** (scale - 127) * factor)[None].expand(rows, N)
+            assert torch.equal(out.double(), want), (scale, factor)
+    a = torch.full((rows, K), 2.0 ** -100, dtype=BF, device=DEV)
+    out = zeros((rows, N), BF)
+    s[0, 3, 17] = 255   # of channel 3 alone
+    s[0, 7, 100] = 254  # 6 * 2^127, of channel 7 alone
+    B.check(B.mp_expert_matmul_mxfp4(1, rows, N, K, a, w, s, None, out, err))
+    torch.cuda.synchronize()
+    assert bool(out[:, 3].isnan().all()) and int(out.isnan().sum()) == rows
+    assert bool((out[:, 7] == math.inf).all()) and int(out.isinf().sum()) == rows
+    assert int(err) == 0
+
+
+def test_mxfp4_of_the_librarys_own_quantiser():
+    """Weights as the quantising all-gather leaves them with one rank."""
+    g = gen(42)
+    E, N, K, counts = 3, 136, 256, [4, 0, 70]
+    full = torch.randn((E, N, K), generator=g, device=DEV).to(BF)
+    w, s = zeros((E, N, K // 2), torch.uint8), zeros((E, N, K // 32), torch.uint8)
+    B.check(B.mp_allgatherv_mxfp4(1, K, [E * N], full, w, s))
+    a, err = values((74, K), g, False), zeros(1, torch.int32)
+    out = zeros((74, N), BF)
+    B.check(B.mp_expert_matmul_mxfp4(E, 74, N, K, a, w, s, offsets(counts), out, err))
+    torch.cuda.synchronize()
+    ref = fp4_ref(w, s)
+    # e2m1 rounds by at most a quarter of a value of its block's size
+    assert float((ref - full.double()).norm() / full.double().norm()) < 0.25
+    for sl, e in ((slice(0, 4), 0), (slice(4, 74), 2)):
+        y, size = a[sl].double() @ ref[e].t(), a[sl].double().abs() @ ref[e].abs().t()
+        assert bool(((out[sl].double() - y).abs() <= 2.0 ** -8 * y.abs() + K * 2 * U * size).all())
+    assert int(err) == 0
+
+
+@pytest.mark.parametrize("rows,shift", [(2, 1), (2, 8), (140, 1), (140, 4)])
+def test_mxfp4_alignments_infinities_and_bad_offsets(rows, shift):
+    """Scales at any address; infinity and NaN stay in their row; offsets out of order."""
+    g = gen(43)
+    N, K, E = 264, 512, 2
+    w, s0 = fp4_weights((E, N, K), g)
+    flat = zeros(s0.numel() + shift, torch.uint8)
+    flat[shift:] = s0.flatten()
+    s = flat[shift:].view(s0.shape)
+    a, err = values((rows, K), g, True), zeros(1, torch.int32)
+    ref = fp4_ref(w, s)
+    half = rows // 2
+    off = offsets([half, rows - half])
+    clean, dirty = Guarded((rows, N), BF), Guarded((rows, N), BF)
+    B.check(B.mp_expert_matmul_mxfp4(E, rows, N, K, a, w, s, off, clean.t, err))
+    a2 = a.clone()
+    a2[half - 1, 3], a2[half, 4] = math.nan, math.inf
+    B.check(B.mp_expert_matmul_mxfp4(E, rows, N, K, a2, w, s, off, dirty.t, err))
+    torch.cuda.synchronize()
+    y = torch.cat([a[:half].double() @ ref[0].t(), a[half:].double() @ ref[1].t()])
+    assert torch.equal(clean.t.double(), rounded(y)) and int(err) == 0
+    assert bool(dirty.t[half - 1].isnan().all()) and not bool(dirty.t[half].isfinite().any())
+    keep = [r for r in range(rows) if r not in (half - 1, half)]
+    assert torch.equal(clean.t[keep], dirty.t[keep])
+    for o, bits in (([0, half, rows + 30], B.MP_ERR_CAPACITY), ([0, rows, half], B.MP_ERR_INVALID_ARG),
+                    ([-1, half, rows], B.MP_ERR_INVALID_ARG)):
+        out, e2 = Guarded((rows, N), BF), zeros(1, torch.int32)
+        o = torch.tensor(o, dtype=torch.int32, device=DEV)
+        B.check(B.mp_expert_matmul_mxfp4(E, rows, N, K, a, w, s, o, out.t, e2))
+        torch.cuda.synchronize()
+        assert int(e2) & bits and out.intact()
+        want = rounded(y) if bits == B.MP_ERR_CAPACITY else torch.full_like(y, 7.0)
+        assert torch.equal(out.t.double(), want)
+
+
+def test_mxfp4_many_experts_far_offsets_and_a_graph():
+    g = gen(44)
+    err = zeros(1, torch.int32)
+    E, N, K = 8192, 16, 96
+    counts = np.zeros(E, np.int64)
+    counts[[3, 4000, 8191]] = [2, 1, 130]
+    rows = int(counts.sum())
+    a = values((rows, K), g, True)
+    w, s = fp4_weights((E, N, K), g)
+    out = zeros((rows, N), BF)
+    B.check(B.mp_expert_matmul_mxfp4(E, rows, N, K, a, w, s, offsets(counts), out, err))
+    expert = torch.from_numpy(np.repeat(np.arange(E), counts)).to(DEV)
+    y = torch.einsum("rk,rnk->rn", a.double(), fp4_ref(w[expert], s[expert]))
+    torch.cuda.synchronize()
+    assert torch.equal(out.double(), rounded(y))
+    E, N, K = 1200, 2048, 2048  # 5e9 codes in 2.5e9 bytes
+    w, s = zeros((E, N, K // 2), torch.uint8), zeros((E, N, K // 32), torch.uint8) + 127
+    w[-1], s[-1] = (t[0] for t in fp4_weights((1, N, K), g))
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    off[-1] = 3
+    for rows in (3, 3000):  # the rows that there is room for choose the form
+        room, out = values((rows, K), g, True), zeros((rows, N), BF)
+
+        def call():
+            B.check(B.mp_expert_matmul_mxfp4(E, rows, N, K, room, w, s, off, out, err))
+        call()
+        torch.cuda.synchronize()
+        first = out.clone()
+        assert torch.equal(out[:3].double(), rounded(room[:3].double() @ fp4_ref(w[-1], s[-1]).t()))
+        assert float(out[3:].abs().max() if rows > 3 else 0.0) == 0.0
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        for _ in range(3):
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, first)
+    assert int(err) == 0
