@@ -171,12 +171,17 @@ class RSVPlan:
 class MoELayerPlan:
     """One expert layer: tokens x [R][N][H] and router logits [R][N][E] in, bf16 [R][N][H] out.
 
-    Expert e computes w_down[e] (silu(g) * u), (g, u) = w_gate_up[e] x, on e4m3 rows; its
-    weights are e4m3 with one fp32 scale per 128 x 128 block: w_gate_up [E][2I][H] (the gate's
-    channels first) and w_down [E][H][I].  ``forward`` leaves what ``backward`` needs in the
-    plan's buffers.
+    Expert e computes w_down[e] (silu(g) * u), (g, u) = w_gate_up[e] x, with w_gate_up [E][2I][H]
+    (the gate's channels first) and w_down [E][H][I].  ``weights`` says what these are, and with
+    it what the rows are dispatched and computed in:
+      * "e4m3": codes with one fp32 scale per 128 x 128 block, rows quantised to e4m3;
+      * "bf16": bf16 weights and rows (no scales: None); weights' gradients in ``grad_dtype``,
+        bf16 or fp32;
+      * "mxfp4": 4-bit codes with one UE8M0 scale byte per 32 channels, bf16 rows; forward only
+        (``train=False``).
+    ``forward`` leaves what ``backward`` needs in the plan's buffers.
 
-    The weights' gradients are sums in fp32 of products of e4m3 rows held in f16: relative to
+    For e4m3 the weights' gradients are sums in fp32 of products of e4m3 rows held in f16: relative to
     the largest scale of their 128 channels in the expert's rows, so rows whose scale is
     below 2^-19 of it lose bits and below 2^-30 are lost (``mp_expert_matmul_wgrad_e4m3``).
     """
@@ -184,11 +189,20 @@ class MoELayerPlan:
     def __init__(self, R: int, N: int, K: int, E: int, H: int, I: int, scoring: str = "softmax",
                  normalize: bool = True, scale: float = 1.0, loss_coef: float = 0.01,
                  logits_dtype=torch.float32, recv_capacity: int | None = None, train: bool = True,
-                 device="cuda"):
+                 device="cuda", weights: str = "e4m3", grad_dtype=torch.bfloat16):
         if scoring not in ("softmax", "sigmoid"):
             raise ValueError("scoring must be softmax or sigmoid")
-        if H % B.SCALE_BLOCK or I % B.SCALE_BLOCK:
-            raise ValueError("H and I must be multiples of %d" % B.SCALE_BLOCK)
+        blocks = {"e4m3": B.SCALE_BLOCK, "bf16": 8, "mxfp4": B.MX_BLOCK}
+        if weights not in blocks:
+            raise ValueError("weights must be e4m3, bf16 or mxfp4")
+        if H % blocks[weights] or I % blocks[weights]:
+            raise ValueError("H and I must be multiples of %d" % blocks[weights])
+        if weights == "mxfp4" and train:
+            raise ValueError("4-bit weights have no backward pass: train must be False")
+        if grad_dtype not in ((torch.bfloat16, torch.float32) if weights == "bf16"
+                              else (torch.bfloat16,)):
+            raise ValueError("weights' gradients are bf16, or fp32 for bf16 weights")
+        self.weights = weights
         self.R, self.N, self.K, self.E, self.H, self.I = R, N, K, E, H, I
         self.scoring = B.MP_SOFTMAX if scoring == "softmax" else B.MP_SIGMOID
         self.normalize, self.scale, self.loss_coef = normalize, scale, loss_coef
@@ -210,29 +224,71 @@ class MoELayerPlan:
         # expert-major rows
         self.expert_offsets, self.expert_src_offsets = _i32(E + 1, dev), _i32((E, R), dev)
         self.recv_src_token, self.slot_row = _i32(max(cap, 1), dev), _i32((R, N, K), dev)
-        self.recv_x, self.recv_scales = buf((cap, H), f8), buf((cap, H // nb), f32)
+        # rows between the operators: e4m3 with scales, or bf16 without
+
+        def rows(width):
+            if weights == "e4m3":
+                return buf((cap, width), f8), buf((cap, width // nb), f32)
+            return buf((cap, width), bf16), None
+        self.recv_x, self.recv_scales = rows(H)
         self.row_weights = buf(cap, f32)
         # experts
         self.gate_up = buf((cap, 2 * I), bf16)
-        self.z, self.z_scales = buf((cap, I), f8), buf((cap, I // nb), f32)
+        self.z, self.z_scales = rows(I)
         self.y = buf((cap, H), bf16)
         self.ones = torch.ones((R, N, K), dtype=f32, device=dev)
         self.out = buf((R, N, H), bf16)
         if train:
-            self.dy, self.dy_scales = buf((cap, H), f8), buf((cap, H // nb), f32)
+            self.dy, self.dy_scales = rows(H)
             self.dz = buf((cap, I), bf16)
-            self.d_gate_up = buf((cap, 2 * I), f8)
-            self.d_gate_up_scales = buf((cap, 2 * I // nb), f32)
+            self.d_gate_up, self.d_gate_up_scales = rows(2 * I)
             self.d_row_weights = buf(cap, f32)
             self.d_rows = buf((cap, H), bf16)
             self.d_x = buf((R, N, H), bf16)
-            self.d_w_gate_up, self.d_w_down = buf((E, 2 * I, H), bf16), buf((E, H, I), bf16)
+            self.d_w_gate_up = buf((E, 2 * I, H), grad_dtype)
+            self.d_w_down = buf((E, H, I), grad_dtype)
             self.d_topk_weights = buf((R, N, K), f32)
             self.d_logits = buf((R, N, E), logits_dtype)
 
     @property
     def _num_rows(self):
         return self.expert_offsets[self.E:]
+
+    # The operators of each kind of weights, with the plan's sizes.
+
+    def _product(self, N, K, rows, scales, w, w_scales, out, stream):
+        size = (self.E, self.cap, N, K)
+        if self.weights == "bf16":
+            B.check(B.mp_expert_matmul_bf16(*size, rows, w, self.expert_offsets, out, self.dev_err,
+                                            stream), "mp_expert_matmul_bf16")
+        elif self.weights == "mxfp4":
+            B.check(B.mp_expert_matmul_mxfp4(*size, rows, w, w_scales, self.expert_offsets, out,
+                                             self.dev_err, stream), "mp_expert_matmul_mxfp4")
+        else:
+            B.check(B.mp_expert_matmul_e4m3(*size, rows, scales, w, w_scales, self.expert_offsets,
+                                            out, self.dev_err, stream), "mp_expert_matmul_e4m3")
+
+    def _rows_grad(self, N, K, dy, dy_scales, w, w_scales, dx, stream):
+        size = (self.E, self.cap, N, K)
+        if self.weights == "bf16":
+            B.check(B.mp_expert_matmul_dgrad_bf16(*size, dy, w, self.expert_offsets, dx,
+                                                  self.dev_err, stream),
+                    "mp_expert_matmul_dgrad_bf16")
+        else:
+            B.check(B.mp_expert_matmul_dgrad_e4m3(*size, dy, dy_scales, w, w_scales,
+                                                  self.expert_offsets, dx, self.dev_err, stream),
+                    "mp_expert_matmul_dgrad_e4m3")
+
+    def _weights_grad(self, N, K, dy, dy_scales, rows, scales, dw, accumulate, stream):
+        size = (self.E, self.cap, N, K)
+        if self.weights == "bf16":
+            B.check(B.mp_expert_matmul_wgrad_bf16(*size, dy, rows, self.expert_offsets, accumulate,
+                                                  dw, self.dev_err, stream),
+                    "mp_expert_matmul_wgrad_bf16")
+        else:
+            B.check(B.mp_expert_matmul_wgrad_e4m3(*size, dy, dy_scales, rows, scales,
+                                                  self.expert_offsets, dw, self.dev_err, stream),
+                    "mp_expert_matmul_wgrad_e4m3")
 
     def forward(self, x, logits, w_gate_up, w_gate_up_scales, w_down, w_down_scales, bias=None,
                 active=None, stream=None):
@@ -246,52 +302,61 @@ class MoELayerPlan:
                            self.dev_err, self.workspace, stream), "mp_route")
         # (small batches: the dispatch that counts for itself is one kernel)
         counts = self.num_tokens_per_expert if R * N * K > 16384 else None
-        B.check(B.mp_dispatch_ll_quant(R, N, K, E, H, B.MP_Q_E4M3, 0, x, self.topk_idx, counts,
-                                       cap, self.expert_offsets, self.expert_src_offsets,
-                                       self.recv_src_token, self.slot_row, self.recv_x,
-                                       self.recv_scales, self.dev_err, stream),
-                "mp_dispatch_ll_quant")
+        placed = (self.expert_offsets, self.expert_src_offsets, self.recv_src_token, self.slot_row,
+                  self.recv_x, self.recv_scales, self.dev_err, stream)
+        if self.weights == "e4m3":
+            B.check(B.mp_dispatch_ll_quant(R, N, K, E, H, B.MP_Q_E4M3, 0, x, self.topk_idx, counts,
+                                           cap, *placed), "mp_dispatch_ll_quant")
+        else:
+            B.check(B.mp_dispatch_ll(R, N, K, E, H, B.MP_BF16, 0, x, None, self.topk_idx, counts,
+                                     cap, *placed), "mp_dispatch_ll")
         B.check(B.mp_ll_row_weights(R, N, K, self.topk_weights, self.slot_row, cap,
                                     self.row_weights, stream), "mp_ll_row_weights")
-        B.check(B.mp_expert_matmul_e4m3(E, cap, 2 * I, H, self.recv_x, self.recv_scales, w_gate_up,
-                                        w_gate_up_scales, self.expert_offsets, self.gate_up,
-                                        self.dev_err, stream), "mp_expert_matmul_e4m3")
-        B.check(B.mp_swiglu_e4m3(cap, I, self.gate_up, self.row_weights, self._num_rows, self.z,
-                                 self.z_scales, stream), "mp_swiglu_e4m3")
-        B.check(B.mp_expert_matmul_e4m3(E, cap, H, I, self.z, self.z_scales, w_down, w_down_scales,
-                                        self.expert_offsets, self.y, self.dev_err, stream),
-                "mp_expert_matmul_e4m3")
+        self._product(2 * I, H, self.recv_x, self.recv_scales, w_gate_up, w_gate_up_scales,
+                      self.gate_up, stream)
+        if self.weights == "e4m3":
+            B.check(B.mp_swiglu_e4m3(cap, I, self.gate_up, self.row_weights, self._num_rows,
+                                     self.z, self.z_scales, stream), "mp_swiglu_e4m3")
+        else:
+            B.check(B.mp_swiglu_bf16(cap, I, self.gate_up, self.row_weights, self._num_rows,
+                                     self.z, stream), "mp_swiglu_bf16")
+        self._product(H, I, self.z, self.z_scales, w_down, w_down_scales, self.y, stream)
         B.check(B.mp_combine_ll(R, N, K, H, self.y, cap, self.slot_row, self.ones, self.out,
                                 self.dev_err, stream), "mp_combine_ll")
         return self.out
 
     def backward(self, d_out, logits, w_gate_up, w_gate_up_scales, w_down, w_down_scales,
-                 d_balance_loss=None, active=None, stream=None):
+                 d_balance_loss=None, active=None, stream=None, accumulate: bool = False):
         """Gradients of a forward pass, from the output's (and the losses'): d_x, d_logits,
-        d_w_gate_up, d_w_down of the plan."""
+        d_w_gate_up, d_w_down of the plan.  With ``accumulate`` (fp32 weights' gradients) the
+        last two are added to what they hold, for several batches per update."""
+        if accumulate and self.d_w_down.dtype is not torch.float32:
+            raise ValueError("only fp32 weights' gradients add up")
         R, N, K, E, H, I, cap = (self.R, self.N, self.K, self.E, self.H, self.I, self.cap)
         B._arr(d_out, "d_out", torch.bfloat16, R * N * H)
-        B.check(B.mp_dispatch_ll_rows_quant(R, N, K, H, B.MP_Q_E4M3, d_out, self.slot_row, cap,
-                                            self.dy, self.dy_scales, stream),
-                "mp_dispatch_ll_rows_quant")
-        B.check(B.mp_expert_matmul_dgrad_e4m3(E, cap, H, I, self.dy, self.dy_scales, w_down,
-                                              w_down_scales, self.expert_offsets, self.dz,
-                                              self.dev_err, stream), "mp_expert_matmul_dgrad_e4m3")
-        B.check(B.mp_expert_matmul_wgrad_e4m3(E, cap, H, I, self.dy, self.dy_scales, self.z,
-                                              self.z_scales, self.expert_offsets, self.d_w_down,
-                                              self.dev_err, stream), "mp_expert_matmul_wgrad_e4m3")
-        B.check(B.mp_swiglu_backward_e4m3(cap, I, self.gate_up, self.row_weights, self.dz,
-                                          self._num_rows, self.d_gate_up, self.d_gate_up_scales,
-                                          self.d_row_weights, stream), "mp_swiglu_backward_e4m3")
-        B.check(B.mp_expert_matmul_wgrad_e4m3(E, cap, 2 * I, H, self.d_gate_up,
-                                              self.d_gate_up_scales, self.recv_x,
-                                              self.recv_scales, self.expert_offsets,
-                                              self.d_w_gate_up, self.dev_err, stream),
-                "mp_expert_matmul_wgrad_e4m3")
-        B.check(B.mp_expert_matmul_dgrad_e4m3(E, cap, 2 * I, H, self.d_gate_up,
-                                              self.d_gate_up_scales, w_gate_up, w_gate_up_scales,
-                                              self.expert_offsets, self.d_rows, self.dev_err,
-                                              stream), "mp_expert_matmul_dgrad_e4m3")
+        if self.weights == "e4m3":
+            B.check(B.mp_dispatch_ll_rows_quant(R, N, K, H, B.MP_Q_E4M3, d_out, self.slot_row, cap,
+                                                self.dy, self.dy_scales, stream),
+                    "mp_dispatch_ll_rows_quant")
+        else:
+            B.check(B.mp_dispatch_ll_rows(R, N, K, H, B.MP_BF16, d_out, None, self.slot_row, cap,
+                                          self.dy, None, stream), "mp_dispatch_ll_rows")
+        self._rows_grad(H, I, self.dy, self.dy_scales, w_down, w_down_scales, self.dz, stream)
+        self._weights_grad(H, I, self.dy, self.dy_scales, self.z, self.z_scales, self.d_w_down,
+                           accumulate, stream)
+        if self.weights == "e4m3":
+            B.check(B.mp_swiglu_backward_e4m3(cap, I, self.gate_up, self.row_weights, self.dz,
+                                              self._num_rows, self.d_gate_up,
+                                              self.d_gate_up_scales, self.d_row_weights, stream),
+                    "mp_swiglu_backward_e4m3")
+        else:
+            B.check(B.mp_swiglu_backward_bf16(cap, I, self.gate_up, self.row_weights, self.dz,
+                                              self._num_rows, self.d_gate_up, self.d_row_weights,
+                                              stream), "mp_swiglu_backward_bf16")
+        self._weights_grad(2 * I, H, self.d_gate_up, self.d_gate_up_scales, self.recv_x,
+                           self.recv_scales, self.d_w_gate_up, accumulate, stream)
+        self._rows_grad(2 * I, H, self.d_gate_up, self.d_gate_up_scales, w_gate_up,
+                        w_gate_up_scales, self.d_rows, stream)
         B.check(B.mp_combine_ll(R, N, K, H, self.d_rows, cap, self.slot_row, self.ones, self.d_x,
                                 self.dev_err, stream), "mp_combine_ll")
         B.check(B.mp_ll_row_weights_backward(R, N, K, self.d_row_weights, cap, self.slot_row,
