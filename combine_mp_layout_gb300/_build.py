@@ -18,7 +18,7 @@ LIB = os.path.join(PKG, "libmp_layout.so")
 UNITS = ["mp_abi", "mp_layout_kernels", "mp_copy_kernels", "mp_noalloc", "mp_expert_abi",
          "mp_route", "mp_expert_matmul", "mp_expert_wgrad", "mp_swiglu", "mp_expert_bf16_abi",
          "mp_expert_matmul_bf16", "mp_expert_matmul_mxfp4", "mp_expert_wgrad_bf16",
-         "mp_swiglu_bf16"]
+         "mp_expert_rows", "mp_swiglu_bf16"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 

@@ -213,6 +213,11 @@ cudaError_t launch_expert_matmul_bf16(int E, int rows, int N, int K, bool dgrad,
                                       const void* w, const int32_t* expert_offsets, void* out,
                                       int32_t* dev_err, cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
+  if (!dgrad && rows <= 8) {
+    const cudaError_t e =
+        launch_expert_rows(E, rows, N, K, a, w, nullptr, expert_offsets, out, dev_err, st);
+    if (e != cudaErrorNotSupported) return e;
+  }
   RaggedArgs p = {};
   p.E = E;
   p.rows = rows;

@@ -345,6 +345,11 @@ cudaError_t launch_expert_matmul_mxfp4(int E, int rows, int N, int K, const void
                                        const int32_t* expert_offsets, void* out, int32_t* dev_err,
                                        cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
+  if (rows <= 8 || rows / 4 <= E) {
+    const cudaError_t e =
+        launch_expert_rows(E, rows, N, K, a, w, w_scales, expert_offsets, out, dev_err, st);
+    if (e != cudaErrorNotSupported) return e;
+  }
   RaggedArgs p = {};
   p.E = E;
   p.rows = rows;

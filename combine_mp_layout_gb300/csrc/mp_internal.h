@@ -262,6 +262,12 @@ cudaError_t launch_expert_matmul_mxfp4(int E, int rows, int N, int K, const void
                                        const int32_t* expert_offsets, void* out, int32_t* dev_err,
                                        cudaStream_t stream);
 
+// Both forward products for few rows each (w_scales NULL: bf16 weights).
+// cudaErrorNotSupported, with nothing launched, outside its limits.
+cudaError_t launch_expert_rows(int E, int rows, int N, int K, const void* a, const void* w,
+                               const unsigned char* w_scales, const int32_t* expert_offsets,
+                               void* out, int32_t* dev_err, cudaStream_t stream);
+
 // The gated activation on bf16 rows, and its gradient.
 cudaError_t launch_swiglu_bf16(int rows, int I, const void* gate_up, const float* row_weights,
                                const int32_t* num_rows, void* out, cudaStream_t stream);

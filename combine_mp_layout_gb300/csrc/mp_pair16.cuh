@@ -163,10 +163,10 @@ struct RaggedArgs {
   int32_t* dev_err;
 };
 
-// Exclusive prefix over experts of their number of row tiles, into pre[0 .. E].
-// Offsets that are negative or decrease leave no tiles at all (overlapping
+// Exclusive prefix over experts of their number of tiles of ROWS rows, into
+// pre[0 .. E].  Offsets that are negative or decrease leave no tiles at all (overlapping
 // experts could make more of them than the launcher's check allows for).
-template <int THREADS>
+template <int THREADS, int ROWS = kBR>
 __device__ void tile_prefix(const RaggedArgs& p, int* pre, int* scan) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.E + THREADS - 1) / THREADS;
@@ -175,7 +175,7 @@ __device__ void tile_prefix(const RaggedArgs& p, int* pre, int* scan) {
   for (int e = e0; e < e1; ++e) {
     int lo, hi;
     rows_of(p.expert_offsets, p.rows, e, lo, hi);
-    pre[e] = (hi - lo + kBR - 1) / kBR;
+    pre[e] = (hi - lo + ROWS - 1) / ROWS;
     sum += pre[e];
     bad |= offset_errors(p.expert_offsets, p.rows, e);
   }
@@ -205,15 +205,21 @@ struct Tile {
   int e, row0, nrows, n, col0;  // n: nrows rounded up to whole units
 };
 
-// Tile t in the order: experts ascending; within an expert, bands of kBandTiles
-// row tiles, in a band channels slowest, so that the tiles running at one time
-// share few weight channels and a band's rows.
-__device__ __forceinline__ Tile tile_at(const RaggedArgs& p, const int* pre, int ncol, int t) {
-  int lo = 0, hi = p.E;  // pre[lo] * ncol <= t < pre[hi] * ncol
+// The expert that tile t belongs to: pre[e] * ncol <= t < pre[e + 1] * ncol.
+__device__ __forceinline__ int expert_of(const int* pre, int E, int ncol, int t) {
+  int lo = 0, hi = E;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (pre[mid] * ncol <= t) lo = mid; else hi = mid;
   }
+  return lo;
+}
+
+// Tile t in the order: experts ascending; within an expert, bands of kBandTiles
+// row tiles, in a band channels slowest, so that the tiles running at one time
+// share few weight channels and a band's rows.
+__device__ __forceinline__ Tile tile_at(const RaggedArgs& p, const int* pre, int ncol, int t) {
+  const int lo = expert_of(pre, p.E, ncol, t);
   const int mt = pre[lo + 1] - pre[lo];
   const int local = t - pre[lo] * ncol;
   const int band = local / (kBandTiles * ncol);
