@@ -134,7 +134,7 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
   }
   if (warp == 1) tmem_alloc<true>(&tail->tmem, 512);
   pdl_wait_prior_grid();  // (nothing of the above touches global memory)
-  tile_prefix<kThreads>(p, pre, tail->scan);
+  tile_prefix<kThreads>(p, kBR, pre, tail->scan);
   cluster_sync_all();  // the barriers and TMEM of all blocks are ready
   tcgen05_fence_after();
   const uint32_t tmem = tail->tmem;

@@ -5,10 +5,10 @@
 // block takes 128 output channels of one expert and up to eight of its rows, a warp
 // of its own keeps a ring of 16 KB pieces (128 channels x 128 bytes) full by TMA,
 // and sixteen warps multiply from there with mma.m16n8k16 (the channels are the M
-// side, the rows the N side): a warp 16 channels and one half of each piece's
-// reduction.  A tensor-core tile of 256 x 32 would spend longer on its pipeline's
-// start, and for 4-bit weights on writing the converted weights to shared memory.
-// With few blocks, clusters share a reduction; sums are joined in a fixed order.
+// side, the rows the N side): a warp 32 channels and half of every other piece.  A tile of
+// the tensor core's (256 x 32) would spend longer on its pipeline's start, and for
+// 4-bit weights on writing the converted weights to shared memory.  With few blocks,
+// clusters share a reduction; sums are joined in a fixed order.
 //
 // bf16 weights: products exact, sums fp32.
 //
@@ -31,11 +31,19 @@ namespace mp {
 
 namespace {
 
-constexpr int kVR = 8;                     // rows of a block: the MMA's columns
-constexpr int kHalfWarps = kBC / 16;       // warps that cover the channels once
-constexpr int kMulWarps = 2 * kHalfWarps;
+constexpr int kVR = 8;                     // most rows of a block: the MMA's columns
+// Warps take the pieces in two sets.  A slot of the ring belongs to one set (the
+// ring is even): a warp that met a slot after a piece of the other set could find
+// that piece still on its way, and its wait for the next one already over.
+constexpr int kSets = 2;
+constexpr int kHalves = 2;                 // of a piece's reduction, each to other warps
+constexpr int kHalfWarps = kBC / 32;       // warps of a half: 32 channels each
+constexpr int kSetWarps = kHalves * kHalfWarps;
+constexpr int kMulWarps = kSets * kSetWarps;
+constexpr int kSums = kSets * kHalves;
 constexpr int kThreads = (kMulWarps + 1) * 32;
 constexpr int kPiece = kBC * 128;          // bytes of a piece of weights
+constexpr int kScales = kBC * 16;          // and of its MXFP4 scales: 16 bytes per channel
 constexpr int kMaxPieces = 8;              // in the ring
 constexpr int kMaxVecParts = 8;            // blocks that share a reduction: one cluster
 
@@ -48,17 +56,18 @@ struct Form {
 
 struct VecArgs {
   int E, rows, N, K;
-  int pieces;                    // of the ring
+  int room;                      // rows of a block that there is room for: 4 or 8
+  int pieces;                    // of the ring, even
   int steps;                     // most reduction steps of a block, whole pieces
   const uint16_t* a;             // bf16 [rows][K]
   const unsigned char* scales;   // MXFP4: [E][N][K/32]
-  int vec;                       // four scales are one aligned word
+  int tma_scales;                // these can be loaded by TMA
   RaggedArgs r;                  // for the tiles' prefix
 };
 
 struct VecTail {
   uint64_t raw[kMaxPieces], rawfree[kMaxPieces];
-  alignas(16) float part[2][kVR][kBC];  // sums of the two halves: [row][channel]
+  alignas(16) float part[kSums][kVR][kBC];  // sums of set and half: [row][channel]
   int failed;
   int scan[kThreads / 32];
 };
@@ -67,9 +76,10 @@ template <bool FP4>
 __host__ __device__ constexpr int row_stride(int steps) { return steps * 2 + Form<FP4>::kPad; }
 
 template <bool FP4>
-size_t vec_smem_bytes(int E, int steps, int pieces) {
-  return size_t(pieces) * kPiece + size_t(kVR) * row_stride<FP4>(steps) +
-         (FP4 ? size_t(steps / 32) * kVR * 4 : 0) + sizeof(VecTail) + size_t(E + 1) * 4;
+size_t vec_smem_bytes(int E, int room, int steps, int pieces) {
+  return size_t(pieces) * (kPiece + (FP4 ? kScales : 0)) +
+         size_t(room) * row_stride<FP4>(steps) +
+         (FP4 ? size_t(steps / 32) * room * 4 : 0) + sizeof(VecTail) + size_t(E + 1) * 4;
 }
 
 template <bool F16>
@@ -158,7 +168,7 @@ __device__ __forceinline__ void stage_rows(const VecArgs& p, int row0, int nrows
       uint4* dst = reinterpret_cast<uint4*>(xs + r * stride + g * 64);
 #pragma unroll
       for (int j = 0; j < 4; ++j) dst[j] = to_f16(v[j], by);
-      sx[g * kVR + r] = __uint_as_float(uint32_t(127 + ex - 10) << 23);
+      sx[g * p.room + r] = __uint_as_float(uint32_t(127 + ex - 10) << 23);
     }
   } else {
     const int vecs = steps / 8;
@@ -170,54 +180,85 @@ __device__ __forceinline__ void stage_rows(const VecArgs& p, int row0, int nrows
   }
 }
 
-// This warp's half of a piece of bf16 weights: 32 steps.  Which reduction steps
+// A warp's 32 channels and half of a piece of bf16 weights.  Which reduction steps
 // meet in an MMA is free as long as both operands agree: a lane's are one of the
 // chunks of 16 bytes 2t and 2t + 1, which no two lanes read from the same banks.
-__device__ __forceinline__ void multiply_bf16(const unsigned char* piece, const unsigned char* x,
-                                              int half, int ch, int g, int t, float (&acc)[4]) {
-  const unsigned char* w0 = piece + (ch + g) * 128;
+__device__ __forceinline__ void multiply_bf16(const unsigned char* w0, const unsigned char* x,
+                                              int half, int g, int t, float (&acc)[2][4]) {
   const int c = 2 * t + half;
-  const uint4 lo = *reinterpret_cast<const uint4*>(w0 + ((c ^ g) << 4));
-  const uint4 hi = *reinterpret_cast<const uint4*>(w0 + 8 * 128 + ((c ^ g) << 4));
   const uint4 b = *reinterpret_cast<const uint4*>(x + c * 16);
-  mma_16x8x16<false>(acc, lo.x, hi.x, lo.y, hi.y, b.x, b.y);
-  mma_16x8x16<false>(acc, lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const unsigned char* wm = w0 + m * 16 * 128 + ((c ^ g) << 4);
+    const uint4 lo = *reinterpret_cast<const uint4*>(wm);
+    const uint4 hi = *reinterpret_cast<const uint4*>(wm + 8 * 128);
+    mma_16x8x16<false>(acc[m], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+    mma_16x8x16<false>(acc[m], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+  }
 }
 
-// This warp's half of a piece of MXFP4 weights: four groups of 32 steps.  s0, s1:
-// the four scale bytes of channels g and g + 8.
+// Byte j of four scale bytes as the exponent of an fp32 number.
+__device__ __forceinline__ float exponent_of(uint32_t s4, int j) {
+  const uint32_t v = j == 3 ? s4 >> 1 : s4 << (23 - 8 * j);
+  return __uint_as_float(v & 0x7f800000u);
+}
+// The same whatever the byte is (`more` is not in it): 2^(s - 127 + 10), or from 245
+// on 2^(s - 127), and `by` the 2^10 that is put on the sum instead.
+__device__ __forceinline__ float any_exponent_of(uint32_t s4, int j, float& by) {
+  const uint32_t e = (s4 >> (8 * j)) & 255u;
+  by = e > 244u ? 1024.0f : 1.0f;
+  return __uint_as_float(e == 255u ? 0x7fc00000u : (e > 244u ? e : e + 10u) << 23);
+}
+
+// A warp's 32 channels and half of a piece of MXFP4 weights: four groups of 32
+// steps, a lane 8 of them for channels g, g + 8, g + 16 and g + 24, whose scale
+// bytes are s.  sx: the rows' powers of two, `room` for each group.
 template <bool LARGE>
-__device__ __forceinline__ void multiply_fp4(const unsigned char* piece, const unsigned char* x,
-                                             const float* sx, int half, int ch, int g, int t,
-                                             uint32_t s0, uint32_t s1, float2 (&acc)[2]) {
-  const unsigned char* w0 = piece + (ch + g) * 128 + t * 4;
+__device__ __forceinline__ void multiply_fp4(const unsigned char* w0, const unsigned char* x,
+                                             const float* sx, int room, int half, int g, int t,
+                                             const uint32_t (&s)[4], float (&acc)[2][4]) {
+  w0 += t * 4;
+  x += t * 16;
+  // 2^10 more, which the rows' powers of two lack (below 192: no carry between bytes)
+  const uint32_t more = LARGE ? 0u : 0x0a0a0a0au;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int c = half * 4 + i;
-    uint32_t lo[4], hi[4];
-    codes_to_f16(*reinterpret_cast<const uint32_t*>(w0 + ((c ^ g) << 4)), lo);
-    codes_to_f16(*reinterpret_cast<const uint32_t*>(w0 + 8 * 128 + ((c ^ g) << 4)), hi);
-    const uint32_t e0 = (s0 >> (8 * i)) & 255u, e1 = (s1 >> (8 * i)) & 255u;
-    if constexpr (LARGE) {
-      overflow(e0, lo);
-      overflow(e1, hi);
+    const uint4 b = *reinterpret_cast<const uint4*>(x + c * 64);
+    const float2 sx2 = *reinterpret_cast<const float2*>(sx + c * room);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const unsigned char* wm = w0 + m * 16 * 128 + ((c ^ g) << 4);
+      const uint32_t e0 = s[2 * m] + more, e1 = s[2 * m + 1] + more;
+      uint32_t lo[4], hi[4];
+      codes_to_f16(*reinterpret_cast<const uint32_t*>(wm), lo);
+      codes_to_f16(*reinterpret_cast<const uint32_t*>(wm + 8 * 128), hi);
+      if constexpr (LARGE) {
+        overflow((e0 >> (8 * i)) & 255u, lo);
+        overflow((e1 >> (8 * i)) & 255u, hi);
+      }
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      mma_16x8x16<true>(v, lo[0], hi[0], lo[1], hi[1], b.x, b.y);
+      mma_16x8x16<true>(v, lo[2], hi[2], lo[3], hi[3], b.z, b.w);
+      float f0, f1;
+      if constexpr (LARGE) {
+        float by0, by1;
+        f0 = any_exponent_of(e0, i, by0);
+        f1 = any_exponent_of(e1, i, by1);
+        v[0] *= by0;
+        v[1] *= by0;
+        v[2] *= by1;
+        v[3] *= by1;
+      } else {
+        f0 = exponent_of(e0, i);
+        f1 = exponent_of(e1, i);
+      }
+      const float2 v0 = mul2(make_float2(v[0], v[1]), sx2), v1 = mul2(make_float2(v[2], v[3]), sx2);
+      acc[m][0] = fmaf(v0.x, f0, acc[m][0]);
+      acc[m][1] = fmaf(v0.y, f0, acc[m][1]);
+      acc[m][2] = fmaf(v1.x, f1, acc[m][2]);
+      acc[m][3] = fmaf(v1.y, f1, acc[m][3]);
     }
-    const uint4 b = *reinterpret_cast<const uint4*>(x + c * 64 + t * 16);
-    float2 sx2 = *reinterpret_cast<const float2*>(sx + c * kVR + 2 * t);
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    mma_16x8x16<true>(v, lo[0], hi[0], lo[1], hi[1], b.x, b.y);
-    mma_16x8x16<true>(v, lo[2], hi[2], lo[3], hi[3], b.z, b.w);
-    float f0, f1;  // 2^(s - 127 + 10)
-    if constexpr (LARGE) {  // some scale is past 2^117: without the 2^10
-      sx2 = mul2(sx2, make_float2(1024.0f, 1024.0f));
-      f0 = e0 == 0 ? 0x1p-127f : __uint_as_float(e0 == 255u ? 0x7fc00000u : e0 << 23);
-      f1 = e1 == 0 ? 0x1p-127f : __uint_as_float(e1 == 255u ? 0x7fc00000u : e1 << 23);
-    } else {
-      f0 = __uint_as_float((e0 + 10u) << 23);
-      f1 = __uint_as_float((e1 + 10u) << 23);
-    }
-    acc[0] = fma2(mul2(make_float2(v[0], v[1]), sx2), make_float2(f0, f0), acc[0]);
-    acc[1] = fma2(mul2(make_float2(v[2], v[3]), sx2), make_float2(f1, f1), acc[1]);
   }
 }
 
@@ -225,32 +266,52 @@ __device__ __forceinline__ void mul_warps_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kMulWarps * 32) : "memory");
 }
 
-// SPLIT: one unit (expert's rows, channels) per cluster, each block a part of the
-// reduction; else blocks take units in turn.
+// Unit u: four or eight rows (at most) of an expert by 128 channels, channels fastest.
+struct Unit {
+  int e, row0, nrows, col0;
+};
+__device__ __forceinline__ Unit unit_at(const VecArgs& p, const int* pre, int ncol, int u) {
+  Unit n;
+  n.e = expert_of(pre, p.E, ncol, u);
+  const int local = u - pre[n.e] * ncol;
+  int r0, r1;
+  rows_of(p.r.expert_offsets, p.rows, n.e, r0, r1);
+  n.row0 = r0 + local / ncol * p.room;
+  n.nrows = min(p.room, r1 - n.row0);
+  n.col0 = local % ncol * kBC;
+  return n;
+}
+
+// SPLIT: one unit per cluster, each block a part of the reduction; else each block
+// takes a run of units, so that it seldom has other rows to fetch.
 template <bool FP4, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
-mp_k_expert_rows(const __grid_constant__ CUtensorMap map_w, const VecArgs p) {
+mp_k_expert_rows(const __grid_constant__ CUtensorMap map_w,
+                 const __grid_constant__ CUtensorMap map_s, const VecArgs p) {
   constexpr int kSteps = Form<FP4>::kSteps;
   extern __shared__ __align__(1024) unsigned char pieces[];
-  unsigned char* xs = pieces + size_t(p.pieces) * kPiece;
-  float* sx = reinterpret_cast<float*>(xs + kVR * row_stride<FP4>(p.steps));
-  VecTail* tail = reinterpret_cast<VecTail*>(sx + (FP4 ? p.steps / 32 * kVR : 0));
+  unsigned char* scales = pieces + size_t(p.pieces) * kPiece;
+  unsigned char* xs = scales + (FP4 ? size_t(p.pieces) * kScales : 0);
+  float* sx = reinterpret_cast<float*>(xs + p.room * row_stride<FP4>(p.steps));
+  VecTail* tail = reinterpret_cast<VecTail*>(sx + (FP4 ? p.steps / 32 * p.room : 0));
   int* pre = reinterpret_cast<int*>(tail + 1);
   const int warp = warp_index(), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.pieces; ++i) {
       mbar_init(&tail->raw[i], 1);
-      mbar_init(&tail->rawfree[i], kMulWarps);
+      mbar_init(&tail->rawfree[i], kSetWarps);
     }
     tail->failed = 0;
     mbar_init_fence();
   }
   pdl_wait_prior_grid();  // (nothing of the above touches global memory)
-  tile_prefix<kThreads, kVR>(p.r, pre, tail->scan);
+  tile_prefix<kThreads>(p.r, p.room, pre, tail->scan);
   const int parts = SPLIT ? int(cluster_size()) : 1, part = SPLIT ? int(cluster_rank()) : 0;
   const int ncol = ceil_div(p.N, kBC);
   const int units = pre[p.E] * ncol;  // below 2^30: the launcher checks
-  const int first = blockIdx.x / parts, stride = SPLIT ? max(units, 1) : int(gridDim.x);
+  const int64_t blocks = gridDim.x / parts, block = blockIdx.x / parts;
+  const int first = SPLIT ? int(block) : int(units * block / blocks);
+  const int last = SPLIT ? min(first + 1, units) : int(units * (block + 1) / blocks);
   const int np = ceil_div(p.K, kSteps);
   const int lo = np * part / parts, hi = np * (part + 1) / parts;  // pieces of this block
   volatile int* failed = &tail->failed;
@@ -260,18 +321,21 @@ mp_k_expert_rows(const __grid_constant__ CUtensorMap map_w, const VecArgs p) {
     if (elect_one()) {
       RingAt s;
       bool ok = true;
-      for (int u = first; u < units && ok; u += stride) {
-        const int e = expert_of(pre, p.E, ncol, u);
-        const int ch = (u - pre[e] * ncol) / (pre[e + 1] - pre[e]) * kBC;
+      for (int u = first; u < last && ok; ++u) {
+        const Unit n = unit_at(p, pre, ncol, u);
         for (int i = lo; i < hi; ++i, s.next(p.pieces)) {
           if (s.round > 0 &&
               !bounded_wait_idle(&tail->rawfree[s.slot], (s.round - 1) & 1u, failed)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&tail->raw[s.slot], kPiece);
-          tma_load_3d(pieces + s.slot * kPiece, &map_w, i * (FP4 ? 128 : kSteps), ch, e,
+          mbar_arrive_expect_tx(&tail->raw[s.slot],
+                                kPiece + (FP4 && p.tma_scales ? kScales : 0));
+          tma_load_3d(pieces + s.slot * kPiece, &map_w, i * (FP4 ? 128 : kSteps), n.col0, n.e,
                       &tail->raw[s.slot]);
+          if (FP4 && p.tma_scales)  // (x in whole 16 bytes: two pieces' scales)
+            tma_load_3d(scales + s.slot * kScales, &map_s, i * 8 & ~15, n.col0, n.e,
+                        &tail->raw[s.slot]);
         }
       }
       // every load has landed and been used before the block may end
@@ -284,110 +348,105 @@ mp_k_expert_rows(const __grid_constant__ CUtensorMap map_w, const VecArgs p) {
       cluster_sync_all();
     }
   } else {
-    const int half = warp / kHalfWarps, ch = warp % kHalfWarps * 16;
+    const int set = warp / kSetWarps, half = warp % kSetWarps / kHalfWarps;
+    const int ch = warp % kHalfWarps * 32;
     const int g = lane >> 2, t = lane & 3;
     const int groups = p.K / 32;
+    // MXFP4 scales that TMA cannot load: those of this warp's half of piece i, of four
+    // channels, from where they are
+    auto fetch_scales = [&](const Unit& n, int i, uint32_t (&sc)[4]) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        // (past the last channel or step: codes are zeros, any scale will do)
+        const unsigned char* from =
+            p.scales + (int64_t(n.e) * p.N + min(n.col0 + ch + g + 8 * c, p.N - 1)) * groups;
+        sc[c] = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          sc[c] |= uint32_t(__ldg(from + min(i * 8 + half * 4 + j, groups - 1))) << (8 * j);
+      }
+    };
     RingAt s;
     bool ok = true;
+    Unit n = {};
+    if (first < last) n = unit_at(p, pre, ncol, first);
+    int staged = -1;  // the first row of those in shared memory
     // (SPLIT: blocks without a unit meet the others at the cluster's barriers)
-    for (int u = first; u < units || (SPLIT && u == first); u += stride) {
-      const bool live = u < units;
-      int e = 0, row0 = 0, nrows = 0, col0 = 0;
-      if (live) {
-        e = expert_of(pre, p.E, ncol, u);
-        const int mt = pre[e + 1] - pre[e], local = u - pre[e] * ncol;
-        int r0, r1;
-        rows_of(p.r.expert_offsets, p.rows, e, r0, r1);
-        col0 = local / mt * kBC;
-        row0 = r0 + local % mt * kVR;
-        nrows = min(kVR, r1 - row0);
-        stage_rows<FP4>(p, row0, nrows, lo * kSteps, (hi - lo) * kSteps, xs, sx);
+    for (int u = first; u < last || (SPLIT && u == first); ++u) {
+      const bool live = u < last;
+      if (live && staged != n.row0) {
+        stage_rows<FP4>(p, n.row0, n.nrows, lo * kSteps, (hi - lo) * kSteps, xs, sx);
+        staged = n.row0;
       }
-      mul_warps_sync();
-      if (live && ok) {
-        const unsigned char* x = xs + g * row_stride<FP4>(p.steps);
-        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if constexpr (FP4) {
-          float2 acc2[2] = {};
-          // (channels past the last one: codes are zeros, any scale will do)
-          const unsigned char* sc0 =
-              p.scales + (int64_t(e) * p.N + min(col0 + ch + g, p.N - 1)) * groups;
-          const unsigned char* sc1 =
-              p.scales + (int64_t(e) * p.N + min(col0 + ch + g + 8, p.N - 1)) * groups;
-          auto scales4 = [&](const unsigned char* sc, int i) -> uint32_t {
-            const int at = i * 8 + half * 4;
-            if (p.vec) return __ldg(reinterpret_cast<const uint32_t*>(sc + min(at, groups - 4)));
-            uint32_t v = 0;
+      mul_warps_sync();  // the rows are there, and the sums of the unit before are used up
+      if (live) {
+        const unsigned char* x = xs + (g & (p.room - 1)) * row_stride<FP4>(p.steps);
+        float acc[2][4] = {};
+        for (int i = lo; i < hi; ++i, s.next(p.pieces)) {
+          if ((s.slot & 1) != set) continue;
+          uint32_t sc[4];
+          if (FP4 && !p.tma_scales) fetch_scales(n, i, sc);
+          ok = ok && bounded_wait_warp(&tail->raw[s.slot], s.round & 1u, failed);
+          if (!ok) break;
+          const unsigned char* w0 = pieces + s.slot * kPiece + (ch + g) * 128;
+          const unsigned char* xp = x + (i - lo) * kSteps * 2;
+          if constexpr (FP4) {
+            const float* sp = sx + (i - lo) * (kSteps / 32) * p.room + ((2 * t) & (p.room - 1));
+            if (p.tma_scales) {
+              const unsigned char* from =
+                  scales + s.slot * kScales + (ch + g) * 16 + (i & 1) * 8 + half * 4;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              v |= uint32_t(__ldg(sc + min(at + j, groups - 1))) << (8 * j);
-            return v;
-          };
-          // the scales of a piece, one piece ahead of their use
-          uint32_t a0 = scales4(sc0, lo), a1 = scales4(sc1, lo);
-          for (int i = lo; i < hi; ++i, s.next(p.pieces)) {
-            const uint32_t s0 = a0, s1 = a1;
-            if (i + 1 < hi) {
-              a0 = scales4(sc0, i + 1);
-              a1 = scales4(sc1, i + 1);
+              for (int c = 0; c < 4; ++c)
+                sc[c] = *reinterpret_cast<const uint32_t*>(from + c * 8 * 16);
             }
-            ok = bounded_wait_warp(&tail->raw[s.slot], s.round & 1u, failed);
-            if (!ok) break;
-            const unsigned char* piece = pieces + s.slot * kPiece;
-            const unsigned char* xp = x + (i - lo) * kSteps * 2;
-            const float* sp = sx + (i - lo) * (kSteps / 32) * kVR;
-            const bool large = (__vcmpgtu4(s0, 0xf4f4f4f4u) | __vcmpgtu4(s1, 0xf4f4f4f4u)) != 0;
-            if (__any_sync(kFull, large))
-              multiply_fp4<true>(piece, xp, sp, half, ch, g, t, s0, s1, acc2);
+            uint32_t large = 0;  // scales from 2^65 on (192): the careful form
+#pragma unroll
+            for (int c = 0; c < 4; ++c) large |= sc[c] & (sc[c] << 1);
+            if (__any_sync(kFull, (large & 0x80808080u) != 0))
+              multiply_fp4<true>(w0, xp, sp, p.room, half, g, t, sc, acc);
             else
-              multiply_fp4<false>(piece, xp, sp, half, ch, g, t, s0, s1, acc2);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tail->rawfree[s.slot]);
+              multiply_fp4<false>(w0, xp, sp, p.room, half, g, t, sc, acc);
+          } else {
+            multiply_bf16(w0, xp, half, g, t, acc);
           }
-          acc[0] = acc2[0].x;
-          acc[1] = acc2[0].y;
-          acc[2] = acc2[1].x;
-          acc[3] = acc2[1].y;
-        } else {
-          for (int i = lo; i < hi; ++i, s.next(p.pieces)) {
-            ok = bounded_wait_warp(&tail->raw[s.slot], s.round & 1u, failed);
-            if (!ok) break;
-            multiply_bf16(pieces + s.slot * kPiece, x + (i - lo) * kSteps * 2, half, ch, g, t,
-                          acc);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tail->rawfree[s.slot]);
-          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tail->rawfree[s.slot]);
         }
-        tail->part[half][2 * t][ch + g] = acc[0];
-        tail->part[half][2 * t + 1][ch + g] = acc[1];
-        tail->part[half][2 * t][ch + g + 8] = acc[2];
-        tail->part[half][2 * t + 1][ch + g + 8] = acc[3];
+        const int sum = set * kHalves + half;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          tail->part[sum][2 * t][ch + m * 16 + g] = acc[m][0];
+          tail->part[sum][2 * t + 1][ch + m * 16 + g] = acc[m][1];
+          tail->part[sum][2 * t][ch + m * 16 + g + 8] = acc[m][2];
+          tail->part[sum][2 * t + 1][ch + m * 16 + g + 8] = acc[m][3];
+        }
       }
       if constexpr (SPLIT) cluster_sync_all(); else mul_warps_sync();
-      // two channels of a row per thread; halves, then parts, in ascending order
-      for (int i = part * kMulWarps * 32 + int(threadIdx.x); live && i < nrows * (kBC / 2);
+      // two channels of a row per thread; sets and halves, then parts, ascending
+      for (int i = part * kMulWarps * 32 + int(threadIdx.x); live && i < n.nrows * (kBC / 2);
            i += parts * kMulWarps * 32) {
         const int r = i / (kBC / 2), c = i % (kBC / 2) * 2;
         float2 sum = make_float2(0.0f, 0.0f);
-        if constexpr (SPLIT) {
-          for (int z = 0; z < parts; ++z)
+        for (int z = 0; z < parts; ++z) {
+          float2 v[kSums];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float2 v;
+          for (int h = 0; h < kSums; ++h) {
+            if constexpr (SPLIT)
               asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-                           : "=f"(v.x), "=f"(v.y)
+                           : "=f"(v[h].x), "=f"(v[h].y)
                            : "r"(map_to_rank(&tail->part[h][r][c], uint32_t(z)))
                            : "memory");
-              sum = add2(sum, v);
-            }
-        } else {
-          sum = add2(*reinterpret_cast<const float2*>(&tail->part[0][r][c]),
-                     *reinterpret_cast<const float2*>(&tail->part[1][r][c]));
+            else
+              v[h] = *reinterpret_cast<const float2*>(&tail->part[h][r][c]);
+          }
+#pragma unroll
+          for (int h = 0; h < kSums; ++h) sum = add2(sum, v[h]);
         }
-        if (col0 + c < p.N)
-          *reinterpret_cast<uint32_t*>(p.r.out + int64_t(row0 + r) * p.N + col0 + c) =
+        if (n.col0 + c < p.N)
+          *reinterpret_cast<uint32_t*>(p.r.out + int64_t(n.row0 + r) * p.N + n.col0 + c) =
               pack_bf16x2_rn(sum.x, sum.y);
       }
+      if (u + 1 < last) n = unit_at(p, pre, ncol, u + 1);
       if constexpr (SPLIT) {
         cluster_sync_all();  // the other blocks have read this one's sums
         break;
@@ -399,41 +458,49 @@ mp_k_expert_rows(const __grid_constant__ CUtensorMap map_w, const VecArgs p) {
 }
 
 template <bool FP4, bool SPLIT>
-cudaError_t launch_as(const VecArgs& p, const CUtensorMap& mw, int blocks, int parts,
+cudaError_t launch_as(const VecArgs& p, const CUtensorMap& mw, const CUtensorMap& ms, int blocks, int parts,
                       cudaStream_t st) {
   static thread_local bool configured[64] = {};
   const cudaError_t e = allow_smem(mp_k_expert_rows<FP4, SPLIT>, configured);
   if (e != cudaSuccess) return e;
   return launch_waiting(mp_k_expert_rows<FP4, SPLIT>, dim3(unsigned(blocks)), dim3(kThreads),
-                        vec_smem_bytes<FP4>(p.E, p.steps, p.pieces), st,
-                        SPLIT ? unsigned(parts) : 0u, mw, p);
+                        vec_smem_bytes<FP4>(p.E, p.room, p.steps, p.pieces), st,
+                        SPLIT ? unsigned(parts) : 0u, mw, ms, p);
 }
 
 // cudaErrorNotSupported, with nothing launched, where this form is not meant for it.
 template <bool FP4>
 cudaError_t launch_rows(VecArgs p, const void* w, cudaStream_t st) {
   constexpr int kSteps = Form<FP4>::kSteps;
-  const int64_t chunks = std::min<int64_t>(p.rows, int64_t(p.rows) / kVR + p.E);
+  // Room for four rows while the experts have two on average: the rows' place is the
+  // ring's (7168 steps: eight pieces instead of four).
+  p.room = p.rows <= 4 || p.rows / 2 < p.E ? 4 : kVR;
+  const int64_t chunks = std::min<int64_t>(p.rows, int64_t(p.rows) / p.room + p.E);
   const int64_t units = chunks * ceil_div(p.N, kBC);
   const int np = ceil_div(p.K, kSteps);
   int parts = 1;
   while (parts < kMaxVecParts && units * 2 * parts <= sm_count() && np >= 4 * parts) parts *= 2;
   p.steps = ceil_div(np, parts) * kSteps;
   p.pieces = kMaxPieces;
-  while (p.pieces > 2 && vec_smem_bytes<FP4>(p.E, p.steps, p.pieces) > size_t(kMaxBlockSmem))
-    --p.pieces;
+  while (p.pieces > 2 &&
+         vec_smem_bytes<FP4>(p.E, p.room, p.steps, p.pieces) > size_t(kMaxBlockSmem))
+    p.pieces -= 2;
   if (units >= (int64_t(1) << 30) ||
-      vec_smem_bytes<FP4>(p.E, p.steps, p.pieces) > size_t(kMaxBlockSmem))
+      vec_smem_bytes<FP4>(p.E, p.room, p.steps, p.pieces) > size_t(kMaxBlockSmem))
     return cudaErrorNotSupported;
-  CUtensorMap mw;
+  CUtensorMap mw, ms = {};
   const bool map_ok =
       FP4 ? make_map_3d(&mw, w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(p.K) / 2,
                         uint64_t(p.N), uint64_t(p.E), 128, kBC)
           : make_map_3d(&mw, w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, uint64_t(p.K),
                         uint64_t(p.N), uint64_t(p.E), kSteps, kBC);
   if (!map_ok) return cudaErrorInvalidValue;
-  if (parts > 1) return launch_as<FP4, true>(p, mw, int(units) * parts, parts, st);
-  return launch_as<FP4, false>(p, mw, int(std::min<int64_t>(units, sm_count())), 1, st);
+  if (p.tma_scales &&
+      !make_map_3d(&ms, p.scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(p.K) / 32,
+                   uint64_t(p.N), uint64_t(p.E), 16, kBC, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorInvalidValue;
+  if (parts > 1) return launch_as<FP4, true>(p, mw, ms, int(units) * parts, parts, st);
+  return launch_as<FP4, false>(p, mw, ms, int(std::min<int64_t>(units, sm_count())), 1, st);
 }
 
 }  // namespace
@@ -448,7 +515,9 @@ cudaError_t launch_expert_rows(int E, int rows, int N, int K, const void* a, con
   p.K = K;
   p.a = static_cast<const uint16_t*>(a);
   p.scales = w_scales;
-  p.vec = K % 128 == 0 && (reinterpret_cast<uintptr_t>(w_scales) & 3u) == 0;
+  // TMA wants rows of whole 16 bytes, and a base aligned to them
+  p.tma_scales =
+      w_scales != nullptr && K % 512 == 0 && (reinterpret_cast<uintptr_t>(w_scales) & 15u) == 0;
   p.r.expert_offsets = expert_offsets;
   p.r.out = static_cast<uint16_t*>(out);
   p.r.dev_err = dev_err;

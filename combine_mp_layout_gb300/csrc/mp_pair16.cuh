@@ -18,11 +18,12 @@ namespace mp {
 constexpr int kMaxBlockSmem = 232448;  // bytes of shared memory a block may have
 
 // ---------------------------------------------------------------------------
-// Host: tensor maps with the 128-byte swizzle over [depth][rows][cols].
+// Host: tensor maps over [depth][rows][cols], with the 128-byte swizzle.
 // ---------------------------------------------------------------------------
 inline bool make_map_3d(CUtensorMap* map, const void* base, CUtensorMapDataType type, int elem,
                         uint64_t cols, uint64_t rows, uint64_t depth, uint32_t box_cols,
-                        uint32_t box_rows) {
+                        uint32_t box_rows,
+                        CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   const EncodeTiledFn fn = encode_tiled();
   if (fn == nullptr) return false;
   const cuuint64_t dims[3] = {cols, rows, depth};
@@ -30,7 +31,7 @@ inline bool make_map_3d(CUtensorMap* map, const void* base, CUtensorMapDataType 
   const cuuint32_t box[3] = {box_cols, box_rows, 1};
   const cuuint32_t step[3] = {1, 1, 1};
   return fn(map, type, 3, const_cast<void*>(base), dims, strides, box, step,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 inline bool make_map_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
@@ -163,11 +164,11 @@ struct RaggedArgs {
   int32_t* dev_err;
 };
 
-// Exclusive prefix over experts of their number of tiles of ROWS rows, into
-// pre[0 .. E].  Offsets that are negative or decrease leave no tiles at all (overlapping
+// Exclusive prefix over experts of their number of tiles of `most` rows,
+// into pre[0 .. E].  Offsets that are negative or decrease leave no tiles at all (overlapping
 // experts could make more of them than the launcher's check allows for).
-template <int THREADS, int ROWS = kBR>
-__device__ void tile_prefix(const RaggedArgs& p, int* pre, int* scan) {
+template <int THREADS>
+__device__ void tile_prefix(const RaggedArgs& p, int most, int* pre, int* scan) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.E + THREADS - 1) / THREADS;
   const int e0 = min(tid * per, p.E), e1 = min(e0 + per, p.E);
@@ -175,7 +176,7 @@ __device__ void tile_prefix(const RaggedArgs& p, int* pre, int* scan) {
   for (int e = e0; e < e1; ++e) {
     int lo, hi;
     rows_of(p.expert_offsets, p.rows, e, lo, hi);
-    pre[e] = (hi - lo + ROWS - 1) / ROWS;
+    pre[e] = (hi - lo + most - 1) / most;
     sum += pre[e];
     bad |= offset_errors(p.expert_offsets, p.rows, e);
   }

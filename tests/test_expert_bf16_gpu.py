@@ -79,6 +79,9 @@ MM = [  # counts, N, K, slack rows at the end
     ([1], 4096, 2048, 0),
     ([2500], 384, 264, 0),
     ([40] * 90, 520, 200, 0),
+    ([2, 0, 3, 1], 4104, 64, 0),
+    ([2, 1, 2], 16392, 200, 1),
+    ([8], 776, 7168, 0),
 ]
 
 
@@ -591,6 +594,9 @@ MX = [  # counts, N, K, slack rows at the end
     ([1], 4096, 2048, 0),
     ([4], 4096, 7168, 0),
     ([40] * 90, 520, 224, 0),
+    ([2, 0, 3, 1, 9] * 30, 392, 256, 0),   # one piece of the reduction, several units a block
+    ([3, 1, 6, 2] * 20, 1160, 736, 5),     # three pieces, several units a block
+    ([1, 2, 3] * 9, 4104, 2048, 0),
 ]
 
 
