@@ -25,7 +25,7 @@ bool product_args_ok(int E, int rows, int N, int K, const void* a, const void* w
   if (E < 1 || E > MP_MAX_EXPERTS || rows < 0 || N < 1 || K < 1) return false;
   if (N % 8 != 0 || K % 8 != 0 || N > INT32_MAX - 1024 || K > INT32_MAX - 1024) return false;
   if (rows > INT32_MAX - 1024) return false;  // a tile's last row index stays an int
-  if (int64_t(N) * K >= k40 / 2) return false;  // a tensor map's stride, in bytes
+  if (int64_t(N) * K >= k40 / 4) return false;  // a tensor map's stride, in bytes (fp32)
   if (!dev_err || (!expert_offsets && E != 1)) return false;
   if (rows > 0 && !a) return false;
   if ((rows > 0 || w_always) && !w) return false;

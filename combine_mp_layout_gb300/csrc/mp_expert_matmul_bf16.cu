@@ -40,7 +40,7 @@ constexpr int kThreads = (kEpiFirst + kEpiWarps) * 32;
 struct Tail {
   uint64_t full[kMaxStages], empty[kMaxStages];  // full: of the pair's first block
   uint64_t tfull[2], tempty[2];
-  alignas(16) unsigned char turn[kEpiWarps][2][kTurn];
+  alignas(16) unsigned char turned[kEpiWarps][2][kTurned];
   uint32_t tmem;
   int failed;
   int scan[kThreads / 32];
@@ -75,14 +75,16 @@ mp_k_expert_matmul_bf16(const __grid_constant__ CUtensorMap map_w,
   }
   if (warp == 1) tmem_alloc<true>(&tail->tmem, 512);
   pdl_wait_prior_grid();  // (nothing of the above touches global memory)
-  tile_prefix<kThreads>(p, kBR, pre, tail->scan);
+  const int ncol = ceil_div(p.out_cols, 2 * kBC);
+  const int pairs = SPLIT ? 1 : int(gridDim.x) / 2;
+  tile_prefix<kThreads>(p, SPLIT ? kBR : tile_rows<kThreads>(p, ncol, pairs, tail->scan), pre,
+                        tail->scan);
   cluster_sync_all();  // the barriers and TMEM of all blocks are ready
   tcgen05_fence_after();
   const uint32_t tmem = tail->tmem;
-  const int ncol = ceil_div(p.out_cols, 2 * kBC);
   const int tiles = pre[p.E] * ncol;  // below 2^31: the C ABI checks
   const int parts = SPLIT ? int(cluster_size()) / 2 : 1, part = SPLIT ? crank / 2 : 0;
-  const int first = blockIdx.x / (2 * parts), step = SPLIT ? max(tiles, 1) : int(gridDim.x) / 2;
+  const int first = blockIdx.x / (2 * parts), step = SPLIT ? max(tiles, 1) : pairs;
   const int nk = ceil_div(p.red, kBK);
   const int kb_lo = SPLIT ? int(int64_t(nk) * part / parts) : 0;
   const int kb_hi = SPLIT ? int(int64_t(nk) * (part + 1) / parts) : nk;
@@ -96,8 +98,7 @@ mp_k_expert_matmul_bf16(const __grid_constant__ CUtensorMap map_w,
       for (int t = first; t < tiles && ok; t += step) {
         const Tile tl = tile_at(p, pre, ncol, t);
         const int half = tl.n / 2, row = tl.row0 + rank * half;
-        const int box = row_box(half);
-        const uint32_t bytes = uint32_t(kStageC + (16 << box) * kBK * 2);
+        const uint32_t bytes = uint32_t(kStageC + half * kBK * 2);
         const int ch = tl.col0 + rank * kBC;
         for (int kb = kb_lo; kb < kb_hi; ++kb, s.next(p.stages)) {
           if (s.round > 0 &&
@@ -114,7 +115,7 @@ mp_k_expert_matmul_bf16(const __grid_constant__ CUtensorMap map_w,
           } else {
             tma_load_3d_pair(sc, &map_w, kb * kBK, ch, tl.e, bar);
           }
-          tma_load_2d_pair(sc + kStageC, &map_r.m[box], kb * kBK, row, bar);
+          load_rows(sc + kStageC, map_r, kb * kBK, row, half, bar);
         }
       }
       // every load has landed and been used before the block may end
@@ -148,7 +149,7 @@ mp_k_expert_matmul_bf16(const __grid_constant__ CUtensorMap map_w,
   } else {
     // ---- accumulators to bf16 rows
     const int q = warp & 3;  // the TMEM lanes this warp may read: 32 q ..
-    unsigned char* turn = tail->turn[warp - kEpiFirst][0];
+    unsigned char* turned = tail->turned[warp - kEpiFirst][0];
     uint32_t nt = 0;
     for (int t = first; t < tiles; t += step, ++nt) {
       const Tile tl = tile_at(p, pre, ncol, t);
@@ -160,7 +161,7 @@ mp_k_expert_matmul_bf16(const __grid_constant__ CUtensorMap map_w,
       if (SPLIT)
         store_part(tl, q, src, stages);  // (the stages are done with)
       else if (ch < p.out_cols)
-        write_tile(p, tl, ch, src, turn);
+        write_tile(p, tl, ch, src, turned);
       tcgen05_fence_before();
       __syncwarp();
       if (lane == 0) arrive_at(map_to_rank(&tail->tempty[buf], even));
@@ -200,7 +201,7 @@ cudaError_t launch_mm(const RaggedArgs& p, const void* a, const void* w, int N, 
                    uint64_t(p.E), 64, DGRAD ? kBK : kBC) ||
       !make_row_maps(&mr, a, p.red, p.rows))
     return cudaErrorInvalidValue;
-  const int64_t tiles = most_tiles(p);
+  const int64_t tiles = most_row_tiles(p.E, p.rows, kBR) * ceil_div(p.out_cols, 2 * kBC);
   const int parts = parts_for(tiles, ceil_div(p.red, kBK), 2);
   if (parts > 1) return launch_as<DGRAD, true>(p, mw, mr, int(tiles) * 2 * parts, parts, st);
   const int pairs = int(std::min<int64_t>(tiles, sm_count() / 2));

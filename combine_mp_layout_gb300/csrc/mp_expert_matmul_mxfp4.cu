@@ -45,7 +45,7 @@ struct Tail {
   uint64_t conv[kMaxStages];                     // this block's weights of a stage are written
   uint64_t raw[kRaw], rawfree[kRaw];
   uint64_t tfull[2], tempty[2];
-  alignas(16) unsigned char turn[kEpiWarps][2][kTurn];
+  alignas(16) unsigned char turned[kEpiWarps][2][kTurned];
   uint32_t tmem;
   int failed;
   int scan[kThreads / 32];
@@ -134,14 +134,16 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
   }
   if (warp == 1) tmem_alloc<true>(&tail->tmem, 512);
   pdl_wait_prior_grid();  // (nothing of the above touches global memory)
-  tile_prefix<kThreads>(p, kBR, pre, tail->scan);
+  const int ncol = ceil_div(p.out_cols, 2 * kBC);
+  const int pairs = SPLIT ? 1 : int(gridDim.x) / 2;
+  tile_prefix<kThreads>(p, SPLIT ? kBR : tile_rows<kThreads>(p, ncol, pairs, tail->scan), pre,
+                        tail->scan);
   cluster_sync_all();  // the barriers and TMEM of all blocks are ready
   tcgen05_fence_after();
   const uint32_t tmem = tail->tmem;
-  const int ncol = ceil_div(p.out_cols, 2 * kBC);
   const int tiles = pre[p.E] * ncol;  // below 2^31: the C ABI checks
   const int parts = SPLIT ? int(cluster_size()) / 2 : 1, part = SPLIT ? crank / 2 : 0;
-  const int first = blockIdx.x / (2 * parts), step = SPLIT ? max(tiles, 1) : int(gridDim.x) / 2;
+  const int first = blockIdx.x / (2 * parts), step = SPLIT ? max(tiles, 1) : pairs;
   // raw stages of this pair's part of the reduction, and stages
   const int nk = ceil_div(p.red, kBK), nr = ceil_div(p.red, kRawSteps * kBK);
   const int rb_lo = SPLIT ? int(int64_t(nr) * part / parts) : 0;
@@ -157,7 +159,6 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
       for (int t = first; t < tiles && ok; t += step) {
         const Tile tl = tile_at(p, pre, ncol, t);
         const int half = tl.n / 2, row = tl.row0 + rank * half;
-        const int box = row_box(half);
         for (int kb = kb_lo; kb < kb_hi; ++kb, s.next(p.stages)) {
           if (s.round > 0 &&
               !bounded_wait_idle(&tail->empty[s.slot], (s.round - 1) & 1u, failed)) {
@@ -165,9 +166,8 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
             break;
           }
           const uint32_t bar = map_to_rank(&tail->full[s.slot], even);
-          arrive_expect_at(bar, uint32_t((16 << box) * kBK * 2));
-          tma_load_2d_pair(stages + size_t(s.slot) * kStage + kStageC, &map_r.m[box], kb * kBK,
-                           row, bar);
+          arrive_expect_at(bar, uint32_t(half * kBK * 2));
+          load_rows(stages + size_t(s.slot) * kStage + kStageC, map_r, kb * kBK, row, half, bar);
         }
       }
       // every load has landed and been used before the block may end
@@ -201,7 +201,7 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
   } else if (warp < kRawWarp) {
     // ---- accumulators to bf16 rows
     const int q = warp & 3;  // the TMEM lanes this warp may read: 32 q ..
-    unsigned char* turn = tail->turn[warp - kEpiFirst][0];
+    unsigned char* turned = tail->turned[warp - kEpiFirst][0];
     uint32_t nt = 0;
     for (int t = first; t < tiles; t += step, ++nt) {
       const Tile tl = tile_at(p, pre, ncol, t);
@@ -213,7 +213,7 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
       if (SPLIT)
         store_part(tl, q, src, stages);  // (the stages are done with)
       else if (ch < p.out_cols)
-        write_tile(p, tl, ch, src, turn);
+        write_tile(p, tl, ch, src, turned);
       tcgen05_fence_before();
       __syncwarp();
       if (lane == 0) arrive_at(map_to_rank(&tail->tempty[buf], even));
@@ -261,7 +261,7 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
     const int r = ((warp - kConvFirst) % kGroupWarps) * 32 + lane;
     const int groups = p.red / 32;
     RingAt s, rs;
-    int turn = 0;
+    int group_of = 0;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
       const Tile tl = tile_at(p, pre, ncol, t);
@@ -286,8 +286,8 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
         if (!ok) break;
         const unsigned char* src = raws + rs.slot * kRawStage + r * 128;
         const int steps = min(kRawSteps, kb_hi - rb * kRawSteps);
-        for (int i = 0; i < steps; ++i, turn ^= 1, s.next(p.stages)) {
-          if (turn != group) continue;
+        for (int i = 0; i < steps; ++i, group_of ^= 1, s.next(p.stages)) {
+          if (group_of != group) continue;
           const uint4 c0 = *reinterpret_cast<const uint4*>(src + (((2 * i) ^ (r & 7)) << 4));
           const uint4 c1 = *reinterpret_cast<const uint4*>(src + (((2 * i + 1) ^ (r & 7)) << 4));
           const uint32_t two = (i < 2 ? now.x : now.y) >> (16 * (i & 1));
@@ -369,10 +369,11 @@ cudaError_t launch_expert_matmul_mxfp4(int E, int rows, int N, int K, const void
                    uint64_t(E), kRawSteps * kBK / 2, kBC) ||
       !make_row_maps(&mr, a, K, rows))
     return cudaErrorInvalidValue;
-  const int64_t tiles = most_tiles(p);
+  const int64_t tiles = most_row_tiles(p.E, p.rows, kBR) * ceil_div(p.out_cols, 2 * kBC);
   const int parts = parts_for(tiles, ceil_div(K, kBK), 2 * kRawSteps);
   if (parts > 1) return launch_as<true>(p, fw, mw, mr, int(tiles) * 2 * parts, parts, st);
-  return launch_as<false>(p, fw, mw, mr, 2 * int(std::min<int64_t>(tiles, sm_count() / 2)), 1, st);
+  const int pairs = int(std::min<int64_t>(tiles, sm_count() / 2));
+  return launch_as<false>(p, fw, mw, mr, 2 * pairs, 1, st);
 }
 
 }  // namespace mp

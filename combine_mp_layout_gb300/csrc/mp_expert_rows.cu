@@ -475,8 +475,7 @@ cudaError_t launch_rows(VecArgs p, const void* w, cudaStream_t st) {
   // Room for four rows while the experts have two on average: the rows' place is the
   // ring's (7168 steps: eight pieces instead of four).
   p.room = p.rows <= 4 || p.rows / 2 < p.E ? 4 : kVR;
-  const int64_t chunks = std::min<int64_t>(p.rows, int64_t(p.rows) / p.room + p.E);
-  const int64_t units = chunks * ceil_div(p.N, kBC);
+  const int64_t units = most_row_tiles(p.E, p.rows, p.room) * ceil_div(p.N, kBC);
   const int np = ceil_div(p.K, kSteps);
   int parts = 1;
   while (parts < kMaxVecParts && units * 2 * parts <= sm_count() && np >= 4 * parts) parts *= 2;

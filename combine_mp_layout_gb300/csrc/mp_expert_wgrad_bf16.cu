@@ -36,6 +36,7 @@ constexpr int kWStage = 2 * kWOperand;
 constexpr int kChunk = kWRows * 128;          // 64 channels (128 bytes) of a stage's rows
 constexpr int kWStages = 6;
 constexpr int kEpiWarps = 4;
+constexpr int kSlab = 32 * 128;               // 128 bytes of 32 finished rows
 constexpr int kClearWarp = 2, kEpiFirst = 3;
 constexpr int kWThreads = (kEpiFirst + kEpiWarps) * 32;
 
@@ -44,7 +45,6 @@ struct WArgs {
   const int32_t* expert_offsets;
   void* dw;
   int32_t* dev_err;
-  int out32;       // rows of dw are 32-byte aligned
   int accumulate;  // fp32: add to dw
   int patience;    // of the waits for whole tiles
 };
@@ -56,7 +56,8 @@ struct WTail {
   uint32_t tmem;
   int failed;
 };
-constexpr size_t kWSmem = size_t(kWStages) * kWStage + sizeof(WTail);
+constexpr size_t kWSmem = size_t(kWStages) * kWStage + kEpiWarps * 2 * kSlab + sizeof(WTail);
+static_assert(kWSmem <= size_t(kMaxBlockSmem));
 
 struct WTile {
   int e, lo, hi, n0, k0;  // n0, k0: of the pair
@@ -86,9 +87,11 @@ __device__ __forceinline__ int half_cols(const WArgs& p, const WTile& w) {
 template <bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
 mp_k_expert_wgrad_bf16(const __grid_constant__ CUtensorMap map_dy,
-                       const __grid_constant__ CUtensorMap map_a, const WArgs p) {
+                       const __grid_constant__ CUtensorMap map_a,
+                       const __grid_constant__ CUtensorMap map_dw, const WArgs p) {
   extern __shared__ __align__(1024) unsigned char stages[];
-  WTail* tail = reinterpret_cast<WTail*>(stages + size_t(kWStages) * kWStage);
+  WTail* tail = reinterpret_cast<WTail*>(stages + size_t(kWStages) * kWStage +
+                                         kEpiWarps * 2 * kSlab);
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const int rank = int(cluster_rank());
   if (threadIdx.x == 0) {
@@ -211,9 +214,14 @@ mp_k_expert_wgrad_bf16(const __grid_constant__ CUtensorMap map_dy,
       if (lane == 0) arrive_at(map_to_rank(&tail->full[at], 0));
     }
   } else {
-    // ---- accumulators to weights' gradients; an expert without rows gets zeros
+    // ---- accumulators to weights' gradients; an expert without rows gets zeros.  A
+    // warp's 32 rows go out in slabs 128 bytes wide, through shared memory (a lane its
+    // row, swizzled) and TMA, so that the weights' rows are written in whole lines.
+    constexpr int kCols = F32 ? 32 : 64;  // of a slab
     const int q = warp & 3;  // the TMEM lanes this warp may read: 32 q ..
+    unsigned char* slabs = stages + size_t(kWStages) * kWStage + q * 2 * kSlab;
     uint32_t nt = 0;  // tiles with products so far
+    int at = 0;       // the slab buffer in turn
     for (int t = first; t < tiles; t += stride) {
       const WTile w = wtile_at(p, t);
       const bool some = w.hi > w.lo;
@@ -222,58 +230,58 @@ mp_k_expert_wgrad_bf16(const __grid_constant__ CUtensorMap map_dy,
       if (some && !bounded_wait_idle_warp(&tail->tfull[buf], (nt >> 1) & 1u, failed, p.patience))
         break;
       tcgen05_fence_after();
-      const int n = w.n0 + rank * kWC + q * 32 + lane;
-      const int64_t at = (int64_t(w.e) * p.N + n) * p.K + w.k0;
-      const int cols = min(2 * kWC, p.K - w.k0);  // a multiple of 8
-      for (int c = 0; c < cols; c += 16) {
-        float2 v[8];
-        if (some) {
-          tmem_ld_x16(tmem + buf * 256 + c + (uint32_t(q) << 21), v);
-          tmem_wait_ld(v);
-        } else {
+      const int n0 = w.n0 + rank * kWC + q * 32;
+      const uint32_t src = tmem + buf * 256 + (uint32_t(q) << 21);
+      if (n0 < p.N) {
+        const float* before =
+            F32 ? static_cast<const float*>(p.dw) +
+                      (int64_t(w.e) * p.N + min(n0 + lane, p.N - 1)) * p.K + w.k0
+                : nullptr;
+        for (int c = 0; c < 2 * kWC && w.k0 + c < p.K; c += kCols, at ^= 1) {
+          unsigned char* slab = slabs + at * kSlab;
+          if (lane == 0) bulk_wait_read<1>();  // what went out of this buffer has
+          __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = make_float2(0.0f, 0.0f);
-        }
-        if (n < p.N) {
-          if constexpr (F32) {
-            float* dst = static_cast<float*>(p.dw) + at + c;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {  // 8 columns: 32 bytes
-              if (c + h * 8 >= cols) break;
-              float4* d = reinterpret_cast<float4*>(dst + h * 8);
-              float2* x = v + h * 4;
-              if (p.accumulate) {
-                const float4 o0 = d[0], o1 = d[1];
-                x[0] = add2(make_float2(o0.x, o0.y), x[0]);
-                x[1] = add2(make_float2(o0.z, o0.w), x[1]);
-                x[2] = add2(make_float2(o1.x, o1.y), x[2]);
-                x[3] = add2(make_float2(o1.z, o1.w), x[3]);
-              }
-              if (p.out32) {
-                Words<8> o;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  o.w[2 * j] = __float_as_uint(x[j].x);
-                  o.w[2 * j + 1] = __float_as_uint(x[j].y);
-                }
-                st_stream_w<8>(reinterpret_cast<Words<8>*>(d), o);
-              } else {
-                d[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
-                d[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
-              }
-            }
-          } else {
-            uint16_t* dst = static_cast<uint16_t*>(p.dw) + at + c;
-            Words<8> o;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o.w[j] = pack_bf16x2_rn(v[j].x, v[j].y);
-            if (p.out32 && c + 16 <= cols) {
-              st_stream_w<8>(reinterpret_cast<Words<8>*>(dst), o);
+          for (int h = 0; h < kCols / 16; ++h) {  // 16 columns: 64 or 32 bytes of a row
+            float2 v[8];
+            if (some) {
+              tmem_ld_x16(src + c + h * 16, v);
+              tmem_wait_ld(v);
             } else {
-              uint4* d = reinterpret_cast<uint4*>(dst);
-              d[0] = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
-              if (c + 16 <= cols) d[1] = make_uint4(o.w[4], o.w[5], o.w[6], o.w[7]);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] = make_float2(0.0f, 0.0f);
             }
+            uint4* row = reinterpret_cast<uint4*>(slab + lane * 128);
+            if constexpr (F32) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (p.accumulate) {
+                  const int col = c + h * 16 + j * 4;
+                  const float4 o = w.k0 + col < p.K
+                                       ? *reinterpret_cast<const float4*>(before + col)
+                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                  v[2 * j] = add2(make_float2(o.x, o.y), v[2 * j]);
+                  v[2 * j + 1] = add2(make_float2(o.z, o.w), v[2 * j + 1]);
+                }
+                row[(h * 4 + j) ^ (lane & 7)] =
+                    make_uint4(__float_as_uint(v[2 * j].x), __float_as_uint(v[2 * j].y),
+                               __float_as_uint(v[2 * j + 1].x), __float_as_uint(v[2 * j + 1].y));
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                row[(h * 2 + j) ^ (lane & 7)] = make_uint4(
+                    pack_bf16x2_rn(v[4 * j].x, v[4 * j].y),
+                    pack_bf16x2_rn(v[4 * j + 1].x, v[4 * j + 1].y),
+                    pack_bf16x2_rn(v[4 * j + 2].x, v[4 * j + 2].y),
+                    pack_bf16x2_rn(v[4 * j + 3].x, v[4 * j + 3].y));
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {  // (what lies past N or K is not written)
+            tma_store_3d(&map_dw, w.k0 + c, n0, w.e, slab);
+            bulk_commit();
           }
         }
       }
@@ -284,6 +292,7 @@ mp_k_expert_wgrad_bf16(const __grid_constant__ CUtensorMap map_dy,
         ++nt;
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   __syncwarp();
@@ -297,13 +306,18 @@ mp_k_expert_wgrad_bf16(const __grid_constant__ CUtensorMap map_dy,
 template <bool F32>
 cudaError_t launch_wgrad(const WArgs& p, const CUtensorMap& mdy, const CUtensorMap& ma,
                          cudaStream_t st) {
+  CUtensorMap mdw;
+  if (!make_map_3d(&mdw, p.dw,
+                   F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                   F32 ? 4 : 2, uint64_t(p.K), uint64_t(p.N), uint64_t(p.E), F32 ? 32 : 64, 32))
+    return cudaErrorInvalidValue;
   static thread_local bool configured[64] = {};
   const cudaError_t e = allow_smem(mp_k_expert_wgrad_bf16<F32>, configured);
   if (e != cudaSuccess) return e;
   const int64_t tiles = int64_t(p.E) * ceil_div(p.N, 2 * kWC) * ceil_div(p.K, 2 * kWC);
   const int pairs = int(std::min<int64_t>(tiles, sm_count() / 2));
   return launch_waiting(mp_k_expert_wgrad_bf16<F32>, dim3(unsigned(2 * pairs)), dim3(kWThreads),
-                        kWSmem, st, 0, mdy, ma, p);
+                        kWSmem, st, 0, mdy, ma, mdw, p);
 }
 
 }  // namespace
@@ -316,7 +330,6 @@ cudaError_t launch_expert_wgrad_bf16(int E, int rows, int N, int K, const void* 
   p.expert_offsets = expert_offsets;
   p.dw = dw;
   p.dev_err = dev_err;
-  p.out32 = (reinterpret_cast<uintptr_t>(dw) & 31u) == 0 && (f32 || K % 16 == 0);
   p.accumulate = accumulate;
   p.patience = 1 + rows / (1 << 20);
   CUtensorMap mdy = {}, ma = {};

@@ -89,6 +89,16 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
       : "memory");
 }
+// A box from shared memory to the array, in the current bulk async-group; what
+// lies outside the array is not written.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int y, int z,
+                                             const void* src) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+          map),
+      "r"(x), "r"(y), "r"(z), "r"(smem_addr(src))
+      : "memory");
+}
 // An arrival (with bytes to come) on a barrier at a shared::cluster address.
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -152,7 +162,7 @@ constexpr int kStage = kStageC + kStageR;
 constexpr int kMaxParts = 4;              // pairs that share a tile's reduction: one cluster
 constexpr int kBandTiles = 8;             // row tiles per band of the tile order
 constexpr int kEpiWarps = 4;
-constexpr int kTurn = 16 * 32 * 2;        // bytes of 16 rows x 32 channels
+constexpr int kTurned = 16 * 32 * 2;        // bytes of 16 rows x 32 channels
 
 struct RaggedArgs {
   int E, rows, out_cols, red;             // out_cols, red: N and K, or K and N
@@ -164,9 +174,24 @@ struct RaggedArgs {
   int32_t* dev_err;
 };
 
-// Exclusive prefix over experts of their number of tiles of `most` rows,
-// into pre[0 .. E].  Offsets that are negative or decrease leave no tiles at all (overlapping
-// experts could make more of them than the launcher's check allows for).
+// Adds up a value of every thread; all threads get the sum.
+template <int THREADS>
+__device__ __forceinline__ int block_sum(int v, int* scan) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  if ((threadIdx.x & 31) == 0) scan[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int sum = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) sum += scan[w];
+  __syncthreads();
+  return sum;
+}
+
+// Exclusive prefix over experts of their number of tiles of `most` rows, into
+// pre[0 .. E].  Offsets that are negative or decrease leave no tiles at all
+// (overlapping experts could make more of them than the launcher's check allows
+// for).
 template <int THREADS>
 __device__ void tile_prefix(const RaggedArgs& p, int most, int* pre, int* scan) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -200,6 +225,38 @@ __device__ void tile_prefix(const RaggedArgs& p, int most, int* pre, int* scan) 
   }
   if (tid == THREADS - 1) pre[p.E] = bad ? 0 : base + incl;
   __syncthreads();
+}
+
+// The most rows of a tile: 256, or 224 or 192 where their tiles fill the pairs'
+// turns better.  A turn takes about as long as its tiles' units of 32 rows on
+// average and 1.25 more (measured, 4096 x 7168: 38.4 us with 256 rows, 34.3 with
+// 224, 32.7 with 211), so a smaller tile has to save whole turns.  (32 experts of
+// about 1,024 rows, 2,048 channels from 7168: 17 turns of 6.5 units, not 16 of 7.2.)
+template <int THREADS>
+__device__ int tile_rows(const RaggedArgs& p, int ncol, int pairs, int* scan) {
+  int units = 0, tiles[3] = {0, 0, 0};
+  for (int e = threadIdx.x; e < p.E; e += THREADS) {
+    int lo, hi;
+    rows_of(p.expert_offsets, p.rows, e, lo, hi);
+    const int u = (hi - lo + kUnit - 1) / kUnit;
+    units += u;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) tiles[i] += (u + 7 - i) / (8 - i);
+  }
+  units = block_sum<THREADS>(units, scan);
+  int best = 8;
+  float least = INFINITY;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const float t = float(block_sum<THREADS>(tiles[i], scan));
+    if (i > 0 && t * ncol >= 0x1p30f) break;  // (their number stays an int)
+    const float cost = ceilf(t * ncol / pairs) * (units / fmaxf(t, 1.0f) + 1.25f);
+    if (cost < least) {
+      least = cost;
+      best = 8 - i;
+    }
+  }
+  return best * kUnit;
 }
 
 struct Tile {
@@ -249,17 +306,25 @@ __device__ __forceinline__ void cluster_end() {
   tcgen05_fence_after();
 }
 
-// A box of a tile's rows: half of them per block, in the smallest of four sizes.
+// A tile's rows, half of them per block: a multiple of 16 (up to 128), loaded as
+// the boxes of 16, 32, 64 and 128 rows that it is the sum of.
 struct RowMaps {
-  CUtensorMap m[4];                       // 16, 32, 64 and 128 rows
+  CUtensorMap m[4];
 };
 inline bool make_row_maps(RowMaps* r, const void* a, int red, int rows) {
   for (int i = 0; i < 4; ++i)
     if (!make_map_bf16(&r->m[i], a, uint64_t(red), uint64_t(rows), kBK, 16u << i)) return false;
   return true;
 }
-__device__ __forceinline__ int row_box(int half) {
-  return half > 64 ? 3 : half > 32 ? 2 : half > 16 ? 1 : 0;
+__device__ __forceinline__ void load_rows(unsigned char* dst, const RowMaps& maps, int k, int row,
+                                          int half, uint32_t bar) {
+#pragma unroll
+  for (int i = 3; i >= 0; --i)
+    if (half & (16 << i)) {
+      tma_load_2d_pair(dst, &maps.m[i], k, row, bar);
+      dst += (16 << i) * kBK * 2;
+      row += 16 << i;
+    }
 }
 
 // The products of one stage: four K = 16 steps.
@@ -276,10 +341,10 @@ __device__ __forceinline__ void stage_products(const unsigned char* stage, uint3
 }
 
 // A finished accumulator, this warp's 32 channels from `ch` on, to bf16 rows.
-// `src`: its TMEM lanes and first column; `turn`: 2 * kTurn bytes of its own, in
+// `src`: its TMEM lanes and first column; `turned`: 2 * kTurned bytes of its own, in
 // which 16 rows x 32 channels at a time are turned around.
 __device__ __forceinline__ void write_tile(const RaggedArgs& p, const Tile& tl, int ch,
-                                           uint32_t src, unsigned char* turn) {
+                                           uint32_t src, unsigned char* turned) {
   const int lane = threadIdx.x & 31;
   const int r = lane >> 1, h = (lane & 1) * 16;  // the row and channels that it stores
   const int left = p.out_cols - (ch + h);        // a multiple of 8 (or <= 0)
@@ -292,7 +357,7 @@ __device__ __forceinline__ void write_tile(const RaggedArgs& p, const Tile& tl, 
     for (int b = 0; b < 2; ++b) {  // 16 rows; the next 16 on their way from TMEM
       const int c = c0 + b * 16;
       if (c + 16 < tl.n) tmem_ld_x16(src + c + 16, v[b ^ 1]);
-      uint16_t* tw = reinterpret_cast<uint16_t*>(turn + b * kTurn) + lane;
+      uint16_t* tw = reinterpret_cast<uint16_t*>(turned + b * kTurned) + lane;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t two = pack_bf16x2_rn(v[b][j].x, v[b][j].y);
@@ -301,7 +366,7 @@ __device__ __forceinline__ void write_tile(const RaggedArgs& p, const Tile& tl, 
       }
       __syncwarp();
       if (c + r < tl.nrows) {
-        const uint4* tr = reinterpret_cast<const uint4*>(turn + b * kTurn + r * 64 + h * 2);
+        const uint4* tr = reinterpret_cast<const uint4*>(turned + b * kTurned + r * 64 + h * 2);
         const uint4 x = tr[0], y = tr[1];
         if (p.out32 && left >= 16) {
           const Words<8> o = {{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}};
@@ -372,10 +437,10 @@ inline int parts_for(int64_t tiles, int stages, int least) {
     parts *= 2;
   return parts;
 }
-// Row tiles times channel tiles, at most (one short row tile per expert).
-inline int64_t most_tiles(const RaggedArgs& p) {
-  const int64_t row_tiles = std::min<int64_t>(p.rows, int64_t(p.rows) / kBR + p.E);
-  return row_tiles * ceil_div(p.out_cols, 2 * kBC);
+// Tiles of `most` rows, at most: every expert's first row starts one.
+inline int64_t most_row_tiles(int E, int rows, int most) {
+  const int used = std::min(E, rows);
+  return used + (int64_t(rows) - used) / most;
 }
 
 }  // namespace mp

@@ -832,7 +832,7 @@ int mp_swiglu_backward_e4m3(int rows, int I, const void *gate_up, const float *r
  *   in   expert_offsets  int32 [E+1], or NULL for E == 1 (all rows)
  *   out  out             bf16 [rows][N]; rows of no expert are not written
  * Checks: 1 <= E <= 8192, rows >= 0, N and K multiples of 8 (both > 0), rows, N, K
- *   <= 2^31 - 1025, N*K < 2^39, (rows/256 + E) * ceil(N/256) < 2^31 - 4096,
+ *   <= 2^31 - 1025, N*K < 2^38, (rows/256 + E) * ceil(N/256) < 2^31 - 4096,
  *   non-NULL buffers (a and out when rows == 0), a, w and out 16-byte aligned.
  * Device errors: MP_ERR_CAPACITY (an offset past `rows`; it is cut off there),
  *   MP_ERR_INVALID_ARG (offsets that decrease or are negative; nothing is
