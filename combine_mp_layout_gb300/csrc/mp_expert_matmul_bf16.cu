@@ -77,7 +77,7 @@ mp_k_expert_matmul_bf16(const __grid_constant__ CUtensorMap map_w,
   pdl_wait_prior_grid();  // (nothing of the above touches global memory)
   const int ncol = ceil_div(p.out_cols, 2 * kBC);
   const int pairs = SPLIT ? 1 : int(gridDim.x) / 2;
-  tile_prefix<kThreads>(p, SPLIT ? kBR : tile_rows<kThreads>(p, ncol, pairs, tail->scan), pre,
+  tile_prefix<kThreads>(p, SPLIT ? kBR : tile_rows<kThreads>(p, kBR, ncol, pairs, tail->scan), pre,
                         tail->scan);
   cluster_sync_all();  // the barriers and TMEM of all blocks are ready
   tcgen05_fence_after();
@@ -93,12 +93,13 @@ mp_k_expert_matmul_bf16(const __grid_constant__ CUtensorMap map_w,
   if (warp == 0) {
     // ---- loads: one lane keeps the ring of stages full
     if (elect_one()) {
+      const uint32_t stage0 = smem_addr(stages), full0 = map_to_rank(&tail->full[0], even);
       RingAt s;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
         const Tile tl = tile_at(p, pre, ncol, t);
-        const int half = tl.n / 2, row = tl.row0 + rank * half;
-        const uint32_t bytes = uint32_t(kStageC + half * kBK * 2);
+        const RowBoxes rows(map_r, tl, rank);
+        const uint32_t bytes = kStageC + rows.bytes;
         const int ch = tl.col0 + rank * kBC;
         for (int kb = kb_lo; kb < kb_hi; ++kb, s.next(p.stages)) {
           if (s.round > 0 &&
@@ -106,8 +107,7 @@ mp_k_expert_matmul_bf16(const __grid_constant__ CUtensorMap map_w,
             ok = false;
             break;
           }
-          unsigned char* sc = stages + size_t(s.slot) * kStage;
-          const uint32_t bar = map_to_rank(&tail->full[s.slot], even);
+          const uint32_t sc = stage0 + uint32_t(s.slot) * kStage, bar = full0 + s.slot * 8;
           arrive_expect_at(bar, bytes);
           if constexpr (DGRAD) {
             tma_load_3d_pair(sc, &map_w, ch, kb * kBK, tl.e, bar);
@@ -115,7 +115,7 @@ mp_k_expert_matmul_bf16(const __grid_constant__ CUtensorMap map_w,
           } else {
             tma_load_3d_pair(sc, &map_w, kb * kBK, ch, tl.e, bar);
           }
-          load_rows(sc + kStageC, map_r, kb * kBK, row, half, bar);
+          rows.load(sc + kStageC, kb * kBK, bar);
         }
       }
       // every load has landed and been used before the block may end
@@ -184,9 +184,6 @@ cudaError_t launch_as(RaggedArgs p, const CUtensorMap& mw, const RowMaps& mr, in
                       int parts, cudaStream_t st) {
   p.stages = kMaxStages;
   while (smem_bytes(p.E, p.stages) > size_t(kMaxBlockSmem)) --p.stages;
-  static thread_local bool configured[64] = {};
-  const cudaError_t e = allow_smem(mp_k_expert_matmul_bf16<DGRAD, SPLIT>, configured);
-  if (e != cudaSuccess) return e;
   return launch_waiting(mp_k_expert_matmul_bf16<DGRAD, SPLIT>, dim3(unsigned(blocks)),
                         dim3(kThreads), smem_bytes(p.E, p.stages), st, unsigned(2 * parts), mw,
                         mr, p);
@@ -195,6 +192,10 @@ cudaError_t launch_as(RaggedArgs p, const CUtensorMap& mw, const RowMaps& mr, in
 template <bool DGRAD>
 cudaError_t launch_mm(const RaggedArgs& p, const void* a, const void* w, int N, int K,
                       cudaStream_t st) {
+  static thread_local bool whole[64] = {}, split[64] = {};
+  cudaError_t e = allow_smem(mp_k_expert_matmul_bf16<DGRAD, false>, whole);
+  if (e == cudaSuccess) e = allow_smem(mp_k_expert_matmul_bf16<DGRAD, true>, split);
+  if (e != cudaSuccess) return e;
   CUtensorMap mw;
   RowMaps mr;
   if (!make_map_3d(&mw, w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, uint64_t(K), uint64_t(N),
@@ -202,7 +203,8 @@ cudaError_t launch_mm(const RaggedArgs& p, const void* a, const void* w, int N, 
       !make_row_maps(&mr, a, p.red, p.rows))
     return cudaErrorInvalidValue;
   const int64_t tiles = most_row_tiles(p.E, p.rows, kBR) * ceil_div(p.out_cols, 2 * kBC);
-  const int parts = parts_for(tiles, ceil_div(p.red, kBK), 2);
+  const int parts = parts_for(mp_k_expert_matmul_bf16<DGRAD, true>, kThreads, tiles, 2, kMaxParts,
+                              ceil_div(p.red, kBK), 4);
   if (parts > 1) return launch_as<DGRAD, true>(p, mw, mr, int(tiles) * 2 * parts, parts, st);
   const int pairs = int(std::min<int64_t>(tiles, sm_count() / 2));
   return launch_as<DGRAD, false>(p, mw, mr, 2 * pairs, 1, st);
@@ -214,7 +216,7 @@ cudaError_t launch_expert_matmul_bf16(int E, int rows, int N, int K, bool dgrad,
                                       const void* w, const int32_t* expert_offsets, void* out,
                                       int32_t* dev_err, cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
-  if (!dgrad && rows <= 8) {
+  if (!dgrad && (rows <= 16 || rows / 4 <= E)) {
     const cudaError_t e =
         launch_expert_rows(E, rows, N, K, a, w, nullptr, expert_offsets, out, dev_err, st);
     if (e != cudaErrorNotSupported) return e;

@@ -5,16 +5,17 @@
 //   out[r][n] = sum over k of a[r][k] * 2^(s[e][n][k/32] - 127) * c[e][n][k]
 //
 // A code times its scale is a bf16 number (exactly: two significant bits, and the
-// smallest scale leaves 2^-128), so the weights are turned into bf16 on their way
-// into shared memory and the products are exact; sums are fp32, rounded once.
+// smallest scale leaves 2^-128), so the weights are turned into bf16 on their way to
+// the tensor core and the products are exact; sums are fp32, rounded once.
 //
-// Layout: that of the bf16 products, a tile of 256 channels by up to 256 rows per
-// pair of blocks.  The codes come by TMA into a ring of raw stages (128 channels x
-// 256 reduction steps, 16 KB); eight warps, in two groups that take alternate
-// stages of 64 steps, turn them into the MMA's operand, a thread a channel's 64
-// codes; one warp hands finished stages over to the tensor core's proxy (a proxy
-// fence waits for the loads that its thread has in flight, and the converting
-// warps have the scales' underway).
+// Layout: that of the bf16 products, a tile of 256 channels by up to 192 rows per
+// pair of blocks, but the weights' operand (the MMA's M side) lies in TMEM: four
+// stages of 64 steps, 32 columns each, beside two accumulators of 192.  In shared
+// memory each stage would have to be written and read there, 32 KB beside the 40 KB
+// of the codes and rows, more than the products' time allows for (8,191 rows over 32
+// experts, 7168 x 2048: 204 us).  The codes come by TMA into a ring of raw stages (128
+// channels x 256 reduction steps, 16 KB); sixteen warps, in four groups with a stage
+// each, turn them into bf16, a thread a channel's 64 codes.
 #include <algorithm>
 #include <cstdint>
 #include <cuda.h>
@@ -26,23 +27,34 @@ namespace mp {
 
 namespace {
 
-constexpr int kMaxStages = 4;
-constexpr int kRaw = 4;                        // raw stages
+// TMEM is two accumulators of MOST columns (a tile's most rows) and stages of 64
+// steps of weights in the rest.  192 rows leave four stages, 160 six: with few rows
+// per expert the products of a stage are short and more of them have to be under way
+// (8,191 rows over 32 experts, 2048 x 7168: 227 us with four stages, 181 with six;
+// 32,768 rows, 4096 x 7168: 1,110 and 1,150 us).
+constexpr int kWeightCols = kBK / 2;           // TMEM columns of a stage of weights
+template <int MOST>
+struct Form {
+  static constexpr int kStages = (512 - 2 * MOST) / kWeightCols;
+  static constexpr int kRowStage = MOST / 2 * kBK * 2;
+};
+constexpr int kMaxStages = 6;
+constexpr int kRaw = 6;                        // raw stages
 constexpr int kRawSteps = 4;                   // stages of 64 in a raw stage of 256
 constexpr int kRawStage = kBC * kRawSteps * kBK / 2;
 constexpr int kGroupWarps = kBC / 32;          // a thread per channel
-constexpr int kEpiFirst = 2, kRawWarp = kEpiFirst + kEpiWarps, kHandWarp = kRawWarp + 1,
-              kConvFirst = kHandWarp + 1;
-constexpr int kThreads = (kConvFirst + 2 * kGroupWarps) * 32;
+constexpr int kGroups = 4;                     // that take the stages in turn
+constexpr int kConvWarps = kGroups * kGroupWarps;
+constexpr int kEpiFirst = 2, kRawWarp = kEpiFirst + kEpiWarps, kConvFirst = kRawWarp + 1;
+constexpr int kThreads = (kConvFirst + kConvWarps) * 32;
 
 struct Fp4Weights {
   const unsigned char* scales;                 // [E][N][K/32]
-  int vec;                                     // 8 scales of 256 steps are one aligned word
+  int vec;                                     // two scales of 64 steps are one aligned word
 };
 
 struct Tail {
   uint64_t full[kMaxStages], empty[kMaxStages];  // full: of the pair's first block
-  uint64_t conv[kMaxStages];                     // this block's weights of a stage are written
   uint64_t raw[kRaw], rawfree[kRaw];
   uint64_t tfull[2], tempty[2];
   alignas(16) unsigned char turned[kEpiWarps][2][kTurned];
@@ -51,8 +63,13 @@ struct Tail {
   int scan[kThreads / 32];
 };
 
-size_t smem_bytes(int E, int stages) {
-  return size_t(stages) * kStage + size_t(kRaw) * kRawStage + sizeof(Tail) + size_t(E + 1) * 4;
+template <int MOST>
+__host__ __device__ constexpr size_t ring_bytes() {
+  return size_t(kRaw) * kRawStage + size_t(Form<MOST>::kStages) * Form<MOST>::kRowStage;
+}
+template <int MOST>
+size_t smem_bytes(int E) {
+  return ring_bytes<MOST>() + sizeof(Tail) + size_t(E + 1) * 4;
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -72,7 +89,8 @@ __device__ __forceinline__ uint32_t large_multiplier(uint32_t s) {
 }
 
 // Eight e2m1 codes as bf16 pairs in order, 2^-126 times their value: sign to bit
-// 15, the two exponent bits and the mantissa bit to bits 8 to 6.
+// 15, the two exponent bits and the mantissa bit to bits 8 to 6 (both shifts are
+// one product).
 __device__ __forceinline__ void codes8(uint32_t w, uint32_t (&o)[4]) {
   const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
 #pragma unroll
@@ -84,9 +102,9 @@ __device__ __forceinline__ void codes8(uint32_t w, uint32_t (&o)[4]) {
   }
 }
 
-// 32 codes (16 bytes) with their scale, to four 16-byte chunks.
+// 32 codes (16 bytes) with their scale, to 16 pairs.
 template <bool LARGE>
-__device__ __forceinline__ void convert32(const uint4& codes, uint32_t s, uint4 (&out)[4]) {
+__device__ __forceinline__ void convert32(const uint4& codes, uint32_t s, uint32_t* out) {
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
   const uint32_t m = LARGE ? 0x7e807e80u : multiplier(s);
 #pragma unroll
@@ -95,35 +113,61 @@ __device__ __forceinline__ void convert32(const uint4& codes, uint32_t s, uint4 
     codes8(w[i], o);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      o[j] = mul_bf16x2(o[j], m);
-      if (LARGE) o[j] = mul_bf16x2(o[j], large_multiplier(s));
+      out[4 * i + j] = mul_bf16x2(o[j], m);
+      if (LARGE) out[4 * i + j] = mul_bf16x2(out[4 * i + j], large_multiplier(s));
     }
-    out[i] = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
+// 32 words of each lane to 32 columns of this warp's TMEM lanes.
+__device__ __forceinline__ void tmem_st_x32(uint32_t dst, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(dst),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
+      "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
+      "r"(v[30]), "r"(v[31])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Pair only: M = 256 channels from both blocks' TMEM.
+__device__ __forceinline__ void mma_pair_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                              bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
+      : "memory");
+}
+
 // SPLIT: one tile per cluster, each of its pairs a part of the reduction.
-template <bool SPLIT>
+template <int MOST, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
                          const __grid_constant__ RowMaps map_r, const RaggedArgs p,
                          const Fp4Weights fw) {
-  extern __shared__ __align__(1024) unsigned char stages[];
-  unsigned char* raws = stages + size_t(p.stages) * kStage;
-  Tail* tail = reinterpret_cast<Tail*>(raws + size_t(kRaw) * kRawStage);
+  constexpr int kStages = Form<MOST>::kStages, kRowStage = Form<MOST>::kRowStage;
+  static_assert(kStages <= kMaxStages);
+  static_assert(ring_bytes<MOST>() >= size_t(MOST) * kBC * 4);  // holds a part's sums
+  extern __shared__ __align__(1024) unsigned char raws[];
+  unsigned char* stages = raws + size_t(kRaw) * kRawStage;
+  Tail* tail = reinterpret_cast<Tail*>(raws + ring_bytes<MOST>());
   int* pre = reinterpret_cast<int*>(tail + 1);
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const int crank = int(cluster_rank()), rank = crank & 1, even = crank & ~1;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&tail->full[i], 4);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&tail->full[i], 2 + 2 * kGroupWarps);
       mbar_init(&tail->empty[i], 1);
-      mbar_init(&tail->conv[i], kGroupWarps);
     }
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(&tail->raw[i], 1);
-      mbar_init(&tail->rawfree[i], 2 * kGroupWarps);
+      mbar_init(&tail->rawfree[i], kConvWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tail->tfull[i], 1);
@@ -136,11 +180,11 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
   pdl_wait_prior_grid();  // (nothing of the above touches global memory)
   const int ncol = ceil_div(p.out_cols, 2 * kBC);
   const int pairs = SPLIT ? 1 : int(gridDim.x) / 2;
-  tile_prefix<kThreads>(p, SPLIT ? kBR : tile_rows<kThreads>(p, ncol, pairs, tail->scan), pre,
+  tile_prefix<kThreads>(p, SPLIT ? MOST : tile_rows<kThreads>(p, MOST, ncol, pairs, tail->scan), pre,
                         tail->scan);
   cluster_sync_all();  // the barriers and TMEM of all blocks are ready
   tcgen05_fence_after();
-  const uint32_t tmem = tail->tmem;
+  const uint32_t tmem = tail->tmem, weights = tmem + 2 * MOST;
   const int tiles = pre[p.E] * ncol;  // below 2^31: the C ABI checks
   const int parts = SPLIT ? int(cluster_size()) / 2 : 1, part = SPLIT ? crank / 2 : 0;
   const int first = blockIdx.x / (2 * parts), step = SPLIT ? max(tiles, 1) : pairs;
@@ -154,24 +198,25 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
   if (warp == 0) {
     // ---- rows: one lane keeps the ring of stages full
     if (elect_one()) {
+      const uint32_t stage0 = smem_addr(stages), full0 = map_to_rank(&tail->full[0], even);
       RingAt s;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
         const Tile tl = tile_at(p, pre, ncol, t);
-        const int half = tl.n / 2, row = tl.row0 + rank * half;
-        for (int kb = kb_lo; kb < kb_hi; ++kb, s.next(p.stages)) {
+        const RowBoxes rows(map_r, tl, rank);
+        for (int kb = kb_lo; kb < kb_hi; ++kb, s.next(kStages)) {
           if (s.round > 0 &&
               !bounded_wait_idle(&tail->empty[s.slot], (s.round - 1) & 1u, failed)) {
             ok = false;
             break;
           }
-          const uint32_t bar = map_to_rank(&tail->full[s.slot], even);
-          arrive_expect_at(bar, uint32_t(half * kBK * 2));
-          load_rows(stages + size_t(s.slot) * kStage + kStageC, map_r, kb * kBK, row, half, bar);
+          const uint32_t bar = full0 + s.slot * 8;
+          arrive_expect_at(bar, rows.bytes);
+          rows.load(stage0 + s.slot * kRowStage, kb * kBK, bar);
         }
       }
       // every load has landed and been used before the block may end
-      for (int i = 0; i < p.stages; ++i, s.next(p.stages))
+      for (int i = 0; i < kStages; ++i, s.next(kStages))
         if (s.round > 0) bounded_wait_idle(&tail->empty[s.slot], (s.round - 1) & 1u, failed);
     }
   } else if (warp == 1) {
@@ -190,10 +235,13 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
           ok = bounded_wait(&tail->full[s.slot], s.round & 1u, failed);
           if (!ok) break;
           tcgen05_fence_after();
-          stage_products<false>(stages + size_t(s.slot) * kStage, tmem + buf * kBR, idesc,
-                                kb == kb_lo);
+          const uint64_t dr = smem_desc_sw128(smem_addr(stages + s.slot * kRowStage), 16, 1024);
+#pragma unroll
+          for (int k = 0; k < kBK / 16; ++k)
+            mma_pair_tmem(tmem + buf * MOST, weights + s.slot * kWeightCols + k * 8,
+                          dr + ((k * 32) >> 4), idesc, kb > kb_lo || k > 0);
           commit_to_pair(&tail->empty[s.slot], even);
-          s.next(p.stages);
+          s.next(kStages);
         }
         if (ok) commit_to_pair(&tail->tfull[buf], even);
       }
@@ -208,10 +256,10 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
       const uint32_t buf = nt & 1u;
       if (!bounded_wait_idle_warp(&tail->tfull[buf], (nt >> 1) & 1u, failed, p.patience)) break;
       tcgen05_fence_after();
-      const uint32_t src = tmem + buf * kBR + (uint32_t(q) << 21);
+      const uint32_t src = tmem + buf * MOST + (uint32_t(q) << 21);
       const int ch = tl.col0 + rank * kBC + q * 32;
       if (SPLIT)
-        store_part(tl, q, src, stages);  // (the stages are done with)
+        store_part(tl, q, src, raws);  // (the rings are done with)
       else if (ch < p.out_cols)
         write_tile(p, tl, ch, src, turned);
       tcgen05_fence_before();
@@ -241,76 +289,64 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
       for (int i = 0; i < kRaw; ++i, s.next(kRaw))
         if (s.round > 0) bounded_wait_idle(&tail->rawfree[s.slot], (s.round - 1) & 1u, failed);
     }
-  } else if (warp == kHandWarp) {
-    // ---- each stage that this block's warps have written, on to the products
-    if (elect_one()) {
-      RingAt s;
-      bool ok = true;
-      for (int t = first; t < tiles && ok; t += step) {
-        for (int kb = kb_lo; kb < kb_hi; ++kb, s.next(p.stages)) {
-          ok = bounded_wait(&tail->conv[s.slot], s.round & 1u, failed);
-          if (!ok) break;
-          fence_proxy_async_smem();
-          arrive_at(map_to_rank(&tail->full[s.slot], even));
-        }
-      }
-    }
   } else {
-    // ---- codes to bf16: a thread 64 codes of channel r in every other stage
-    const int group = (warp - kConvFirst) / kGroupWarps;
-    const int r = ((warp - kConvFirst) % kGroupWarps) * 32 + lane;
+    // ---- codes to bf16: a thread 64 codes of channel r in every fourth stage, for the
+    // TMEM lanes 32 q .. that its warp may write.  (A group skips stages, but none of
+    // their slots can be a phase behind: it has waited for the use of a slot not four
+    // stages before.)
+    const int group = (warp - kConvFirst) / kGroupWarps, q = warp & 3;
+    const int r = q * 32 + lane;
     const int groups = p.red / 32;
-    RingAt s, rs;
-    int group_of = 0;
+    RingAt rs;
+    uint32_t count = 0;  // stages before the raw stage at hand
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
       const Tile tl = tile_at(p, pre, ncol, t);
       // (channels past the last one: codes are zeros, any scale will do)
       const int ch = min(tl.col0 + rank * kBC + r, p.out_cols - 1);
       const unsigned char* sc = fw.scales + (int64_t(tl.e) * p.out_cols + ch) * groups;
-      // the scales of a raw stage, one stage ahead of their use
-      auto scales8 = [&](int rb) -> uint2 {
-        const int g = rb * 8;
-        if (fw.vec) return __ldg(reinterpret_cast<const uint2*>(sc + g));
-        uint32_t v[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          v[i >> 2] |= uint32_t(__ldg(sc + min(g + i, groups - 1))) << (8 * (i & 3));
-        return make_uint2(v[0], v[1]);
+      auto scales2 = [&](int kb) -> uint32_t {  // of the stage's two groups of 32
+        if (fw.vec) return __ldg(reinterpret_cast<const uint16_t*>(sc + 2 * min(kb, nk - 1)));
+        return __ldg(sc + min(2 * kb, groups - 1)) |
+               uint32_t(__ldg(sc + min(2 * kb + 1, groups - 1))) << 8;
       };
-      uint2 ahead = scales8(rb_lo);
+      // this group's first stage of the tile; its next scales are loaded one ahead
+      int mine = kb_lo + ((group - int(count)) & (kGroups - 1));
+      uint32_t ahead = scales2(mine);
       for (int rb = rb_lo; rb < rb_hi && ok; ++rb, rs.next(kRaw)) {
-        const uint2 now = ahead;
-        if (rb + 1 < rb_hi) ahead = scales8(rb + 1);
         ok = bounded_wait_warp(&tail->raw[rs.slot], rs.round & 1u, failed);
         if (!ok) break;
-        const unsigned char* src = raws + rs.slot * kRawStage + r * 128;
-        const int steps = min(kRawSteps, kb_hi - rb * kRawSteps);
-        for (int i = 0; i < steps; ++i, group_of ^= 1, s.next(p.stages)) {
-          if (group_of != group) continue;
+        const int end = min((rb + 1) * kRawSteps, kb_hi);
+        if (mine < end) {
+          const int i = mine - rb * kRawSteps;
+          const unsigned char* src = raws + rs.slot * kRawStage + r * 128;
           const uint4 c0 = *reinterpret_cast<const uint4*>(src + (((2 * i) ^ (r & 7)) << 4));
           const uint4 c1 = *reinterpret_cast<const uint4*>(src + (((2 * i + 1) ^ (r & 7)) << 4));
-          const uint32_t two = (i < 2 ? now.x : now.y) >> (16 * (i & 1));
-          const uint32_t s0 = two & 255u, s1 = (two >> 8) & 255u;
-          uint4 o[2][4];
-          if (__any_sync(kFull, s0 > 128u || s1 > 128u)) {
-            convert32<true>(c0, s0, o[0]);
-            convert32<true>(c1, s1, o[1]);
-          } else {
-            convert32<false>(c0, s0, o[0]);
-            convert32<false>(c1, s1, o[1]);
-          }
-          if (s.round > 0) ok = bounded_wait_warp(&tail->empty[s.slot], (s.round - 1) & 1u, failed);
-          if (!ok) break;
-          unsigned char* dst = stages + size_t(s.slot) * kStage + r * 128;
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(dst + ((j ^ (r & 7)) << 4)) = o[j >> 2][j & 3];
           __syncwarp();
-          if (lane == 0) mbar_arrive(&tail->conv[s.slot]);
+          if (lane == 0) mbar_arrive(&tail->rawfree[rs.slot]);
+          const uint32_t s0 = ahead & 255u, s1 = ahead >> 8;
+          mine += kGroups;
+          ahead = scales2(mine);
+          uint32_t o[32];
+          if (__any_sync(kFull, s0 > 128u || s1 > 128u)) {
+            convert32<true>(c0, s0, o);
+            convert32<true>(c1, s1, o + 16);
+          } else {
+            convert32<false>(c0, s0, o);
+            convert32<false>(c1, s1, o + 16);
+          }
+          const uint32_t at = count + i, slot = at % kStages, round = at / kStages;
+          if (round > 0) ok = bounded_wait_warp(&tail->empty[slot], (round - 1) & 1u, failed);
+          if (!ok) break;
+          tcgen05_fence_after();
+          tmem_st_x32(weights + slot * kWeightCols + (uint32_t(q) << 21), o);
+          tcgen05_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_at(map_to_rank(&tail->full[slot], even));
+        } else if (lane == 0) {  // (a short last raw stage)
+          mbar_arrive(&tail->rawfree[rs.slot]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tail->rawfree[rs.slot]);
+        count += end - rb * kRawSteps;
       }
     }
   }
@@ -319,23 +355,35 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
     __syncwarp();
     cluster_sync_all();
     if (first < tiles)
-      join_parts<kThreads>(p, tile_at(p, pre, ncol, first), rank, part, parts, stages);
+      join_parts<kThreads>(p, tile_at(p, pre, ncol, first), rank, part, parts, raws);
   }
   cluster_end();
   if (warp == 1) tmem_dealloc<true>(tmem, 512);
   if (threadIdx.x == 0 && tail->failed) raise_error(p.dev_err, MP_ERR_TIMEOUT);
 }
 
-template <bool SPLIT>
-cudaError_t launch_as(RaggedArgs p, const Fp4Weights& fw, const CUtensorMap& mw,
+template <int MOST, bool SPLIT>
+cudaError_t launch_as(const RaggedArgs& p, const Fp4Weights& fw, const CUtensorMap& mw,
                       const RowMaps& mr, int blocks, int parts, cudaStream_t st) {
-  p.stages = kMaxStages;
-  while (smem_bytes(p.E, p.stages) > size_t(kMaxBlockSmem)) --p.stages;
-  static thread_local bool configured[64] = {};
-  const cudaError_t e = allow_smem(mp_k_expert_matmul_mxfp4<SPLIT>, configured);
+  return launch_waiting(mp_k_expert_matmul_mxfp4<MOST, SPLIT>, dim3(unsigned(blocks)),
+                        dim3(kThreads), smem_bytes<MOST>(p.E), st, unsigned(2 * parts), mw, mr, p,
+                        fw);
+}
+
+template <int MOST>
+cudaError_t launch_tiles(const RaggedArgs& p, const Fp4Weights& fw, const CUtensorMap& mw,
+                         const RowMaps& mr, cudaStream_t st) {
+  static thread_local bool whole[64] = {}, split[64] = {};
+  cudaError_t e = allow_smem(mp_k_expert_matmul_mxfp4<MOST, false>, whole);
+  if (e == cudaSuccess) e = allow_smem(mp_k_expert_matmul_mxfp4<MOST, true>, split);
   if (e != cudaSuccess) return e;
-  return launch_waiting(mp_k_expert_matmul_mxfp4<SPLIT>, dim3(unsigned(blocks)), dim3(kThreads),
-                        smem_bytes(p.E, p.stages), st, unsigned(2 * parts), mw, mr, p, fw);
+  const int64_t tiles = most_row_tiles(p.E, p.rows, MOST) * ceil_div(p.out_cols, 2 * kBC);
+  const int parts = parts_for(mp_k_expert_matmul_mxfp4<MOST, true>, kThreads, tiles, 2, kMaxParts,
+                              ceil_div(p.red, kRawSteps * kBK), 4);
+  if (parts > 1)
+    return launch_as<MOST, true>(p, fw, mw, mr, int(tiles) * 2 * parts, parts, st);
+  const int pairs = int(std::min<int64_t>(tiles, sm_count() / 2));
+  return launch_as<MOST, false>(p, fw, mw, mr, 2 * pairs, 1, st);
 }
 
 }  // namespace
@@ -345,7 +393,7 @@ cudaError_t launch_expert_matmul_mxfp4(int E, int rows, int N, int K, const void
                                        const int32_t* expert_offsets, void* out, int32_t* dev_err,
                                        cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
-  if (rows <= 8 || rows / 4 <= E) {
+  if (rows <= 16 || rows / 8 <= E) {
     const cudaError_t e =
         launch_expert_rows(E, rows, N, K, a, w, w_scales, expert_offsets, out, dev_err, st);
     if (e != cudaErrorNotSupported) return e;
@@ -362,18 +410,15 @@ cudaError_t launch_expert_matmul_mxfp4(int E, int rows, int N, int K, const void
   p.dev_err = dev_err;
   Fp4Weights fw;
   fw.scales = w_scales;
-  fw.vec = K % (kRawSteps * kBK) == 0 && (reinterpret_cast<uintptr_t>(w_scales) & 7u) == 0;
+  fw.vec = K % kBK == 0 && (reinterpret_cast<uintptr_t>(w_scales) & 1u) == 0;
   CUtensorMap mw;
   RowMaps mr;
   if (!make_map_3d(&mw, w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(K) / 2, uint64_t(N),
                    uint64_t(E), kRawSteps * kBK / 2, kBC) ||
       !make_row_maps(&mr, a, K, rows))
     return cudaErrorInvalidValue;
-  const int64_t tiles = most_row_tiles(p.E, p.rows, kBR) * ceil_div(p.out_cols, 2 * kBC);
-  const int parts = parts_for(tiles, ceil_div(K, kBK), 2 * kRawSteps);
-  if (parts > 1) return launch_as<true>(p, fw, mw, mr, int(tiles) * 2 * parts, parts, st);
-  const int pairs = int(std::min<int64_t>(tiles, sm_count() / 2));
-  return launch_as<false>(p, fw, mw, mr, 2 * pairs, 1, st);
+  return rows / 640 < E ? launch_tiles<160>(p, fw, mw, mr, st)
+                        : launch_tiles<192>(p, fw, mw, mr, st);
 }
 
 }  // namespace mp

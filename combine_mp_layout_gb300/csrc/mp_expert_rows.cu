@@ -458,11 +458,8 @@ mp_k_expert_rows(const __grid_constant__ CUtensorMap map_w,
 }
 
 template <bool FP4, bool SPLIT>
-cudaError_t launch_as(const VecArgs& p, const CUtensorMap& mw, const CUtensorMap& ms, int blocks, int parts,
-                      cudaStream_t st) {
-  static thread_local bool configured[64] = {};
-  const cudaError_t e = allow_smem(mp_k_expert_rows<FP4, SPLIT>, configured);
-  if (e != cudaSuccess) return e;
+cudaError_t launch_as(const VecArgs& p, const CUtensorMap& mw, const CUtensorMap& ms, int blocks,
+                      int parts, cudaStream_t st) {
   return launch_waiting(mp_k_expert_rows<FP4, SPLIT>, dim3(unsigned(blocks)), dim3(kThreads),
                         vec_smem_bytes<FP4>(p.E, p.room, p.steps, p.pieces), st,
                         SPLIT ? unsigned(parts) : 0u, mw, ms, p);
@@ -472,13 +469,17 @@ cudaError_t launch_as(const VecArgs& p, const CUtensorMap& mw, const CUtensorMap
 template <bool FP4>
 cudaError_t launch_rows(VecArgs p, const void* w, cudaStream_t st) {
   constexpr int kSteps = Form<FP4>::kSteps;
+  static thread_local bool whole[64] = {}, split[64] = {};
+  cudaError_t e = allow_smem(mp_k_expert_rows<FP4, false>, whole);
+  if (e == cudaSuccess) e = allow_smem(mp_k_expert_rows<FP4, true>, split);
+  if (e != cudaSuccess) return e;
   // Room for four rows while the experts have two on average: the rows' place is the
   // ring's (7168 steps: eight pieces instead of four).
   p.room = p.rows <= 4 || p.rows / 2 < p.E ? 4 : kVR;
   const int64_t units = most_row_tiles(p.E, p.rows, p.room) * ceil_div(p.N, kBC);
   const int np = ceil_div(p.K, kSteps);
-  int parts = 1;
-  while (parts < kMaxVecParts && units * 2 * parts <= sm_count() && np >= 4 * parts) parts *= 2;
+  const int parts =
+      parts_for(mp_k_expert_rows<FP4, true>, kThreads, units, 1, kMaxVecParts, np, 2);
   p.steps = ceil_div(np, parts) * kSteps;
   p.pieces = kMaxPieces;
   while (p.pieces > 2 &&

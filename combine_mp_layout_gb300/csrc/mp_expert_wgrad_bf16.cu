@@ -126,6 +126,8 @@ mp_k_expert_wgrad_bf16(const __grid_constant__ CUtensorMap map_dy,
   if (warp == 0) {
     // ---- loads: one lane keeps the ring of stages full
     if (elect_one()) {
+      const uint32_t stage0 = smem_addr(stages), full0 = map_to_rank(&tail->full[0], 0);
+      const uint32_t last0 = map_to_rank(&tail->last[0], uint32_t(rank));
       RingAt s;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += stride) {
@@ -140,12 +142,11 @@ mp_k_expert_wgrad_bf16(const __grid_constant__ CUtensorMap map_dy,
             ok = false;
             break;
           }
-          unsigned char* dst = stages + size_t(s.slot) * kWStage;
+          const uint32_t dst = stage0 + uint32_t(s.slot) * kWStage;
           const int row = w.lo + i * kWRows;
           // a stage to be cleared goes to this block's clearing warp first
           const bool whole = rest == 0 || i + 1 < steps;
-          const uint32_t bar = whole ? map_to_rank(&tail->full[s.slot], 0)
-                                     : map_to_rank(&tail->last[s.slot], uint32_t(rank));
+          const uint32_t bar = (whole ? full0 : last0) + s.slot * 8;
           arrive_expect_at(bar, bytes);
           tma_load_2d_pair(dst, &map_dy, n, row, bar);
           tma_load_2d_pair(dst + kChunk, &map_dy, n + 64, row, bar);

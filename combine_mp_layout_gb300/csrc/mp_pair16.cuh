@@ -65,19 +65,21 @@ __host__ __device__ constexpr uint32_t mma_idesc_bf16(int m, int n, bool a_mn, b
 
 // TMA loads into this block's shared memory whose bytes are counted on a barrier
 // of this block or of the other one of its pair (a shared::cluster address).
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int x, int y,
+// (dst: a shared address.  What a loading thread does per stage is kept short: its
+// instructions wait their turn among the other warps'.)
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y,
                                                  uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
-      "bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+      "bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, int x, int y,
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int x, int y,
                                                  int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
-      "bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      "bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
@@ -227,13 +229,15 @@ __device__ void tile_prefix(const RaggedArgs& p, int most, int* pre, int* scan) 
   __syncthreads();
 }
 
-// The most rows of a tile: 256, or 224 or 192 where their tiles fill the pairs'
-// turns better.  A turn takes about as long as its tiles' units of 32 rows on
-// average and 1.25 more (measured, 4096 x 7168: 38.4 us with 256 rows, 34.3 with
-// 224, 32.7 with 211), so a smaller tile has to save whole turns.  (32 experts of
-// about 1,024 rows, 2,048 channels from 7168: 17 turns of 6.5 units, not 16 of 7.2.)
+// The most rows of a tile: `most` (256 or 192), or 32 or 64 fewer where their tiles
+// fill the pairs' turns better.  A turn takes about as long as its tiles' units of 32
+// rows on average and 1.25 more (measured with bf16 weights, 4096 x 7168: 38.4 us with
+// 256 rows, 34.3 with 224, 32.7 with 211), so a smaller tile has to save whole turns.
+// (32 experts of about 1,024 rows, 2,048 channels from 7168: 17 turns of 6.5 units
+// take 535 us, 16 of 7.2 units 550.)
 template <int THREADS>
-__device__ int tile_rows(const RaggedArgs& p, int ncol, int pairs, int* scan) {
+__device__ int tile_rows(const RaggedArgs& p, int most, int ncol, int pairs, int* scan) {
+  const int full = most / kUnit;
   int units = 0, tiles[3] = {0, 0, 0};
   for (int e = threadIdx.x; e < p.E; e += THREADS) {
     int lo, hi;
@@ -241,10 +245,10 @@ __device__ int tile_rows(const RaggedArgs& p, int ncol, int pairs, int* scan) {
     const int u = (hi - lo + kUnit - 1) / kUnit;
     units += u;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) tiles[i] += (u + 7 - i) / (8 - i);
+    for (int i = 0; i < 3; ++i) tiles[i] += (u + full - i - 1) / (full - i);
   }
   units = block_sum<THREADS>(units, scan);
-  int best = 8;
+  int best = full;
   float least = INFINITY;
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
@@ -253,7 +257,7 @@ __device__ int tile_rows(const RaggedArgs& p, int ncol, int pairs, int* scan) {
     const float cost = ceilf(t * ncol / pairs) * (units / fmaxf(t, 1.0f) + 1.25f);
     if (cost < least) {
       least = cost;
-      best = 8 - i;
+      best = full - i;
     }
   }
   return best * kUnit;
@@ -306,8 +310,8 @@ __device__ __forceinline__ void cluster_end() {
   tcgen05_fence_after();
 }
 
-// A tile's rows, half of them per block: a multiple of 16 (up to 128), loaded as
-// the boxes of 16, 32, 64 and 128 rows that it is the sum of.
+// A tile's rows, half of them per block: a multiple of 16 (up to 128), loaded as one
+// or two boxes of 16, 32, 64 or 128 rows (112 as 128: the stage has the room).
 struct RowMaps {
   CUtensorMap m[4];
 };
@@ -316,16 +320,27 @@ inline bool make_row_maps(RowMaps* r, const void* a, int red, int rows) {
     if (!make_map_bf16(&r->m[i], a, uint64_t(red), uint64_t(rows), kBK, 16u << i)) return false;
   return true;
 }
-__device__ __forceinline__ void load_rows(unsigned char* dst, const RowMaps& maps, int k, int row,
-                                          int half, uint32_t bar) {
-#pragma unroll
-  for (int i = 3; i >= 0; --i)
-    if (half & (16 << i)) {
-      tma_load_2d_pair(dst, &maps.m[i], k, row, bar);
-      dst += (16 << i) * kBK * 2;
-      row += 16 << i;
-    }
-}
+struct RowBoxes {
+  const CUtensorMap *one, *two;  // two: NULL if one box is all
+  int row, row2;                 // their first rows
+  uint32_t at2, bytes;           // of the second box in the stage; of both
+  __device__ __forceinline__ RowBoxes(const RowMaps& maps, const Tile& tl, int rank) {
+    int half = tl.n / 2;
+    row = row2 = tl.row0 + rank * half;
+    if (half == 112) half = 128;
+    const int big = half >= 128 ? 3 : half >= 64 ? 2 : half >= 32 ? 1 : 0;
+    const int rest = half - (16 << big);  // 0, 16 or 32
+    one = &maps.m[big];
+    two = rest == 0 ? nullptr : &maps.m[rest == 32 ? 1 : 0];
+    row2 += 16 << big;
+    at2 = uint32_t(16 << big) * kBK * 2;
+    bytes = uint32_t(half) * kBK * 2;
+  }
+  __device__ __forceinline__ void load(uint32_t dst, int k, uint32_t bar) const {
+    tma_load_2d_pair(dst, one, k, row, bar);
+    if (two != nullptr) tma_load_2d_pair(dst + at2, two, k, row2, bar);
+  }
+};
 
 // The products of one stage: four K = 16 steps.
 template <bool C_MN>
@@ -429,13 +444,46 @@ __device__ __forceinline__ void join_parts(const RaggedArgs& p, const Tile& tl, 
   }
 }
 
-// How many pairs share a tile's reduction: with few tiles, clusters of two or
-// four, while all of them run at once and each has `least` stages.
-inline int parts_for(int64_t tiles, int stages, int least) {
-  int parts = 1;
-  while (parts < kMaxParts && tiles * 2 * parts <= sm_count() / 2 && stages >= 2 * least * parts)
-    parts *= 2;
-  return parts;
+// How many clusters of `size` blocks of a kernel, with as much shared memory as there
+// is, run at once; asked once per kernel, device and thread.  (On 152 SMs 76 of two
+// blocks, 36 of four, 23 of six, 15 of eight.)
+template <typename Kernel>
+inline int clusters_at_once(Kernel kernel, int threads, int size) {
+  struct Known { int dev[64][9] = {}; };
+  static thread_local Known known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || size > 8) return 0;
+  if (dev >= 0 && dev < 64 && known.dev[dev][size] > 0) return known.dev[dev][size] - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(size * 16));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = kMaxBlockSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(size);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();  // (not this call's to report)
+    n = 0;
+  }
+  if (dev >= 0 && dev < 64) known.dev[dev][size] = n + 1;
+  return n;
+}
+
+// The most parts, up to `most`, that a reduction can be shared in by clusters of
+// `per` blocks a part so that all of `tiles` clusters run at once and each part has
+// `least` of the reduction's stages.
+template <typename Kernel>
+inline int parts_for(Kernel kernel, int threads, int64_t tiles, int per, int most, int stages,
+                     int least) {
+  for (int parts = most; parts > 1; --parts)
+    if (stages >= parts * least && tiles * per * parts <= sm_count() &&
+        tiles <= clusters_at_once(kernel, threads, per * parts))
+      return parts;
+  return 1;
 }
 // Tiles of `most` rows, at most: every expert's first row starts one.
 inline int64_t most_row_tiles(int E, int rows, int most) {
