@@ -34,11 +34,11 @@ bool product_args_ok(int E, int rows, int N, int K, const void* a, const void* w
          aligned_to(expert_offsets, 4) && aligned_to(dev_err, 4);
 }
 
-// Row tiles of 256 rows, at most one short one per expert, times column tiles of
+// Row tiles of `most` rows, at most one short one per expert, times column tiles of
 // 256 channels; and as many more as there can be blocks, so that a loop over tiles
 // ends before its counter does.
-bool tiles_ok(int E, int rows, int cols) {
-  return (int64_t(rows) / 256 + E) * ((int64_t(cols) + 255) / 256) < k31 - 4096;
+bool tiles_ok(int E, int rows, int cols, int most) {
+  return (int64_t(rows) / most + E) * ((int64_t(cols) + 255) / 256) < k31 - 4096;
 }
 
 bool gate_args_ok(int rows, int I) {
@@ -53,7 +53,7 @@ int mp_expert_matmul_bf16(int E, int rows, int N, int K, const void* a, const vo
                           const int32_t* expert_offsets, void* out, int32_t* dev_err,
                           mp_stream_t stream) {
   if (!product_args_ok(E, rows, N, K, a, w, true, expert_offsets, out, false, dev_err) ||
-      !tiles_ok(E, rows, N))
+      !tiles_ok(E, rows, N, 256))
     return MP_ERR_INVALID_ARG;
   return status_of(launch_expert_matmul_bf16(E, rows, N, K, false, a, w, expert_offsets, out,
                                              dev_err, reinterpret_cast<cudaStream_t>(stream)));
@@ -63,7 +63,7 @@ int mp_expert_matmul_dgrad_bf16(int E, int rows, int N, int K, const void* dy, c
                                 const int32_t* expert_offsets, void* dx, int32_t* dev_err,
                                 mp_stream_t stream) {
   if (!product_args_ok(E, rows, N, K, dy, w, true, expert_offsets, dx, false, dev_err) ||
-      !tiles_ok(E, rows, K))
+      !tiles_ok(E, rows, K, 256))
     return MP_ERR_INVALID_ARG;
   return status_of(launch_expert_matmul_bf16(E, rows, N, K, true, dy, w, expert_offsets, dx,
                                              dev_err, reinterpret_cast<cudaStream_t>(stream)));
@@ -85,7 +85,7 @@ int mp_expert_matmul_mxfp4(int E, int rows, int N, int K, const void* a, const v
                            const uint8_t* w_scales, const int32_t* expert_offsets, void* out,
                            int32_t* dev_err, mp_stream_t stream) {
   if (!product_args_ok(E, rows, N, K, a, w, true, expert_offsets, out, false, dev_err) ||
-      K % MP_MX_BLOCK != 0 || !w_scales || !tiles_ok(E, rows, N))
+      K % MP_MX_BLOCK != 0 || !w_scales || !tiles_ok(E, rows, N, 160))
     return MP_ERR_INVALID_ARG;
   return status_of(launch_expert_matmul_mxfp4(E, rows, N, K, a, w, w_scales, expert_offsets, out,
                                               dev_err, reinterpret_cast<cudaStream_t>(stream)));

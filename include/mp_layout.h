@@ -877,15 +877,18 @@ int mp_expert_matmul_wgrad_bf16(int E, int rows, int N, int K, const void *dy, c
  * mp_expert_matmul_mxfp4 -- mp_expert_matmul_bf16 with 4-bit weights, as
  * mp_allgatherv_mxfp4 (with R = 1, a weight's rows being the rows) quantises them:
  *   out[r][n] = bf16( sum over k of a[r][k] * 2^(w_scales[e][n][k/32] - 127) * w[e][n][k] )
- * The weights are exact in bf16, so are the products; sums fp32, one rounding.
+ * The weights are exact in bf16, so are the products; sums fp32, one rounding.  With
+ * few rows (up to 16, or below 8 (E + 1)) a row's values are held in f16, per 32
+ * channels relative to a power of two: those below 2^-32 of the 32's largest lose
+ * bits, at most 2^-40 of it.
  *   in   a         bf16 [rows][K]
  *   in   w         uint8 [E][N][K/2]: two e2m1 codes a byte, the even k in the low
  *                  nibble (0, 1/2, 1, 3/2, 2, 3, 4, 6; bit 3 the sign)
  *   in   w_scales  uint8 [E][N][K/32]: UE8M0, 255 makes its 32 weights NaN
  *   out  out       bf16 [rows][N]; rows of no expert are not written
  * A weight past bf16's largest number (from 2^128) is infinite.
- * Checks and device errors as mp_expert_matmul_bf16, with K % 32 == 0 and w_scales
- *   (of any alignment) not NULL.
+ * Checks and device errors as mp_expert_matmul_bf16, with K % 32 == 0, w_scales (of
+ *   any alignment) not NULL and (rows/160 + E) * ceil(N/256) < 2^31 - 4096.
  */
 #define MP_MX_BLOCK 32
 int mp_expert_matmul_mxfp4(int E, int rows, int N, int K, const void *a, const void *w,

@@ -58,7 +58,8 @@ def test_wgrad_rejects(L, bad):
 
 
 @no_gpu
-@pytest.mark.parametrize("bad", BAD[:-11] + BAD[-9:] + [dict(K=48), dict(K=72), dict(s=_p(0))])
+@pytest.mark.parametrize("bad", BAD[:-11] + BAD[-9:] + [
+    dict(K=48), dict(K=72), dict(s=_p(0)), dict(rows=2 ** 31 - 1025, N=160 * 256)])
 def test_mxfp4_rejects(L, bad):
     a = dict(MM, s=_p(FAKE + 1), **bad) if "s" not in bad else dict(MM, **bad)
     assert L.mp_expert_matmul_mxfp4(a["E"], a["rows"], a["N"], a["K"], a["a"], a["w"], a["s"],

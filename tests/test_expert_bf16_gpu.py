@@ -120,7 +120,8 @@ def test_matmul(kind, counts, N, K, slack, exact):
 
 WG = [([1], 8, 8, 0), ([0, 1, 63, 65, 0], 136, 392, 7), ([64, 128, 5], 256, 264, 0),
       ([300, 0, 411], 384, 640, 1), ([5, 70, 0, 0, 130, 64, 1, 2], 248, 1024, 0),
-      ([1500], 520, 1160, 0), ([7] * 300, 256, 296, 0)]
+      ([1500], 520, 1160, 0), ([7] * 300, 256, 296, 0), ([3001], 264, 392, 2),
+      ([700, 0, 1, 1900], 256, 248, 0), ([40, 2000], 8, 520, 1)]
 
 
 @pytest.mark.parametrize("exact", [True, False])
@@ -625,14 +626,16 @@ def test_mxfp4(counts, N, K, slack, exact):
     assert bool((buf.t[lo:] == 7.0).all())
 
 
+@pytest.mark.parametrize("groups", [253, 256])  # scales that TMA cannot load, and can
 @pytest.mark.parametrize("rows", [1, 5, 300])
-def test_mxfp4_scales_of_any_size(rows):
+def test_mxfp4_scales_of_any_size(rows, groups):
     """One term per output: the weight itself, through all codes and scales that leave it finite
     (6 * 2^125 is the largest), with a token that brings the product into range."""
-    N, K = 16, 32 * 253
+    N, K = 16, 32 * groups
     w = torch.arange(16, dtype=torch.uint8, device=DEV)  # channel n: code n everywhere
     w = (w | (w << 4))[:, None].expand(N, K // 2).contiguous()[None]
-    s = torch.arange(253, dtype=torch.uint8, device=DEV)[None].expand(N, 253).contiguous()[None]
+    s = torch.arange(groups, device=DEV).clamp(max=252).to(torch.uint8)
+    s = s[None].expand(N, groups).contiguous()[None]
     err = zeros(1, torch.int32)
     table = torch.tensor(E2M1 + [-v for v in E2M1], dtype=torch.float64, device=DEV)
     for scale in (0, 1, 3, 60, 126, 127, 128, 129, 130, 200, 251, 252):
@@ -748,3 +751,102 @@ def test_mxfp4_many_experts_far_offsets_and_a_graph():
             torch.cuda.synchronize()
             assert torch.equal(out, first)
     assert int(err) == 0
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+def test_mxfp4_rows_of_any_size(rows):
+    """Values of a row far apart: each group of 32 channels has its own largest, from 2^-133 to
+    2^127, and one term of it counts (the others' codes are 0), so that nothing is rounded away."""
+    N, groups = 24, 256
+    K = 32 * groups
+    g = gen(45)
+    w = torch.zeros((1, N, K), dtype=torch.uint8, device=DEV)
+    pick = torch.randint(0, 32, (groups,), generator=g, device=DEV)
+    at = torch.arange(groups, device=DEV) * 32 + pick
+    s = torch.full((1, N, groups), 127, dtype=torch.uint8, device=DEV)
+    packed = None
+    for group in (0, 1, 130, 255):
+        # channel n reads group `group` alone, with code n & 7 and the sign of n >= 8
+        w.zero_()
+        w[0, :, at[group]] = (torch.arange(N, device=DEV) % 16).to(torch.uint8)
+        packed = (w[..., 0::2] | (w[..., 1::2] << 4)).contiguous()
+        a = zeros((rows, K), BF)
+        a[:, at] = torch.exp2(torch.arange(groups, device=DEV).double() - 133).clamp(
+            max=2.0 ** 120).to(BF) * 1.0
+        a[1::2] *= -1
+        out, err = zeros((rows, N), BF), zeros(1, torch.int32)
+        B.check(B.mp_expert_matmul_mxfp4(1, rows, N, K, a, packed, s, None, out, err))
+        torch.cuda.synchronize()
+        want = a.double() @ fp4_ref(packed, s)[0].t()
+        assert torch.equal(out.double(), rounded(want)), group
+        assert int(err) == 0
+
+
+# ------------------------------------------------------------------ many sizes
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_problems(seed):
+    """Sizes drawn over the forms that the launchers choose among (rows, split reductions, tiles of
+    each size), whole numbers throughout: bit-equal."""
+    r = np.random.default_rng(1000 + seed)
+    E = int(r.choice([1, 1, 2, 3, 5, 8, 20, 64]))
+    rows = int(np.exp(r.uniform(0, np.log(3000))))
+    N, K = 8 * int(np.exp(r.uniform(0, np.log(160)))), 32 * int(np.exp(r.uniform(0, np.log(50))))
+    p = r.dirichlet(np.full(E, r.choice([0.2, 1.0, 20.0])))
+    counts = r.multinomial(rows, p)
+    g = gen(seed)
+    a, dy, w = values((rows, K), g, True), values((rows, N), g, True), values((E, N, K), g, True)
+    codes, s = fp4_weights((E, N, K), g)
+    ref = fp4_ref(codes, s)
+    off, err = offsets(counts), zeros(1, torch.int32)
+    y, y4, dx = Guarded((rows, N), BF), Guarded((rows, N), BF), Guarded((rows, K), BF)
+    dw, dw32 = Guarded((E, N, K), BF), Guarded((E, N, K), torch.float32)
+    B.check(B.mp_expert_matmul_bf16(E, rows, N, K, a, w, off, y.t, err))
+    B.check(B.mp_expert_matmul_mxfp4(E, rows, N, K, a, codes, s, off, y4.t, err))
+    B.check(B.mp_expert_matmul_dgrad_bf16(E, rows, N, K, dy, w, off, dx.t, err))
+    B.check(B.mp_expert_matmul_wgrad_bf16(E, rows, N, K, dy, a, off, False, dw.t, err))
+    B.check(B.mp_expert_matmul_wgrad_bf16(E, rows, N, K, dy, a, off, True, dw32.t, err))
+    torch.cuda.synchronize()
+    assert int(err) == 0 and all(b.intact() for b in (y, y4, dx, dw, dw32))
+    lo = 0
+    for e, n in enumerate(counts):
+        x, d = a[lo:lo + n].double(), dy[lo:lo + n].double()
+        assert torch.equal(y.t[lo:lo + n].double(), rounded(x @ w[e].double().t()))
+        assert torch.equal(y4.t[lo:lo + n].double(), rounded(x @ ref[e].t()))
+        assert torch.equal(dx.t[lo:lo + n].double(), rounded(d @ w[e].double()))
+        assert torch.equal(dw.t[e].double(), rounded(d.t() @ x))
+        assert torch.equal(dw32.t[e].double(), d.t() @ x + 7.0)
+        lo += n
+
+
+def test_first_calls_in_a_capture():
+    """A process whose first calls are captured (limits are raised and asked for there)."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from combine_mp_layout_gb300 import binding as B
+dev = dict(device="cuda")
+E, N, K = 2, 64, 512
+off = {n: torch.tensor([0, n // 2, n], dtype=torch.int32, **dev) for n in (2, 60, 600)}
+a = {n: torch.ones((n, K), dtype=torch.bfloat16, **dev) for n in off}
+w = torch.ones((E, N, K), dtype=torch.bfloat16, **dev)
+w4 = torch.full((E, N, K // 2), 0x22, dtype=torch.uint8, **dev)
+s = torch.full((E, N, K // 32), 127, dtype=torch.uint8, **dev)
+out = {(n, k): torch.zeros((n, N), dtype=torch.bfloat16, **dev) for n in off for k in (0, 1)}
+dw, err = torch.zeros((E, N, K), **dev), torch.zeros(1, dtype=torch.int32, **dev)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    for n in off:
+        B.check(B.mp_expert_matmul_bf16(E, n, N, K, a[n], w, off[n], out[n, 0], err))
+        B.check(B.mp_expert_matmul_mxfp4(E, n, N, K, a[n], w4, s, off[n], out[n, 1], err))
+    B.check(B.mp_expert_matmul_wgrad_bf16(E, 60, N, K, out[60, 0], a[60], off[60], False, dw, err))
+graph.replay()
+torch.cuda.synchronize()
+assert int(err) == 0 and all(bool((t == K).all()) for t in out.values())
+assert bool((dw == 30 * K).all())
+print("fine")
+"""
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "fine" in done.stdout, done.stderr[-2000:]
