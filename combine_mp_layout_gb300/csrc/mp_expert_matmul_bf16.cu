@@ -77,7 +77,7 @@ mp_k_expert_matmul_bf16(const __grid_constant__ CUtensorMap map_w,
   pdl_wait_prior_grid();  // (nothing of the above touches global memory)
   const int ncol = ceil_div(p.out_cols, 2 * kBC);
   const int pairs = SPLIT ? 1 : int(gridDim.x) / 2;
-  tile_prefix<kThreads>(p, SPLIT ? kBR : tile_rows<kThreads>(p, kBR, ncol, pairs, tail->scan), pre,
+  tile_prefix<kThreads>(p, SPLIT ? kBR : tile_rows<kThreads>(p, kBR, 0.0f, ncol, pairs, tail->scan), pre,
                         tail->scan);
   cluster_sync_all();  // the barriers and TMEM of all blocks are ready
   tcgen05_fence_after();
@@ -98,7 +98,7 @@ mp_k_expert_matmul_bf16(const __grid_constant__ CUtensorMap map_w,
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
         const Tile tl = tile_at(p, pre, ncol, t);
-        const RowBoxes rows(map_r, tl, rank);
+        const RowBoxes rows(map_r, tl.row0, tl.n, rank);
         const uint32_t bytes = kStageC + rows.bytes;
         const int ch = tl.col0 + rank * kBC;
         for (int kb = kb_lo; kb < kb_hi; ++kb, s.next(p.stages)) {

@@ -8,15 +8,23 @@
 // smallest scale leaves 2^-128), so the weights are turned into bf16 on their way to
 // the tensor core and the products are exact; sums are fp32, rounded once.
 //
-// Layout: that of the bf16 products, a tile of 256 channels by up to 192 rows per
-// pair of blocks, but the weights' operand (the MMA's M side) lies in TMEM: four
-// stages of 64 steps, 32 columns each, beside two accumulators of 192.  In shared
-// memory each stage would have to be written and read there, 32 KB beside the 40 KB
-// of the codes and rows, more than the products' time allows for (8,191 rows over 32
-// experts, 7168 x 2048: 204 us).  The codes come by TMA into a ring of raw stages (128
-// channels x 256 reduction steps, 16 KB); sixteen warps, in four groups with a stage
-// each, turn them into bf16, a thread a channel's 64 codes.
+// Layout: that of the bf16 products, a tile of 256 channels by a number of rows per
+// pair of blocks, but the weights' operand (the MMA's M side) lies in TMEM, in four or
+// six stages of 64 steps, 32 columns each, beside the accumulators.  In shared memory
+// each stage would have to be written and read there, 32 KB beside the 40 KB of the
+// codes and rows, more than the products' time allows for (512 rows over 32 experts,
+// 4096 x 7168: 240 us, so 180).  The codes come by TMA into a ring of raw stages (128
+// channels x 256 reduction steps, 16 KB); sixteen warps, in four groups that take the
+// stages in turn, turn them into bf16, a thread a channel's 64 codes.
+//
+// A stage's conversion takes as long as the products of some 200 rows, so what counts
+// is how seldom a weight is converted: tiles are of up to 288 rows with one
+// accumulator, or, where that saves no tiles, of up to 192 or 160 with two (and the
+// write of a tile under the next one's products).  8,191 rows over 32 experts, 7168 x
+// 2048: 172 us (1.40 PFLOP/s), 204 with 192 rows; 32,768 rows, 4096 x 7168: 1.10 ms
+// (1.74 PFLOP/s).
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -27,19 +35,19 @@ namespace mp {
 
 namespace {
 
-// TMEM is two accumulators of MOST columns (a tile's most rows) and stages of 64
-// steps of weights in the rest.  192 rows leave four stages, 160 six: with few rows
-// per expert the products of a stage are short and more of them have to be under way
-// (8,191 rows over 32 experts, 2048 x 7168: 227 us with four stages, 181 with six;
-// 32,768 rows, 4096 x 7168: 1,110 and 1,150 us).
+// TMEM is one or two accumulators of MOST columns (a tile's most rows) and stages of
+// 64 steps of weights in the rest.
 constexpr int kWeightCols = kBK / 2;           // TMEM columns of a stage of weights
 template <int MOST>
 struct Form {
-  static constexpr int kStages = (512 - 2 * MOST) / kWeightCols;
+  static constexpr int kAccs = MOST > 224 ? 1 : 2;
+  static constexpr int kStages = MOST > 224 ? 6 : (512 - 2 * MOST) / kWeightCols;
   static constexpr int kRowStage = MOST / 2 * kBK * 2;
+  static constexpr int kRaw = MOST > 224 ? 5 : 6;  // raw stages
+  static_assert(kAccs * MOST + kStages * kWeightCols <= 512);
 };
-constexpr int kMaxStages = 6;
-constexpr int kRaw = 6;                        // raw stages
+constexpr int kMaxStages = 6, kMaxRaw = 6;
+constexpr float kLeastTurn = 6.5f;             // a stage's conversion, in units of 32 rows
 constexpr int kRawSteps = 4;                   // stages of 64 in a raw stage of 256
 constexpr int kRawStage = kBC * kRawSteps * kBK / 2;
 constexpr int kGroupWarps = kBC / 32;          // a thread per channel
@@ -55,7 +63,7 @@ struct Fp4Weights {
 
 struct Tail {
   uint64_t full[kMaxStages], empty[kMaxStages];  // full: of the pair's first block
-  uint64_t raw[kRaw], rawfree[kRaw];
+  uint64_t raw[kMaxRaw], rawfree[kMaxRaw];
   uint64_t tfull[2], tempty[2];
   alignas(16) unsigned char turned[kEpiWarps][2][kTurned];
   uint32_t tmem;
@@ -65,7 +73,8 @@ struct Tail {
 
 template <int MOST>
 __host__ __device__ constexpr size_t ring_bytes() {
-  return size_t(kRaw) * kRawStage + size_t(Form<MOST>::kStages) * Form<MOST>::kRowStage;
+  return size_t(Form<MOST>::kRaw) * kRawStage +
+         size_t(Form<MOST>::kStages) * Form<MOST>::kRowStage;
 }
 template <int MOST>
 size_t smem_bytes(int E) {
@@ -144,6 +153,9 @@ __device__ __forceinline__ void mma_pair_tmem(uint32_t d, uint32_t a, uint64_t b
       : "memory");
 }
 
+// Of a tile's rows those that one MMA takes: all, or 160 of 288.
+__device__ __forceinline__ int first_rows(int n) { return n <= kBR ? n : 160; }
+
 // SPLIT: one tile per cluster, each of its pairs a part of the reduction.
 template <int MOST, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -151,7 +163,8 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
                          const __grid_constant__ RowMaps map_r, const RaggedArgs p,
                          const Fp4Weights fw) {
   constexpr int kStages = Form<MOST>::kStages, kRowStage = Form<MOST>::kRowStage;
-  static_assert(kStages <= kMaxStages);
+  constexpr int kRaw = Form<MOST>::kRaw, kAccs = Form<MOST>::kAccs;
+  static_assert(kStages <= kMaxStages && kRaw <= kMaxRaw);
   static_assert(ring_bytes<MOST>() >= size_t(MOST) * kBC * 4);  // holds a part's sums
   extern __shared__ __align__(1024) unsigned char raws[];
   unsigned char* stages = raws + size_t(kRaw) * kRawStage;
@@ -180,11 +193,11 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
   pdl_wait_prior_grid();  // (nothing of the above touches global memory)
   const int ncol = ceil_div(p.out_cols, 2 * kBC);
   const int pairs = SPLIT ? 1 : int(gridDim.x) / 2;
-  tile_prefix<kThreads>(p, SPLIT ? MOST : tile_rows<kThreads>(p, MOST, ncol, pairs, tail->scan), pre,
+  tile_prefix<kThreads>(p, SPLIT ? MOST : tile_rows<kThreads>(p, MOST, kLeastTurn, ncol, pairs, tail->scan), pre,
                         tail->scan);
   cluster_sync_all();  // the barriers and TMEM of all blocks are ready
   tcgen05_fence_after();
-  const uint32_t tmem = tail->tmem, weights = tmem + 2 * MOST;
+  const uint32_t tmem = tail->tmem, weights = tmem + kAccs * MOST;
   const int tiles = pre[p.E] * ncol;  // below 2^31: the C ABI checks
   const int parts = SPLIT ? int(cluster_size()) / 2 : 1, part = SPLIT ? crank / 2 : 0;
   const int first = blockIdx.x / (2 * parts), step = SPLIT ? max(tiles, 1) : pairs;
@@ -203,7 +216,11 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
         const Tile tl = tile_at(p, pre, ncol, t);
-        const RowBoxes rows(map_r, tl, rank);
+        // (rows past the first 256 are another MMA's)
+        const int n1 = first_rows(tl.n), n2 = tl.n - n1;
+        const RowBoxes rows(map_r, tl.row0, n1, rank);
+        const RowBoxes more(map_r, tl.row0 + n1, max(n2, kUnit), rank);
+        const uint32_t bytes = rows.bytes + (n2 > 0 ? more.bytes : 0);
         for (int kb = kb_lo; kb < kb_hi; ++kb, s.next(kStages)) {
           if (s.round > 0 &&
               !bounded_wait_idle(&tail->empty[s.slot], (s.round - 1) & 1u, failed)) {
@@ -211,8 +228,10 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
             break;
           }
           const uint32_t bar = full0 + s.slot * 8;
-          arrive_expect_at(bar, rows.bytes);
+          arrive_expect_at(bar, bytes);
           rows.load(stage0 + s.slot * kRowStage, kb * kBK, bar);
+          if (MOST > kBR && n2 > 0)
+            more.load(stage0 + s.slot * kRowStage + n1 / 2 * kBK * 2, kb * kBK, bar);
         }
       }
       // every load has landed and been used before the block may end
@@ -227,10 +246,12 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step, ++nt) {
         const Tile tl = tile_at(p, pre, ncol, t);
-        const uint32_t idesc = mma_idesc_bf16(2 * kBC, tl.n, false, false);
-        const uint32_t buf = nt & 1u;
-        if (nt >= 2)
-          ok = bounded_wait(&tail->tempty[buf], ((nt >> 1) - 1) & 1u, failed, p.patience);
+        const int n1 = first_rows(tl.n), n2 = tl.n - n1;
+        const uint32_t idesc = mma_idesc_bf16(2 * kBC, n1, false, false);
+        const uint32_t idesc2 = mma_idesc_bf16(2 * kBC, max(n2, kUnit), false, false);
+        const uint32_t buf = nt % kAccs;
+        if (nt >= kAccs)
+          ok = bounded_wait(&tail->tempty[buf], (nt / kAccs - 1) & 1u, failed, p.patience);
         for (int kb = kb_lo; kb < kb_hi && ok; ++kb) {
           ok = bounded_wait(&tail->full[s.slot], s.round & 1u, failed);
           if (!ok) break;
@@ -240,6 +261,13 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
           for (int k = 0; k < kBK / 16; ++k)
             mma_pair_tmem(tmem + buf * MOST, weights + s.slot * kWeightCols + k * 8,
                           dr + ((k * 32) >> 4), idesc, kb > kb_lo || k > 0);
+          if (MOST > kBR && n2 > 0) {
+            const uint64_t dm = dr + ((n1 / 2 * kBK * 2) >> 4);
+#pragma unroll
+            for (int k = 0; k < kBK / 16; ++k)
+              mma_pair_tmem(tmem + n1, weights + s.slot * kWeightCols + k * 8,
+                            dm + ((k * 32) >> 4), idesc2, kb > kb_lo || k > 0);
+          }
           commit_to_pair(&tail->empty[s.slot], even);
           s.next(kStages);
         }
@@ -253,8 +281,8 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
     uint32_t nt = 0;
     for (int t = first; t < tiles; t += step, ++nt) {
       const Tile tl = tile_at(p, pre, ncol, t);
-      const uint32_t buf = nt & 1u;
-      if (!bounded_wait_idle_warp(&tail->tfull[buf], (nt >> 1) & 1u, failed, p.patience)) break;
+      const uint32_t buf = nt % kAccs;
+      if (!bounded_wait_idle_warp(&tail->tfull[buf], (nt / kAccs) & 1u, failed, p.patience)) break;
       tcgen05_fence_after();
       const uint32_t src = tmem + buf * MOST + (uint32_t(q) << 21);
       const int ch = tl.col0 + rank * kBC + q * 32;
@@ -370,6 +398,24 @@ cudaError_t launch_as(const RaggedArgs& p, const Fp4Weights& fw, const CUtensorM
                         fw);
 }
 
+// About how long tiles of up to MOST rows take, for experts with equal numbers of rows
+// (and a spread of their root): the pairs' turns times what a turn of this form was
+// measured to take, in us for 2,048 steps.  (32 experts, 7168 x 2048, with 160 / 192 /
+// 288 rows: 140 rows each 111 / 125 / 124 us, 256: 201 / 208 / 162, 320: 247 / 217 / 236,
+// 512: 379 / 340 / 308, 700: 475 / 409 / 411.)
+template <int MOST>
+float tiles_time(const RaggedArgs& p) {
+  const int used = std::min(p.E, p.rows);
+  const float each = float(p.rows) / float(used);
+  const float tiles = std::ceil((each + (used > 1 ? std::sqrt(each) : 0.0f)) / MOST);
+  const float turns =
+      std::ceil(tiles * used * ceil_div(p.out_cols, 2 * kBC) / float(sm_count() / 2));
+  const float turn = MOST == 160 ? 8.2f
+                     : MOST == 192 ? 8.6f
+                                   : 10.7f + 0.035f * std::max(each / tiles - 200.0f, -28.0f);
+  return turns * turn;
+}
+
 template <int MOST>
 cudaError_t launch_tiles(const RaggedArgs& p, const Fp4Weights& fw, const CUtensorMap& mw,
                          const RowMaps& mr, cudaStream_t st) {
@@ -417,8 +463,11 @@ cudaError_t launch_expert_matmul_mxfp4(int E, int rows, int N, int K, const void
                    uint64_t(E), kRawSteps * kBK / 2, kBC) ||
       !make_row_maps(&mr, a, K, rows))
     return cudaErrorInvalidValue;
-  return rows / 640 < E ? launch_tiles<160>(p, fw, mw, mr, st)
-                        : launch_tiles<192>(p, fw, mw, mr, st);
+  const float t160 = tiles_time<160>(p), t192 = tiles_time<192>(p);
+  if (smem_bytes<288>(E) <= size_t(kMaxBlockSmem) && tiles_time<288>(p) < std::min(t160, t192))
+    return launch_tiles<288>(p, fw, mw, mr, st);
+  return t160 <= t192 ? launch_tiles<160>(p, fw, mw, mr, st)
+                      : launch_tiles<192>(p, fw, mw, mr, st);
 }
 
 }  // namespace mp

@@ -229,14 +229,15 @@ __device__ void tile_prefix(const RaggedArgs& p, int most, int* pre, int* scan) 
   __syncthreads();
 }
 
-// The most rows of a tile: `most` (256 or 192), or 32 or 64 fewer where their tiles
-// fill the pairs' turns better.  A turn takes about as long as its tiles' units of 32
-// rows on average and 1.25 more (measured with bf16 weights, 4096 x 7168: 38.4 us with
-// 256 rows, 34.3 with 224, 32.7 with 211), so a smaller tile has to save whole turns.
+// The most rows of a tile: `most`, or 32 or 64 fewer where their tiles fill the
+// pairs' turns better.  A turn takes about as long as its tiles' units of 32 rows on
+// average and 1.25 more (measured with bf16 weights, 4096 x 7168: 38.4 us with 256
+// rows, 34.3 with 224, 32.7 with 211), so a smaller tile has to save whole turns.
 // (32 experts of about 1,024 rows, 2,048 channels from 7168: 17 turns of 6.5 units
-// take 535 us, 16 of 7.2 units 550.)
+// take 535 us, 16 of 7.2 units 550.)  `least_turn`: what one takes whatever its rows.
 template <int THREADS>
-__device__ int tile_rows(const RaggedArgs& p, int most, int ncol, int pairs, int* scan) {
+__device__ int tile_rows(const RaggedArgs& p, int most, float least_turn, int ncol, int pairs,
+                         int* scan) {
   const int full = most / kUnit;
   int units = 0, tiles[3] = {0, 0, 0};
   for (int e = threadIdx.x; e < p.E; e += THREADS) {
@@ -254,7 +255,8 @@ __device__ int tile_rows(const RaggedArgs& p, int most, int ncol, int pairs, int
   for (int i = 0; i < 3; ++i) {
     const float t = float(block_sum<THREADS>(tiles[i], scan));
     if (i > 0 && t * ncol >= 0x1p30f) break;  // (their number stays an int)
-    const float cost = ceilf(t * ncol / pairs) * (units / fmaxf(t, 1.0f) + 1.25f);
+    const float turn = fmaxf(units / fmaxf(t, 1.0f) + 1.25f, least_turn);
+    const float cost = ceilf(t * ncol / pairs) * turn;
     if (cost < least) {
       least = cost;
       best = full - i;
@@ -324,9 +326,9 @@ struct RowBoxes {
   const CUtensorMap *one, *two;  // two: NULL if one box is all
   int row, row2;                 // their first rows
   uint32_t at2, bytes;           // of the second box in the stage; of both
-  __device__ __forceinline__ RowBoxes(const RowMaps& maps, const Tile& tl, int rank) {
-    int half = tl.n / 2;
-    row = row2 = tl.row0 + rank * half;
+  __device__ __forceinline__ RowBoxes(const RowMaps& maps, int row0, int n, int rank) {
+    int half = n / 2;
+    row = row2 = row0 + rank * half;
     if (half == 112) half = 128;
     const int big = half >= 128 ? 3 : half >= 64 ? 2 : half >= 32 ? 1 : 0;
     const int rest = half - (16 << big);  // 0, 16 or 32

@@ -598,6 +598,10 @@ MX = [  # counts, N, K, slack rows at the end
     ([2, 0, 3, 1, 9] * 30, 392, 256, 0),   # one piece of the reduction, several units a block
     ([3, 1, 6, 2] * 20, 1160, 736, 5),     # three pieces, several units a block
     ([1, 2, 3] * 9, 4104, 2048, 0),
+    ([285], 264, 544, 0),
+    ([300, 0, 270, 288, 577, 100], 520, 736, 1),
+    ([256, 257, 288, 289] * 12, 776, 352, 0),
+    ([900, 650], 264, 352, 0),
 ]
 
 
