@@ -14,10 +14,10 @@
 //
 // MXFP4 weights: one instruction turns two codes into f16, several fewer than bf16
 // takes (83 against 34 codes per clock and SM with the products), so here the rows
-// become f16 as well.  That is exact in all that matters: per row and 32 channels
+// become f16 as well: per row and 32 channels
 // they are divided by a power of two that brings the largest into [2^15, 2^16), so
 // values down to 2^-32 of it keep all their eight bits, and what is lost of smaller
-// ones is at most 2^-40 of it; rows of very small values (below 2^-93) are divided
+// ones is at most 2^-40 of it; where the largest is below 2^-94 they are divided
 // by less, and lose nothing.  The products of 32 channels are summed by the tensor
 // core, then multiplied by both powers of two and added up in fp32.
 #include <algorithm>

@@ -649,6 +649,9 @@ int mp_dispatch_ll_quant(int R, int N, int K, int E, int H, int qformat, int ran
  *   -> mp_swiglu_backward_e4m3 -> mp_expert_matmul_dgrad_e4m3 -> mp_combine_ll,
  *   mp_expert_matmul_wgrad_e4m3 for both weights, and
  *   mp_ll_row_weights_backward -> mp_route_backward.
+ * On bf16 rows the same with mp_dispatch_ll (MP_BF16), mp_dispatch_ll_rows, and
+ * mp_expert_matmul_bf16 or (forward) mp_expert_matmul_mxfp4, mp_swiglu_bf16 and
+ * their gradients.
  */
 
 /* Score functions of the router. */
