@@ -19,8 +19,8 @@
 // writes whole 64-byte pieces of the output's rows.
 //
 // Warps of a block: one loads, one (of the pair's first block) issues the MMAs,
-// four write finished tiles while the next one's products run into the second
-// accumulator.
+// eight write finished tiles while the next one's products run into the second
+// accumulator (with four the writing set the pace of short reductions).
 #include <algorithm>
 #include <cstdint>
 #include <cuda.h>
@@ -33,7 +33,8 @@ namespace mp {
 namespace {
 
 constexpr int kMaxStages = 6;
-constexpr int kEpiFirst = 2;
+constexpr int kEpiWarps = 8, kEpiFirst = 2;
+constexpr int kShare = kEpiWarps / 4;           // warps that share a quarter of the channels
 constexpr int kThreads = (kEpiFirst + kEpiWarps) * 32;
 
 // Shared memory after the stages (1024-byte aligned, as the swizzle wants them).
@@ -128,9 +129,10 @@ mp_k_expert_matmul_bf16(const __grid_constant__ CUtensorMap map_w,
       RingAt s;
       uint32_t nt = 0;
       bool ok = true;
-      for (int t = first; t < tiles && ok; t += step, ++nt) {
-        const Tile tl = tile_at(p, pre, ncol, t);
-        const uint32_t idesc = mma_idesc_bf16(2 * kBC, tl.n, DGRAD, false);
+      // (the next tile is looked up while this one's last products run)
+      int n = first < tiles ? tile_at(p, pre, ncol, first).n : 0, next = 0;
+      for (int t = first; t < tiles && ok; t += step, ++nt, n = next) {
+        const uint32_t idesc = mma_idesc_bf16(2 * kBC, n, DGRAD, false);
         const uint32_t buf = nt & 1u;
         if (nt >= 2)
           ok = bounded_wait(&tail->tempty[buf], ((nt >> 1) - 1) & 1u, failed, p.patience);
@@ -144,11 +146,13 @@ mp_k_expert_matmul_bf16(const __grid_constant__ CUtensorMap map_w,
           s.next(p.stages);
         }
         if (ok) commit_to_pair(&tail->tfull[buf], even);
+        if (t + step < tiles) next = tile_at(p, pre, ncol, t + step).n;
       }
     }
   } else {
     // ---- accumulators to bf16 rows
     const int q = warp & 3;  // the TMEM lanes this warp may read: 32 q ..
+    const int mine = (warp - kEpiFirst) >> 2;
     unsigned char* turned = tail->turned[warp - kEpiFirst][0];
     uint32_t nt = 0;
     for (int t = first; t < tiles; t += step, ++nt) {
@@ -159,9 +163,9 @@ mp_k_expert_matmul_bf16(const __grid_constant__ CUtensorMap map_w,
       const uint32_t src = tmem + buf * kBR + (uint32_t(q) << 21);
       const int ch = tl.col0 + rank * kBC + q * 32;
       if (SPLIT)
-        store_part(tl, q, src, stages);  // (the stages are done with)
+        store_part<kShare>(tl, q, src, mine, stages);  // (the stages are done with)
       else if (ch < p.out_cols)
-        write_tile(p, tl, ch, src, turned);
+        write_tile<kShare>(p, tl, ch, src, mine, turned);
       tcgen05_fence_before();
       __syncwarp();
       if (lane == 0) arrive_at(map_to_rank(&tail->tempty[buf], even));

@@ -53,6 +53,7 @@ constexpr int kRawStage = kBC * kRawSteps * kBK / 2;
 constexpr int kGroupWarps = kBC / 32;          // a thread per channel
 constexpr int kGroups = 4;                     // that take the stages in turn
 constexpr int kConvWarps = kGroups * kGroupWarps;
+constexpr int kEpiWarps = 4, kShare = kEpiWarps / 4;  // (eight take time from the converting ones)
 constexpr int kEpiFirst = 2, kRawWarp = kEpiFirst + kEpiWarps, kConvFirst = kRawWarp + 1;
 constexpr int kThreads = (kConvFirst + kConvWarps) * 32;
 
@@ -244,9 +245,11 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
       RingAt s;
       uint32_t nt = 0;
       bool ok = true;
-      for (int t = first; t < tiles && ok; t += step, ++nt) {
-        const Tile tl = tile_at(p, pre, ncol, t);
-        const int n1 = first_rows(tl.n), n2 = tl.n - n1;
+      // (the next tile is looked up while this one's last products run; in the loop over
+      // the stages it costs MXFP4 weights up to a tenth)
+      int n = first < tiles ? tile_at(p, pre, ncol, first).n : 0, next = 0;
+      for (int t = first; t < tiles && ok; t += step, ++nt, n = next) {
+        const int n1 = first_rows(n), n2 = n - n1;
         const uint32_t idesc = mma_idesc_bf16(2 * kBC, n1, false, false);
         const uint32_t idesc2 = mma_idesc_bf16(2 * kBC, max(n2, kUnit), false, false);
         const uint32_t buf = nt % kAccs;
@@ -272,11 +275,13 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
           s.next(kStages);
         }
         if (ok) commit_to_pair(&tail->tfull[buf], even);
+        if (t + step < tiles) next = tile_at(p, pre, ncol, t + step).n;
       }
     }
   } else if (warp < kRawWarp) {
     // ---- accumulators to bf16 rows
     const int q = warp & 3;  // the TMEM lanes this warp may read: 32 q ..
+    const int share = (warp - kEpiFirst) >> 2;
     unsigned char* turned = tail->turned[warp - kEpiFirst][0];
     uint32_t nt = 0;
     for (int t = first; t < tiles; t += step, ++nt) {
@@ -287,9 +292,9 @@ mp_k_expert_matmul_mxfp4(const __grid_constant__ CUtensorMap map_w,
       const uint32_t src = tmem + buf * MOST + (uint32_t(q) << 21);
       const int ch = tl.col0 + rank * kBC + q * 32;
       if (SPLIT)
-        store_part(tl, q, src, raws);  // (the rings are done with)
+        store_part<kShare>(tl, q, src, share, raws);  // (the rings are done with)
       else if (ch < p.out_cols)
-        write_tile(p, tl, ch, src, turned);
+        write_tile<kShare>(p, tl, ch, src, share, turned);
       tcgen05_fence_before();
       __syncwarp();
       if (lane == 0) arrive_at(map_to_rank(&tail->tempty[buf], even));

@@ -39,6 +39,7 @@ constexpr int kWStage = 2 * kWOperand;
 constexpr int kChunk = kWRows * 128;          // 64 channels (128 bytes) of a stage's rows
 constexpr int kWStages = 6;
 constexpr int kSlab = 32 * 128;               // 128 bytes of 32 finished rows
+constexpr int kEpiWarps = 4;
 constexpr int kClearWarp = 2, kEpiFirst = 3;
 constexpr int kWThreads = (kEpiFirst + kEpiWarps) * 32;
 

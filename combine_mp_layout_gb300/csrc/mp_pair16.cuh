@@ -167,7 +167,6 @@ constexpr int kStageR = kBR / 2 * kBK * 2;
 constexpr int kStage = kStageC + kStageR;
 constexpr int kMaxParts = 4;              // pairs that share a tile's reduction: one cluster
 constexpr int kBandTiles = 8;             // row tiles per band of the tile order
-constexpr int kEpiWarps = 4;
 constexpr int kTurned = 16 * 32 * 2;        // bytes of 16 rows x 32 channels
 
 struct RaggedArgs {
@@ -293,18 +292,20 @@ __device__ __forceinline__ Tile tile_at(const RaggedArgs& p, const int* pre, int
   const int band = local / (kBandTiles * ncol);
   const int rem = local - band * kBandTiles * ncol;
   const int mb = min(kBandTiles, mt - band * kBandTiles);
-  const int m = band * kBandTiles + rem % mb;
+  const int nt = rem / mb, m = band * kBandTiles + rem - nt * mb;
   int r0, r1;
   rows_of(p.expert_offsets, p.rows, lo, r0, r1);
-  // the expert's rows in whole units, spread evenly over its tiles
+  // the expert's rows in whole units, spread evenly over its tiles: the first `rest` of
+  // them have one unit more.  (Every role finds its tiles by itself, in the time that
+  // the products of a short reduction wait for: no long divisions.)
   const int units = (r1 - r0 + kUnit - 1) / kUnit;
-  const int u0 = int(int64_t(units) * m / mt), u1 = int(int64_t(units) * (m + 1) / mt);
+  const int each = units / mt, rest = units - each * mt;
   Tile tile;
   tile.e = lo;
-  tile.row0 = r0 + u0 * kUnit;
-  tile.n = (u1 - u0) * kUnit;
+  tile.row0 = r0 + (m * each + min(m, rest)) * kUnit;
+  tile.n = (each + (m < rest ? 1 : 0)) * kUnit;
   tile.nrows = min(tile.n, r1 - tile.row0);
-  tile.col0 = rem / mb * 2 * kBC;
+  tile.col0 = nt * 2 * kBC;
   return tile;
 }
 
@@ -361,23 +362,26 @@ __device__ __forceinline__ void stage_products(const unsigned char* stage, uint3
                  dr + ((k * 32) >> 4), idesc, !first || k > 0);
 }
 
-// A finished accumulator, this warp's 32 channels from `ch` on, to bf16 rows.
-// `src`: its TMEM lanes and first column; `turned`: 2 * kTurned bytes of its own, in
-// which 16 rows x 32 channels at a time are turned around.
+// A finished accumulator, this warp's 32 channels from `ch` on and every SHARE-th 32
+// rows from the `mine`-th on, to bf16 rows.  `src`: its TMEM lanes and first column;
+// `turned`: 2 * kTurned bytes of its own, in which 16 rows x 32 channels at a time are
+// turned around.
+template <int SHARE>
 __device__ __forceinline__ void write_tile(const RaggedArgs& p, const Tile& tl, int ch,
-                                           uint32_t src, unsigned char* turned) {
+                                           uint32_t src, int mine, unsigned char* turned) {
+  if (mine * 32 >= tl.n) return;
   const int lane = threadIdx.x & 31;
   const int r = lane >> 1, h = (lane & 1) * 16;  // the row and channels that it stores
   const int left = p.out_cols - (ch + h);        // a multiple of 8 (or <= 0)
   uint16_t* dst = p.out + int64_t(tl.row0 + r) * p.out_cols + ch + h;
   float2 v[2][8];
-  tmem_ld_x16(src, v[0]);
+  tmem_ld_x16(src + mine * 32, v[0]);
   tmem_wait_ld(v[0]);
-  for (int c0 = 0; c0 < tl.n; c0 += 32) {
+  for (int c0 = mine * 32; c0 < tl.n; c0 += SHARE * 32) {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {  // 16 rows; the next 16 on their way from TMEM
-      const int c = c0 + b * 16;
-      if (c + 16 < tl.n) tmem_ld_x16(src + c + 16, v[b ^ 1]);
+      const int c = c0 + b * 16, next = b == 0 ? c + 16 : c0 + SHARE * 32;
+      if (next < tl.n) tmem_ld_x16(src + next, v[b ^ 1]);
       uint16_t* tw = reinterpret_cast<uint16_t*>(turned + b * kTurned) + lane;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -398,22 +402,25 @@ __device__ __forceinline__ void write_tile(const RaggedArgs& p, const Tile& tl, 
           if (left >= 16) d[1] = y;
         }
       }
-      if (c + 16 < tl.n) tmem_wait_ld(v[b ^ 1]);
+      if (next < tl.n) tmem_wait_ld(v[b ^ 1]);
     }
   }
 }
 
-// fp32 sums of a part of the reduction into shared memory: [row][channel].
-__device__ __forceinline__ void store_part(const Tile& tl, int q, uint32_t src, void* stages) {
-  float* mine = reinterpret_cast<float*>(stages) + q * 32 + (threadIdx.x & 31);
-  for (int c = 0; c < tl.n; c += 16) {
+// fp32 sums of a part of the reduction into shared memory, [row][channel]; rows shared
+// among warps as above.
+template <int SHARE>
+__device__ __forceinline__ void store_part(const Tile& tl, int q, uint32_t src, int mine,
+                                           void* stages) {
+  float* to = reinterpret_cast<float*>(stages) + q * 32 + (threadIdx.x & 31);
+  for (int c = mine * 16; c < tl.n; c += SHARE * 16) {
     float2 v[8];
     tmem_ld_x16(src + c, v);
     tmem_wait_ld(v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      mine[(c + 2 * j) * kBC] = v[j].x;
-      mine[(c + 2 * j + 1) * kBC] = v[j].y;
+      to[(c + 2 * j) * kBC] = v[j].x;
+      to[(c + 2 * j + 1) * kBC] = v[j].y;
     }
   }
 }
