@@ -21,8 +21,8 @@
 // is how seldom a weight is converted: tiles are of up to 288 rows with one
 // accumulator, or, where that saves no tiles, of up to 192 or 160 with two (and the
 // write of a tile under the next one's products).  8,191 rows over 32 experts, 7168 x
-// 2048: 172 us (1.40 PFLOP/s), 204 with 192 rows; 32,768 rows, 4096 x 7168: 1.10 ms
-// (1.74 PFLOP/s).
+// 2048: 169 us (1.42 PFLOP/s), 204 with 192 rows; 32,768 rows, 4096 x 7168: 1.05 ms
+// (1.83 PFLOP/s).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

@@ -14,12 +14,16 @@
 //
 // MXFP4 weights: one instruction turns two codes into f16, several fewer than bf16
 // takes (83 against 34 codes per clock and SM with the products), so here the rows
-// become f16 as well: per row and 32 channels
-// they are divided by a power of two that brings the largest into [2^15, 2^16), so
-// values down to 2^-32 of it keep all their eight bits, and what is lost of smaller
-// ones is at most 2^-40 of it; where the largest is below 2^-94 they are divided
-// by less, and lose nothing.  The products of 32 channels are summed by the tensor
-// core, then multiplied by both powers of two and added up in fp32.
+// become f16 as well: per row and 32 channels they are divided by a power of two that
+// brings the largest into [2^15, 2^16), so values down to 2^-32 of it keep all their
+// eight bits, and what is lost of smaller ones is at most 2^-40 of it; where the
+// largest is below 2^-94 they are divided by less, and lose nothing.  The products of
+// 32 channels are summed by the tensor core, then multiplied by both powers of two and
+// added up in fp32.
+//
+// Measured, 4096 x 7168: one bf16 row 13.1 us (4.5 TB/s of weights; 8.2 us with the
+// weights in L2), one MXFP4 row 8.3; 61 MXFP4 rows over 32 experts 95 to 99 us (4.3
+// TB/s; 60% of the issue slots; 70 us without the products).
 #include <algorithm>
 #include <cstdint>
 #include <cuda.h>
@@ -497,6 +501,7 @@ cudaError_t launch_rows(VecArgs p, const void* w, cudaStream_t st) {
   const int parts =
       parts_for(mp_k_expert_rows<FP4, true, 4>, kThreads, units, 1, kMaxVecParts, np, 2);
   p.steps = ceil_div(np, parts) * kSteps;
+  if (p.steps > (1 << 16)) return cudaErrorNotSupported;  // (no room for the rows)
   p.pieces = kMaxPieces;
   while (p.pieces > 2 &&
          vec_smem_bytes<FP4>(p.E, p.room, p.steps, p.pieces) > size_t(kMaxBlockSmem))

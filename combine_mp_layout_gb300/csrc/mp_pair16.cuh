@@ -167,7 +167,7 @@ constexpr int kStageR = kBR / 2 * kBK * 2;
 constexpr int kStage = kStageC + kStageR;
 constexpr int kMaxParts = 4;              // pairs that share a tile's reduction: one cluster
 constexpr int kBandTiles = 8;             // row tiles per band of the tile order
-constexpr int kTurned = 16 * 32 * 2;        // bytes of 16 rows x 32 channels
+constexpr int kTurned = 16 * 32 * 2;      // bytes of 16 rows x 32 channels
 
 struct RaggedArgs {
   int E, rows, out_cols, red;             // out_cols, red: N and K, or K and N
@@ -458,7 +458,7 @@ __device__ __forceinline__ void join_parts(const RaggedArgs& p, const Tile& tl, 
 }
 
 // How many clusters of `size` blocks of a kernel, with as much shared memory as there
-// is, run at once; asked once per kernel, device and thread.  (On 152 SMs 76 of two
+// is, run at once; asked once per kind of kernel, device and thread.  (On 152 SMs 76 of two
 // blocks, 36 of four, 23 of six, 15 of eight.)
 template <typename Kernel>
 inline int clusters_at_once(Kernel kernel, int threads, int size) {

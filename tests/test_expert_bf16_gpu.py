@@ -328,6 +328,39 @@ def test_rows_past_32_bit_offsets():
     assert int(err) == 0
 
 
+@pytest.mark.parametrize("form", ["bf16", "mxfp4", "dgrad", "wgrad"])
+def test_longest_reductions(form):
+    """Nearly 2^31 steps, few of them not zero, at both ends."""
+    err = zeros(1, torch.int32)
+    if form == "wgrad":  # its reduction is over the rows
+        rows = 2 ** 31 - 1025
+        dy, a = zeros((rows, 8), BF), zeros((rows, 8), BF)
+        dy[0], dy[-1], a[0], a[-1] = 1.0, 2.0, 3.0, 5.0
+        dw = zeros((1, 8, 8)) + 7
+        B.check(B.mp_expert_matmul_wgrad_bf16(1, rows, 8, 8, dy, a, None, False, dw, err))
+        torch.cuda.synchronize()
+        assert bool((dw == 13.0).all()) and int(err) == 0
+        return
+    K = 2 ** 31 - 1056
+    a, out = zeros((1, K), BF), zeros((1, 8), BF)
+    a[0, 0], a[0, 1], a[0, -1] = 1.0, 3.0, 2.0
+    if form == "mxfp4":
+        w = zeros((1, 8, K // 2), torch.uint8)
+        s = torch.full((1, 8, K // 32), 127, dtype=torch.uint8, device=DEV)
+        w[..., 0], w[..., -1] = 0x24, 0x40  # codes 4 (2) and 2 (1); 0 and 4 (2)
+        B.check(B.mp_expert_matmul_mxfp4(1, 1, 8, K, a, w, s, None, out, err))
+    elif form == "bf16":
+        w = zeros((1, 8, K), BF)
+        w[..., 0], w[..., 1], w[..., -1] = 2.0, 1.0, 2.0
+        B.check(B.mp_expert_matmul_bf16(1, 1, 8, K, a, w, None, out, err))
+    else:  # the same sums, over the weights' other axis
+        w = zeros((1, K, 8), BF)
+        w[0, 0], w[0, 1], w[0, -1] = 2.0, 1.0, 2.0
+        B.check(B.mp_expert_matmul_dgrad_bf16(1, 1, K, 8, a, w, None, out, err))
+    torch.cuda.synchronize()
+    assert bool((out == 9.0).all()) and int(err) == 0
+
+
 def test_without_rows_and_many_experts():
     g = gen(19)
     err = zeros(1, torch.int32)
