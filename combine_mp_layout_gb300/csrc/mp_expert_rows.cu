@@ -8,7 +8,9 @@
 // side, the rows the N side): a warp 32 channels of a piece or half of one.  A tile of
 // the tensor core's (256 x 32) would spend longer on its pipeline's start, and for
 // 4-bit weights on writing the converted weights to shared memory.  With few blocks,
-// clusters share a reduction; sums are joined in a fixed order.
+// clusters share a reduction; sums are joined in a fixed order: a block's own first, so
+// that the first block of a cluster fetches one of each other block, all at once (eight
+// MXFP4 rows 10.2 -> 9.3 us; every block fetching a share of all sums before).
 //
 // bf16 weights: products exact, sums fp32.
 //
@@ -22,8 +24,9 @@
 // added up in fp32.
 //
 // Measured, 4096 x 7168: one bf16 row 13.1 us (4.5 TB/s of weights; 8.2 us with the
-// weights in L2), one MXFP4 row 8.3; 61 MXFP4 rows over 32 experts 95 to 99 us (4.3
-// TB/s; 60% of the issue slots; 70 us without the products).
+// weights in L2), one MXFP4 row 8.1; MXFP4 rows over 32 experts, one each 94 us (5.3 TB/s),
+// two each 104 (70 without the products; 60% of the issue slots), 61 drawn at random 85 to
+// 99 by how many experts have none.
 #include <algorithm>
 #include <cstdint>
 #include <cuda.h>
@@ -439,31 +442,38 @@ mp_k_expert_rows(const __grid_constant__ CUtensorMap map_w,
           tail->part[sum][2 * t + 1][ch + m * 16 + g + 8] = acc[m][3];
         }
       }
-      if constexpr (SPLIT) cluster_sync_all(); else mul_warps_sync();
-      // two channels of a row per thread; sets and halves, then parts, ascending
-      for (int i = part * kMulWarps * 32 + int(threadIdx.x); live && i < n.nrows * (kBC / 2);
-           i += parts * kMulWarps * 32) {
-        const int r = i / (kBC / 2), c = i % (kBC / 2) * 2;
-        float2 sum = make_float2(0.0f, 0.0f);
-        for (int z = 0; z < parts; ++z) {
-          float2 v[kSums];
+      mul_warps_sync();
+      // two channels of a row per thread: sets and halves in ascending order, then parts
+      static_assert(kMulWarps * 32 == kVR * (kBC / 2));
+      const int r = int(threadIdx.x) / (kBC / 2), c = int(threadIdx.x) % (kBC / 2) * 2;
+      const bool mine = live && r < n.nrows;
+      float2 sum = make_float2(0.0f, 0.0f);
+      if (mine) {
 #pragma unroll
-          for (int h = 0; h < kSums; ++h) {
-            if constexpr (SPLIT)
-              asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-                           : "=f"(v[h].x), "=f"(v[h].y)
-                           : "r"(map_to_rank(&tail->part[h][r][c], uint32_t(z)))
-                           : "memory");
-            else
-              v[h] = *reinterpret_cast<const float2*>(&tail->part[h][r][c]);
-          }
-#pragma unroll
-          for (int h = 0; h < kSums; ++h) sum = add2(sum, v[h]);
-        }
-        if (n.col0 + c < p.N)
-          *reinterpret_cast<uint32_t*>(p.r.out + int64_t(n.row0 + r) * p.N + n.col0 + c) =
-              pack_bf16x2_rn(sum.x, sum.y);
+        for (int h = 0; h < kSums; ++h)
+          sum = add2(sum, *reinterpret_cast<const float2*>(&tail->part[h][r][c]));
       }
+      if constexpr (SPLIT) {
+        // the first block adds up the parts, all on their way before the first is needed
+        if (mine) *reinterpret_cast<float2*>(&tail->part[0][r][c]) = sum;
+        cluster_sync_all();
+        if (mine && part == 0) {
+          float2 v[kMaxVecParts];
+#pragma unroll
+          for (int z = 1; z < kMaxVecParts; ++z)
+            if (z < parts)
+              asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                           : "=f"(v[z].x), "=f"(v[z].y)
+                           : "r"(map_to_rank(&tail->part[0][r][c], uint32_t(z)))
+                           : "memory");
+#pragma unroll
+          for (int z = 1; z < kMaxVecParts; ++z)
+            if (z < parts) sum = add2(sum, v[z]);
+        }
+      }
+      if (mine && part == 0 && n.col0 + c < p.N)
+        *reinterpret_cast<uint32_t*>(p.r.out + int64_t(n.row0 + r) * p.N + n.col0 + c) =
+            pack_bf16x2_rn(sum.x, sum.y);
       if (u + 1 < last) n = unit_at(p, pre, ncol, u + 1);
       if constexpr (SPLIT) {
         cluster_sync_all();  // the other blocks have read this one's sums
