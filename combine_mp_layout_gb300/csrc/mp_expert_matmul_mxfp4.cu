@@ -93,9 +93,11 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t multiplier(uint32_t s) {
   return (s + 126u) * 0x00800080u;
 }
-// Above that the two factors are put on one after the other; 255 is NaN.
+// Where a warp meets a scale above that, its two factors are put on one after the other,
+// and those of all the other scales too: 2^126, then 2^(s-127) for any s (at 0 that is a
+// subnormal number); 255 is NaN.
 __device__ __forceinline__ uint32_t large_multiplier(uint32_t s) {
-  return s == 255u ? 0x7fc07fc0u : s * 0x00800080u;
+  return s == 255u ? 0x7fc07fc0u : s == 0u ? 0x00400040u : s * 0x00800080u;
 }
 
 // Eight e2m1 codes as bf16 pairs in order, 2^-126 times their value: sign to bit
