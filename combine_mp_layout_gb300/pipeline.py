@@ -179,7 +179,8 @@ class MoELayerPlan:
         bf16 or fp32;
       * "mxfp4": 4-bit codes with one UE8M0 scale byte per 32 channels, bf16 rows; forward only
         (``train=False``).
-    ``forward`` leaves what ``backward`` needs in the plan's buffers.
+    ``forward`` leaves what ``backward`` needs in the plan's buffers; a plan made with
+    ``train=False`` has none for the gradients and refuses ``backward``.
 
     For e4m3 the weights' gradients are sums in fp32 of products of e4m3 rows held in f16: relative to
     the largest scale of their 128 channels in the expert's rows, so rows whose scale is
@@ -202,7 +203,7 @@ class MoELayerPlan:
         if grad_dtype not in ((torch.bfloat16, torch.float32) if weights == "bf16"
                               else (torch.bfloat16,)):
             raise ValueError("weights' gradients are bf16, or fp32 for bf16 weights")
-        self.weights = weights
+        self.weights, self.train = weights, train
         self.R, self.N, self.K, self.E, self.H, self.I = R, N, K, E, H, I
         self.scoring = B.MP_SOFTMAX if scoring == "softmax" else B.MP_SIGMOID
         self.normalize, self.scale, self.loss_coef = normalize, scale, loss_coef
@@ -330,6 +331,8 @@ class MoELayerPlan:
         """Gradients of a forward pass, from the output's (and the losses'): d_x, d_logits,
         d_w_gate_up, d_w_down of the plan.  With ``accumulate`` (fp32 weights' gradients) the
         last two are added to what they hold, for several batches per update."""
+        if not self.train:
+            raise ValueError("the plan was made for the forward pass alone (train=False)")
         if accumulate and self.d_w_down.dtype is not torch.float32:
             raise ValueError("only fp32 weights' gradients add up")
         R, N, K, E, H, I, cap = (self.R, self.N, self.K, self.E, self.H, self.I, self.cap)
