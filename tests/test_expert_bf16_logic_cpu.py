@@ -5,6 +5,8 @@ import re
 import pytest
 import torch
 
+from combine_mp_layout_gb300 import binding as B
+from tests.test_expert_bf16_cpu import BAD, L, MM, _p, no_gpu  # noqa: F401 (L: a fixture)
 from tests.test_expert_kernel_logic_cpu import run_c, source
 
 
@@ -35,3 +37,13 @@ def test_mxfp4_scales_of_both_conversions(tmp_path):
     assert float(bf16([first & 0xffff])[0]) == 2.0 ** 126
     assert bf16([v & 0xffff for v in careful[:255]]).tolist() == exact
     assert bool(bf16([careful[255] & 0xffff]).isnan().all())
+
+
+@no_gpu
+@pytest.mark.parametrize("bad", [b for b in BAD if b.get("K") != 2 ** 26])
+def test_mxfp4_rejects_all_that_the_products_do(L, bad):
+    """Every refusal of the bf16 product (but of as many column tiles as only its gradient has),
+    rows that are missing among them."""
+    a = dict(MM, **bad)
+    assert L.mp_expert_matmul_mxfp4(a["E"], a["rows"], a["N"], a["K"], a["a"], a["w"], _p(),
+                                    a["off"], a["out"], a["err"], _p(0)) == B.MP_ERR_INVALID_ARG
