@@ -789,7 +789,8 @@ int mp_expert_matmul_wgrad_e4m3(int E, int rows, int N, int K, const void *dy,
  * quantised for the second:
  *   z[r][i] = w[r] * g / (1 + exp(-g)) * u,   g = gate_up[r][i], u = gate_up[r][I + i],
  * in fp32 (the exponential's argument rounded: a relative error of up to 2e-7 at
- * gates of -4, 3.4e-6 at -84), then per 128 channels scale = amax * (1 / 448) (NaNs
+ * gates of -4, 3.4e-6 at -84; 0 for gates below -88.7, where exp(-g) is infinite in
+ * fp32), then per 128 channels scale = amax * (1 / 448) (NaNs
  * left out of the amax; 1 where that is below 2^-126) and code = e4m3(z * (1 / scale)),
  * with reciprocals rounded to fp32: the scale is within one ulp of amax / 448, z *
  * (1 / scale) within 1.5 ulp of z / scale.
@@ -902,7 +903,10 @@ int mp_expert_matmul_mxfp4(int E, int rows, int N, int K, const void *a, const v
  * mp_swiglu_bf16 -- the gated activation between an expert's two bf16 products:
  *   out[r][i] = bf16( w[r] * g / (1 + exp(-g)) * u ),
  *   g = gate_up[r][i], u = gate_up[r][I + i],
- * in fp32 (the exponential as in mp_swiglu_e4m3), one rounding.
+ * in fp32, one rounding.  The exponential's argument is rounded: a relative error of up
+ * to 2e-7 at gates of -4, 4e-6 at -84, 2e-5 at -177.  Gates below that, whose exp(g) is
+ * below 2^-255, give 0; up to there exp(g) is carried in two factors, so that a large
+ * u brings the product back into bf16's range (in the gradient d_out too).
  *   in   gate_up      bf16 [rows][2I]: the gate's channels, then the up ones
  *   in   row_weights  fp32 [rows], or NULL for 1 (see mp_swiglu_e4m3)
  *   in   num_rows     int32 [1] on the device: rows in use, or NULL for all
