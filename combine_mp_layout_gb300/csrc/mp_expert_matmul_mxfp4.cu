@@ -82,12 +82,6 @@ size_t smem_bytes(int E) {
   return ring_bytes<MOST>() + sizeof(Tail) + size_t(E + 1) * 4;
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // The bf16 multiplier (twice) that belongs to a scale for codes as `codes8` leaves
 // them, 2^-126 times their value: 2^126 * 2^(s-127) up to s = 128.
 __device__ __forceinline__ uint32_t multiplier(uint32_t s) {
@@ -98,20 +92,6 @@ __device__ __forceinline__ uint32_t multiplier(uint32_t s) {
 // subnormal number); 255 is NaN.
 __device__ __forceinline__ uint32_t large_multiplier(uint32_t s) {
   return s == 255u ? 0x7fc07fc0u : s == 0u ? 0x00400040u : s * 0x00800080u;
-}
-
-// Eight e2m1 codes as bf16 pairs in order, 2^-126 times their value: sign to bit
-// 15, the two exponent bits and the mantissa bit to bits 8 to 6 (both shifts are
-// one product).
-__device__ __forceinline__ void codes8(uint32_t w, uint32_t (&o)[4]) {
-  const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // code 2i to bits 0-3, code 2i+1 to bits 16-19 (selector 8: a byte's sign bit, here 0)
-    uint32_t two;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(two) : "r"(even), "r"(odd), "r"(0x8480 + i * 0x1111));
-    o[i] = (two * 0x1040u) & 0x81c081c0u;
-  }
 }
 
 // 32 codes (16 bytes) with their scale, to 16 pairs.

@@ -18,10 +18,11 @@
 // takes (83 against 34 codes per clock and SM with the products), so here the rows
 // become f16 as well: per row and 32 channels they are divided by a power of two that
 // brings the largest into [2^15, 2^16), so values down to 2^-32 of it keep all their
-// eight bits, and what is lost of smaller ones is at most 2^-40 of it; where the
-// largest is below 2^-94 they are divided by less, and lose nothing.  The products of
-// 32 channels are summed by the tensor core, then multiplied by both powers of two and
-// added up in fp32.
+// eight bits.  Where a row that a block takes has a value below that, the block's rows
+// stay bf16 and the codes become bf16 too (WIDE): then the power of two leaves the
+// largest at 2^101 at most, and only values below 2^-99 beside one of 2^100 or more can
+// lose bits.  The products of 32 channels are summed by the tensor core, then multiplied
+// by both powers of two and added up in fp32.
 //
 // Measured, 4096 x 7168: one bf16 row 13.1 us (4.5 TB/s of weights; 8.2 us with the
 // weights in L2), one MXFP4 row 8.1; MXFP4 rows over 32 experts, one each 94 us (5.3 TB/s),
@@ -76,6 +77,7 @@ struct VecTail {
   uint64_t raw[kMaxPieces], rawfree[kMaxPieces];
   alignas(16) float part[kSums][kVR][kBC];  // sums of set and half: [row][channel]
   int failed;
+  int wide;                      // the first row of those that f16 cannot hold
   int scan[kThreads / 32];
 };
 
@@ -113,15 +115,24 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&o)[4]) {
       : "r"(w));
 }
 
-// The codes that the scale 2^(e - 127) takes past bf16's largest number (from 2^128)
-// count as infinite, as they do where the weights become bf16.
+// The same as bf16 pairs.
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t (&o)[4]) {
+  codes8(w, o);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = mul_bf16x2(o[i], 0x7e807e80u);  // (2^126)
+}
+
+// The codes (f16, or bf16 where WIDE) that the scale 2^(e - 127) takes past bf16's
+// largest number (from 2^128) count as infinite, as they do in the tiles' weights.
+template <bool WIDE>
 __device__ __forceinline__ void overflow(uint32_t e, uint32_t (&o)[4]) {
   if (e < 253u || e == 255u) return;
-  const uint32_t from = e == 254u ? 0x4000u : 0x4400u;  // 2 or 4 in f16
+  constexpr uint32_t kInf = WIDE ? 0x7f80u : 0x7c00u;
+  const uint32_t from = e == 254u ? 0x4000u : WIDE ? 0x4080u : 0x4400u;  // 2 or 4
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if ((o[i] & 0x7fffu) >= from) o[i] = (o[i] & 0xffff8000u) | 0x7c00u;
-    if (((o[i] >> 16) & 0x7fffu) >= from) o[i] = (o[i] & 0x8000ffffu) | 0x7c000000u;
+    if ((o[i] & 0x7fffu) >= from) o[i] = (o[i] & 0xffff8000u) | kInf;
+    if (((o[i] >> 16) & 0x7fffu) >= from) o[i] = (o[i] & 0x8000ffffu) | kInf << 16;
   }
 }
 
@@ -142,6 +153,25 @@ __device__ __forceinline__ uint32_t largest(uint32_t top, const uint4& v) {
   return top;
 }
 
+// The least magnitudes' bits but zero's, less one, of eight bf16 values and `least`, for
+// even and odd values apart.
+__device__ __forceinline__ uint32_t smallest2(uint32_t least, const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("{\n .reg .b32 t;\n add.u16x2 t, %1, %2;\n min.u16x2 %0, %0, t;\n}"
+        : "+r"(least)
+        : "r"(w[i] & 0x7fff7fffu), "r"(~0u));
+  return least;
+}
+
+// Eight bf16 values times a power of two, as bf16 or f16.
+__device__ __forceinline__ uint4 times_bf16(const uint4& v, float by) {
+  return make_uint4(pack_bf16x2_rn(bf16_lo(v.x) * by, bf16_hi(v.x) * by),
+                    pack_bf16x2_rn(bf16_lo(v.y) * by, bf16_hi(v.y) * by),
+                    pack_bf16x2_rn(bf16_lo(v.z) * by, bf16_hi(v.z) * by),
+                    pack_bf16x2_rn(bf16_lo(v.w) * by, bf16_hi(v.w) * by));
+}
 __device__ __forceinline__ uint4 to_f16(const uint4& v, float by) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t o[4];
@@ -152,12 +182,12 @@ __device__ __forceinline__ uint4 to_f16(const uint4& v, float by) {
 }
 
 // The rows of a block into shared memory: for bf16 weights as they are, for MXFP4
-// ones as f16 with a power of two per row and 32 channels (2^-10 of it is stored:
-// a sum of products times that stays within fp32, and the scale it is multiplied by
-// next gets the 2^10 back).
-template <bool FP4>
+// ones as f16, or bf16 where WIDE, with a power of two per row and 32 channels (2^-10 of
+// it is stored: a sum of products times that stays within fp32, and the scale it is
+// multiplied by next gets the 2^10 back).  `wide` becomes row0 where f16 has lost bits.
+template <bool FP4, bool WIDE>
 __device__ __forceinline__ void stage_rows(const VecArgs& p, int row0, int nrows, int k0, int steps,
-                                           unsigned char* xs, float* sx) {
+                                           unsigned char* xs, float* sx, volatile int* wide) {
   const int stride = row_stride<FP4>(p.steps);
   if constexpr (FP4) {
     const int groups = steps / 32;
@@ -170,11 +200,18 @@ __device__ __forceinline__ void stage_rows(const VecArgs& p, int row0, int nrows
       uint32_t top = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) top = largest(top, v[j]);
-      const int ex = max(int(top >> 7) - 127 - 15, -109);
+      const int ex = max(int(top >> 7) - 127 - (WIDE ? 100 : 15), -109);
       const float by = __uint_as_float(uint32_t(127 - ex) << 23);
       uint4* dst = reinterpret_cast<uint4*>(xs + r * stride + g * 64);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) dst[j] = to_f16(v[j], by);
+      for (int j = 0; j < 4; ++j) dst[j] = WIDE ? times_bf16(v[j], by) : to_f16(v[j], by);
+      if (!WIDE && ex > -109) {  // (at -109 the rows' least value is f16's least)
+        uint32_t least = ~0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) least = smallest2(least, v[j]);
+        if (min(least & 0xffffu, least >> 16) < (uint32_t(ex + 110) << 7) - 1u)
+          *wide = row0;  // below 2^(ex - 17)
+      }
       sx[g * p.room + r] = __uint_as_float(uint32_t(127 + ex - 10) << 23);
     }
   } else {
@@ -220,11 +257,11 @@ __device__ __forceinline__ float any_exponent_of(uint32_t s4, int j, float& by) 
 // A warp's 32 channels and half of a piece of MXFP4 weights: four groups of 32
 // steps, a lane 8 of them for channels g, g + 8, g + 16 and g + 24, whose scale
 // bytes are s.  sx: the rows' powers of two, `room` for each group.
-template <bool LARGE>
-__device__ __forceinline__ void multiply_fp4(const unsigned char* w0, const unsigned char* x,
+template <bool LARGE, bool WIDE>
+__device__ __forceinline__ void multiply_fp4(const unsigned char* from, const unsigned char* x,
                                              const float* sx, int room, int half, int g, int t,
                                              const uint32_t (&s)[4], float (&acc)[2][4]) {
-  w0 += t * 4;
+  from += t * 4;
   x += t * 16;
   // 2^10 more, which the rows' powers of two lack (below 192: no carry between bytes)
   const uint32_t more = LARGE ? 0u : 0x0a0a0a0au;
@@ -235,18 +272,25 @@ __device__ __forceinline__ void multiply_fp4(const unsigned char* w0, const unsi
     const float2 sx2 = *reinterpret_cast<const float2*>(sx + c * room);
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      const unsigned char* wm = w0 + m * 16 * 128 + ((c ^ g) << 4);
+      const unsigned char* wm = from + m * 16 * 128 + ((c ^ g) << 4);
       const uint32_t e0 = s[2 * m] + more, e1 = s[2 * m + 1] + more;
       uint32_t lo[4], hi[4];
-      codes_to_f16(*reinterpret_cast<const uint32_t*>(wm), lo);
-      codes_to_f16(*reinterpret_cast<const uint32_t*>(wm + 8 * 128), hi);
+      const uint32_t w0 = *reinterpret_cast<const uint32_t*>(wm);
+      const uint32_t w1 = *reinterpret_cast<const uint32_t*>(wm + 8 * 128);
+      if constexpr (WIDE) {
+        codes_to_bf16(w0, lo);
+        codes_to_bf16(w1, hi);
+      } else {
+        codes_to_f16(w0, lo);
+        codes_to_f16(w1, hi);
+      }
       if constexpr (LARGE) {
-        overflow((e0 >> (8 * i)) & 255u, lo);
-        overflow((e1 >> (8 * i)) & 255u, hi);
+        overflow<WIDE>((e0 >> (8 * i)) & 255u, lo);
+        overflow<WIDE>((e1 >> (8 * i)) & 255u, hi);
       }
       float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      mma_16x8x16<true>(v, lo[0], hi[0], lo[1], hi[1], b.x, b.y);
-      mma_16x8x16<true>(v, lo[2], hi[2], lo[3], hi[3], b.z, b.w);
+      mma_16x8x16<!WIDE>(v, lo[0], hi[0], lo[1], hi[1], b.x, b.y);
+      mma_16x8x16<!WIDE>(v, lo[2], hi[2], lo[3], hi[3], b.z, b.w);
       float f0, f1;
       if constexpr (LARGE) {
         float by0, by1;
@@ -289,12 +333,87 @@ __device__ __forceinline__ Unit unit_at(const VecArgs& p, const int* pre, int nc
   return n;
 }
 
+// MXFP4 scales that TMA cannot load: those of half of piece i, of a lane's four channels
+// from c0 on, from where they are.
+__device__ __forceinline__ void fetch_scales(const VecArgs& p, const Unit& n, int c0, int i,
+                                             int half, uint32_t (&sc)[4]) {
+  const int groups = p.K / 32;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    // (past the last channel or step: codes are zeros, any scale will do)
+    const unsigned char* from =
+        p.scales + (int64_t(n.e) * p.N + min(n.col0 + c0 + 8 * c, p.N - 1)) * groups;
+    sc[c] = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      sc[c] |= uint32_t(__ldg(from + min(i * 8 + half * 4 + j, groups - 1))) << (8 * j);
+  }
+}
+
+// Rows that f16 cannot hold: staged as bf16, and a warp's share of a unit's products.
+// Functions of their own, called where they are needed: as a branch in the kernel's loop,
+// or as a second loop beside it, they cost all other rows up to 7%, as calls 1 to 2%.
+// (4096 x 7168, one row each over 32 experts: 217 us with such rows, 95 without; one row of
+// one expert 14.6 and 8.9.)
+__device__ __noinline__ void stage_wide(const VecArgs& p, const Unit n, int lo, int hi,
+                                        unsigned char* xs, float* sx) {
+  constexpr int kSteps = Form<true>::kSteps;
+  stage_rows<true, true>(p, n.row0, n.nrows, lo * kSteps, (hi - lo) * kSteps, xs, sx, nullptr);
+}
+
+struct WideSums {
+  float acc[8];
+  RingAt s;
+  bool ok;
+};
+template <int SETS>
+__device__ __noinline__ WideSums wide_products(const VecArgs& p, const Unit n,
+                                               const unsigned char* pieces, const unsigned char* x,
+                                               const float* sx, VecTail* tail, int lo, int hi,
+                                               RingAt s, bool ok) {
+  constexpr int kSteps = Form<true>::kSteps;
+  constexpr int kHalves = 4 / SETS, kSetWarps = kHalves * kChWarps;
+  const unsigned char* scales = pieces + size_t(p.pieces) * kPiece;
+  const int warp = warp_index(), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int set = warp / kSetWarps, half0 = kHalves > 1 ? warp % kSetWarps / kChWarps : 0;
+  const int ch = warp % kChWarps * 32;
+  float acc[2][4] = {};
+  for (int i = lo; i < hi; ++i, s.next(p.pieces)) {
+    if (s.slot % SETS != set) continue;
+    ok = ok && bounded_wait_warp(&tail->raw[s.slot], s.round & 1u, &tail->failed);
+    if (!ok) break;
+    const unsigned char* from = pieces + s.slot * kPiece + (ch + g) * 128;
+    const float* sp = sx + (i - lo) * (kSteps / 32) * p.room + ((2 * t) & (p.room - 1));
+#pragma unroll 1
+    for (int half = half0; half < 2; half += kHalves) {
+      uint32_t sc[4];
+      if (p.tma_scales) {
+        const unsigned char* at =
+            scales + s.slot * kScales + (ch + g) * 16 + (i & 1) * 8 + half * 4;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sc[c] = *reinterpret_cast<const uint32_t*>(at + c * 8 * 16);
+      } else {
+        fetch_scales(p, n, ch + g, i, half, sc);
+      }
+      multiply_fp4<true, true>(from, x + (i - lo) * kSteps * 2, sp, p.room, half, g, t, sc, acc);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&tail->rawfree[s.slot]);
+  }
+  WideSums r;
+#pragma unroll
+  for (int m = 0; m < 8; ++m) r.acc[m] = acc[m / 4][m % 4];
+  r.s = s;
+  r.ok = ok;
+  return r;
+}
+
 // SPLIT: one unit per cluster, each block a part of the reduction; else each block
 // takes a run of units, so that it seldom has other rows to fetch.
 template <bool FP4, bool SPLIT, int SETS>
 __global__ void __launch_bounds__(kThreads, 1)
 mp_k_expert_rows(const __grid_constant__ CUtensorMap map_w,
-                 const __grid_constant__ CUtensorMap map_s, const VecArgs p) {
+                 const __grid_constant__ CUtensorMap map_s, const __grid_constant__ VecArgs p) {
   constexpr int kSteps = Form<FP4>::kSteps;
   constexpr int kHalves = 4 / SETS;  // of a piece's reduction that go to other warps
   constexpr int kSetWarps = kHalves * kChWarps;
@@ -311,6 +430,7 @@ mp_k_expert_rows(const __grid_constant__ CUtensorMap map_w,
       mbar_init(&tail->rawfree[i], kSetWarps);
     }
     tail->failed = 0;
+    tail->wide = -1;
     mbar_init_fence();
   }
   pdl_wait_prior_grid();  // (nothing of the above touches global memory)
@@ -360,21 +480,6 @@ mp_k_expert_rows(const __grid_constant__ CUtensorMap map_w,
     const int set = warp / kSetWarps, half0 = kHalves > 1 ? warp % kSetWarps / kChWarps : 0;
     const int ch = warp % kChWarps * 32;
     const int g = lane >> 2, t = lane & 3;
-    const int groups = p.K / 32;
-    // MXFP4 scales that TMA cannot load: those of half of piece i, of four channels,
-    // from where they are
-    auto fetch_scales = [&](const Unit& n, int i, int half, uint32_t (&sc)[4]) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        // (past the last channel or step: codes are zeros, any scale will do)
-        const unsigned char* from =
-            p.scales + (int64_t(n.e) * p.N + min(n.col0 + ch + g + 8 * c, p.N - 1)) * groups;
-        sc[c] = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          sc[c] |= uint32_t(__ldg(from + min(i * 8 + half * 4 + j, groups - 1))) << (8 * j);
-      }
-    };
     RingAt s;
     bool ok = true;
     Unit n = {};
@@ -383,21 +488,35 @@ mp_k_expert_rows(const __grid_constant__ CUtensorMap map_w,
     // (SPLIT: blocks without a unit meet the others at the cluster's barriers)
     for (int u = first; u < last || (SPLIT && u == first); ++u) {
       const bool live = u < last;
-      if (live && staged != n.row0) {
-        stage_rows<FP4>(p, n.row0, n.nrows, lo * kSteps, (hi - lo) * kSteps, xs, sx);
+      const bool fresh = live && staged != n.row0;
+      if (fresh) {
+        stage_rows<FP4, false>(p, n.row0, n.nrows, lo * kSteps, (hi - lo) * kSteps, xs, sx,
+                               &tail->wide);
         staged = n.row0;
       }
       mul_warps_sync();  // the rows are there, and the sums of the unit before are used up
+      const bool wide = FP4 && live && *static_cast<volatile const int*>(&tail->wide) == n.row0;
+      if (wide && fresh) {
+        stage_wide(p, n, lo, hi, xs, sx);
+        mul_warps_sync();
+      }
       if (live) {
         const unsigned char* x = xs + (g & (p.room - 1)) * row_stride<FP4>(p.steps);
         float acc[2][4] = {};
-        for (int i = lo; i < hi; ++i, s.next(p.pieces)) {
+        if (wide) {
+          const WideSums ws = wide_products<SETS>(p, n, pieces, x, sx, tail, lo, hi, s, ok);
+#pragma unroll
+          for (int m = 0; m < 8; ++m) acc[m / 4][m % 4] = ws.acc[m];
+          s = ws.s;
+          ok = ws.ok;
+        }
+        for (int i = wide ? hi : lo; i < hi; ++i, s.next(p.pieces)) {
           if (s.slot % SETS != set) continue;
           // (scales that are fetched are on their way during the wait)
           uint32_t sc[2 / kHalves][4];
 #pragma unroll
           for (int h = 0; h < 2 / kHalves; ++h)
-            if (FP4 && !p.tma_scales) fetch_scales(n, i, half0 + h, sc[h]);
+            if (FP4 && !p.tma_scales) fetch_scales(p, n, ch + g, i, half0 + h, sc[h]);
           ok = ok && bounded_wait_warp(&tail->raw[s.slot], s.round & 1u, failed);
           if (!ok) break;
           const unsigned char* w0 = pieces + s.slot * kPiece + (ch + g) * 128;
@@ -420,11 +539,11 @@ mp_k_expert_rows(const __grid_constant__ CUtensorMap map_w,
             if (__any_sync(kFull, (large & 0x80808080u) != 0)) {
 #pragma unroll
               for (int h = 0; h < 2 / kHalves; ++h)
-                multiply_fp4<true>(w0, xp, sp, p.room, half0 + h, g, t, sc[h], acc);
+                multiply_fp4<true, false>(w0, xp, sp, p.room, half0 + h, g, t, sc[h], acc);
             } else {
 #pragma unroll
               for (int h = 0; h < 2 / kHalves; ++h)
-                multiply_fp4<false>(w0, xp, sp, p.room, half0 + h, g, t, sc[h], acc);
+                multiply_fp4<false, false>(w0, xp, sp, p.room, half0 + h, g, t, sc[h], acc);
             }
           } else {
 #pragma unroll

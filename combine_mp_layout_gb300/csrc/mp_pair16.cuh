@@ -1,6 +1,6 @@
 // mp_pair16.cuh -- what the bf16 products of the experts share: tensor maps of
-// bf16 arrays, loads and arrivals within a pair of blocks, and where a tile of
-// the ragged rows lies.
+// bf16 arrays, loads and arrivals within a pair of blocks, 4-bit codes as bf16, and
+// where a tile of the ragged rows lies.
 #pragma once
 
 #include <algorithm>
@@ -121,6 +121,26 @@ __device__ __forceinline__ void commit_to_pair(uint64_t* bar, int even) {
       "[%0], %1;" ::"r"(smem_addr(bar)),
       "h"(uint16_t(3u << even))
       : "memory");
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Eight e2m1 codes as bf16 pairs in order, 2^-126 times their value: sign to bit
+// 15, the two exponent bits and the mantissa bit to bits 8 to 6 (both shifts are
+// one product).
+__device__ __forceinline__ void codes8(uint32_t w, uint32_t (&o)[4]) {
+  const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // code 2i to bits 0-3, code 2i+1 to bits 16-19 (selector 8: a byte's sign bit, here 0)
+    uint32_t two;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(two) : "r"(even), "r"(odd), "r"(0x8480 + i * 0x1111));
+    o[i] = (two * 0x1040u) & 0x81c081c0u;
+  }
 }
 
 // A position in a ring of n slots: the slot and how often the ring went round.

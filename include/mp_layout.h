@@ -882,9 +882,11 @@ int mp_expert_matmul_wgrad_bf16(int E, int rows, int N, int K, const void *dy, c
  * mp_allgatherv_mxfp4 (with R = 1, a weight's rows being the rows) quantises them:
  *   out[r][n] = bf16( sum over k of a[r][k] * 2^(w_scales[e][n][k/32] - 127) * w[e][n][k] )
  * The weights are exact in bf16, so are the products; sums fp32, one rounding.  With
- * few rows (up to 16, or below 8 (E + 1)) a row's values are held in f16, per 32
- * channels relative to a power of two: those below 2^-32 of the 32's largest lose
- * bits, at most 2^-40 of it.
+ * few rows (`rows` up to 16, or below 8 (E + 1)) a row's values and the codes are
+ * multiplied first and each sum of 32 channels by the scale, just as exactly (but for
+ * values below 2^-99 beside one of 2^100 or more in the same 32: those below 2^-226 of
+ * the 32's largest can lose bits).  A row with values below 2^-32 of the largest of their
+ * 32 takes a slower form there, up to 2.5 times the time.
  *   in   a         bf16 [rows][K]
  *   in   w         uint8 [E][N][K/2]: two e2m1 codes a byte, the even k in the low
  *                  nibble (0, 1/2, 1, 3/2, 2, 3, 4, 6; bit 3 the sign)

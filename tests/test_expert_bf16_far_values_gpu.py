@@ -129,3 +129,96 @@ def test_swiglu_far_gates_leave_their_neighbours_alone(I):
     rest = far.clone()
     rest[3, 5] = rest[4, 6] = False
     assert float(b[0][rest].abs().max()) == 0.0
+
+
+# ------------------------------------------------------------------ rows whose values lie far apart
+
+
+@pytest.mark.parametrize("rows", [1, 3, 7, 16, 128])  # the row form, tiles
+@pytest.mark.parametrize("K,scale", [(224, 127), (512, 127), (512, 60), (512, 200), (736, 252)])
+@pytest.mark.parametrize("largest", [127, 60, 0, -60])
+def test_mxfp4_small_values_beside_large_ones(rows, K, scale, largest):
+    """The first of every 32 values of a row is the largest, and its weights are 0; the others are
+    2^-1 to 2^-220 of it with all of bf16's bits, and each is what one channel reads: it comes out
+    as if it stood alone, whatever the number of rows.  (Where that is below bf16's normal numbers
+    it may be off by bf16's smallest step: fp32 has few bits there too.)"""
+    N = K
+    k = torch.arange(K, device=DEV)
+    away = 1 + (k * 7) % 220
+    value = torch.ldexp(1 + ((k * 37) % 128).double() / 128, largest - away)
+    value[::32] = 1.5 * 2.0 ** (largest - 1)
+    a = value.to(BF)[None].expand(rows, K).contiguous()
+    a[1::2] *= -1
+    codes = torch.zeros((1, N, K), dtype=torch.int64, device=DEV)
+    codes[0, k, k] = torch.where(k % 32 == 0, 0, 1 + k % 7) + 8 * (k % 2)
+    w, s = packed(codes), torch.full((1, N, K // 32), scale, dtype=torch.uint8, device=DEV)
+    out, err = zeros((rows, N), BF), zeros(1, torch.int32)
+    B.check(B.mp_expert_matmul_mxfp4(1, rows, N, K, a, w, s, None, out, err))
+    torch.cuda.synchronize()
+    want = rounded(a.double() * fp4_ref(w, s)[0].diagonal())
+    differ = (out.double() != want) & ((want.abs() >= 2.0 ** -126)
+                                       | ((out.double() - want).abs() > 2.0 ** -133))
+    assert int(differ.sum()) == 0, [(int(c), float(a[0, c]), float(out[r, c]), float(want[r, c]))
+                                    for r, c in differ.nonzero()[:6].tolist()]
+    assert int(err) == 0
+
+
+@pytest.mark.parametrize("rows", [2, 6, 140])
+def test_mxfp4_far_values_of_one_row_and_the_rest(rows):
+    """Row 0 has values far apart, infinity and NaN where channels 1 and 2 alone have weights that
+    are not 0; the other rows keep their bits, and an infinite weight makes the smallest value
+    infinite."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(52)
+    N, K = 264, 512
+    codes = torch.randint(0, 16, (1, N, K), generator=g, device=DEV)
+    a = torch.randn((rows, K), generator=g, device=DEV).round().clamp(-2, 2).to(BF)
+    s = torch.full((1, N, K // 32), 127, dtype=torch.uint8, device=DEV)
+    codes[0, 3], codes[0, 3, 40] = 0, 7
+    s[0, 3, 1] = 254                     # 6 * 2^127, of channel 3 alone
+    w, err = packed(codes), zeros(1, torch.int32)
+    clean, dirty = zeros((rows, N), BF), zeros((rows, N), BF)
+    B.check(B.mp_expert_matmul_mxfp4(1, rows, N, K, a, w, s, None, clean, err))
+    b = a.clone()
+    b[0] = 0
+    b[0, 32], b[0, 40], b[0, 41] = 2.0 ** 60, -2.0 ** -100, 1.0
+    B.check(B.mp_expert_matmul_mxfp4(1, rows, N, K, b, w, s, None, dirty, err))
+    torch.cuda.synchronize()
+    assert torch.equal(clean[1:, :3], dirty[1:, :3]) and torch.equal(clean[1:, 4:], dirty[1:, 4:])
+    assert float(dirty[0, 3]) == -math.inf
+    ref = fp4_ref(w, s)[0]
+    y, size = b[0].double() @ ref.t(), b[0].double().abs() @ ref.abs().t()
+    rest = torch.arange(N, device=DEV) != 3
+    # (three terms: 2^-23 a step of their sum, and the rounding to bf16)
+    tol = 2.0 ** -8 * y.abs() + 3 * 2.0 ** -23 * size
+    assert bool(((dirty[0].double() - y).abs() <= tol)[rest].all())
+    b[0, 300], b[0, 41] = math.nan, math.inf
+    B.check(B.mp_expert_matmul_mxfp4(1, rows, N, K, b, w, s, None, dirty, err))
+    torch.cuda.synchronize()
+    assert bool(dirty[0].isnan().all()) and torch.equal(clean[1:, 4:], dirty[1:, 4:])
+    assert int(err) == 0
+
+
+def test_mxfp4_rows_of_both_kinds_in_turn():
+    """Many experts of a few rows each, every other expert's with values far apart: a block that
+    takes several experts one after the other takes each one's rows as they want it."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(53)
+    E, N, K, each = 40, 1160, 736, 3
+    rows = E * each
+    codes = torch.randint(0, 16, (E, N, K), generator=g, device=DEV)
+    codes[..., 0::32] = 0
+    w = packed(codes)
+    s = torch.randint(126, 129, (E, N, K // 32), generator=g, device=DEV, dtype=torch.uint8)
+    a = torch.randint(-2, 3, (rows, K), generator=g, device=DEV).to(BF)
+    expert = torch.arange(rows, device=DEV) // each
+    far = expert % 2 == 1
+    a[far] *= 2.0 ** -50                 # all but the first of 32 values, whose weights are 0
+    a[far, 0::32] = 3.0
+    off = (torch.arange(E + 1, device=DEV) * each).to(torch.int32)
+    out, err = zeros((rows, N), BF), zeros(1, torch.int32)
+    B.check(B.mp_expert_matmul_mxfp4(E, rows, N, K, a, w, s, off, out, err))
+    torch.cuda.synchronize()
+    want = torch.cat([a[e * each:(e + 1) * each].double() @ fp4_ref(w[e], s[e]).t()
+                      for e in range(E)])
+    assert torch.equal(out.double(), rounded(want)) and int(err) == 0
