@@ -222,3 +222,36 @@ def test_mxfp4_rows_of_both_kinds_in_turn():
     want = torch.cat([a[e * each:(e + 1) * each].double() @ fp4_ref(w[e], s[e]).t()
                       for e in range(E)])
     assert torch.equal(out.double(), rounded(want)) and int(err) == 0
+
+
+@pytest.mark.parametrize("rows", [2, 8, 128])
+@pytest.mark.parametrize("far", [False, True])  # values far apart in the row
+@pytest.mark.parametrize("scale", [245, 252, 253, 254, 255])
+def test_mxfp4_largest_scales(rows, far, scale):
+    """Every code at the largest scales: what passes bf16's largest number is infinite, 255 is
+    NaN."""
+    N, K, at = 32, 512, 103
+    n = torch.arange(N, device=DEV)
+    codes = torch.zeros((1, N, K), dtype=torch.int64, device=DEV)
+    codes[0, :, at] = n % 16
+    s = torch.full((1, N, K // 32), 127, dtype=torch.uint8, device=DEV)
+    s[0, :, at // 32] = scale
+    s[0, 16:, at // 32] = 127            # (neighbours in the warp)
+    w = packed(codes)
+    a = zeros((rows, K), BF)
+    a[:, at] = 2.0 ** -100
+    if far:
+        a[:, at + 1] = 2.0 ** 20         # (its weights are 0, but not of scale 255)
+    ref = fp4_ref(w, torch.clamp(s, max=254))[0, :, at]
+    want = ref * 2.0 ** -100
+    want = torch.where(ref.abs() >= 2.0 ** 128, torch.copysign(torch.full_like(ref, math.inf), ref),
+                       want)
+    if scale == 255:
+        want[:16] = math.nan
+    out, err = zeros((rows, N), BF), zeros(1, torch.int32)
+    B.check(B.mp_expert_matmul_mxfp4(1, rows, N, K, a, w, s, None, out, err))
+    torch.cuda.synchronize()
+    got = out.double()
+    same = (got == rounded(want)) | (got.isnan() & want.isnan())
+    assert bool(same.all()), (got[0] - want).nonzero()
+    assert int(err) == 0
