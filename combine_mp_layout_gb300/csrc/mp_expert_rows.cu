@@ -24,10 +24,11 @@
 // lose bits.  The products of 32 channels are summed by the tensor core, then multiplied
 // by both powers of two and added up in fp32.
 //
-// Measured, 4096 x 7168: one bf16 row 13.1 us (4.5 TB/s of weights; 8.2 us with the
-// weights in L2), one MXFP4 row 8.1; MXFP4 rows over 32 experts, one each 94 us (5.3 TB/s),
-// two each 104 (70 without the products; 60% of the issue slots), 61 drawn at random 85 to
-// 99 by how many experts have none.
+// Measured, 4096 x 7168: one bf16 row 13.3 us (4.4 TB/s of weights; 8.2 us with the
+// weights in L2), one MXFP4 row 8.1; MXFP4 rows over 32 experts, one each 95 us (5.2 TB/s),
+// two each 106 (59% of the issue slots; 70 us without the products), 61 drawn at random 88
+// to 100 by how many experts have none.  (The look for values that f16 cannot hold is 1 to
+// 2% of these.)
 #include <algorithm>
 #include <cstdint>
 #include <cuda.h>

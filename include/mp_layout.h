@@ -831,6 +831,11 @@ int mp_swiglu_backward_e4m3(int rows, int I, const void *gate_up, const float *r
  *   out[r][n] = bf16( sum over k of a[r][k] * w[e][n][k] )
  * for the rows expert_offsets[e] <= r < expert_offsets[e+1] of every expert e;
  * products exact, sums fp32, one rounding.
+ * `rows` and E alone choose the kernel: up to 16 rows, or below 4 (E + 1), an expert's
+ * weights are read once for every 4 or 8 of its rows, as decoding wants it; above that
+ * once for up to 256, as it pays from about four rows an expert on.  So with few `rows`
+ * most of them on one expert take up to four times (256 rows) what they would in tiles,
+ * but no longer than as many spread over all experts.
  *   in   a               bf16 [rows][K]
  *   in   w               bf16 [E][N][K]
  *   in   expert_offsets  int32 [E+1], or NULL for E == 1 (all rows)
@@ -861,7 +866,9 @@ int mp_expert_matmul_dgrad_bf16(int E, int rows, int N, int K, const void *dy, c
 /*
  * mp_expert_matmul_wgrad_bf16 -- the gradient of the weights:
  *   g[e][n][k] = sum over the rows r of expert e of dy[r][n] * a[r][k]
- * products exact, sums fp32; dw = bf16(g) (MP_BF16), dw = g (MP_FP32), or dw += g
+ * products exact, sums fp32 (which the tensor core cuts where an fp32 addition rounds:
+ * off by 7e-7 in the 2-norm at 1,200 rows, plain fp32 sums by 2e-7); dw = bf16(g)
+ * (MP_BF16), dw = g (MP_FP32), or dw += g
  * (MP_FP32 with accumulate != 0: one fp32 addition per weight, so that several
  * batches' gradients add up in one array).  Experts without rows get zeros, or keep
  * what they have with accumulate (so do, here, those whose offsets decrease; a
@@ -886,7 +893,10 @@ int mp_expert_matmul_wgrad_bf16(int E, int rows, int N, int K, const void *dy, c
  * multiplied first and each sum of 32 channels by the scale, just as exactly (but for
  * values below 2^-99 beside one of 2^100 or more in the same 32: those below 2^-226 of
  * the 32's largest can lose bits).  A row with values below 2^-32 of the largest of their
- * 32 takes a slower form there, up to 2.5 times the time.
+ * 32 takes a slower form there, up to 2.5 times the time.  `rows` and E alone choose the
+ * kernel, as in mp_expert_matmul_bf16; most rows on one expert take up to seven times
+ * (2,047 rows, 256 experts) what they would in tiles there, but no longer than as many
+ * spread over all experts; and few rows in an array with room for many take the tiles.
  *   in   a         bf16 [rows][K]
  *   in   w         uint8 [E][N][K/2]: two e2m1 codes a byte, the even k in the low
  *                  nibble (0, 1/2, 1, 3/2, 2, 3, 4, 6; bit 3 the sign)
