@@ -833,9 +833,10 @@ int mp_swiglu_backward_e4m3(int rows, int I, const void *gate_up, const float *r
  * products exact, sums fp32, one rounding.
  * `rows` and E alone choose the kernel: up to 16 rows, or below 4 (E + 1), an expert's
  * weights are read once for every 4 or 8 of its rows, as decoding wants it; above that
- * once for up to 256, as it pays from about four rows an expert on.  So with few `rows`
- * most of them on one expert take up to four times (256 rows) what they would in tiles,
- * but no longer than as many spread over all experts.
+ * once for up to 256, as it pays from about four rows an expert on.  How the rows lie
+ * over the experts is not known to it: few `rows` that are all one expert's take up to
+ * four times (256 rows) what they would in tiles, which is less than as many spread over
+ * the experts take; all but one each on one expert take up to a sixth more than those.
  *   in   a               bf16 [rows][K]
  *   in   w               bf16 [E][N][K]
  *   in   expert_offsets  int32 [E+1], or NULL for E == 1 (all rows)
@@ -894,9 +895,9 @@ int mp_expert_matmul_wgrad_bf16(int E, int rows, int N, int K, const void *dy, c
  * values below 2^-99 beside one of 2^100 or more in the same 32: those below 2^-226 of
  * the 32's largest can lose bits).  A row with values below 2^-32 of the largest of their
  * 32 takes a slower form there, up to 2.5 times the time.  `rows` and E alone choose the
- * kernel, as in mp_expert_matmul_bf16; most rows on one expert take up to seven times
- * (2,047 rows, 256 experts) what they would in tiles there, but no longer than as many
- * spread over all experts; and few rows in an array with room for many take the tiles.
+ * kernel, as in mp_expert_matmul_bf16.  2,047 rows and 256 experts, for example: spread
+ * evenly 0.6 of the time of the tiles, all but one each on one expert 1.06 of it, all on
+ * one 7 times.  Few rows in an array with room for many take the tiles.
  *   in   a         bf16 [rows][K]
  *   in   w         uint8 [E][N][K/2]: two e2m1 codes a byte, the even k in the low
  *                  nibble (0, 1/2, 1, 3/2, 2, 3, 4, 6; bit 3 the sign)
